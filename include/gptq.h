@@ -78,7 +78,8 @@ typedef enum {
     GPTQ_OP_HESSIAN_TOKENS = 5,
     GPTQ_OP_SMOOTH = 6, /* gptq_smooth_scales */
     GPTQ_OP_AWQ = 7,    /* gptq_awq_search (cfg: bits, symmetric, group_size) */
-    GPTQ_OP_CALIBRATE = 8 /* gptq_calibrate_hessian (d_in, n_tok) */
+    GPTQ_OP_CALIBRATE = 8, /* gptq_calibrate_hessian (d_in, n_tok) */
+    GPTQ_OP_GEMV = 10      /* gptq_gemv, gptq_gemv_gated (d_in, n_tok = M) */
 } gptq_op;
 
 /*
@@ -388,6 +389,96 @@ GPTQ_API gptq_status gptq_w4a16_gemm(const void *X, gptq_dtype x_dtype, int64_t 
                                      const int32_t *kperm, const uint32_t *packed, const float *scales,
                                      const float *zeros, int32_t group_size, int64_t d_out, float *Y, int64_t ldy,
                                      void *ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * A quantized layer in its packed form, or a stack of equal ones (the experts
+ * of a mixture), as gptq_pack_codes writes it:
+ *   W[o][k] = (q[o][k] - zeros[o][k/g]) * scales[o][k/g]
+ * with q[o][k] the b-bit packed column k of row o and g = group_size (0: d_in).
+ * A stack of E holds its matrices one after the other: packed
+ * [E][d_out][d_in*bits/32], scales and zeros [E][d_out][d_in/g], kperm [E][d_in].
+ * The struct lives on the host and is read during the call; its pointers are
+ * device pointers.
+ */
+typedef struct {
+    const uint32_t *packed; /* 16-byte aligned */
+    const float *scales;
+    const float *zeros;   /* integers in 0 .. 2^bits - 1, as the quantizer stores them */
+    const int32_t *kperm; /* the perm the codes were packed with, or NULL */
+    int64_t d_out, d_in;  /* d_in a multiple of 32, at most 2^20; d_out at most 2^30 */
+    int32_t bits;         /* 2, 3, 4 or 8 */
+    int32_t group_size;   /* a multiple of 32 that divides d_in, or 0 */
+} gptq_packed;
+
+/*
+ * Products of a few tokens with a packed layer (page "LLM 量化方法原理与实现
+ * 详解", §6.2: weight-only quantization, 16-bit activations; §2.2: (q - z) s),
+ * the single-token form of serving it:
+ *
+ *   gptq_gemv        Y[m][o] = sum_k X[m][kperm ? kperm[k] : k] W[o][k] + bias[o]
+ *   gptq_gemv_gated  H[m][o] = silu(G[m][o]) * U[m][o], the first half of a gated
+ *                    MLP: G and U are the products with `gate` and `up`, and
+ *                    silu(v) = v / (1 + exp(-v)).
+ *
+ *   X       fp16 or bf16 [M][ldx], one row per token, 0 <= M <= 16; 16-byte
+ *           aligned, ldx >= d_in and a multiple of 8.
+ *   w       the layer.  gate and up agree in d_out, d_in, bits, group_size and
+ *           kperm (they see the same inputs, hence one Hessian and one order).
+ *   bias    [d_out] fp32 or NULL.
+ *   Y, H    fp16, bf16 or fp32 [M][ldy] out, ldy >= d_out; not X's memory.
+ *   ws      scratch of gptq_workspace_bytes(GPTQ_OP_GEMV, 0, d_in, M, NULL), used
+ *           (and needed) only with a kperm; 16-byte aligned.
+ * Sums are fp32 over exact products of the integers q - z (bf16 X with 2-4
+ * bits: 2^bits + q, less (2^bits + z) times the sum of x) with x; the scale
+ * multiplies a group's sum; the result is rounded once.  Deterministic.  A
+ * token whose activations are not all finite gets results that are not finite
+ * or NaN, in its own row only.  Out-of-range kperm entries are clamped.
+ * M == 0 is a no-op.  GPTQ_ERR_UNSUPPORTED for other bits, M, group sizes or
+ * sizes than the above (more tokens: gptq_w4a16_gemm).
+ */
+GPTQ_API gptq_status gptq_gemv(const void *X, gptq_dtype x_dtype, int64_t M, int64_t ldx, const gptq_packed *w,
+                               const float *bias, void *Y, gptq_dtype y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
+                               hipStream_t stream);
+GPTQ_API gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t M, int64_t ldx, const gptq_packed *gate,
+                                     const gptq_packed *up, void *H, gptq_dtype h_dtype, int64_t ldh, void *ws,
+                                     size_t ws_bytes, hipStream_t stream);
+
+/*
+ * A whole mixture-of-experts layer for a few tokens, its experts packed:
+ *
+ *   L[t][e] = sum_i X[t][i] router[e][i];  p = softmax(L[t]) over the experts
+ *   ids[t]  = the top_k experts of the largest L, in descending order, ties to
+ *             the lower index; weights[t][j] = p[ids[t][j]], divided by their
+ *             sum when renormalize
+ *   Y[t]    = sum_j weights[t][j] Down_e h,  h = silu(Gate_e x) * (Up_e x),
+ *             x = X[t], e = ids[t][j]
+ *
+ *   X       fp16 or bf16 [T][ldx], 0 <= T <= 16, 16-byte aligned, ldx >= d and a
+ *           multiple of 8.
+ *   router  [n_experts][d] in router_dtype (fp32, or X's type), 16-byte aligned;
+ *           its products are summed in fp64, since a rounding could change the
+ *           choice.  A NaN logit ranks below every number.  NULL: the caller
+ *           routes, and ids and weights are inputs.
+ *   gate, up  stacks of n_experts layers [d_ff][d]; down: [d][d_ff].  gate and up
+ *           agree as in gptq_gemv_gated.  All three have the same bits.
+ *   ids     [T][top_k] int32 and weights [T][top_k] fp32: outputs (either may be
+ *           NULL) with a router, inputs without.  As inputs, an id outside
+ *           0 .. n_experts - 1 adds nothing (padding), and one that a token
+ *           names twice counts with the sum of its weights.
+ *   Y       fp16, bf16 or fp32 [T][ldy] out, ldy >= d; not X's memory.
+ *   ws      scratch of gptq_moe_workspace_bytes(), 16-byte aligned.
+ * 1 <= top_k <= min(n_experts, 16), n_experts <= 512.  h is rounded to X's type
+ * between the two products, as the layers of an unpacked model round it; every
+ * sum is fp32 (the router's fp64), the result is rounded once.  Deterministic.
+ * T == 0 is a no-op.
+ */
+GPTQ_API gptq_status gptq_moe_layer(const void *X, gptq_dtype x_dtype, int64_t T, int64_t ldx, const void *router,
+                                    gptq_dtype router_dtype, int32_t n_experts, int32_t top_k, int32_t renormalize,
+                                    const gptq_packed *gate, const gptq_packed *up, const gptq_packed *down,
+                                    int32_t *ids, float *weights, void *Y, gptq_dtype y_dtype, int64_t ldy, void *ws,
+                                    size_t ws_bytes, hipStream_t stream);
+GPTQ_API gptq_status gptq_moe_workspace_bytes(int64_t T, int64_t d, int64_t d_ff, int32_t n_experts, int32_t top_k,
+                                              size_t *out);
 
 /*
  * Kernel timing for benchmarks (off by default).  While enabled, the column

@@ -57,6 +57,77 @@ gptq_status check_quantize(float *W, int64_t d_out, int64_t d_in, const float *U
     return GPTQ_OK;
 }
 
+bool few_dtype(gptq_dtype t) { return t == GPTQ_DT_BF16 || t == GPTQ_DT_F16; }
+bool out_dtype(gptq_dtype t) { return few_dtype(t) || t == GPTQ_DT_F32; }
+
+// A packed layer, or a stack of them, for the few-token products.
+gptq_status check_packed(const gptq_packed *w, const char *fn, const char *name) {
+    if (!w) return fail(GPTQ_ERR_INVALID_ARG, "%s: %s is NULL", fn, name);
+    if (w->d_out <= 0 || w->d_in <= 0) return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: sizes must be > 0", fn, name);
+    if (w->bits < 2 || w->bits > 8) return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: bits=%d outside 2..8", fn, name, w->bits);
+    if (w->group_size < 0 || (w->group_size > 0 && w->d_in % w->group_size != 0))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: group_size does not divide d_in", fn, name);
+    if (w->bits != 2 && w->bits != 3 && w->bits != 4 && w->bits != 8)
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: bits must be 2, 3, 4 or 8", fn, name);
+    if (w->d_in % 32 != 0 || w->group_size % 32 != 0)
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: d_in and group_size must be multiples of 32", fn, name);
+    if (w->d_in > ((int64_t)1 << 20) || w->d_out > ((int64_t)1 << 30))
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: d_in above 2^20 or d_out above 2^30", fn, name);
+    if (!w->packed || !w->scales || !w->zeros) return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: NULL pointer", fn, name);
+    if (!aligned(w->packed) || !aligned(w->scales, 4) || !aligned(w->zeros, 4) || (w->kperm && !aligned(w->kperm, 4)))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: packed must be 16-byte aligned, the other pointers 4-byte aligned", fn, name);
+    return GPTQ_OK;
+}
+
+gptq_status check_pair(const gptq_packed *gate, const gptq_packed *up, const char *fn) {
+    gptq_status st = check_packed(gate, fn, "gate");
+    if (st == GPTQ_OK) st = check_packed(up, fn, "up");
+    if (st != GPTQ_OK) return st;
+    if (gate->d_out != up->d_out || gate->d_in != up->d_in || gate->bits != up->bits || gate->group_size != up->group_size ||
+        gate->kperm != up->kperm)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: gate and up must agree in sizes, bits, group_size and kperm", fn);
+    return GPTQ_OK;
+}
+
+// Activations and results of a few-token product.
+gptq_status check_few(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, int64_t d_in, const void *Y, gptq_dtype y_dt,
+                      int64_t ldy, int64_t d_out, const char *fn) {
+    if (!few_dtype(x_dt) || !out_dtype(y_dt))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: activations must be fp16 or bf16, results fp16, bf16 or fp32", fn);
+    if (M > 0 && (!X || !Y)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (ldx < d_in || ldy < d_out) return fail(GPTQ_ERR_INVALID_ARG, "%s: leading dimension too small", fn);
+    if (!aligned(X) || ldx % 8 != 0 || !aligned(Y, y_dt == GPTQ_DT_F32 ? 4 : 2))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: X must be 16-byte aligned with ldx a multiple of 8, Y aligned to its type", fn);
+    return GPTQ_OK;
+}
+
+gptq_status run_gemv_checked(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed *w,
+                             const gptq_packed *up, const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws,
+                             size_t ws_bytes, hipStream_t stream, const char *fn) {
+    if (M < 0) return fail(GPTQ_ERR_INVALID_ARG, "%s: M must be >= 0", fn);
+    if (M > 16) return fail(GPTQ_ERR_UNSUPPORTED, "%s: at most 16 tokens", fn);
+    gptq_status st = check_few(X, x_dt, M, ldx, w->d_in, Y, y_dt, ldy, w->d_out, fn);
+    if (st != GPTQ_OK) return st;
+    if (bias && !aligned(bias, 4)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned bias", fn);
+    if (M == 0) return GPTQ_OK;
+    const size_t need = w->kperm ? gptq::gemv_ws_bytes(M, w->d_in) : 0;
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
+    if (need > 0 && !aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    return hip_status(gptq::run_gemv(X, x_dt, M, ldx, *w, up, bias, Y, y_dt, ldy, ws, stream), fn);
+}
+
+gptq_status check_moe_sizes(int64_t T, int64_t d, int64_t d_ff, int32_t n_experts, int32_t top_k, const char *fn) {
+    if (T < 0 || d <= 0 || d_ff <= 0 || n_experts <= 0 || top_k <= 0 || top_k > n_experts)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: bad sizes (1 <= top_k <= n_experts)", fn);
+    if (T > gptq::kMoeMaxTokens || n_experts > gptq::kMoeMaxExperts || top_k > gptq::kMoeMaxTopK)
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: at most %d tokens, %d experts and %d of them per token", fn,
+                    gptq::kMoeMaxTokens, gptq::kMoeMaxExperts, gptq::kMoeMaxTopK);
+    if (d > ((int64_t)1 << 20) || d_ff > ((int64_t)1 << 20))
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: d or d_ff above 2^20", fn);
+    return GPTQ_OK;
+}
+
 // Scratch memory of gptq_quantize_layer_noalloc: one fixed array per device,
 // part of the library's device image (the runtime places it on each device
 // the library runs on, for the life of the process).  In host code `scratch`
@@ -152,6 +223,9 @@ gptq_status gptq_workspace_bytes(int op, int64_t d_out, int64_t d_in, int64_t n_
         *out = gptq::awq_ws_bytes(d_out, d_in, *cfg);
         return GPTQ_OK;
     }
+    case GPTQ_OP_GEMV:
+        *out = gptq::gemv_ws_bytes(n_tok, d_in);
+        return GPTQ_OK;
     case GPTQ_OP_W4A16:  // the largest plan over the group sizes (the plan depends on g only through 32, 64, 128 | g)
         *out = std::max(gptq::w4a16_ws_bytes(n_tok, d_in, d_out, 32),
                         std::max(gptq::w4a16_ws_bytes(n_tok, d_in, d_out, 64), gptq::w4a16_ws_bytes(n_tok, d_in, d_out, 128)));
@@ -378,6 +452,62 @@ gptq_status gptq_w4a16_gemm(const void *X, gptq_dtype x_dtype, int64_t M, int64_
     const size_t need = gptq::w4a16_ws_bytes(M, d_in, d_out, g);
     if (!ws || ws_bytes < need) return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
     return hip_status(gptq::run_w4a16(X, M, d_in, ldx, kperm, packed, scales, zeros, g, d_out, Y, ldy, ws, stream), fn);
+}
+
+gptq_status gptq_gemv(const void *X, gptq_dtype x_dtype, int64_t M, int64_t ldx, const gptq_packed *w, const float *bias,
+                      void *Y, gptq_dtype y_dtype, int64_t ldy, void *ws, size_t ws_bytes, hipStream_t stream) {
+    const char *fn = "gptq_gemv";
+    const gptq_status st = check_packed(w, fn, "w");
+    if (st != GPTQ_OK) return st;
+    return run_gemv_checked(X, x_dtype, M, ldx, w, nullptr, bias, Y, y_dtype, ldy, ws, ws_bytes, stream, fn);
+}
+
+gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t M, int64_t ldx, const gptq_packed *gate,
+                            const gptq_packed *up, void *H, gptq_dtype h_dtype, int64_t ldh, void *ws, size_t ws_bytes,
+                            hipStream_t stream) {
+    const char *fn = "gptq_gemv_gated";
+    const gptq_status st = check_pair(gate, up, fn);
+    if (st != GPTQ_OK) return st;
+    return run_gemv_checked(X, x_dtype, M, ldx, gate, up, nullptr, H, h_dtype, ldh, ws, ws_bytes, stream, fn);
+}
+
+gptq_status gptq_moe_workspace_bytes(int64_t T, int64_t d, int64_t d_ff, int32_t n_experts, int32_t top_k, size_t *out) {
+    const char *fn = "gptq_moe_workspace_bytes";
+    if (!out) return fail(GPTQ_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    const gptq_status st = check_moe_sizes(T, d, d_ff, n_experts, top_k, fn);
+    if (st != GPTQ_OK) return st;
+    *out = gptq::moe_ws_bytes(T, d, d_ff, n_experts, top_k);
+    return GPTQ_OK;
+}
+
+gptq_status gptq_moe_layer(const void *X, gptq_dtype x_dtype, int64_t T, int64_t ldx, const void *router,
+                           gptq_dtype router_dtype, int32_t n_experts, int32_t top_k, int32_t renormalize,
+                           const gptq_packed *gate, const gptq_packed *up, const gptq_packed *down, int32_t *ids,
+                           float *weights, void *Y, gptq_dtype y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
+                           hipStream_t stream) {
+    const char *fn = "gptq_moe_layer";
+    gptq_status st = check_pair(gate, up, fn);
+    if (st == GPTQ_OK) st = check_packed(down, fn, "down");
+    if (st == GPTQ_OK) st = check_moe_sizes(T, gate->d_in, gate->d_out, n_experts, top_k, fn);
+    if (st != GPTQ_OK) return st;
+    if (down->d_in != gate->d_out || down->d_out != gate->d_in || down->bits != gate->bits)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: down must be [d][d_ff] with the bits of gate [d_ff][d]", fn);
+    st = check_few(X, x_dtype, T, ldx, gate->d_in, Y, y_dtype, ldy, gate->d_in, fn);
+    if (st != GPTQ_OK) return st;
+    if (router && router_dtype != GPTQ_DT_F32 && router_dtype != x_dtype)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: the router must be fp32 or of X's type", fn);
+    if (T > 0 && !router && (!ids || !weights))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: without a router, ids and weights are inputs", fn);
+    if ((router && !aligned(router)) || (ids && !aligned(ids, 4)) || (weights && !aligned(weights, 4)))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    if (T == 0) return GPTQ_OK;
+    const size_t need = gptq::moe_ws_bytes(T, gate->d_in, gate->d_out, n_experts, top_k);
+    if (!ws || ws_bytes < need)
+        return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
+    if (!aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    return hip_status(gptq::run_moe(X, x_dtype, T, ldx, router, router_dtype, n_experts, top_k, renormalize ? 1 : 0, *gate,
+                                    *up, *down, ids, weights, Y, y_dtype, ldy, ws, stream),
+                      fn);
 }
 
 }  // extern "C"

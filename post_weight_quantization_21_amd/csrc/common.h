@@ -117,6 +117,20 @@ hipError_t run_w4a16(const void *X, int64_t M, int64_t d_in, int64_t ldx, const 
                      float *Y, int64_t ldy, void *ws, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// Packed layers for a few tokens (gemv.hip, moe.hip)
+// ---------------------------------------------------------------------------
+size_t gemv_ws_bytes(int64_t M, int64_t d_in);
+// up: NULL for the plain product, else the second matrix of the gated one.
+hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,
+                    const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws, hipStream_t s);
+constexpr int kMoeMaxTokens = 16, kMoeMaxTopK = 16, kMoeMaxExperts = 512;
+size_t moe_ws_bytes(int64_t T, int64_t d, int64_t d_ff, int n_experts, int top_k);
+hipError_t run_moe(const void *X, gptq_dtype x_dt, int64_t T, int64_t ldx, const void *router, gptq_dtype router_dt,
+                   int n_experts, int top_k, int renormalize, const gptq_packed &gate, const gptq_packed &up,
+                   const gptq_packed &down, int32_t *ids, float *weights, void *Y, gptq_dtype y_dt, int64_t ldy,
+                   void *ws, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Per-channel scaling before the pass (prepass.hip)
 // ---------------------------------------------------------------------------
 hipError_t run_channel_stats(const void *X, gptq_dtype dt, int64_t d_in, int64_t n_tok, int64_t ldx, float *absmax,

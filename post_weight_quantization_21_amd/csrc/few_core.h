@@ -1,0 +1,346 @@
+// Products of at most sixteen rows of activations with packed b-bit weights
+// (b = 2, 3, 4, 8): the part one wave computes, shared by the matrix-vector
+// products (gemv.hip) and the experts' products (moe.hip).
+//
+//   acc[m][o] = sum_k x[m][k] (q[o][k] - z[o][k/g]) s[o][k/g]
+//
+// A row's codes are a little-endian bit stream; 32 codes (a "unit") are b whole
+// words.  A wave owns 16 weight rows per tile and walks K in steps of 128
+// columns: lane l = 16 kb + r reads unit 4 step + kb of row r and turns it into
+// four fragments of eight 16-bit floats; v_mfma_f32_16x16x32 multiplies a
+// fragment (lane: column r of B, eight K values) with the same columns of x
+// (lane: row m = l % 16 of A).  Which K a slot holds does not matter as long as
+// x and the weights agree, so a fragment takes the codes in whatever order they
+// unpack cheapest, and x follows.
+//
+// The result has its weight row in the lane's column (D[4 kb + i][r], i = 0..3,
+// m = 4 kb + i), so scale and zero are one value per lane.  The matrix cores
+// are not what bounds these products: at full HBM rate they are busy a quarter
+// of the time for one token as for sixteen, so M <= 16 runs on them throughout.
+#pragma once
+
+#include "common.h"
+
+namespace gptq {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int kFewRows = 16;    // rows of activations
+constexpr int kTileRows = 16;   // weight rows of a tile
+constexpr int kUnit = 32;       // codes of a unit: b words
+constexpr int kStep = 128;      // columns of a step: one unit per lane row
+constexpr int64_t kFewMaxIn = (int64_t)1 << 20;  // columns a packed matrix may have (32-bit offsets within a row)
+
+// Exact quotients n / d of small numbers: n, d < 2^15 (units and steps of a row).
+struct SmallDiv {
+    uint32_t magic;  // floor(2^32 / d) + 1, or 0 for d = 1
+    __device__ __forceinline__ uint32_t div(uint32_t n) const { return magic ? __umulhi(n, magic) : n; }
+};
+inline SmallDiv small_div(uint32_t d) { return {d <= 1 ? 0u : (uint32_t)((uint64_t(1) << 32) / d + 1)}; }
+
+// One stack of packed matrices as the kernels see it.
+struct PackedDev {
+    const uint32_t *packed;
+    const float *scales, *zeros;
+    int32_t d_out, words, groups;  // rows, words per row, groups per row
+    int32_t units;                 // units per row (d_in / 32)
+    int32_t split;                 // a group ends inside a step: fold per unit
+    SmallDiv by;                   // steps (split: units) per group
+};
+
+PackedDev packed_dev(const gptq_packed &w);  // gemv.hip
+
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {  // a's upper half with b's lower half
+    const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t &a, uint32_t &b) {  // a's odd rows of 16 lanes with b's even rows
+    const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = r[0];
+    b = r[1];
+}
+// Registers i x lane rows kb transposed: out[i] in lane row kb = in[kb] of lane row i.
+__device__ __forceinline__ void transpose4(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d) {
+    swap32(a, c);
+    swap32(b, d);
+    swap16(a, b);
+    swap16(c, d);
+}
+// out[j] = v of lane row j, in every lane row.
+__device__ __forceinline__ void spread4(float v, float out[4]) {
+    uint32_t a = __float_as_uint(v), b = a;
+    swap32(a, b);
+    uint32_t c = a, d = b;
+    swap16(a, c);
+    swap16(b, d);
+    out[0] = __uint_as_float(a);
+    out[1] = __uint_as_float(c);
+    out[2] = __uint_as_float(b);
+    out[3] = __uint_as_float(d);
+}
+
+template <typename T>
+struct Vec8;
+template <>
+struct Vec8<_Float16> {
+    typedef f16x8 V;
+    __device__ static floatx4 mma(V a, V b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+};
+template <>
+struct Vec8<__bf16> {
+    typedef bf16x8 V;
+    __device__ static floatx4 mma(V a, V b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+};
+
+// Bits [at, at + b) of a unit, at a compile-time position.
+template <int b>
+__device__ __forceinline__ uint32_t code_at(const uint32_t *w, int c) {
+    const int at = b * c, i = at >> 5, sh = at & 31;
+    uint32_t v = sh + b > 32 ? __builtin_amdgcn_alignbit(w[i + 1], w[i], sh) : w[i] >> sh;
+    return sh + b == 32 ? v : v & ((1u << b) - 1u);
+}
+
+// Fragment i of a unit (eight codes) as 16-bit floats of which column j comes
+// from code col(i, j).  fp16 gives q - z, exactly: masking a code into mantissa
+// bits [s, s + b) of an fp16 with exponent 10 makes 1024 + q 2^s, and a packed
+// multiply-add with 2^-s takes the rest away without rounding.  bf16 has no
+// packed arithmetic, so it gives 2^b + q (the code shifted to the top of the
+// mantissa) and the caller takes (2^b + z) sum x away with one more matrix
+// instruction per fragment, whose B operand is the constant -(2^b + z); only
+// the fp32 sums round.  Eight-bit codes fill bf16's significand, so they go
+// through fp32: q - z is an integer of at most 255 and exact in bf16.
+template <int b, typename T>
+struct Codes {
+    typedef typename Vec8<T>::V V;
+    static constexpr bool kHalf = sizeof(T) == 2 && !__is_same(T, __bf16);
+    static constexpr bool kOffset = !kHalf && b < 8;  // fragments hold 2^b + q
+    uint32_t magic;
+    uint32_t zb;       // offset form: the pair -(2^b + z) in bf16
+    f16x2 z16[5];      // fp16: the pair 2^(10 - s) + z for s = 0, 2, 4, 6, 8
+    float z;
+
+    __device__ __forceinline__ Codes() {
+        magic = kHalf ? 0x64006400u : (uint32_t)(0x3F80 + 128 * b) * 0x10001u;  // fp16 1024, bf16 2^b
+        asm volatile("" : "+v"(magic));  // a register operand: VOP3 takes no literal
+    }
+    __device__ __forceinline__ void set_zero(float zero) {
+        z = zero;
+        if constexpr (kOffset) {
+            zb = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)(-((float)(1 << b) + zero)), (__bf16)(-((float)(1 << b) + zero))});
+        }
+        if constexpr (kHalf) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) {
+                const _Float16 v = (_Float16)((float)(1024 >> (2 * i)) + zero);
+                z16[i] = (f16x2){v, v};
+            }
+        }
+    }
+    __device__ __forceinline__ V zero_frag() const {
+        u32x4 v = {zb, zb, zb, zb};
+        return __builtin_bit_cast(V, v);
+    }
+    // Column of the unit that slot j of fragment i holds.
+    __host__ __device__ static constexpr int col(int i, int j) {
+        if (b == 4) return 8 * i + (j >> 1) + 4 * (j & 1);
+        if (b == 2) return 16 * (i >> 1) + 4 * (i & 1) + (j >> 1) + 8 * (j & 1);
+        return 8 * i + j;
+    }
+    // Pair p (slots 2p and 2p + 1) of fragment i.
+    __device__ __forceinline__ uint32_t pair(const uint32_t *w, int i, int p) const {
+        constexpr uint32_t m = ((1u << b) - 1u) * 0x10001u;
+        if constexpr (b == 8) {
+            const uint32_t v = w[2 * i + (p >> 1)];
+            if constexpr (kHalf) {
+                const uint32_t h = __builtin_amdgcn_perm(magic, v, p & 1 ? 0x07030702u : 0x07010700u);
+                return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, h) - z16[0]);
+            } else {
+                const float lo = (float)((v >> (16 * (p & 1))) & 255u) - z, hi = (float)((v >> (16 * (p & 1) + 8)) & 255u) - z;
+                return __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)lo, (__bf16)hi});
+            }
+        } else if constexpr (b == 3) {
+            const uint32_t v = code_at<3>(w, 8 * i + 2 * p) | (code_at<3>(w, 8 * i + 2 * p + 1) << 16);
+            if constexpr (kHalf) return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v | magic) - z16[0]);
+            return (v << 4) | magic;
+        } else {  // codes b c and b c + 16 of a word
+            const uint32_t v = b == 4 ? w[i] : w[i >> 1];
+            const int at = b == 4 ? 4 * p : 2 * (4 * (i & 1) + p);
+            if constexpr (kHalf) {
+                const int base = at >= 8 ? 8 : 0, s = at - base;  // masked in place at shifts of 0 .. 6
+                const f16x2 h = __builtin_bit_cast(f16x2, ((base ? v >> base : v) & (m << s)) | magic);
+                if (s == 0) return __builtin_bit_cast(uint32_t, h - z16[0]);
+                const _Float16 f = (_Float16)(1.0f / (float)(1 << s));
+                return __builtin_bit_cast(uint32_t, h * (f16x2){f, f} - z16[s / 2]);
+            }
+            constexpr int top = 7 - b;  // the code's place in the mantissa
+            return ((at > top ? v >> (at - top) : v << (top - at)) & (m << top)) | magic;
+        }
+    }
+    __device__ __forceinline__ V frag(const uint32_t *w, int i) const {
+        u32x4 v = {pair(w, i, 0), pair(w, i, 1), pair(w, i, 2), pair(w, i, 3)};
+        return __builtin_bit_cast(V, v);
+    }
+    // Fragment i of x from the unit's 32 columns in their own order (16 words).
+    __device__ __forceinline__ static V xfrag(const uint32_t *x, int i) {
+        u32x4 v;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int c0 = col(i, 2 * p), c1 = col(i, 2 * p + 1);
+            if (c1 == c0 + 1)
+                v[p] = x[c0 / 2];
+            else
+                v[p] = __builtin_amdgcn_perm(x[c1 / 2], x[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
+        }
+        return __builtin_bit_cast(V, v);
+    }
+};
+
+template <typename V>
+__device__ __forceinline__ void transpose_frags(V f[4]) {
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+        u32x4 a = __builtin_bit_cast(u32x4, f[0]), c = __builtin_bit_cast(u32x4, f[1]);
+        u32x4 d = __builtin_bit_cast(u32x4, f[2]), e = __builtin_bit_cast(u32x4, f[3]);
+        uint32_t q0 = a[p], q1 = c[p], q2 = d[p], q3 = e[p];
+        transpose4(q0, q1, q2, q3);
+        a[p] = q0;
+        c[p] = q1;
+        d[p] = q2;
+        e[p] = q3;
+        f[0] = __builtin_bit_cast(V, a);
+        f[1] = __builtin_bit_cast(V, c);
+        f[2] = __builtin_bit_cast(V, d);
+        f[3] = __builtin_bit_cast(V, e);
+    }
+}
+
+template <int b>
+__device__ __forceinline__ void load_unit(const uint32_t *p, uint32_t *w) {
+    if constexpr (b == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x, w[1] = v.y;
+    } else if constexpr (b == 3) {
+        const uint3 v = *reinterpret_cast<const uint3 *>(p);  // 4-byte aligned: a row of 32 n codes is 12 n bytes
+        w[0] = v.x, w[1] = v.y, w[2] = v.z;
+    } else {
+#pragma unroll
+        for (int i = 0; i < b / 4; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+        }
+    }
+}
+
+// The wave's sums over steps [s0, s1) for R tiles of 16 weight rows, added to
+// acc.  row[r]: the lane's weight row of tile r (already clamped into the
+// matrix) in the stack w[r]; x: the lane's row of activations (token l % 16,
+// clamped).  kSplit: groups of 32 or 64 or 96 ... columns end inside a step, so
+// the fragments of the four lane rows are transposed to make each matrix
+// instruction cover one unit, and the fold with the scale runs per unit;
+// otherwise it runs per step.
+template <int b, typename T, int R, bool kSplit>
+__device__ __forceinline__ void few_product(const PackedDev *w, const int64_t *row, const T *x, int s0, int s1,
+                                            floatx4 *acc) {
+    typedef typename Vec8<T>::V V;
+    const int lane = threadIdx.x % kWave, kb = lane >> 4;
+    const int units = w[0].units;
+    const uint32_t *wp[R];
+    const float *sp[R], *zp[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        wp[r] = w[r].packed + row[r] * w[r].words;
+        sp[r] = w[r].scales + row[r] * w[r].groups;
+        zp[r] = w[r].zeros + row[r] * w[r].groups;
+    }
+    Codes<b, T> codes[R];
+    uint32_t cur[R][b], nxt[R][b];
+    float cs[R], cz[R], ns[R], nz[R];
+    auto load = [&](int step, uint32_t (*dst)[b], float *ds, float *dz) {
+        int u = 4 * step + kb;
+        u = u < units ? u : units - 1;
+        const uint32_t gi = kSplit ? w[0].by.div(u) : w[0].by.div(step);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            load_unit<b>(wp[r] + (int64_t)u * b, dst[r]);
+            ds[r] = sp[r][gi];
+            dz[r] = zp[r][gi];
+        }
+    };
+    if (s0 >= s1) return;
+    load(s0, nxt, ns, nz);
+    for (int s = s0; s < s1; ++s) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+#pragma unroll
+            for (int i = 0; i < b; ++i) cur[r][i] = nxt[r][i];
+            cs[r] = ns[r];
+            cz[r] = nz[r];
+        }
+        const int u = 4 * s + kb;
+        uint32_t xw[16];
+        const uint4 *xp = reinterpret_cast<const uint4 *>(x + (int64_t)kUnit * (u < units ? u : units - 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint4 v = xp[i];
+            if (u >= units) v = make_uint4(0, 0, 0, 0);
+            xw[4 * i] = v.x, xw[4 * i + 1] = v.y, xw[4 * i + 2] = v.z, xw[4 * i + 3] = v.w;
+        }
+        if (s + 1 < s1) load(s + 1, nxt, ns, nz);
+        V xf[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xf[i] = Codes<b, T>::xfrag(xw, i);
+        if constexpr (kSplit) transpose_frags(xf);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            V wf[4];
+            codes[r].set_zero(cz[r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wf[i] = codes[r].frag(cur[r], i);
+            if constexpr (kSplit) {
+                float sc[4], zc[4];
+                spread4(cs[r], sc);
+                if constexpr (Codes<b, T>::kOffset) spread4(cz[r], zc);
+                transpose_frags(wf);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if constexpr (Codes<b, T>::kOffset) {
+                        codes[r].set_zero(zc[i]);
+                        g = Vec8<T>::mma(xf[i], codes[r].zero_frag(), g);
+                    }
+                    g = Vec8<T>::mma(xf[i], wf[i], g);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[r][j] = fmaf(sc[i], g[j], acc[r][j]);
+                }
+            } else {
+                floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (Codes<b, T>::kOffset) g = Vec8<T>::mma(xf[i], codes[r].zero_frag(), g);
+                    g = Vec8<T>::mma(xf[i], wf[i], g);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[r][j] = fmaf(cs[r], g[j], acc[r][j]);
+            }
+        }
+    }
+}
+
+// Rounding of a result to the output's type, to nearest even.
+__device__ __forceinline__ void store_as(void *y, int64_t i, gptq_dtype dt, float v) {
+    if (dt == GPTQ_DT_F32)
+        static_cast<float *>(y)[i] = v;
+    else if (dt == GPTQ_DT_BF16)
+        static_cast<__bf16 *>(y)[i] = (__bf16)v;
+    else
+        static_cast<_Float16 *>(y)[i] = (_Float16)v;
+}
+
+__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+}  // namespace gptq

@@ -1,0 +1,104 @@
+"""The few-token products in fp64, with the error bounds their GPU tests use.
+
+Bounds.  A sum of n fp32 terms accumulated in any order is off by at most
+n u sum|terms| (u = 2^-24, one rounding per addition; products of a 16-bit
+float and a small integer are exact in fp32).  bf16 activations with 2-4 bits
+sum (2^b + q) x and -(2^b + z) x as separate terms, so the terms are larger
+than (q - z) x; the scale multiplies a group's sum (one rounding each, counted
+with the groups).  The result is rounded once to its type: half an ulp, or half
+the smallest subnormal.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+U = 2.0 ** -24
+EPS_HALF = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11, "fp32": 2.0 ** -24}  # half a step, relative to the value
+TINY_HALF = {"bf16": 2.0 ** -134, "fp16": 2.0 ** -25, "fp32": 2.0 ** -150}
+
+
+def make_packed(rng, oracle, d_out, d_in, bits, group, perm=False, n=None):
+    """A random packed layer (n: a stack): dict of host arrays."""
+    lead = () if n is None else (n,)
+    g = group or d_in
+    codes = rng.integers(0, 2 ** bits, size=lead + (d_out, d_in), dtype=np.uint8)
+    scales = rng.uniform(0.2, 1.0, size=lead + (d_out, d_in // g)).astype(np.float32) * np.float32(2.0 / (2 ** bits * np.sqrt(d_in)))
+    zeros = rng.integers(0, 2 ** bits, size=lead + (d_out, d_in // g)).astype(np.float32)
+    kperm = None
+    if perm:
+        kperm = np.stack([rng.permutation(d_in) for _ in range(n or 1)]).astype(np.int32)
+        kperm = kperm if n is not None else kperm[0]
+    flat = codes.reshape(-1, d_in)
+    packed = oracle.pack_codes(flat, bits).reshape(lead + (d_out, -1))
+    return dict(q=codes, packed=packed, scales=scales, zeros=zeros, kperm=kperm, bits=bits, group=group)
+
+
+def matrix(w, e=None):
+    """(W_hat, the magnitude of the summed terms per weight) in packed column order, fp64."""
+    q, s, z = (w[k] if e is None else w[k][e] for k in ("q", "scales", "zeros"))
+    gi = np.arange(q.shape[1]) // (w["group"] or q.shape[1])
+    q, s, z = q.astype(np.float64), s.astype(np.float64)[:, gi], z.astype(np.float64)[:, gi]
+    return (q - z) * s, (2.0 ** w["bits"] * 2 + q + z) * s
+
+
+def product(x, w, e=None, dx=None):
+    """x [M][d_in] fp64 times the packed layer: (value, error bound of the fp32 sums), with an error dx of x."""
+    order = w["kperm"] if e is None or w["kperm"] is None else w["kperm"][e]
+    if order is not None:
+        x = x[:, order]
+        dx = None if dx is None else dx[:, order]
+    W, A = matrix(w, e)
+    n = 2 * x.shape[1] + 2 * w["scales"].shape[-1] + 32  # both terms of a code, a group's scale, the waves' sums
+    bound = n * U * (np.abs(x) @ A.T)
+    if dx is not None:
+        bound = bound + dx @ (np.abs(W) + n * U * A).T
+    return x @ W.T, bound
+
+
+def rounded(v, bound, out):
+    """The bound after the result's rounding to `out`."""
+    return bound + EPS_HALF[out] * (np.abs(v) + bound) + TINY_HALF[out]
+
+
+def silu_mul(g, dg, u, du):
+    """silu(g) u and its bound: |silu'| <= 1.1; exp, the division and two products within 8 ulp of fp32."""
+    with np.errstate(over="ignore"):
+        sg = g / (1.0 + np.exp(-g))
+    v = sg * u
+    dv = 1.1 * dg * np.abs(u) + np.abs(sg) * du + 1.1 * dg * du
+    return v, dv + 16 * U * (np.abs(v) + dv)
+
+
+def route(x, router, top_k, renormalize):
+    """(ids, weights) of the router in fp64; descending logits, ties to the lower index."""
+    logits = x @ router.T
+    p = np.exp(logits - logits.max(axis=1, keepdims=True))
+    p /= p.sum(axis=1, keepdims=True)
+    ids = np.argsort(-logits, axis=1, kind="stable")[:, :top_k]
+    w = np.take_along_axis(p, ids, axis=1)
+    return ids.astype(np.int32), w / w.sum(axis=1, keepdims=True) if renormalize else w
+
+
+def moe(x, dt, gate, up, down, ids, weights, out):
+    """The experts' sum for x [T][d] in fp64 with h rounded nowhere, and the bound that counts its rounding to dt."""
+    T, k = ids.shape
+    E = gate["q"].shape[0]
+    y = np.zeros((T, down["q"].shape[1]))
+    b = np.zeros_like(y)
+    mag = np.zeros_like(y)
+    for t in range(T):
+        for j in range(k):
+            e = int(ids[t, j])
+            if not 0 <= e < E:
+                continue
+            g, dg = product(x[t:t + 1], gate, e)
+            u, du = product(x[t:t + 1], up, e)
+            h, dh = silu_mul(g, dg, u, du)
+            dh = rounded(h, dh, dt)
+            v, dv = product(h, down, e, dh)
+            w = abs(float(weights[t, j]))
+            y[t] += float(weights[t, j]) * v[0]
+            b[t] += w * dv[0]
+            mag[t] += w * (np.abs(v[0]) + dv[0])
+    # the weight's own rounding and product, the waves' sums (a handful of additions per expert)
+    return y, rounded(y, b + (16 + 4 * k) * U * mag, out)
