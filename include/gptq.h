@@ -467,8 +467,8 @@ GPTQ_API gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t 
  *           names twice counts with the sum of its weights.
  *   Y       fp16, bf16 or fp32 [T][ldy] out, ldy >= d; not X's memory.
  *   ws      scratch of gptq_moe_workspace_bytes(), 16-byte aligned.
- * 1 <= top_k <= min(n_experts, 16), n_experts <= 512.  h is rounded to X's type
- * between the two products, as the layers of an unpacked model round it; every
+ * 1 <= top_k <= min(n_experts, 16), n_experts <= 512.  h passes between the two
+ * products with 16 significant bits (24 for an fp32 Y), in bf16 pieces; every
  * sum is fp32 (the router's fp64), the result is rounded once.  Deterministic.
  * T == 0 is a no-op.
  */

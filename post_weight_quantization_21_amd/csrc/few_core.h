@@ -19,6 +19,8 @@
 // of the time for one token as for sixteen, so M <= 16 runs on them throughout.
 #pragma once
 
+#include <algorithm>
+
 #include "common.h"
 
 namespace gptq {
@@ -236,100 +238,223 @@ __device__ __forceinline__ void load_unit(const uint32_t *p, uint32_t *w) {
     }
 }
 
-// The wave's sums over steps [s0, s1) for R tiles of 16 weight rows, added to
-// acc.  row[r]: the lane's weight row of tile r (already clamped into the
-// matrix) in the stack w[r]; x: the lane's row of activations (token l % 16,
-// clamped).  kSplit: groups of 32 or 64 or 96 ... columns end inside a step, so
-// the fragments of the four lane rows are transposed to make each matrix
-// instruction cover one unit, and the fold with the scale runs per unit;
-// otherwise it runs per step.
-template <int b, typename T, int R, bool kSplit>
-__device__ __forceinline__ void few_product(const PackedDev *w, const int64_t *row, const T *x, int s0, int s1,
-                                            floatx4 *acc) {
-    typedef typename Vec8<T>::V V;
-    const int lane = threadIdx.x % kWave, kb = lane >> 4;
-    const int units = w[0].units;
-    const uint32_t *wp[R];
-    const float *sp[R], *zp[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        wp[r] = w[r].packed + row[r] * w[r].words;
-        sp[r] = w[r].scales + row[r] * w[r].groups;
-        zp[r] = w[r].zeros + row[r] * w[r].groups;
+// How a workgroup of kFewWaves waves shares a product: `slices` waves split K
+// between them on each of kFewWaves / slices row tiles.
+constexpr int kFewWaves = 8;
+constexpr int kFewThreads = kFewWaves * kWave;
+// x is staged in LDS in chunks of at most this many 16-bit values, two buffers.
+constexpr int kChunkValues = 16384;
+constexpr int kXPad = 8;  // values after each staged row: sixteen rows start in different banks
+
+// Rows of activations: row m of plane p is base + p * plane + row(m) * ld.
+struct XRows {
+    const uint16_t *base;
+    int64_t ld, plane;
+    const int32_t *row;  // row numbers, or NULL for m itself
+};
+
+// Steps of K that a chunk of `rows` staged rows holds, at most all of them.
+__host__ __device__ inline int chunk_steps(int rows, int steps) {
+    const int c = kChunkValues / (rows * kStep);
+    return c < steps ? c : steps;
+}
+__host__ __device__ inline int staged_ld(int chunk) { return chunk * kStep + kXPad; }
+// LDS bytes of a product of 1 .. max_rows rows of `planes` planes: the staged
+// activations, or the waves' sums after it.
+inline size_t few_lds_bytes(int max_rows, int planes, int units) {
+    const int steps = (units + 3) / 4;
+    size_t bytes = (size_t)kFewWaves * kFewRows * kTileRows * 4;
+    for (int m = 1; m <= max_rows; ++m) {
+        const int chunk = chunk_steps(planes * m, steps);
+        const size_t one = (size_t)planes * m * staged_ld(chunk) * 2;
+        bytes = std::max(bytes, chunk < steps ? 2 * one : one);
     }
-    Codes<b, T> codes[R];
-    uint32_t cur[R][b], nxt[R][b];
-    float cs[R], cz[R], ns[R], nz[R];
-    auto load = [&](int step, uint32_t (*dst)[b], float *ds, float *dz) {
-        int u = 4 * step + kb;
-        u = u < units ? u : units - 1;
-        const uint32_t gi = kSplit ? w[0].by.div(u) : w[0].by.div(step);
+    return bytes;
+}
+
+// Columns [128 c0, 128 (c0 + n)) of the M rows (P planes of them) staged for the
+// matrix cores: row-major, each unit's four fragments in slot order, zeros past
+// the last unit (a step may hold fewer than four).
+template <int b, typename T, int P>
+struct StageX {
+    typedef typename Vec8<T>::V V;
+    static constexpr int kPerThread = (kChunkValues / kUnit + kFewThreads - 1) / kFewThreads;
+    uint4 v[kPerThread][4];
+    __device__ __forceinline__ void load(const XRows &x, int M, int c0, int n, int units) {
+        const int per_row = 4 * n, items = P * M * per_row;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            load_unit<b>(wp[r] + (int64_t)u * b, dst[r]);
-            ds[r] = sp[r][gi];
-            dz[r] = zp[r][gi];
-        }
-    };
-    if (s0 >= s1) return;
-    load(s0, nxt, ns, nz);
-    for (int s = s0; s < s1; ++s) {
+        for (int k = 0; k < kPerThread; ++k) {
+            const int it = threadIdx.x + k * kFewThreads;
+            const int r = it / per_row, u = 4 * c0 + it - r * per_row;
+            const int p = r / M, m = r - p * M;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
+            for (int i = 0; i < 4; ++i) v[k][i] = make_uint4(0, 0, 0, 0);
+            if (it < items && u < units) {
+                const uint16_t *src = x.base + p * x.plane + (int64_t)(x.row ? x.row[m] : m) * x.ld + u * kUnit;
 #pragma unroll
-            for (int i = 0; i < b; ++i) cur[r][i] = nxt[r][i];
-            cs[r] = ns[r];
-            cz[r] = nz[r];
-        }
-        const int u = 4 * s + kb;
-        uint32_t xw[16];
-        const uint4 *xp = reinterpret_cast<const uint4 *>(x + (int64_t)kUnit * (u < units ? u : units - 1));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint4 v = xp[i];
-            if (u >= units) v = make_uint4(0, 0, 0, 0);
-            xw[4 * i] = v.x, xw[4 * i + 1] = v.y, xw[4 * i + 2] = v.z, xw[4 * i + 3] = v.w;
-        }
-        if (s + 1 < s1) load(s + 1, nxt, ns, nz);
-        V xf[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) xf[i] = Codes<b, T>::xfrag(xw, i);
-        if constexpr (kSplit) transpose_frags(xf);
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            V wf[4];
-            codes[r].set_zero(cz[r]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) wf[i] = codes[r].frag(cur[r], i);
-            if constexpr (kSplit) {
-                float sc[4], zc[4];
-                spread4(cs[r], sc);
-                if constexpr (Codes<b, T>::kOffset) spread4(cz[r], zc);
-                transpose_frags(wf);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if constexpr (Codes<b, T>::kOffset) {
-                        codes[r].set_zero(zc[i]);
-                        g = Vec8<T>::mma(xf[i], codes[r].zero_frag(), g);
-                    }
-                    g = Vec8<T>::mma(xf[i], wf[i], g);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[r][j] = fmaf(sc[i], g[j], acc[r][j]);
-                }
-            } else {
-                floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if constexpr (Codes<b, T>::kOffset) g = Vec8<T>::mma(xf[i], codes[r].zero_frag(), g);
-                    g = Vec8<T>::mma(xf[i], wf[i], g);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[r][j] = fmaf(cs[r], g[j], acc[r][j]);
+                for (int i = 0; i < 4; ++i) v[k][i] = reinterpret_cast<const uint4 *>(src)[i];
             }
         }
     }
+    __device__ __forceinline__ void store(uint16_t *xs, int M, int n, int ld) const {
+        const int per_row = 4 * n, items = P * M * per_row;
+#pragma unroll
+        for (int k = 0; k < kPerThread; ++k) {
+            const int it = threadIdx.x + k * kFewThreads;
+            if (it >= items) continue;
+            const int r = it / per_row, u = it - r * per_row;
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[4 * i] = v[k][i].x, w[4 * i + 1] = v[k][i].y, w[4 * i + 2] = v[k][i].z, w[4 * i + 3] = v[k][i].w;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) *reinterpret_cast<V *>(xs + r * ld + u * kUnit + 8 * i) = Codes<b, T>::xfrag(w, i);
+        }
+    }
+};
+
+// The wave's sums for a tile of 16 weight rows over its slice of K, from x
+// staged chunk by chunk; every wave of the workgroup calls it, with the same x.
+// row: the lane's weight row (clamped into the matrix) in the stack w.  kSplit:
+// groups end inside a step, so the fragments of the four lane rows are
+// transposed to make each matrix instruction cover one unit, and the fold with
+// the scale runs per unit; otherwise it runs per step.
+//
+// The weights stream through registers: a body of S steps is loaded while the
+// one before it is computed, so a wave keeps S to 2S KB (4 bits) in flight.
+// Scales and zeros come with it: without kSplit lane row kb reads those of step
+// kb of the body and the rows trade them (spread4), one load for four steps.
+template <int b, typename T, int P, bool kSplit>
+__device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row, const XRows &x, int M, int slice,
+                                               int slices, uint16_t *lds) {
+    typedef typename Vec8<T>::V V;
+    typedef Codes<b, T> C;
+    constexpr int S = b == 8 || (kSplit && P > 1) ? 2 : 4;
+    constexpr int NS = kSplit ? S : 1;
+    const int lane = threadIdx.x % kWave, kb = lane >> 4;
+    const int units = w.units, steps = (units + 3) / 4;
+    const int chunk = chunk_steps(P * M, steps), ld = staged_ld(chunk);
+    const uint32_t *wp = w.packed + row * w.words;
+    const float *sp = w.scales + row * w.groups, *zp = w.zeros + row * w.groups;
+    const SmallDiv by = w.by;
+    struct Body {
+        uint32_t w[S][b];
+        float s[NS], z[NS];
+    } nxt, cur;
+    auto load = [&](Body &d, int step) {
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+            const int u = std::min(4 * (step + j) + kb, units - 1);  // past the end: loaded again, not used
+            load_unit<b>(wp + u * b, d.w[j]);
+            if constexpr (kSplit) {
+                const uint32_t gi = by.div(u);
+                d.s[j] = sp[gi], d.z[j] = zp[gi];
+            }
+        }
+        if constexpr (!kSplit) {
+            const uint32_t gi = by.div(std::min(step + (kb & (S - 1)), steps - 1));
+            d.s[0] = sp[gi], d.z[0] = zp[gi];
+        }
+    };
+    floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    StageX<b, T, P> stage;
+    stage.load(x, M, 0, chunk, units);
+    int s = slice * chunk / slices, end = (slice + 1) * chunk / slices;  // of the first chunk
+    load(nxt, s);
+    stage.store(lds, M, chunk, ld);
+    __syncthreads();
+    uint16_t *buf = lds, *other = lds + P * M * ld;
+    C codes;
+    const int m = std::min(lane & 15, M - 1);
+    for (int c0 = 0; c0 < steps; c0 += chunk) {
+        const int c1 = c0 + chunk, n1 = std::min(chunk, steps - c1);  // the next chunk, if n1 > 0
+        if (n1 > 0) stage.load(x, M, c1, n1, units);
+        const int next = c1 + slice * n1 / slices;
+        const uint16_t *xl = buf + m * ld + kb * (kSplit ? 8 : kUnit);
+        if (s >= end) load(nxt, next);  // fewer steps than slices: nothing here for this wave
+        for (; s < end; s += S) {
+            cur = nxt;
+            load(nxt, s + S < end ? s + S : next);
+            float sc[4], zc[4];
+            if constexpr (!kSplit) {
+                spread4(cur.s[0], sc);
+                spread4(cur.z[0], zc);
+            }
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                if (s + j >= end) break;
+                V xf[P][4];
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        xf[p][i] = *reinterpret_cast<const V *>(xl + p * M * ld + (s + j - c0) * kStep + i * (kSplit ? kUnit : 8));
+                V wf[4];
+                if constexpr (kSplit) {
+                    if constexpr (!C::kOffset) codes.set_zero(cur.z[j]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) wf[i] = codes.frag(cur.w[j], i);
+                    spread4(cur.s[j], sc);
+                    if constexpr (C::kOffset) spread4(cur.z[j], zc);
+                    transpose_frags(wf);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if constexpr (C::kOffset) codes.set_zero(zc[i]);
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            if constexpr (C::kOffset) g = Vec8<T>::mma(xf[p][i], codes.zero_frag(), g);
+                            g = Vec8<T>::mma(xf[p][i], wf[i], g);
+                        }
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) acc[t] = fmaf(sc[i], g[t], acc[t]);
+                    }
+                } else {
+                    codes.set_zero(zc[j]);
+                    floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        wf[i] = codes.frag(cur.w[j], i);
+#pragma unroll
+                        for (int p = 0; p < P; ++p) {
+                            if constexpr (C::kOffset) g = Vec8<T>::mma(xf[p][i], codes.zero_frag(), g);
+                            g = Vec8<T>::mma(xf[p][i], wf[i], g);
+                        }
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) acc[t] = fmaf(sc[j], g[t], acc[t]);
+                }
+            }
+        }
+        if (n1 > 0) {
+            stage.store(other, M, n1, ld);
+            __syncthreads();  // the next chunk is staged; this one's buffer is written again a barrier later
+            uint16_t *t = buf;
+            buf = other;
+            other = t;
+            s = next;
+            end = c1 + (slice + 1) * n1 / slices;
+        }
+    }
+    return acc;
 }
+
+// The waves' sums through LDS: after it, sums[wave][m][row] of the workgroup.
+typedef float FewSums[kFewRows][kTileRows];
+__device__ __forceinline__ void few_share(FewSums *sums, int wave, const floatx4 &acc, int M) {
+    const int lane = threadIdx.x % kWave;
+    __syncthreads();  // the staged activations are no longer read
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+        if (4 * (lane >> 4) + t < M) sums[wave][4 * (lane >> 4) + t][lane & 15] = acc[t];
+    __syncthreads();
+}
+// The wave's number in the workgroup, known to be the same in all its lanes.
+__device__ __forceinline__ int few_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
+
+// Waves that split K for one row tile, at most `most`, so that `tiles` tiles make
+// about as many waves as the chip holds at once (16 a compute unit) while a wave
+// keeps at least a body of steps.
+int few_slices(int64_t tiles, int units, int most);
 
 // Rounding of a result to the output's type, to nearest even.
 __device__ __forceinline__ void store_as(void *y, int64_t i, gptq_dtype dt, float v) {

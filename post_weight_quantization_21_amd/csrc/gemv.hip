@@ -1,10 +1,10 @@
 // Products of a few tokens with packed weights: Y = X' W^T (+ bias), and the
 // first half of a gated MLP, H = silu(X' Wg^T) * (X' Wu^T).
 //
-// A workgroup owns 16 weight rows (gated: the same 16 of both matrices, so the
-// activations are read once and the pair meets in registers) and its waves
-// share K; their sums meet in LDS and are added in wave order, so results do
-// not depend on timing.
+// A workgroup of eight waves stages the activations in LDS and owns one to eight
+// tiles of 16 weight rows; the waves of a tile share K and their sums meet in
+// LDS, where they are added in wave order, so results do not depend on timing.
+// Gated, half the tiles are the same rows of the other matrix.
 #include <algorithm>
 
 #include "few_core.h"
@@ -14,56 +14,44 @@ namespace {
 
 struct GemvArgs {
     PackedDev w[2];
-    const void *x;
-    int64_t ldx, M;
+    XRows x;
+    int M, slices;
     const float *bias;
     void *y;
     int64_t ldy;
     gptq_dtype y_dt;
 };
 
-constexpr int kMaxWaves = 16;
-
+// Gated: waves of the even tiles take the gate's rows, those of the odd ones up's.
 template <int b, typename T, bool kGated, bool kSplit>
-__global__ __launch_bounds__(1024) void gemv_kernel(GemvArgs a) {
+__global__ __launch_bounds__(kFewThreads, 4) void gemv_kernel(GemvArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     constexpr int R = kGated ? 2 : 1;
-    __shared__ float red[kMaxWaves][R][kFewRows][kTileRows];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
-    const int64_t r0 = (int64_t)blockIdx.x * kTileRows;
-    const int64_t o = r0 + (lane & 15);
-    const int64_t oc = o < a.w[0].d_out ? o : a.w[0].d_out - 1;
-    const int64_t m = (lane & 15) < a.M ? (lane & 15) : a.M - 1;
-    const int steps = (a.w[0].units + 3) / 4;
-    floatx4 acc[R];
-    int64_t row[R];
+    const int wave = few_wave(), lane = threadIdx.x % kWave;
+    const int tiles = kFewWaves / a.slices / R, tile = wave / a.slices;
+    const int64_t r0 = (int64_t)blockIdx.x * tiles * kTileRows;
+    const int64_t row = std::min<int64_t>(r0 + tile / R * kTileRows + (lane & 15), a.w[0].d_out - 1);
+    const floatx4 acc = few_product<b, T, 1, kSplit>(a.w[kGated ? tile & 1 : 0], row, a.x, a.M, wave % a.slices, a.slices,
+                                                     reinterpret_cast<uint16_t *>(smem));
+    FewSums *sums = reinterpret_cast<FewSums *>(smem);
+    few_share(sums, wave, acc, a.M);
+    for (int n = threadIdx.x; n < a.M * tiles * kTileRows; n += kFewThreads) {
+        const int m = n / (tiles * kTileRows), c = n % (tiles * kTileRows);
+        const int64_t out = r0 + c;
+        if (out >= a.w[0].d_out) continue;
+        float v[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        acc[r] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
-        row[r] = oc;
+        for (int r = 0; r < R; ++r) {
+            v[r] = 0.0f;
+            for (int k = 0; k < a.slices; ++k) v[r] += sums[(c / kTileRows * R + r) * a.slices + k][m][c % kTileRows];
+        }
+        float y;
+        if constexpr (kGated)
+            y = silu_mul(v[0], v[R - 1]);
+        else
+            y = a.bias ? v[0] + a.bias[out] : v[0];
+        store_as(a.y, m * a.ldy + out, a.y_dt, y);
     }
-    few_product<b, T, R, kSplit>(a.w, row, static_cast<const T *>(a.x) + m * a.ldx, wave * steps / waves,
-                                 (wave + 1) * steps / waves, acc);
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) red[wave][r][4 * (lane >> 4) + j][lane & 15] = acc[r][j];
-    __syncthreads();
-    const int n = threadIdx.x;  // token n / 16, row n % 16
-    if (n >= a.M * kTileRows) return;
-    const int64_t out = r0 + (n & 15);
-    if (out >= a.w[0].d_out) return;
-    float v[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        v[r] = 0.0f;
-        for (int w = 0; w < waves; ++w) v[r] += red[w][r][n >> 4][n & 15];
-    }
-    float y;
-    if constexpr (kGated)
-        y = silu_mul(v[0], v[R - 1]);
-    else
-        y = a.bias ? v[0] + a.bias[out] : v[0];
-    store_as(a.y, (n >> 4) * a.ldy + out, a.y_dt, y);
 }
 
 // The activations in packed column order: Xg[m][k] = X[m][kperm[k]].
@@ -78,20 +66,18 @@ __global__ __launch_bounds__(256) void gather_kernel(const uint16_t *__restrict_
 
 template <int b, typename T>
 void launch_gemv(const GemvArgs &a, bool gated, hipStream_t s) {
-    const int steps = (a.w[0].units + 3) / 4;
-    // two steps per wave at least (below, the waves only add to the final sum), and 256 threads for the epilogue
-    const int waves = std::clamp(steps / 2, 4, kMaxWaves);
-    const dim3 grid((unsigned)ceil_div(a.w[0].d_out, kTileRows)), block(waves * kWave);
+    const dim3 grid((unsigned)ceil_div(a.w[0].d_out, kTileRows * (kFewWaves / a.slices / (gated ? 2 : 1))));
+    const size_t lds = few_lds_bytes(a.M, 1, a.w[0].units);
     if (gated) {
         if (a.w[0].split)
-            gemv_kernel<b, T, true, true><<<grid, block, 0, s>>>(a);
+            gemv_kernel<b, T, true, true><<<grid, kFewThreads, lds, s>>>(a);
         else
-            gemv_kernel<b, T, true, false><<<grid, block, 0, s>>>(a);
+            gemv_kernel<b, T, true, false><<<grid, kFewThreads, lds, s>>>(a);
     } else {
         if (a.w[0].split)
-            gemv_kernel<b, T, false, true><<<grid, block, 0, s>>>(a);
+            gemv_kernel<b, T, false, true><<<grid, kFewThreads, lds, s>>>(a);
         else
-            gemv_kernel<b, T, false, false><<<grid, block, 0, s>>>(a);
+            gemv_kernel<b, T, false, false><<<grid, kFewThreads, lds, s>>>(a);
     }
 }
 
@@ -123,6 +109,13 @@ PackedDev packed_dev(const gptq_packed &w) {
     return d;
 }
 
+int few_slices(int64_t tiles, int units, int most) {
+    const int steps = (units + 3) / 4;
+    int slices = 1;
+    while (slices < most && tiles * slices < 4096 && slices * 4 < steps) slices *= 2;
+    return slices;
+}
+
 size_t gemv_ws_bytes(int64_t M, int64_t d_in) { return align_up((size_t)M * (size_t)d_in * 2, 256); }
 
 hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,
@@ -130,9 +123,10 @@ hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, cons
     GemvArgs a;
     a.w[0] = packed_dev(w);
     a.w[1] = packed_dev(up ? *up : w);
-    a.x = X;
-    a.ldx = ldx;
-    a.M = M;
+    a.x = {static_cast<const uint16_t *>(X), ldx, 0, nullptr};
+    a.M = (int)M;
+    a.slices = up ? few_slices(2 * ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves / 2)
+                  : few_slices(ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves);
     a.bias = bias;
     a.y = Y;
     a.ldy = ldy;
@@ -142,8 +136,8 @@ hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, cons
             static_cast<const uint16_t *>(X), ldx, w.d_in, w.kperm, static_cast<uint16_t *>(ws));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        a.x = ws;
-        a.ldx = w.d_in;
+        a.x.base = static_cast<const uint16_t *>(ws);
+        a.x.ld = w.d_in;
     }
     if (x_dt == GPTQ_DT_BF16)
         launch_gemv_bits<__bf16>(a, w.bits, up != nullptr, s);

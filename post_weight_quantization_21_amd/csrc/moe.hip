@@ -3,13 +3,20 @@
 //   router:  L = X R^T in fp64, one workgroup per expert and four tokens
 //   choose:  one workgroup: a wave per token picks its top_k experts; then the
 //            (token, expert) pairs are listed expert by expert
-//   gate/up: a workgroup per listed expert and 16 rows of both matrices; its
-//            pairs are the rows of one 16-row matrix operand (few_core.h), so an
-//            expert's weights are read once however many tokens chose it
-//   down:    a workgroup per 16 rows of the result; its waves share the listed
-//            experts' K steps laid end to end, each adding weight * product to
-//            its own sums per token; the waves' sums are added in wave order
+//   gate/up: workgroups per listed expert and tiles of 16 rows of both matrices;
+//            the expert's pairs are the rows of one 16-row matrix operand
+//            (few_core.h), so its weights are read once however many tokens chose
+//            it
+//   down:    the same for the second product, whose rows by pair are left in fp32
+//   combine: Y[t] = the sum of the token's pairs, expert by expert, weighted
+//
+// h = silu(gate) * up between the products is a sum of bf16 values, two for a
+// 16-bit result and three for an fp32 one (16 and 24 significant bits): each is
+// an operand plane of the down product, whose weights are exact in bf16 up to a
+// constant, so nothing of h is lost that the result could show.  One bf16 or fp16
+// value per h costs 1.5 times the error of the final rounding.
 #include <algorithm>
+#include <cmath>
 
 #include "few_core.h"
 
@@ -17,7 +24,7 @@ namespace gptq {
 namespace {
 
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kMaxWaves = 16;
+constexpr int kChooseWaves = 16;
 
 // The chosen (token, expert) pairs, expert by expert, tokens ascending.
 struct Lists {
@@ -26,6 +33,8 @@ struct Lists {
     int32_t start[kMaxPairs + 1];   // their first pairs
     int32_t token[kMaxPairs];
     float weight[kMaxPairs];
+    int32_t of_count[kMoeMaxTokens];               // a token's pairs ...
+    int32_t of_token[kMoeMaxTokens][kMoeMaxTopK];  // ... in their order
 };
 
 template <typename T>
@@ -77,7 +86,8 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
     __shared__ int32_t sel[kMoeMaxTokens][kMoeMaxTopK];
     __shared__ float wsel[kMoeMaxTokens][kMoeMaxTopK];
     __shared__ uint32_t tokens_of[kMoeMaxExperts];  // bit t: token t chose the expert
-    __shared__ uint32_t wave_sum[kMaxWaves];
+    __shared__ uint32_t wave_sum[kChooseWaves];
+    __shared__ uint8_t token_of[kMaxPairs];
     const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
     constexpr int kPer = kMoeMaxExperts / kWave;
     if (tid < kMoeMaxExperts) tokens_of[tid] = 0;
@@ -168,6 +178,7 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
             float w = 0.0f;
             for (int j = 0; j < top_k; ++j)
                 if (sel[t][j] == tid) w += wsel[t][j];
+            token_of[p] = (uint8_t)t;
             lists->token[p] = t;
             lists->weight[p] = w;
         }
@@ -176,17 +187,31 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
         lists->n = total >> 16;
         lists->start[total >> 16] = total & 0xFFFF;
     }
+    __syncthreads();
+    if (wave < n_tok) {
+        const int pairs = total & 0xFFFF;
+        int n = 0;
+        for (int p0 = 0; p0 < pairs; p0 += kWave) {
+            const bool hit = p0 + lane < pairs && token_of[p0 + lane] == wave;
+            const uint64_t hits = __ballot(hit);
+            if (hit) lists->of_token[wave][n + __popcll(hits & ((1ull << lane) - 1))] = p0 + lane;
+            n += __popcll(hits);
+        }
+        if (lane == 0) lists->of_count[wave] = n;
+    }
 }
 
 // Rows of activations in an expert's packed column order: out[p][k] =
-// in[token of p or p][kperm[expert][k]], one workgroup row per pair.
+// in[token of p or p][kperm[expert][k]], plane by plane.
 __global__ __launch_bounds__(256) void gather_pairs_kernel(const uint16_t *__restrict__ in, int64_t ld, int by_token,
-                                                           const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
+                                                           int64_t plane, const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
                                                            int d, uint16_t *__restrict__ out) {
     const int a = blockIdx.y;
     if (a >= lists->n) return;
     const int k = blockIdx.x * 256 + threadIdx.x;
     if (k >= d) return;
+    in += blockIdx.z * plane;
+    out += blockIdx.z * plane;
     int c = kperm[(int64_t)lists->expert[a] * d + k];
     c = c < 0 ? 0 : (c >= d ? d - 1 : c);
     for (int p = lists->start[a]; p < lists->start[a + 1]; ++p)
@@ -195,93 +220,94 @@ __global__ __launch_bounds__(256) void gather_pairs_kernel(const uint16_t *__res
 
 struct GateUpArgs {
     PackedDev w[2];
-    const void *x;  // rows by token, or by pair (ldx = d) when gathered
+    const uint16_t *x;  // rows by token, or by pair (ldx = d) when gathered
     int64_t ldx;
-    int by_pair;
+    int by_pair, slices, planes;
     const Lists *lists;
-    void *h;
+    __bf16 *h;
+    int64_t h_plane;
 };
 
 template <int b, typename T, bool kSplit>
-__global__ __launch_bounds__(1024) void gate_up_kernel(GateUpArgs a) {
-    __shared__ float red[kMaxWaves][2][kFewRows][kTileRows];
+__global__ __launch_bounds__(kFewThreads, 4) void gate_up_kernel(GateUpArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     if ((int)blockIdx.y >= a.lists->n) return;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
+    const int wave = few_wave(), lane = threadIdx.x % kWave;
+    const int tiles = kFewWaves / a.slices / 2, tile = wave / a.slices;
     const int start = a.lists->start[blockIdx.y], count = a.lists->start[blockIdx.y + 1] - start;
-    const int ff = a.w[0].d_out;
-    const int r0 = blockIdx.x * kTileRows;
-    const int o = std::min(r0 + (lane & 15), ff - 1);
-    const int p = start + std::min(lane & 15, count - 1);
-    const int64_t xr = a.by_pair ? p : a.lists->token[p];
-    const int steps = (a.w[0].units + 3) / 4;
-    const int64_t at = (int64_t)a.lists->expert[blockIdx.y] * ff + o;
-    const int64_t row[2] = {at, at};
-    floatx4 acc[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-    few_product<b, T, 2, kSplit>(a.w, row, static_cast<const T *>(a.x) + xr * a.ldx, wave * steps / waves,
-                                 (wave + 1) * steps / waves, acc);
+    const int ff = a.w[0].d_out, r0 = blockIdx.x * tiles * kTileRows;
+    const int64_t row = (int64_t)a.lists->expert[blockIdx.y] * ff + std::min(r0 + tile / 2 * kTileRows + (lane & 15), ff - 1);
+    const XRows x = {a.by_pair ? a.x + start * a.ldx : a.x, a.ldx, 0, a.by_pair ? nullptr : a.lists->token + start};
+    const floatx4 acc = few_product<b, T, 1, kSplit>(a.w[tile & 1], row, x, count, wave % a.slices, a.slices,
+                                                     reinterpret_cast<uint16_t *>(smem));
+    FewSums *sums = reinterpret_cast<FewSums *>(smem);
+    few_share(sums, wave, acc, count);
+    for (int n = threadIdx.x; n < count * tiles * kTileRows; n += kFewThreads) {
+        const int m = n / (tiles * kTileRows), c = n % (tiles * kTileRows);
+        if (r0 + c >= ff) continue;
+        float v[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) red[wave][r][4 * (lane >> 4) + j][lane & 15] = acc[r][j];
-    __syncthreads();
-    const int n = threadIdx.x;
-    if (n >= count * kTileRows || r0 + (n & 15) >= ff) return;
-    float g = 0.0f, u = 0.0f;
-    for (int w = 0; w < waves; ++w) {
-        g += red[w][0][n >> 4][n & 15];
-        u += red[w][1][n >> 4][n & 15];
+        for (int r = 0; r < 2; ++r)
+            for (int k = 0; k < a.slices; ++k) v[r] += sums[(c / kTileRows * 2 + r) * a.slices + k][m][c % kTileRows];
+        float h = silu_mul(v[0], v[1]);
+        __bf16 *dst = a.h + (int64_t)(start + m) * ff + r0 + c;
+        for (int p = 0; p < a.planes; ++p) {
+            const __bf16 t = (__bf16)h;
+            dst[p * a.h_plane] = t;
+            h -= (float)t;  // exact
+        }
     }
-    static_cast<T *>(a.h)[(int64_t)(start + (n >> 4)) * ff + r0 + (n & 15)] = (T)silu_mul(g, u);
 }
 
 struct DownArgs {
     PackedDev w;
-    const void *h;  // rows by pair
+    const uint16_t *h;  // planes of rows by pair
+    int64_t h_plane;
+    int slices;
     const Lists *lists;
-    int n_tok;
-    void *y;
-    int64_t ldy;
-    gptq_dtype y_dt;
+    float *part;  // rows by pair
 };
 
-template <int b, typename T, bool kSplit>
-__global__ __launch_bounds__(1024) void down_kernel(DownArgs a) {
-    __shared__ float sums[kMaxWaves][kFewRows][kTileRows];
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
-    const int r0 = blockIdx.x * kTileRows, d = a.w.d_out, ff = a.w.units * kUnit;
-    const int o = std::min(r0 + (lane & 15), d - 1);
-    for (int i = lane; i < kFewRows * kTileRows; i += kWave) sums[wave][i / kTileRows][i % kTileRows] = 0.0f;
-    const int steps = (a.w.units + 3) / 4;
-    const int total = a.lists->n * steps;
-    int s = (int)((int64_t)wave * total / waves);
-    const int end = (int)((int64_t)(wave + 1) * total / waves);
-    while (s < end) {
-        const int i = s / steps, s0 = s - i * steps, s1 = std::min(steps, s0 + end - s);
-        const int start = a.lists->start[i], count = a.lists->start[i + 1] - start;
-        const int p = start + std::min(lane & 15, count - 1);
-        const int64_t row[1] = {(int64_t)a.lists->expert[i] * d + o};
-        floatx4 acc[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
-        few_product<b, T, 1, kSplit>(&a.w, row, static_cast<const T *>(a.h) + (int64_t)p * ff, s0, s1, acc);
-        // the wave's own sums: another lane may have written the element before, in order within the wave
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int m = 4 * (lane >> 4) + j;
-            if (m < count) sums[wave][a.lists->token[start + m]][lane & 15] += a.lists->weight[start + m] * acc[0][j];
-        }
-        s += s1 - s0;
+template <int b, int P, bool kSplit>
+__global__ __launch_bounds__(kFewThreads, 4) void down_kernel(DownArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    if ((int)blockIdx.y >= a.lists->n) return;
+    const int wave = few_wave(), lane = threadIdx.x % kWave;
+    const int tiles = kFewWaves / a.slices, tile = wave / a.slices;
+    const int start = a.lists->start[blockIdx.y], count = a.lists->start[blockIdx.y + 1] - start;
+    const int d = a.w.d_out, r0 = blockIdx.x * tiles * kTileRows;
+    const int64_t row = (int64_t)a.lists->expert[blockIdx.y] * d + std::min(r0 + tile * kTileRows + (lane & 15), d - 1);
+    const int64_t ff = a.w.units * kUnit;
+    const XRows x = {a.h + start * ff, ff, a.h_plane, nullptr};
+    const floatx4 acc = few_product<b, __bf16, P, kSplit>(a.w, row, x, count, wave % a.slices, a.slices,
+                                                          reinterpret_cast<uint16_t *>(smem));
+    FewSums *sums = reinterpret_cast<FewSums *>(smem);
+    few_share(sums, wave, acc, count);
+    for (int n = threadIdx.x; n < count * tiles * kTileRows; n += kFewThreads) {
+        const int m = n / (tiles * kTileRows), c = n % (tiles * kTileRows);
+        if (r0 + c >= d) continue;
+        float v = 0.0f;
+        for (int k = 0; k < a.slices; ++k) v += sums[c / kTileRows * a.slices + k][m][c % kTileRows];
+        a.part[(int64_t)(start + m) * d + r0 + c] = v;
     }
-    __syncthreads();
-    const int n = threadIdx.x;
-    if (n >= a.n_tok * kTileRows || r0 + (n & 15) >= d) return;
-    float y = 0.0f;
-    for (int w = 0; w < waves; ++w) y += sums[w][n >> 4][n & 15];
-    store_as(a.y, (int64_t)(n >> 4) * a.ldy + r0 + (n & 15), a.y_dt, y);
 }
 
+__global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ part, const Lists *__restrict__ lists, int d,
+                                                      void *y, int64_t ldy, gptq_dtype y_dt) {
+    const int c = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+    if (c >= d) return;
+    float v = 0.0f;
+    const int n = lists->of_count[t];
+    for (int j = 0; j < n; ++j) {
+        const int p = lists->of_token[t][j];
+        v = fmaf(lists->weight[p], part[(int64_t)p * d + c], v);
+    }
+    store_as(y, t * ldy + c, y_dt, v);
+}
+
+constexpr int kMaxPlanes = 3;
 struct Layout {
-    size_t logits, lists, h, xg, hg, bytes;
+    size_t logits, lists, h, part, xg, hg, bytes;
 };
 Layout layout(int64_t T, int64_t d, int64_t d_ff, int n_experts, int top_k) {
     const size_t pairs = (size_t)T * top_k;
@@ -289,9 +315,10 @@ Layout layout(int64_t T, int64_t d, int64_t d_ff, int n_experts, int top_k) {
     l.logits = 0;
     l.lists = align_up((size_t)T * n_experts * sizeof(double), 256);
     l.h = l.lists + align_up(sizeof(Lists), 256);
-    l.xg = l.h + align_up(pairs * d_ff * 2, 256);
+    l.part = l.h + align_up(kMaxPlanes * pairs * d_ff * 2, 256);
+    l.xg = l.part + align_up(pairs * d * 4, 256);
     l.hg = l.xg + align_up(pairs * d * 2, 256);
-    l.bytes = l.hg + align_up(pairs * d_ff * 2, 256);
+    l.bytes = l.hg + align_up(kMaxPlanes * pairs * d_ff * 2, 256);
     return l;
 }
 
@@ -310,49 +337,67 @@ struct MoeCall {
     char *ws;
 };
 
+template <int b, int P>
+void launch_down(const DownArgs &w, dim3 grid, size_t lds, hipStream_t s) {
+    if (w.w.split)
+        down_kernel<b, P, true><<<grid, kFewThreads, lds, s>>>(w);
+    else
+        down_kernel<b, P, false><<<grid, kFewThreads, lds, s>>>(w);
+}
+
 template <int b, typename T>
 void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
-    const int64_t d = c.gate->d_in, ff = c.gate->d_out;
+    const int64_t d = c.gate->d_in, ff = c.gate->d_out, pairs = c.T * c.top_k;
     Lists *lists = reinterpret_cast<Lists *>(c.ws + l.lists);
-    const unsigned slots = (unsigned)std::min<int64_t>(c.n_experts, c.T * c.top_k);
+    const unsigned slots = (unsigned)std::min<int64_t>(c.n_experts, pairs);
+    // experts that `pairs` independent choices would hit, which the work is spread for
+    const double busy = c.n_experts * (1.0 - std::pow(1.0 - 1.0 / c.n_experts, (double)pairs));
     GateUpArgs g;
     g.w[0] = packed_dev(*c.gate);
     g.w[1] = packed_dev(*c.up);
-    g.x = c.X;
+    g.x = static_cast<const uint16_t *>(c.X);
     g.ldx = c.ldx;
     g.by_pair = 0;
     g.lists = lists;
-    g.h = c.ws + l.h;
+    g.h = reinterpret_cast<__bf16 *>(c.ws + l.h);
+    g.h_plane = pairs * ff;
+    g.planes = c.y_dt == GPTQ_DT_F32 ? 3 : 2;
     if (c.gate->kperm) {
-        gather_pairs_kernel<<<dim3((unsigned)ceil_div(d, 256), slots), 256, 0, s>>>(
-            static_cast<const uint16_t *>(c.X), c.ldx, 1, lists, c.gate->kperm, (int)d, reinterpret_cast<uint16_t *>(c.ws + l.xg));
-        g.x = c.ws + l.xg;
+        uint16_t *xg = reinterpret_cast<uint16_t *>(c.ws + l.xg);
+        gather_pairs_kernel<<<dim3((unsigned)ceil_div(d, 256), slots), 256, 0, s>>>(g.x, c.ldx, 1, 0, lists, c.gate->kperm, (int)d, xg);
+        g.x = xg;
         g.ldx = d;
         g.by_pair = 1;
     }
-    const dim3 grid((unsigned)ceil_div(ff, kTileRows), slots);
-    const int waves = std::clamp((g.w[0].units + 3) / 4 / 2, 4, kMaxWaves);
+    const int64_t gu_tiles = ceil_div(ff, kTileRows);
+    g.slices = few_slices((int64_t)(2 * busy * gu_tiles), g.w[0].units, kFewWaves / 2);
+    const dim3 grid((unsigned)ceil_div(gu_tiles, kFewWaves / g.slices / 2), slots);
+    const size_t lds = few_lds_bytes((int)c.T, 1, g.w[0].units);
     if (g.w[0].split)
-        gate_up_kernel<b, T, true><<<grid, waves * kWave, 0, s>>>(g);
+        gate_up_kernel<b, T, true><<<grid, kFewThreads, lds, s>>>(g);
     else
-        gate_up_kernel<b, T, false><<<grid, waves * kWave, 0, s>>>(g);
+        gate_up_kernel<b, T, false><<<grid, kFewThreads, lds, s>>>(g);
     DownArgs w;
     w.w = packed_dev(*c.down);
-    w.h = g.h;
+    w.h = reinterpret_cast<const uint16_t *>(g.h);
+    w.h_plane = g.h_plane;
     w.lists = lists;
-    w.n_tok = (int)c.T;
-    w.y = c.Y;
-    w.ldy = c.ldy;
-    w.y_dt = c.y_dt;
+    w.part = reinterpret_cast<float *>(c.ws + l.part);
     if (c.down->kperm) {
-        gather_pairs_kernel<<<dim3((unsigned)ceil_div(ff, 256), slots), 256, 0, s>>>(
-            reinterpret_cast<const uint16_t *>(c.ws + l.h), ff, 0, lists, c.down->kperm, (int)ff, reinterpret_cast<uint16_t *>(c.ws + l.hg));
-        w.h = c.ws + l.hg;
+        uint16_t *hg = reinterpret_cast<uint16_t *>(c.ws + l.hg);
+        gather_pairs_kernel<<<dim3((unsigned)ceil_div(ff, 256), slots, g.planes), 256, 0, s>>>(w.h, ff, 0, w.h_plane, lists,
+                                                                                               c.down->kperm, (int)ff, hg);
+        w.h = hg;
     }
-    if (w.w.split)
-        down_kernel<b, T, true><<<(unsigned)ceil_div(d, kTileRows), 1024, 0, s>>>(w);
+    const int64_t tiles = ceil_div(d, kTileRows);
+    w.slices = few_slices((int64_t)(busy * tiles), w.w.units, kFewWaves);
+    const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves / w.slices), slots);
+    const size_t dlds = few_lds_bytes((int)c.T, g.planes, w.w.units);
+    if (g.planes == 3)
+        launch_down<b, 3>(w, dgrid, dlds, s);
     else
-        down_kernel<b, T, false><<<(unsigned)ceil_div(d, kTileRows), 1024, 0, s>>>(w);
+        launch_down<b, 2>(w, dgrid, dlds, s);
+    combine_kernel<<<dim3((unsigned)ceil_div(d, 256), (unsigned)c.T), 256, 0, s>>>(w.part, lists, (int)d, c.Y, c.ldy, c.y_dt);
 }
 
 template <typename T>

@@ -41,14 +41,15 @@ def matrix(w, e=None):
     return (q - z) * s, (2.0 ** w["bits"] * 2 + q + z) * s
 
 
-def product(x, w, e=None, dx=None):
-    """x [M][d_in] fp64 times the packed layer: (value, error bound of the fp32 sums), with an error dx of x."""
+def product(x, w, e=None, dx=None, planes=1):
+    """x [M][d_in] fp64 times the packed layer: (value, error bound of the fp32 sums), with an error dx of x and x
+    given as a sum of `planes` terms."""
     order = w["kperm"] if e is None or w["kperm"] is None else w["kperm"][e]
     if order is not None:
         x = x[:, order]
         dx = None if dx is None else dx[:, order]
     W, A = matrix(w, e)
-    n = 2 * x.shape[1] + 2 * w["scales"].shape[-1] + 32  # both terms of a code, a group's scale, the waves' sums
+    n = 2 * planes * x.shape[1] + 2 * w["scales"].shape[-1] + 32  # both terms of a code, a group's scale, the waves' sums
     bound = n * U * (np.abs(x) @ A.T)
     if dx is not None:
         bound = bound + dx @ (np.abs(W) + n * U * A).T
@@ -79,8 +80,10 @@ def route(x, router, top_k, renormalize):
     return ids.astype(np.int32), w / w.sum(axis=1, keepdims=True) if renormalize else w
 
 
-def moe(x, dt, gate, up, down, ids, weights, out):
-    """The experts' sum for x [T][d] in fp64 with h rounded nowhere, and the bound that counts its rounding to dt."""
+def moe(x, gate, up, down, ids, weights, out):
+    """The experts' sum for x [T][d] in fp64 with h rounded nowhere, and the bound that counts its pieces: two bf16
+    terms (2^-8 of 2^-8 of it is lost) for a 16-bit result, three for fp32."""
+    planes = 3 if out == "fp32" else 2
     T, k = ids.shape
     E = gate["q"].shape[0]
     y = np.zeros((T, down["q"].shape[1]))
@@ -94,8 +97,8 @@ def moe(x, dt, gate, up, down, ids, weights, out):
             g, dg = product(x[t:t + 1], gate, e)
             u, du = product(x[t:t + 1], up, e)
             h, dh = silu_mul(g, dg, u, du)
-            dh = rounded(h, dh, dt)
-            v, dv = product(h, down, e, dh)
+            dh = dh + 2.0 ** (-8 * planes) * (np.abs(h) + dh)
+            v, dv = product(h, down, e, dh, planes)
             w = abs(float(weights[t, j]))
             y[t] += float(weights[t, j]) * v[0]
             b[t] += w * dv[0]
