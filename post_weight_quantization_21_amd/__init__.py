@@ -391,7 +391,7 @@ def w4a16_gemm(X, packed, scales, zeros, group_size: int, d_out: int, kperm=None
 class PackedWeight:
     """A packed layer (or a stack of equal ones) for ``gemv``, ``gemv_gated`` and ``moe_layer``: the tensors and
     their ``gptq_packed``.  Built once, next to the weights; it keeps the tensors alive."""
-    __slots__ = ("packed", "scales", "zeros", "kperm", "stack", "d_out", "d_in", "device", "c")
+    __slots__ = ("packed", "scales", "zeros", "kperm", "stack", "d_out", "d_in", "device", "c", "ref")
 
     def __init__(self, packed, scales, zeros, bits, group_size, kperm):
         import torch
@@ -419,6 +419,7 @@ class PackedWeight:
         self.packed, self.scales, self.zeros, self.kperm, self.device = packed, scales, zeros, kperm, packed.device
         self.c = Packed(packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
                         None if kperm is None else kperm.data_ptr(), self.d_out, self.d_in, bits, group_size)
+        self.ref = ctypes.byref(self.c)
 
 
 def packed_weight(packed, scales, zeros, bits: int = 4, group_size: int = 128, kperm=None) -> PackedWeight:
@@ -427,77 +428,111 @@ def packed_weight(packed, scales, zeros, bits: int = 4, group_size: int = 128, k
     return PackedWeight(packed, scales, zeros, int(bits), int(group_size), kperm)
 
 
-def _dt(dtype):
-    import torch
-    try:
-        return {torch.float32: DT_F32, torch.bfloat16: DT_BF16, torch.float16: DT_F16}[dtype]
-    except KeyError:
-        raise TypeError("tensors must be float16, bfloat16 or float32") from None
+# The few-token calls are made once per layer and token, so their host side is kept short: torch's types and the
+# library's functions are looked up once, and pointers pass as integers.
+_few_state = None
 
 
-def _few(X, Y, d_in, d_out, out_dtype, device):
-    """Checked activations and results of a few-token product: (X's type, Y, Y's type)."""
-    import torch
-    if X.dtype not in (torch.float16, torch.bfloat16):
+def _few_init():
+    global _few_state
+    if _few_state is None:
+        import torch
+        lib = load_library()
+        _few_state = (torch, lib, {torch.float16: DT_F16, torch.bfloat16: DT_BF16},
+                      {torch.float16: DT_F16, torch.bfloat16: DT_BF16, torch.float32: DT_F32})
+    return _few_state
+
+
+def _few_check_x(X, d_in, device, dtypes):
+    dt = dtypes.get(X.dtype)
+    if dt is None:
         raise TypeError("X must be float16 or bfloat16")
     if X.device != device or X.dim() != 2 or X.shape[1] != d_in or X.stride(1) != 1:
         raise ValueError(f"X must be [tokens][{d_in}] on the weights' device, contiguous within a row")
+    return dt
+
+
+def _few_result(X, Y, rows, d_out, out_dtype, device, torch, dtypes):
     if Y is None:
-        Y = torch.empty(X.shape[0], d_out, dtype=out_dtype or X.dtype, device=device)
+        Y = torch.empty((rows, d_out), dtype=out_dtype or X.dtype, device=device)
     elif out_dtype is not None and Y.dtype != out_dtype:
         raise TypeError("out_dtype is not the given result's type")
-    elif Y.device != device or tuple(Y.shape) != (X.shape[0], d_out) or Y.stride(1) != 1:
+    elif Y.device != device or tuple(Y.shape) != (rows, d_out) or Y.stride(1) != 1:
         raise ValueError(f"the result must be [tokens][{d_out}] on the weights' device, contiguous within a row")
-    return _dt(X.dtype), Y, _dt(Y.dtype)
+    dt = dtypes.get(Y.dtype)
+    if dt is None:
+        raise TypeError("the result must be float16, bfloat16 or float32")
+    return Y, dt
 
 
-def _few_stream(stream, device):
-    import torch
+def _few_launch(fn, device, stream, torch, *args):
+    """fn(*args, stream) with the weights' device current, on `stream` or that device's current stream."""
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-    if stream.device != device:
+        raw = torch._C._cuda_getCurrentRawStream(device.index)
+    elif stream.device != device:
         raise ValueError("the stream must be on the weights' device")
-    return ctypes.c_void_p(stream.cuda_stream)
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, raw)
+    if status != OK:
+        _check(status)
 
 
-def _pitch(t):
+def _few_ws(ws, device):
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError("the workspace must be a contiguous tensor on the weights' device")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _pitch(t, rows, cols):
     """Elements between rows (a single row has no next one: torch may report any stride for it)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return t.stride(0) if rows > 1 else cols
 
 
 def gemv(X, w: PackedWeight, bias=None, Y=None, out_dtype=None, ws=None, stream=None):
     """Y = X' W_hat^T (+ bias) for at most 16 tokens: X fp16 or bf16 [M][d_in], w a packed layer of 2, 3, 4 or 8 bits,
     bias fp32 [d_out]; Y [M][d_out] in X's type, or in out_dtype (fp16, bf16, fp32)."""
-    import torch
+    torch, lib, act, res = _few_init()
     if w.stack is not None:
         raise ValueError("gemv takes a single layer, not a stack")
-    xd, Y, yd = _few(X, Y, w.d_in, w.d_out, out_dtype, w.device)
-    if bias is not None and (bias.device != w.device or bias.dtype != torch.float32 or tuple(bias.shape) != (w.d_out,)
+    dev, d_in, d_out, M = w.device, w.d_in, w.d_out, X.shape[0]
+    xd = _few_check_x(X, d_in, dev, act)
+    Y, yd = _few_result(X, Y, M, d_out, out_dtype, dev, torch, res)
+    if bias is not None and (bias.device != dev or bias.dtype != torch.float32 or tuple(bias.shape) != (d_out,)
                              or not bias.is_contiguous()):
-        raise ValueError(f"bias must be a contiguous float32 [{w.d_out}] on the weights' device")
-    if ws is None and w.kperm is not None:
-        ws = _workspace(workspace_bytes(OP_GEMV, w.d_out, w.d_in, X.shape[0]), w.device)
-    with torch.cuda.device(w.device):
-        _check(load_library().gptq_gemv(_ptr(X), xd, X.shape[0], _pitch(X), ctypes.byref(w.c), _ptr(bias), _ptr(Y), yd,
-                                        _pitch(Y), _ptr(ws), 0 if ws is None else ws.numel(), _few_stream(stream, w.device)))
+        raise ValueError(f"bias must be a contiguous float32 [{d_out}] on the weights' device")
+    if w.kperm is None:
+        wp, wn = None, 0
+    else:
+        wp, wn = _few_ws(_workspace(workspace_bytes(OP_GEMV, d_out, d_in, M), dev) if ws is None else ws, dev)
+    _few_launch(lib.gptq_gemv, dev, stream, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), w.ref,
+                None if bias is None else bias.data_ptr(), Y.data_ptr(), yd, _pitch(Y, M, d_out), wp, wn)
     return Y
 
 
 def gemv_gated(X, gate: PackedWeight, up: PackedWeight, H=None, out_dtype=None, ws=None, stream=None):
     """H = silu(X' W_gate^T) * (X' W_up^T), the first half of a gated MLP, for at most 16 tokens; types as in gemv.
     gate and up share one column order (the same kperm tensor), as they share their inputs."""
-    import torch
+    torch, lib, act, res = _few_init()
     if gate.stack is not None or up.stack is not None:
         raise ValueError("gemv_gated takes single layers, not stacks")
-    if up.device != gate.device:
+    dev, d_in, d_ff, M = gate.device, gate.d_in, gate.d_out, X.shape[0]
+    if up.device != dev:
         raise ValueError("gate and up must be on one device")
-    xd, H, hd = _few(X, H, gate.d_in, gate.d_out, out_dtype, gate.device)
-    if ws is None and gate.kperm is not None:
-        ws = _workspace(workspace_bytes(OP_GEMV, gate.d_out, gate.d_in, X.shape[0]), gate.device)
-    with torch.cuda.device(gate.device):
-        _check(load_library().gptq_gemv_gated(_ptr(X), xd, X.shape[0], _pitch(X), ctypes.byref(gate.c),
-                                              ctypes.byref(up.c), _ptr(H), hd, _pitch(H), _ptr(ws),
-                                              0 if ws is None else ws.numel(), _few_stream(stream, gate.device)))
+    xd = _few_check_x(X, d_in, dev, act)
+    H, hd = _few_result(X, H, M, d_ff, out_dtype, dev, torch, res)
+    if gate.kperm is None:
+        wp, wn = None, 0
+    else:
+        wp, wn = _few_ws(_workspace(workspace_bytes(OP_GEMV, d_ff, d_in, M), dev) if ws is None else ws, dev)
+    _few_launch(lib.gptq_gemv_gated, dev, stream, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), gate.ref, up.ref,
+                H.data_ptr(), hd, _pitch(H, M, d_ff), wp, wn)
     return H
 
 
@@ -512,39 +547,46 @@ def moe_layer(X, gate: PackedWeight, up: PackedWeight, down: PackedWeight, route
     """A mixture-of-experts layer for at most 16 tokens: gate, up (stacks [E][d_ff][d]) and down ([E][d][d_ff]) packed,
     X fp16 or bf16 [T][d].  With a router ([E][d], fp32 or X's type) it chooses top_k experts per token; without one,
     ids (int32 [T][top_k]) and weights (fp32 [T][top_k]) are the caller's routing.  Returns (Y, ids, weights)."""
-    import torch
-    E, dev = gate.stack, gate.device
+    torch, lib, act, res = _few_init()
+    E, dev, d, T = gate.stack, gate.device, gate.d_in, X.shape[0]
     if E is None or up.stack != E or down.stack != E:
         raise ValueError("gate, up and down must be stacks of the same number of experts")
     if up.device != dev or down.device != dev:
         raise ValueError("gate, up and down must be on one device")
-    xd, Y, yd = _few(X, Y, gate.d_in, gate.d_in, out_dtype, dev)
-    T, rd = X.shape[0], DT_F32
+    xd = _few_check_x(X, d, dev, act)
+    Y, yd = _few_result(X, Y, T, d, out_dtype, dev, torch, res)
+    rp, rd = None, DT_F32
     if router is None:
         if ids is None or weights is None:
             raise ValueError("without a router, ids and weights are needed")
-        top_k = ids.shape[1] if top_k is None else int(top_k)
+        if top_k is None:
+            top_k = ids.shape[1]
     else:
         if top_k is None:
             raise ValueError("a router needs top_k")
-        top_k = int(top_k)
-        if router.device != dev or tuple(router.shape) != (E, gate.d_in) or not router.is_contiguous():
-            raise ValueError(f"router must be a contiguous [{E}][{gate.d_in}] on the weights' device")
-        rd = _dt(router.dtype)
-        if ids is None:
-            ids = torch.empty(T, top_k, dtype=torch.int32, device=dev)
-        if weights is None:
-            weights = torch.empty(T, top_k, dtype=torch.float32, device=dev)
-    for t, dt in ((ids, torch.int32), (weights, torch.float32)):
-        if t.device != dev or t.dtype != dt or tuple(t.shape) != (T, top_k) or not t.is_contiguous():
-            raise ValueError(f"ids must be int32 and weights float32, contiguous [{T}][{top_k}] on the weights' device")
+        if router.device != dev or tuple(router.shape) != (E, d) or not router.is_contiguous():
+            raise ValueError(f"router must be a contiguous [{E}][{d}] on the weights' device")
+        rp, rd = router.data_ptr(), res.get(router.dtype)
+        if rd is None:
+            raise TypeError("router must be float32 or of X's type")
+    top_k = int(top_k)
+    if not 1 <= top_k <= E:
+        raise ValueError("top_k must be 1 .. the number of experts")
+    if ids is None:
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+    elif ids.device != dev or ids.dtype != torch.int32 or tuple(ids.shape) != (T, top_k) or not ids.is_contiguous():
+        raise ValueError(f"ids must be a contiguous int32 [{T}][{top_k}] on the weights' device")
+    if weights is None:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+    elif weights.device != dev or weights.dtype != torch.float32 or tuple(weights.shape) != (T, top_k) or \
+            not weights.is_contiguous():
+        raise ValueError(f"weights must be a contiguous float32 [{T}][{top_k}] on the weights' device")
     if ws is None:
-        ws = _workspace(moe_workspace_bytes(T, gate.d_in, gate.d_out, E, top_k), dev)
-    with torch.cuda.device(dev):
-        _check(load_library().gptq_moe_layer(_ptr(X), xd, T, _pitch(X), _ptr(router), rd, E, top_k, int(bool(renormalize)),
-                                             ctypes.byref(gate.c), ctypes.byref(up.c), ctypes.byref(down.c), _ptr(ids),
-                                             _ptr(weights), _ptr(Y), yd, _pitch(Y), _ptr(ws), ws.numel(),
-                                             _few_stream(stream, dev)))
+        ws = _workspace(moe_workspace_bytes(T, d, gate.d_out, E, top_k), dev)
+    wp, wn = _few_ws(ws, dev)
+    _few_launch(lib.gptq_moe_layer, dev, stream, torch, X.data_ptr(), xd, T, _pitch(X, T, d), rp, rd, E, top_k,
+                1 if renormalize else 0, gate.ref, up.ref, down.ref, ids.data_ptr(), weights.data_ptr(), Y.data_ptr(), yd,
+                _pitch(Y, T, d), wp, wn)
     return Y, ids, weights
 
 

@@ -238,24 +238,27 @@ __device__ __forceinline__ void load_unit(const uint32_t *p, uint32_t *w) {
     }
 }
 
-// How a workgroup of kFewWaves waves shares a product: `slices` waves split K
-// between them on each of kFewWaves / slices row tiles.
+// How a workgroup of kFewWaves waves shares a product: 2^lg waves (slices) split
+// K between them on each of kFewWaves >> lg row tiles.
 constexpr int kFewWaves = 8;
 constexpr int kFewThreads = kFewWaves * kWave;
-// x is staged in LDS in chunks of at most this many 16-bit values, two buffers.
-constexpr int kChunkValues = 16384;
+constexpr int kFewOccupancy = 4;             // waves per SIMD, which the kernels' registers allow
+constexpr int kFewResident = 256 * 4 * kFewOccupancy;  // waves of the chip at once
+// x is staged in LDS in chunks, a unit of a row per thread, two buffers.
 constexpr int kXPad = 8;  // values after each staged row: sixteen rows start in different banks
 
 // Rows of activations: row m of plane p is base + p * plane + row(m) * ld.
 struct XRows {
     const uint16_t *base;
     int64_t ld, plane;
-    const int32_t *row;  // row numbers, or NULL for m itself
+    bool gathered;  // rows are numbered by `row` of lane m, else m itself
+    int32_t row;
 };
 
-// Steps of K that a chunk of `rows` staged rows holds, at most all of them.
+__host__ __device__ inline int ceil_log2(int n) { return n <= 1 ? 0 : 32 - __builtin_clz((unsigned)(n - 1)); }
+// Steps of K that a chunk of `rows` staged rows (P M) holds, at most all of them.
 __host__ __device__ inline int chunk_steps(int rows, int steps) {
-    const int c = kChunkValues / (rows * kStep);
+    const int c = (kFewThreads / 4) >> ceil_log2(rows);
     return c < steps ? c : steps;
 }
 __host__ __device__ inline int staged_ld(int chunk) { return chunk * kStep + kXPad; }
@@ -263,7 +266,7 @@ __host__ __device__ inline int staged_ld(int chunk) { return chunk * kStep + kXP
 // activations, or the waves' sums after it.
 inline size_t few_lds_bytes(int max_rows, int planes, int units) {
     const int steps = (units + 3) / 4;
-    size_t bytes = (size_t)kFewWaves * kFewRows * kTileRows * 4;
+    size_t bytes = (size_t)kFewWaves * max_rows * kTileRows * 4;
     for (int m = 1; m <= max_rows; ++m) {
         const int chunk = chunk_steps(planes * m, steps);
         const size_t one = (size_t)planes * m * staged_ld(chunk) * 2;
@@ -278,43 +281,39 @@ inline size_t few_lds_bytes(int max_rows, int planes, int units) {
 template <int b, typename T, int P>
 struct StageX {
     typedef typename Vec8<T>::V V;
-    static constexpr int kPerThread = (kChunkValues / kUnit + kFewThreads - 1) / kFewThreads;
-    uint4 v[kPerThread][4];
-    __device__ __forceinline__ void load(const XRows &x, int M, int c0, int n, int units) {
-        const int per_row = 4 * n, items = P * M * per_row;
+    int r, u;             // the thread's staged row (r >= P M: none) and its unit in the chunk
+    const uint16_t *src;  // the row's columns
+    uint4 v[4];
+    __device__ __forceinline__ void init(const XRows &x, int M) {
+        const int lg = 9 - ceil_log2(P * M);  // log2 of the threads per row
+        static_assert(kFewThreads == 512, "threads per row");
+        r = threadIdx.x >> lg;
+        u = threadIdx.x & ((1 << lg) - 1);
+        const int p = P == 1 ? 0 : (r >= M) + (P > 2 && r >= 2 * M), m = r - p * M;
+        const int row = x.gathered ? __shfl(x.row, m) : m;
+        src = x.base + (r < P * M ? p * x.plane + row * x.ld : 0);
+    }
+    __device__ __forceinline__ void load(int M, int c0, int n, int units) {
 #pragma unroll
-        for (int k = 0; k < kPerThread; ++k) {
-            const int it = threadIdx.x + k * kFewThreads;
-            const int r = it / per_row, u = 4 * c0 + it - r * per_row;
-            const int p = r / M, m = r - p * M;
+        for (int i = 0; i < 4; ++i) v[i] = make_uint4(0, 0, 0, 0);
+        if (r < P * M && u < 4 * n && 4 * c0 + u < units) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[k][i] = make_uint4(0, 0, 0, 0);
-            if (it < items && u < units) {
-                const uint16_t *src = x.base + p * x.plane + (int64_t)(x.row ? x.row[m] : m) * x.ld + u * kUnit;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[k][i] = reinterpret_cast<const uint4 *>(src)[i];
-            }
+            for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4 *>(src + (4 * c0 + u) * kUnit)[i];
         }
     }
     __device__ __forceinline__ void store(uint16_t *xs, int M, int n, int ld) const {
-        const int per_row = 4 * n, items = P * M * per_row;
+        if (r >= P * M || u >= 4 * n) return;
+        uint32_t w[16];
 #pragma unroll
-        for (int k = 0; k < kPerThread; ++k) {
-            const int it = threadIdx.x + k * kFewThreads;
-            if (it >= items) continue;
-            const int r = it / per_row, u = it - r * per_row;
-            uint32_t w[16];
+        for (int i = 0; i < 4; ++i) w[4 * i] = v[i].x, w[4 * i + 1] = v[i].y, w[4 * i + 2] = v[i].z, w[4 * i + 3] = v[i].w;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[4 * i] = v[k][i].x, w[4 * i + 1] = v[k][i].y, w[4 * i + 2] = v[k][i].z, w[4 * i + 3] = v[k][i].w;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<V *>(xs + r * ld + u * kUnit + 8 * i) = Codes<b, T>::xfrag(w, i);
-        }
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<V *>(xs + r * ld + u * kUnit + 8 * i) = Codes<b, T>::xfrag(w, i);
     }
 };
 
 // The wave's sums for a tile of 16 weight rows over its slice of K, from x
 // staged chunk by chunk; every wave of the workgroup calls it, with the same x.
-// row: the lane's weight row (clamped into the matrix) in the stack w.  kSplit:
+// row0: the tile's first row in the stack w, rows: its rows there.  kSplit:
 // groups end inside a step, so the fragments of the four lane rows are
 // transposed to make each matrix instruction cover one unit, and the fold with
 // the scale runs per unit; otherwise it runs per step.
@@ -324,8 +323,8 @@ struct StageX {
 // Scales and zeros come with it: without kSplit lane row kb reads those of step
 // kb of the body and the rows trade them (spread4), one load for four steps.
 template <int b, typename T, int P, bool kSplit>
-__device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row, const XRows &x, int M, int slice,
-                                               int slices, uint16_t *lds) {
+__device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row0, int rows, const XRows &x, int M,
+                                               int slice, int lg, uint16_t *lds) {
     typedef typename Vec8<T>::V V;
     typedef Codes<b, T> C;
     constexpr int S = b == 8 || (kSplit && P > 1) ? 2 : 4;
@@ -333,8 +332,9 @@ __device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row, 
     const int lane = threadIdx.x % kWave, kb = lane >> 4;
     const int units = w.units, steps = (units + 3) / 4;
     const int chunk = chunk_steps(P * M, steps), ld = staged_ld(chunk);
-    const uint32_t *wp = w.packed + row * w.words;
-    const float *sp = w.scales + row * w.groups, *zp = w.zeros + row * w.groups;
+    const int rl = std::min(lane & 15, rows - 1);
+    const uint32_t *wp = w.packed + row0 * w.words + (int64_t)rl * w.words;
+    const float *sp = w.scales + row0 * w.groups + rl * w.groups, *zp = w.zeros + row0 * w.groups + rl * w.groups;
     const SmallDiv by = w.by;
     struct Body {
         uint32_t w[S][b];
@@ -357,8 +357,9 @@ __device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row, 
     };
     floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     StageX<b, T, P> stage;
-    stage.load(x, M, 0, chunk, units);
-    int s = slice * chunk / slices, end = (slice + 1) * chunk / slices;  // of the first chunk
+    stage.init(x, M);
+    stage.load(M, 0, chunk, units);
+    int s = slice * chunk >> lg, end = (slice + 1) * chunk >> lg;  // of the first chunk
     load(nxt, s);
     stage.store(lds, M, chunk, ld);
     __syncthreads();
@@ -367,8 +368,8 @@ __device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row, 
     const int m = std::min(lane & 15, M - 1);
     for (int c0 = 0; c0 < steps; c0 += chunk) {
         const int c1 = c0 + chunk, n1 = std::min(chunk, steps - c1);  // the next chunk, if n1 > 0
-        if (n1 > 0) stage.load(x, M, c1, n1, units);
-        const int next = c1 + slice * n1 / slices;
+        if (n1 > 0) stage.load(M, c1, n1, units);
+        const int next = c1 + (slice * n1 >> lg);
         const uint16_t *xl = buf + m * ld + kb * (kSplit ? 8 : kUnit);
         if (s >= end) load(nxt, next);  // fewer steps than slices: nothing here for this wave
         for (; s < end; s += S) {
@@ -432,28 +433,34 @@ __device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row, 
             buf = other;
             other = t;
             s = next;
-            end = c1 + (slice + 1) * n1 / slices;
+            end = c1 + ((slice + 1) * n1 >> lg);
         }
     }
     return acc;
 }
 
-// The waves' sums through LDS: after it, sums[wave][m][row] of the workgroup.
-typedef float FewSums[kFewRows][kTileRows];
-__device__ __forceinline__ void few_share(FewSums *sums, int wave, const floatx4 &acc, int M) {
+// The waves' sums through LDS: after it, sums[(wave * M + m) * 16 + row] of the workgroup.
+__device__ __forceinline__ void few_share(float *sums, int wave, const floatx4 &acc, int M) {
     const int lane = threadIdx.x % kWave;
     __syncthreads();  // the staged activations are no longer read
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
-        if (4 * (lane >> 4) + t < M) sums[wave][4 * (lane >> 4) + t][lane & 15] = acc[t];
+    for (int t = 0; t < 4; ++t) {
+        const int m = 4 * (lane >> 4) + t;
+        if (m < M) sums[(wave * M + m) * kTileRows + (lane & 15)] = acc[t];
+    }
     __syncthreads();
+}
+// Sum over the 2^lg waves from `wave` on of row c of their tile and token m.
+__device__ __forceinline__ float few_sum(const float *sums, int wave, int lg, int M, int m, int c) {
+    float v = 0.0f;
+    for (int k = 0; k < 1 << lg; ++k) v += sums[((wave + k) * M + m) * kTileRows + c];
+    return v;
 }
 // The wave's number in the workgroup, known to be the same in all its lanes.
 __device__ __forceinline__ int few_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
 
-// Waves that split K for one row tile, at most `most`, so that `tiles` tiles make
-// about as many waves as the chip holds at once (16 a compute unit) while a wave
-// keeps at least a body of steps.
+// log2 of the waves that split K for one row tile, at most `most`: as many as
+// `tiles` tiles leave room for on the chip at once while a wave keeps a body of steps.
 int few_slices(int64_t tiles, int units, int most);
 
 // Rounding of a result to the output's type, to nearest even.

@@ -14,8 +14,9 @@ namespace {
 
 struct GemvArgs {
     PackedDev w[2];
-    XRows x;
-    int M, slices;
+    const uint16_t *x;
+    int64_t ldx;
+    int M, lg;
     const float *bias;
     void *y;
     int64_t ldy;
@@ -24,33 +25,29 @@ struct GemvArgs {
 
 // Gated: waves of the even tiles take the gate's rows, those of the odd ones up's.
 template <int b, typename T, bool kGated, bool kSplit>
-__global__ __launch_bounds__(kFewThreads, 4) void gemv_kernel(GemvArgs a) {
+__global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    constexpr int R = kGated ? 2 : 1;
-    const int wave = few_wave(), lane = threadIdx.x % kWave;
-    const int tiles = kFewWaves / a.slices / R, tile = wave / a.slices;
-    const int64_t r0 = (int64_t)blockIdx.x * tiles * kTileRows;
-    const int64_t row = std::min<int64_t>(r0 + tile / R * kTileRows + (lane & 15), a.w[0].d_out - 1);
-    const floatx4 acc = few_product<b, T, 1, kSplit>(a.w[kGated ? tile & 1 : 0], row, a.x, a.M, wave % a.slices, a.slices,
-                                                     reinterpret_cast<uint16_t *>(smem));
-    FewSums *sums = reinterpret_cast<FewSums *>(smem);
+    constexpr int R = kGated ? 2 : 1, LR = kGated ? 1 : 0;
+    const int wave = few_wave(), lg = a.lg;
+    const int lt = 3 - lg - LR;  // log2 of the row tiles
+    const int tile = wave >> lg;
+    const int64_t r0 = (int64_t)blockIdx.x * kTileRows << lt, d_out = a.w[0].d_out;
+    const int64_t rt = std::min(r0 + (tile >> LR) * kTileRows, d_out - 1);
+    const XRows x = {a.x, a.ldx, 0, false, 0};
+    const floatx4 acc = few_product<b, T, 1, kSplit>(kGated && (tile & 1) ? a.w[R - 1] : a.w[0], rt, (int)std::min<int64_t>(kTileRows, d_out - rt),
+                                                     x, a.M, wave & ((1 << lg) - 1), lg, reinterpret_cast<uint16_t *>(smem));
+    float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, a.M);
-    for (int n = threadIdx.x; n < a.M * tiles * kTileRows; n += kFewThreads) {
-        const int m = n / (tiles * kTileRows), c = n % (tiles * kTileRows);
-        const int64_t out = r0 + c;
-        if (out >= a.w[0].d_out) continue;
-        float v[R];
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            v[r] = 0.0f;
-            for (int k = 0; k < a.slices; ++k) v[r] += sums[(c / kTileRows * R + r) * a.slices + k][m][c % kTileRows];
-        }
-        float y;
+    for (int n = threadIdx.x; n < a.M * kTileRows << lt; n += kFewThreads) {
+        const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
+        if (r0 + c >= d_out) continue;
+        const int w0 = (c >> 4) << (LR + lg);
+        float y = few_sum(sums, w0, lg, a.M, m, c & 15);
         if constexpr (kGated)
-            y = silu_mul(v[0], v[R - 1]);
-        else
-            y = a.bias ? v[0] + a.bias[out] : v[0];
-        store_as(a.y, m * a.ldy + out, a.y_dt, y);
+            y = silu_mul(y, few_sum(sums, w0 + (1 << lg), lg, a.M, m, c & 15));
+        else if (a.bias)
+            y += a.bias[r0 + c];
+        store_as(a.y, m * a.ldy + r0 + c, a.y_dt, y);
     }
 }
 
@@ -66,7 +63,7 @@ __global__ __launch_bounds__(256) void gather_kernel(const uint16_t *__restrict_
 
 template <int b, typename T>
 void launch_gemv(const GemvArgs &a, bool gated, hipStream_t s) {
-    const dim3 grid((unsigned)ceil_div(a.w[0].d_out, kTileRows * (kFewWaves / a.slices / (gated ? 2 : 1))));
+    const dim3 grid((unsigned)ceil_div(a.w[0].d_out, kTileRows * ((kFewWaves >> a.lg) / (gated ? 2 : 1))));
     const size_t lds = few_lds_bytes(a.M, 1, a.w[0].units);
     if (gated) {
         if (a.w[0].split)
@@ -111,9 +108,9 @@ PackedDev packed_dev(const gptq_packed &w) {
 
 int few_slices(int64_t tiles, int units, int most) {
     const int steps = (units + 3) / 4;
-    int slices = 1;
-    while (slices < most && tiles * slices < 4096 && slices * 4 < steps) slices *= 2;
-    return slices;
+    int lg = 0;
+    while (2 << lg <= most && (tiles << (lg + 1)) <= kFewResident && (4 << lg) < steps) ++lg;
+    return lg;
 }
 
 size_t gemv_ws_bytes(int64_t M, int64_t d_in) { return align_up((size_t)M * (size_t)d_in * 2, 256); }
@@ -123,10 +120,11 @@ hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, cons
     GemvArgs a;
     a.w[0] = packed_dev(w);
     a.w[1] = packed_dev(up ? *up : w);
-    a.x = {static_cast<const uint16_t *>(X), ldx, 0, nullptr};
+    a.x = static_cast<const uint16_t *>(X);
+    a.ldx = ldx;
     a.M = (int)M;
-    a.slices = up ? few_slices(2 * ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves / 2)
-                  : few_slices(ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves);
+    a.lg = up ? few_slices(2 * ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves / 2)
+              : few_slices(ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves);
     a.bias = bias;
     a.y = Y;
     a.ldy = ldy;
@@ -136,8 +134,8 @@ hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, cons
             static_cast<const uint16_t *>(X), ldx, w.d_in, w.kperm, static_cast<uint16_t *>(ws));
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        a.x.base = static_cast<const uint16_t *>(ws);
-        a.x.ld = w.d_in;
+        a.x = static_cast<const uint16_t *>(ws);
+        a.ldx = w.d_in;
     }
     if (x_dt == GPTQ_DT_BF16)
         launch_gemv_bits<__bf16>(a, w.bits, up != nullptr, s);

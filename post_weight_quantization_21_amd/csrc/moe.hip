@@ -24,17 +24,20 @@ namespace gptq {
 namespace {
 
 constexpr int kMaxPairs = kMoeMaxTokens * kMoeMaxTopK;
-constexpr int kChooseWaves = 16;
 
-// The chosen (token, expert) pairs, expert by expert, tokens ascending.
+// The chosen (token, expert) pairs, numbered expert by expert, tokens ascending.
+struct Expert {  // the a-th expert chosen by any token; count 0 past the last
+    int32_t expert, start, count, pad;  // its pairs
+    int32_t token[kMoeMaxTokens];
+};
+struct Token {  // a token's pairs, ascending
+    int32_t count, pad[3];
+    int32_t pair[kMoeMaxTopK];
+    float weight[kMoeMaxTopK];
+};
 struct Lists {
-    int32_t n;                      // experts chosen by any token
-    int32_t expert[kMaxPairs];      // ... in ascending order
-    int32_t start[kMaxPairs + 1];   // their first pairs
-    int32_t token[kMaxPairs];
-    float weight[kMaxPairs];
-    int32_t of_count[kMoeMaxTokens];               // a token's pairs ...
-    int32_t of_token[kMoeMaxTokens][kMoeMaxTopK];  // ... in their order
+    Token token[kMoeMaxTokens];
+    Expert expert[kMaxPairs];
 };
 
 template <typename T>
@@ -80,70 +83,109 @@ __global__ __launch_bounds__(256) void router_kernel(const T *__restrict__ X, in
         logits[(int64_t)(t0 + t) * n_experts + e] = part[0][t] + part[1][t] + part[2][t] + part[3][t];
 }
 
+// A logit's rank as an unsigned key: ascending with the logit to 43 significant
+// bits, then descending with the expert's index; a NaN lies below every number.
+__device__ __forceinline__ uint64_t rank_key(double v, int e) {
+    uint64_t k = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
+    k = k >> 63 ? ~k : k | (1ull << 63);
+    if (v != v) k = 1ull << 9;  // above "no candidate", which is 0
+    return (k & ~511ull) | (511 - e);
+}
+template <int ctrl, int rows>
+__device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)v, ctrl, rows, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(v >> 32), ctrl, rows, 0xf, false);
+    const uint64_t o = (uint64_t)hi << 32 | lo;
+    return o > v ? o : v;
+}
+// The largest of the wave's values, in every lane: prefix maxima within rows of
+// 16 lanes (row_shr), then across rows (row_bcast), and the last lane's value.
+__device__ __forceinline__ uint64_t wave_max(uint64_t v) {
+    v = dpp_max<0x111, 0xf>(v);
+    v = dpp_max<0x112, 0xf>(v);
+    v = dpp_max<0x114, 0xf>(v);
+    v = dpp_max<0x118, 0xf>(v);
+    v = dpp_max<0x142, 0xa>(v);
+    v = dpp_max<0x143, 0xc>(v);
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
+}
+
 __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__ logits, int n_tok, int n_experts,
-                                                      int top_k, int renormalize, int32_t *ids, float *weights,
+                                                      int top_k, int renormalize, int slots, int32_t *ids, float *weights,
                                                       Lists *lists) {
     __shared__ int32_t sel[kMoeMaxTokens][kMoeMaxTopK];
     __shared__ float wsel[kMoeMaxTokens][kMoeMaxTopK];
     __shared__ uint32_t tokens_of[kMoeMaxExperts];  // bit t: token t chose the expert
-    __shared__ uint32_t wave_sum[kChooseWaves];
+    __shared__ uint32_t wave_sum[kMoeMaxExperts / kWave];
     __shared__ uint8_t token_of[kMaxPairs];
-    const int tid = threadIdx.x, wave = tid / kWave, lane = tid % kWave;
+    __shared__ float weight_of[kMaxPairs];
+    const int tid = threadIdx.x, wave = few_wave(), lane = tid % kWave;
     constexpr int kPer = kMoeMaxExperts / kWave;
     if (tid < kMoeMaxExperts) tokens_of[tid] = 0;
     if (wave < n_tok) {
+        int e = -1;
+        float w = 0.0f;
         if (!logits) {
             if (lane < top_k) {
-                sel[wave][lane] = ids[wave * top_k + lane];
-                wsel[wave][lane] = weights[wave * top_k + lane];
+                e = ids[wave * top_k + lane];
+                w = weights[wave * top_k + lane];
             }
         } else {
             double v[kPer];
-            double top = -INFINITY;
-            uint32_t left = 0;  // bit i: expert lane + 64 i not chosen yet
+            uint64_t key[kPer];  // 0: no candidate (any more)
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                const int e = lane + kWave * i;
-                v[i] = e < n_experts ? logits[(int64_t)wave * n_experts + e] : 0.0;
-                if (e < n_experts) left |= 1u << i;
-            }
-            bool bad = false;  // a NaN logit makes every probability NaN, as the softmax's sum is
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (left >> i & 1) {
-                    bad |= v[i] != v[i];
-                    top = fmax(top, v[i]);
+                const int c = lane + kWave * i;
+                v[i] = 0.0;
+                key[i] = 0;
+                if (kWave * i < n_experts && c < n_experts) {
+                    v[i] = logits[(int64_t)wave * n_experts + c];
+                    key[i] = rank_key(v[i], c);
                 }
-            for (int o = 32; o > 0; o >>= 1) top = fmax(top, __shfl_xor(top, o));
-            double sum = 0.0;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (left >> i & 1) sum += exp(v[i] - top);
-            for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-            if (__any(bad)) sum = NAN;
-            double chosen = 0.0, mine = 0.0;  // sum of the chosen probabilities; lane j: the j-th
+            }
+            uint64_t any_nan = 0;
+            double top = -INFINITY;
             for (int j = 0; j < top_k; ++j) {
-                double bv = -INFINITY;
-                int be = INT32_MAX;  // none
+                uint64_t best = key[0];
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    const double c = v[i] == v[i] ? v[i] : -INFINITY;  // NaN ranks below every number
-                    if ((left >> i & 1) && (be == INT32_MAX || c > bv)) bv = c, be = lane + kWave * i;
-                }
-                for (int o = 32; o > 0; o >>= 1) {
-                    const double ov = __shfl_xor(bv, o);
-                    const int oe = __shfl_xor(be, o);
-                    if (oe != INT32_MAX && (be == INT32_MAX || ov > bv || (ov == bv && oe < be))) bv = ov, be = oe;
-                }
-                if ((be & 63) == lane) left &= ~(1u << (be >> 6));
-                const double p = exp(bv - top) / sum;
-                chosen += p;
-                if (lane == j) {
-                    mine = p;
-                    sel[wave][j] = be;
-                }
+                for (int i = 1; i < kPer; ++i)
+                    if (kWave * i < n_experts) best = key[i] > best ? key[i] : best;
+                best = wave_max(best);
+                const int be = 511 - (int)(best & 511);
+                if (lane == j) e = be;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i)
+                    if (key[i] == best) key[i] = 0;
             }
-            if (lane < top_k) wsel[wave][lane] = (float)(renormalize ? mine / chosen : mine);
+            // softmax: the first choice holds the largest logit
+            const int e0 = __builtin_amdgcn_readfirstlane(e);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (kWave * i < n_experts) {
+                    if (e0 >> 6 == i) top = __shfl(v[i], e0 & 63);
+                    any_nan |= __ballot(v[i] != v[i]);
+                }
+            double sum = 0.0, mine = 0.0;  // lane j < top_k: its chosen logit
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (kWave * i < n_experts) {
+                    if (lane + kWave * i < n_experts) sum += exp(v[i] - top);
+                    const double c = __shfl(v[i], e & 63);
+                    if (e >> 6 == i) mine = c;
+                }
+            for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+            if (any_nan) sum = NAN;  // as the sum over the softmax would be
+            double p = lane < top_k ? exp(mine - top) / sum : 0.0, chosen = p;
+            if (renormalize) {
+                for (int o = kMoeMaxTopK / 2; o > 0; o >>= 1) chosen += __shfl_xor(chosen, o);
+                p /= chosen;
+            }
+            w = (float)p;
+        }
+        if (lane < top_k) {
+            sel[wave][lane] = e;
+            wsel[wave][lane] = w;
         }
     }
     __syncthreads();
@@ -158,11 +200,13 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
     const uint32_t mask = tid < kMoeMaxExperts ? tokens_of[tid] : 0;
     const uint32_t own = (mask ? 0x10000u : 0u) + __popc(mask);
     uint32_t inc = own;
-    for (int o = 1; o < kWave; o <<= 1) {
-        const uint32_t up = __shfl_up(inc, o);
-        if (lane >= o) inc += up;
+    if (tid < kMoeMaxExperts) {
+        for (int o = 1; o < kWave; o <<= 1) {
+            const uint32_t up = __shfl_up(inc, o);
+            if (lane >= o) inc += up;
+        }
+        if (lane == kWave - 1) wave_sum[wave] = inc;
     }
-    if (lane == kWave - 1) wave_sum[wave] = inc;
     __syncthreads();
     uint32_t before = inc - own, total = 0;
     for (int w = 0; w < kMoeMaxExperts / kWave; ++w) {
@@ -170,34 +214,38 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
         total += wave_sum[w];
     }
     if (mask) {
-        int p = before & 0xFFFF;
-        lists->expert[before >> 16] = tid;
-        lists->start[before >> 16] = p;
-        for (uint32_t m = mask; m; m &= m - 1, ++p) {
+        Expert &x = lists->expert[before >> 16];
+        int p = before & 0xFFFF, n = 0;
+        x.expert = tid;
+        x.start = p;
+        x.count = __popc(mask);
+        for (uint32_t m = mask; m; m &= m - 1, ++p, ++n) {
             const int t = __ffs(m) - 1;
             float w = 0.0f;
             for (int j = 0; j < top_k; ++j)
                 if (sel[t][j] == tid) w += wsel[t][j];
+            x.token[n] = t;
             token_of[p] = (uint8_t)t;
-            lists->token[p] = t;
-            lists->weight[p] = w;
+            weight_of[p] = w;
         }
     }
-    if (tid == 0) {
-        lists->n = total >> 16;
-        lists->start[total >> 16] = total & 0xFFFF;
-    }
+    if (tid >= (int)(total >> 16) && tid < slots) lists->expert[tid].count = 0;
     __syncthreads();
     if (wave < n_tok) {
         const int pairs = total & 0xFFFF;
+        Token &x = lists->token[wave];
         int n = 0;
         for (int p0 = 0; p0 < pairs; p0 += kWave) {
             const bool hit = p0 + lane < pairs && token_of[p0 + lane] == wave;
             const uint64_t hits = __ballot(hit);
-            if (hit) lists->of_token[wave][n + __popcll(hits & ((1ull << lane) - 1))] = p0 + lane;
+            if (hit) {
+                const int i = n + __popcll(hits & ((1ull << lane) - 1));
+                x.pair[i] = p0 + lane;
+                x.weight[i] = weight_of[p0 + lane];
+            }
             n += __popcll(hits);
         }
-        if (lane == 0) lists->of_count[wave] = n;
+        if (lane == 0) x.count = n;
     }
 }
 
@@ -206,50 +254,48 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
 __global__ __launch_bounds__(256) void gather_pairs_kernel(const uint16_t *__restrict__ in, int64_t ld, int by_token,
                                                            int64_t plane, const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
                                                            int d, uint16_t *__restrict__ out) {
-    const int a = blockIdx.y;
-    if (a >= lists->n) return;
+    const Expert &e = lists->expert[blockIdx.y];
     const int k = blockIdx.x * 256 + threadIdx.x;
     if (k >= d) return;
     in += blockIdx.z * plane;
     out += blockIdx.z * plane;
-    int c = kperm[(int64_t)lists->expert[a] * d + k];
+    if (e.count == 0) return;
+    int c = kperm[(int64_t)e.expert * d + k];
     c = c < 0 ? 0 : (c >= d ? d - 1 : c);
-    for (int p = lists->start[a]; p < lists->start[a + 1]; ++p)
-        out[(int64_t)p * d + k] = in[(by_token ? lists->token[p] : p) * ld + c];
+    for (int i = 0; i < e.count; ++i)
+        out[(int64_t)(e.start + i) * d + k] = in[(by_token ? e.token[i] : e.start + i) * ld + c];
 }
 
 struct GateUpArgs {
     PackedDev w[2];
     const uint16_t *x;  // rows by token, or by pair (ldx = d) when gathered
     int64_t ldx;
-    int by_pair, slices, planes;
+    int by_pair, lg, planes;
     const Lists *lists;
     __bf16 *h;
     int64_t h_plane;
 };
 
 template <int b, typename T, bool kSplit>
-__global__ __launch_bounds__(kFewThreads, 4) void gate_up_kernel(GateUpArgs a) {
+__global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(GateUpArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    if ((int)blockIdx.y >= a.lists->n) return;
-    const int wave = few_wave(), lane = threadIdx.x % kWave;
-    const int tiles = kFewWaves / a.slices / 2, tile = wave / a.slices;
-    const int start = a.lists->start[blockIdx.y], count = a.lists->start[blockIdx.y + 1] - start;
-    const int ff = a.w[0].d_out, r0 = blockIdx.x * tiles * kTileRows;
-    const int64_t row = (int64_t)a.lists->expert[blockIdx.y] * ff + std::min(r0 + tile / 2 * kTileRows + (lane & 15), ff - 1);
-    const XRows x = {a.by_pair ? a.x + start * a.ldx : a.x, a.ldx, 0, a.by_pair ? nullptr : a.lists->token + start};
-    const floatx4 acc = few_product<b, T, 1, kSplit>(a.w[tile & 1], row, x, count, wave % a.slices, a.slices,
-                                                     reinterpret_cast<uint16_t *>(smem));
-    FewSums *sums = reinterpret_cast<FewSums *>(smem);
+    const Expert &e = a.lists->expert[blockIdx.y];
+    const int token = e.token[threadIdx.x & (kMoeMaxTokens - 1)];
+    const int start = e.start, count = e.count, wave = few_wave(), lg = a.lg;
+    if (count == 0) return;
+    const int lt = 2 - lg;  // log2 of the row tiles
+    const int tile = wave >> lg;
+    const int ff = a.w[0].d_out, r0 = blockIdx.x * kTileRows << lt, rt = std::min(r0 + (tile >> 1) * kTileRows, ff - 1);
+    const XRows x = {a.by_pair ? a.x + start * a.ldx : a.x, a.ldx, 0, !a.by_pair, token};
+    const floatx4 acc = few_product<b, T, 1, kSplit>(tile & 1 ? a.w[1] : a.w[0], (int64_t)e.expert * ff + rt, std::min(kTileRows, ff - rt), x,
+                                                     count, wave & ((1 << lg) - 1), lg, reinterpret_cast<uint16_t *>(smem));
+    float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
-    for (int n = threadIdx.x; n < count * tiles * kTileRows; n += kFewThreads) {
-        const int m = n / (tiles * kTileRows), c = n % (tiles * kTileRows);
+    for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
+        const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
         if (r0 + c >= ff) continue;
-        float v[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-            for (int k = 0; k < a.slices; ++k) v[r] += sums[(c / kTileRows * 2 + r) * a.slices + k][m][c % kTileRows];
-        float h = silu_mul(v[0], v[1]);
+        const int w0 = (c >> 4) << (1 + lg);
+        float h = silu_mul(few_sum(sums, w0, lg, count, m, c & 15), few_sum(sums, w0 + (1 << lg), lg, count, m, c & 15));
         __bf16 *dst = a.h + (int64_t)(start + m) * ff + r0 + c;
         for (int p = 0; p < a.planes; ++p) {
             const __bf16 t = (__bf16)h;
@@ -263,46 +309,45 @@ struct DownArgs {
     PackedDev w;
     const uint16_t *h;  // planes of rows by pair
     int64_t h_plane;
-    int slices;
+    int lg;
     const Lists *lists;
     float *part;  // rows by pair
 };
 
 template <int b, int P, bool kSplit>
-__global__ __launch_bounds__(kFewThreads, 4) void down_kernel(DownArgs a) {
+__global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    if ((int)blockIdx.y >= a.lists->n) return;
-    const int wave = few_wave(), lane = threadIdx.x % kWave;
-    const int tiles = kFewWaves / a.slices, tile = wave / a.slices;
-    const int start = a.lists->start[blockIdx.y], count = a.lists->start[blockIdx.y + 1] - start;
-    const int d = a.w.d_out, r0 = blockIdx.x * tiles * kTileRows;
-    const int64_t row = (int64_t)a.lists->expert[blockIdx.y] * d + std::min(r0 + tile * kTileRows + (lane & 15), d - 1);
+    const Expert &e = a.lists->expert[blockIdx.y];
+    const int start = e.start, count = e.count, wave = few_wave(), lg = a.lg;
+    if (count == 0) return;
+    const int lt = 3 - lg, tile = wave >> lg;
+    const int d = a.w.d_out, r0 = blockIdx.x * kTileRows << lt, rt = std::min(r0 + tile * kTileRows, d - 1);
     const int64_t ff = a.w.units * kUnit;
-    const XRows x = {a.h + start * ff, ff, a.h_plane, nullptr};
-    const floatx4 acc = few_product<b, __bf16, P, kSplit>(a.w, row, x, count, wave % a.slices, a.slices,
-                                                          reinterpret_cast<uint16_t *>(smem));
-    FewSums *sums = reinterpret_cast<FewSums *>(smem);
+    const XRows x = {a.h + start * ff, ff, a.h_plane, false, 0};
+    const floatx4 acc = few_product<b, __bf16, P, kSplit>(a.w, (int64_t)e.expert * d + rt, std::min(kTileRows, d - rt), x, count,
+                                                          wave & ((1 << lg) - 1), lg, reinterpret_cast<uint16_t *>(smem));
+    float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
-    for (int n = threadIdx.x; n < count * tiles * kTileRows; n += kFewThreads) {
-        const int m = n / (tiles * kTileRows), c = n % (tiles * kTileRows);
-        if (r0 + c >= d) continue;
-        float v = 0.0f;
-        for (int k = 0; k < a.slices; ++k) v += sums[c / kTileRows * a.slices + k][m][c % kTileRows];
-        a.part[(int64_t)(start + m) * d + r0 + c] = v;
+    for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
+        const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
+        if (r0 + c < d) a.part[(int64_t)(start + m) * d + r0 + c] = few_sum(sums, (c >> 4) << lg, lg, count, m, c & 15);
     }
 }
 
 __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ part, const Lists *__restrict__ lists, int d,
                                                       void *y, int64_t ldy, gptq_dtype y_dt) {
-    const int c = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    const Token &t = lists->token[blockIdx.y];
     if (c >= d) return;
-    float v = 0.0f;
-    const int n = lists->of_count[t];
-    for (int j = 0; j < n; ++j) {
-        const int p = lists->of_token[t][j];
-        v = fmaf(lists->weight[p], part[(int64_t)p * d + c], v);
-    }
-    store_as(y, t * ldy + c, y_dt, v);
+    const int n = t.count;
+    float v[kMoeMaxTopK], y0 = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kMoeMaxTopK; ++j)
+        if (j < n) v[j] = part[(int64_t)t.pair[j] * d + c];
+#pragma unroll
+    for (int j = 0; j < kMoeMaxTopK; ++j)
+        if (j < n) y0 = fmaf(t.weight[j], v[j], y0);
+    store_as(y, blockIdx.y * ldy + c, y_dt, y0);
 }
 
 constexpr int kMaxPlanes = 3;
@@ -370,8 +415,8 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
         g.by_pair = 1;
     }
     const int64_t gu_tiles = ceil_div(ff, kTileRows);
-    g.slices = few_slices((int64_t)(2 * busy * gu_tiles), g.w[0].units, kFewWaves / 2);
-    const dim3 grid((unsigned)ceil_div(gu_tiles, kFewWaves / g.slices / 2), slots);
+    g.lg = few_slices((int64_t)(2 * busy * gu_tiles), g.w[0].units, kFewWaves / 2);
+    const dim3 grid((unsigned)ceil_div(gu_tiles, (kFewWaves >> g.lg) / 2), slots);
     const size_t lds = few_lds_bytes((int)c.T, 1, g.w[0].units);
     if (g.w[0].split)
         gate_up_kernel<b, T, true><<<grid, kFewThreads, lds, s>>>(g);
@@ -390,8 +435,8 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
         w.h = hg;
     }
     const int64_t tiles = ceil_div(d, kTileRows);
-    w.slices = few_slices((int64_t)(busy * tiles), w.w.units, kFewWaves);
-    const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves / w.slices), slots);
+    w.lg = few_slices((int64_t)(busy * tiles), w.w.units, kFewWaves);
+    const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves >> w.lg), slots);
     const size_t dlds = few_lds_bytes((int)c.T, g.planes, w.w.units);
     if (g.planes == 3)
         launch_down<b, 3>(w, dgrid, dlds, s);
@@ -412,7 +457,8 @@ void launch_moe(const MoeCall &c, const Layout &l, hipStream_t s) {
         else
             router_kernel<T, T><<<grid, 256, 0, s>>>(x, c.ldx, (int)c.T, static_cast<const T *>(c.router), d, c.n_experts, logits);
     }
-    choose_kernel<<<1, 1024, 0, s>>>(logits, (int)c.T, c.n_experts, c.top_k, c.renormalize, c.ids, c.weights,
+    choose_kernel<<<1, 1024, 0, s>>>(logits, (int)c.T, c.n_experts, c.top_k, c.renormalize,
+                                     (int)std::min<int64_t>(c.n_experts, c.T * c.top_k), c.ids, c.weights,
                                      reinterpret_cast<Lists *>(c.ws + l.lists));
     switch (c.gate->bits) {
     case 2: return launch_experts<2, T>(c, l, s);
