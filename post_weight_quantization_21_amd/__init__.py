@@ -490,6 +490,15 @@ def _few_ws(ws, device):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+def _gemv_ws(ws, w, M, device):
+    if ws is None:
+        # needed with a column order, and where the activations exceed what the kernels stage (gptq_gemv)
+        if w.kperm is None and M * (-(-w.d_in // 512) * 512) <= 16384:
+            return None, 0
+        ws = _workspace(workspace_bytes(OP_GEMV, w.d_out, w.d_in, M), device)
+    return _few_ws(ws, device)
+
+
 def _pitch(t, rows, cols):
     """Elements between rows (a single row has no next one: torch may report any stride for it)."""
     return t.stride(0) if rows > 1 else cols
@@ -507,10 +516,7 @@ def gemv(X, w: PackedWeight, bias=None, Y=None, out_dtype=None, ws=None, stream=
     if bias is not None and (bias.device != dev or bias.dtype != torch.float32 or tuple(bias.shape) != (d_out,)
                              or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 [{d_out}] on the weights' device")
-    if w.kperm is None:
-        wp, wn = None, 0
-    else:
-        wp, wn = _few_ws(_workspace(workspace_bytes(OP_GEMV, d_out, d_in, M), dev) if ws is None else ws, dev)
+    wp, wn = _gemv_ws(ws, w, M, dev)
     _few_launch(lib.gptq_gemv, dev, stream, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), w.ref,
                 None if bias is None else bias.data_ptr(), Y.data_ptr(), yd, _pitch(Y, M, d_out), wp, wn)
     return Y
@@ -527,10 +533,7 @@ def gemv_gated(X, gate: PackedWeight, up: PackedWeight, H=None, out_dtype=None, 
         raise ValueError("gate and up must be on one device")
     xd = _few_check_x(X, d_in, dev, act)
     H, hd = _few_result(X, H, M, d_ff, out_dtype, dev, torch, res)
-    if gate.kperm is None:
-        wp, wn = None, 0
-    else:
-        wp, wn = _few_ws(_workspace(workspace_bytes(OP_GEMV, d_ff, d_in, M), dev) if ws is None else ws, dev)
+    wp, wn = _gemv_ws(ws, gate, M, dev)
     _few_launch(lib.gptq_gemv_gated, dev, stream, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), gate.ref, up.ref,
                 H.data_ptr(), hd, _pitch(H, M, d_ff), wp, wn)
     return H

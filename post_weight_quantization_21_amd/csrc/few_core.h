@@ -1,25 +1,31 @@
 // Products of at most sixteen rows of activations with packed b-bit weights
-// (b = 2, 3, 4, 8): the part one wave computes, shared by the matrix-vector
-// products (gemv.hip) and the experts' products (moe.hip).
+// (b = 2, 3, 4, 8), shared by the matrix-vector products (gemv.hip) and the
+// experts' products (moe.hip).
 //
 //   acc[m][o] = sum_k x[m][k] (q[o][k] - z[o][k/g]) s[o][k/g]
 //
 // A row's codes are a little-endian bit stream; 32 codes (a "unit") are b whole
-// words.  A wave owns 16 weight rows per tile and walks K in steps of 128
-// columns: lane l = 16 kb + r reads unit 4 step + kb of row r and turns it into
-// four fragments of eight 16-bit floats; v_mfma_f32_16x16x32 multiplies a
-// fragment (lane: column r of B, eight K values) with the same columns of x
-// (lane: row m = l % 16 of A).  Which K a slot holds does not matter as long as
-// x and the weights agree, so a fragment takes the codes in whatever order they
-// unpack cheapest, and x follows.
+// words.  A wave owns a tile of 16 weight rows and walks K in steps of 128
+// columns, four steps a quad: lane l = 16 kb + r reads unit 4 step + kb of row r
+// and turns it into four fragments of eight 16-bit floats; v_mfma_f32_16x16x32
+// multiplies a fragment (lane: column r of B, eight K values) with the same
+// columns of x (lane: row m = l % 16 of A).  Which K a slot holds does not
+// matter as long as x and the weights agree, so a fragment takes the codes in
+// whatever order they unpack cheapest, and x follows ("prepared" x, below).
 //
 // The result has its weight row in the lane's column (D[4 kb + i][r], i = 0..3,
-// m = 4 kb + i), so scale and zero are one value per lane.  The matrix cores
-// are not what bounds these products: at full HBM rate they are busy a quarter
-// of the time for one token as for sixteen, so M <= 16 runs on them throughout.
+// m = 4 kb + i), so scale and zero are one value per lane.
+//
+// What bounds it: the instructions that unpack (measured at 28672 x 8192, one
+// token: 67 vector instructions per step of 16 x 128 codes kept a compute unit
+// at 8 bytes a clock; 36-40 of them are the unpacking itself).  Hence scales and
+// zero constants come ready from LDS, weights through buffer loads with scalar
+// offsets, and two quads of registers take turns without copies.  The matrix
+// cores are a quarter busy, for one token as for sixteen, so all M run on them.
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.h"
 
@@ -28,12 +34,33 @@ namespace gptq {
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x3 __attribute__((ext_vector_type(3)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kFewRows = 16;    // rows of activations
-constexpr int kTileRows = 16;   // weight rows of a tile
-constexpr int kUnit = 32;       // codes of a unit: b words
-constexpr int kStep = 128;      // columns of a step: one unit per lane row
-constexpr int64_t kFewMaxIn = (int64_t)1 << 20;  // columns a packed matrix may have (32-bit offsets within a row)
+constexpr int kFewRows = 16;   // rows of activations
+constexpr int kTileRows = 16;  // weight rows of a tile
+constexpr int kUnit = 32;      // codes of a unit: b words
+constexpr int kStep = 128;     // columns of a step: one unit per lane row
+constexpr int kQuad = 512;     // columns of a quad of steps: what a wave takes at least
+
+// How a workgroup of kFewWaves waves shares a product: 2^lg waves (slices) split
+// K between them on each of kFewWaves >> lg row tiles.
+constexpr int kFewWaves = 8;
+constexpr int kFewThreads = kFewWaves * kWave;
+constexpr int kFewOccupancy = 4;                       // waves per SIMD, which the kernels' registers allow
+constexpr int kFewResident = 256 * 4 * kFewOccupancy;  // waves of the chip at once
+
+// LDS of a workgroup, two of which share a compute unit's 160 KB: the waves'
+// sums, the scales and zero constants of its rows, and x where it fits.
+constexpr int kStagedValues = 16384;  // of x
+constexpr int kEntries = 4096;        // of (scale, zero constant), 8 bytes
+constexpr int kSumsBytes = kFewWaves * kFewRows * kTileRows * 4;
+
+__host__ __device__ inline int few_steps(int units) { return (units + 3) / 4; }
+__host__ __device__ inline int few_quads(int units) { return (units + 15) / 16; }
+__host__ __device__ inline bool few_staged(int rows, int units) { return rows * few_quads(units) * kQuad <= kStagedValues; }
+__host__ __device__ inline int ceil_log2(int n) { return n <= 1 ? 0 : 32 - __builtin_clz((unsigned)(n - 1)); }
 
 // Exact quotients n / d of small numbers: n, d < 2^15 (units and steps of a row).
 struct SmallDiv {
@@ -42,19 +69,28 @@ struct SmallDiv {
 };
 inline SmallDiv small_div(uint32_t d) { return {d <= 1 ? 0u : (uint32_t)((uint64_t(1) << 32) / d + 1)}; }
 
-// One stack of packed matrices as the kernels see it.
-struct PackedDev {
+// Stacks of packed matrices as the kernels see them: the pointers, and the shape
+// that gate and up share.
+struct FewMat {
     const uint32_t *packed;
     const float *scales, *zeros;
+};
+struct FewShape {
     int32_t d_out, words, groups;  // rows, words per row, groups per row
     int32_t units;                 // units per row (d_in / 32)
-    int32_t split;                 // a group ends inside a step: fold per unit
-    SmallDiv by;                   // steps (split: units) per group
+    int32_t lg;                    // log2 of the slices
+    int32_t phase;                 // quads whose scales fit in LDS
+    SmallDiv by;                   // steps per group, or units per group where groups end inside a step
+    SmallDiv row_pieces;           // prepared 16-byte pieces per row of x
 };
-
-PackedDev packed_dev(const gptq_packed &w);  // gemv.hip
-
-typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+FewMat few_mat(const gptq_packed &w);  // gemv.hip
+// tiles: row tiles that share the chip; most: slices at most.
+FewShape few_shape(const gptq_packed &w, int64_t tiles, int most);
+// Groups end inside a step: the fragments are transposed so that a matrix
+// instruction covers one unit, and the fold with the scale runs per unit.
+bool few_split(const gptq_packed &w);
+// LDS bytes for up to `rows` staged rows of x.
+size_t few_lds_bytes(int rows, int units);
 
 __device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {  // a's upper half with b's lower half
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -73,18 +109,6 @@ __device__ __forceinline__ void transpose4(uint32_t &a, uint32_t &b, uint32_t &c
     swap16(a, b);
     swap16(c, d);
 }
-// out[j] = v of lane row j, in every lane row.
-__device__ __forceinline__ void spread4(float v, float out[4]) {
-    uint32_t a = __float_as_uint(v), b = a;
-    swap32(a, b);
-    uint32_t c = a, d = b;
-    swap16(a, c);
-    swap16(b, d);
-    out[0] = __uint_as_float(a);
-    out[1] = __uint_as_float(c);
-    out[2] = __uint_as_float(b);
-    out[3] = __uint_as_float(d);
-}
 
 template <typename T>
 struct Vec8;
@@ -99,7 +123,21 @@ struct Vec8<__bf16> {
     __device__ static floatx4 mma(V a, V b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
 };
 
-// Bits [at, at + b) of a unit, at a compile-time position.
+// Column of its unit that slot j of fragment f holds, and the way back.
+template <int b>
+__host__ __device__ constexpr int slot_col(int f, int j) {
+    if (b == 4) return 8 * f + (j >> 1) + 4 * (j & 1);
+    if (b == 2) return 16 * (f >> 1) + 4 * (f & 1) + (j >> 1) + 8 * (j & 1);
+    return 8 * f + j;
+}
+template <int b>
+__host__ __device__ constexpr int col_slot(int c) {  // 8 f + j
+    if (b == 4) return (c & ~7) + 2 * (c & 3) + (c >> 2 & 1);
+    if (b == 2) return (c & 16) + 8 * (c >> 2 & 1) + 2 * (c & 3) + (c >> 3 & 1);
+    return c;
+}
+
+// Bits [b c, b c + b) of a unit, at a compile-time position.
 template <int b>
 __device__ __forceinline__ uint32_t code_at(const uint32_t *w, int c) {
     const int at = b * c, i = at >> 5, sh = at & 31;
@@ -107,97 +145,82 @@ __device__ __forceinline__ uint32_t code_at(const uint32_t *w, int c) {
     return sh + b == 32 ? v : v & ((1u << b) - 1u);
 }
 
-// Fragment i of a unit (eight codes) as 16-bit floats of which column j comes
-// from code col(i, j).  fp16 gives q - z, exactly: masking a code into mantissa
-// bits [s, s + b) of an fp16 with exponent 10 makes 1024 + q 2^s, and a packed
-// multiply-add with 2^-s takes the rest away without rounding.  bf16 has no
-// packed arithmetic, so it gives 2^b + q (the code shifted to the top of the
-// mantissa) and the caller takes (2^b + z) sum x away with one more matrix
-// instruction per fragment, whose B operand is the constant -(2^b + z); only
-// the fp32 sums round.  Eight-bit codes fill bf16's significand, so they go
-// through fp32: q - z is an integer of at most 255 and exact in bf16.
+// Fragment f of a unit (eight codes) as 16-bit floats.  fp16 gives q - z,
+// exactly: masking a code into mantissa bits [s, s + b) of an fp16 with exponent
+// 10 makes 1024 + q 2^s, and a packed multiply-add with 2^-s takes the rest away
+// without rounding.  bf16 has no packed arithmetic, so it gives 2^b + q (the code
+// shifted to the top of the mantissa) and the caller takes (2^b + z) sum x away
+// with one more matrix instruction per fragment, whose B operand is the constant
+// -(2^b + z); only the fp32 sums round.  Eight-bit codes fill bf16's significand,
+// so they go through fp32: q - z is an integer of at most 255 and exact in bf16.
 template <int b, typename T>
 struct Codes {
     typedef typename Vec8<T>::V V;
-    static constexpr bool kHalf = sizeof(T) == 2 && !__is_same(T, __bf16);
-    static constexpr bool kOffset = !kHalf && b < 8;  // fragments hold 2^b + q
+    static constexpr bool kF16 = __is_same(T, _Float16);
+    static constexpr bool kOffset = !kF16 && b < 8;  // fragments hold 2^b + q
     uint32_t magic;
-    uint32_t zb;       // offset form: the pair -(2^b + z) in bf16
-    f16x2 z16[5];      // fp16: the pair 2^(10 - s) + z for s = 0, 2, 4, 6, 8
-    float z;
+    uint32_t zc;  // constant(z)
+    f16x2 z2;     // fp16, two bits: 256 + z, 16 + z
 
     __device__ __forceinline__ Codes() {
-        magic = kHalf ? 0x64006400u : (uint32_t)(0x3F80 + 128 * b) * 0x10001u;  // fp16 1024, bf16 2^b
+        magic = kF16 ? 0x64006400u : (uint32_t)(0x3F80 + 128 * b) * 0x10001u;  // fp16 1024, bf16 2^b
         asm volatile("" : "+v"(magic));  // a register operand: VOP3 takes no literal
     }
-    __device__ __forceinline__ void set_zero(float zero) {
-        z = zero;
-        if constexpr (kOffset) {
-            zb = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)(-((float)(1 << b) + zero)), (__bf16)(-((float)(1 << b) + zero))});
-        }
-        if constexpr (kHalf) {
-#pragma unroll
-            for (int i = 0; i < 5; ++i) {
-                const _Float16 v = (_Float16)((float)(1024 >> (2 * i)) + zero);
-                z16[i] = (f16x2){v, v};
-            }
-        }
+    // What the unpacking needs of a zero point: fp16 the pair 1024 + z, 64 + z;
+    // bf16 twice -(2^b + z); bf16 of eight bits z in fp32.
+    __device__ __forceinline__ static uint32_t constant(float z) {
+        if constexpr (kF16) return __builtin_bit_cast(uint32_t, (f16x2){(_Float16)(1024.0f + z), (_Float16)(64.0f + z)});
+        if constexpr (!kOffset) return __float_as_uint(z);
+        const __bf16 v = (__bf16)(-((float)(1 << b) + z));
+        return __builtin_bit_cast(uint32_t, (bf16x2){v, v});
+    }
+    __device__ __forceinline__ void set(uint32_t c) {
+        zc = c;
+        if constexpr (kF16 && b == 2) z2 = __builtin_bit_cast(f16x2, c) - (f16x2){(_Float16)768.0f, (_Float16)48.0f};
     }
     __device__ __forceinline__ V zero_frag() const {
-        u32x4 v = {zb, zb, zb, zb};
+        const u32x4 v = {zc, zc, zc, zc};
         return __builtin_bit_cast(V, v);
     }
-    // Column of the unit that slot j of fragment i holds.
-    __host__ __device__ static constexpr int col(int i, int j) {
-        if (b == 4) return 8 * i + (j >> 1) + 4 * (j & 1);
-        if (b == 2) return 16 * (i >> 1) + 4 * (i & 1) + (j >> 1) + 8 * (j & 1);
-        return 8 * i + j;
+    // 2^(10 - s) + z, twice
+    __device__ __forceinline__ f16x2 bias(int s) const {
+        const f16x2 z = __builtin_bit_cast(f16x2, zc);
+        const _Float16 v = s == 0 ? z[0] : (s == 4 ? z[1] : (s == 2 ? z2[0] : z2[1]));
+        return (f16x2){v, v};
     }
-    // Pair p (slots 2p and 2p + 1) of fragment i.
-    __device__ __forceinline__ uint32_t pair(const uint32_t *w, int i, int p) const {
+    // Pair p (slots 2p and 2p + 1) of fragment f.
+    __device__ __forceinline__ uint32_t pair(const uint32_t *w, int f, int p) const {
         constexpr uint32_t m = ((1u << b) - 1u) * 0x10001u;
         if constexpr (b == 8) {
-            const uint32_t v = w[2 * i + (p >> 1)];
-            if constexpr (kHalf) {
+            const uint32_t v = w[2 * f + (p >> 1)];
+            if constexpr (kF16) {
                 const uint32_t h = __builtin_amdgcn_perm(magic, v, p & 1 ? 0x07030702u : 0x07010700u);
-                return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, h) - z16[0]);
+                return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, h) - bias(0));
             } else {
+                const float z = __uint_as_float(zc);
                 const float lo = (float)((v >> (16 * (p & 1))) & 255u) - z, hi = (float)((v >> (16 * (p & 1) + 8)) & 255u) - z;
                 return __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)lo, (__bf16)hi});
             }
         } else if constexpr (b == 3) {
-            const uint32_t v = code_at<3>(w, 8 * i + 2 * p) | (code_at<3>(w, 8 * i + 2 * p + 1) << 16);
-            if constexpr (kHalf) return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v | magic) - z16[0]);
+            const uint32_t v = code_at<3>(w, 8 * f + 2 * p) | (code_at<3>(w, 8 * f + 2 * p + 1) << 16);
+            if constexpr (kF16) return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, v | magic) - bias(0));
             return (v << 4) | magic;
         } else {  // codes b c and b c + 16 of a word
-            const uint32_t v = b == 4 ? w[i] : w[i >> 1];
-            const int at = b == 4 ? 4 * p : 2 * (4 * (i & 1) + p);
-            if constexpr (kHalf) {
+            const uint32_t v = b == 4 ? w[f] : w[f >> 1];
+            const int at = b == 4 ? 4 * p : 2 * (4 * (f & 1) + p);
+            if constexpr (kF16) {
                 const int base = at >= 8 ? 8 : 0, s = at - base;  // masked in place at shifts of 0 .. 6
                 const f16x2 h = __builtin_bit_cast(f16x2, ((base ? v >> base : v) & (m << s)) | magic);
-                if (s == 0) return __builtin_bit_cast(uint32_t, h - z16[0]);
-                const _Float16 f = (_Float16)(1.0f / (float)(1 << s));
-                return __builtin_bit_cast(uint32_t, h * (f16x2){f, f} - z16[s / 2]);
+                if (s == 0) return __builtin_bit_cast(uint32_t, h - bias(0));
+                const _Float16 r = (_Float16)(1.0f / (float)(1 << s));
+                return __builtin_bit_cast(uint32_t, h * (f16x2){r, r} - bias(s));
             }
             constexpr int top = 7 - b;  // the code's place in the mantissa
             return ((at > top ? v >> (at - top) : v << (top - at)) & (m << top)) | magic;
         }
     }
-    __device__ __forceinline__ V frag(const uint32_t *w, int i) const {
-        u32x4 v = {pair(w, i, 0), pair(w, i, 1), pair(w, i, 2), pair(w, i, 3)};
-        return __builtin_bit_cast(V, v);
-    }
-    // Fragment i of x from the unit's 32 columns in their own order (16 words).
-    __device__ __forceinline__ static V xfrag(const uint32_t *x, int i) {
-        u32x4 v;
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const int c0 = col(i, 2 * p), c1 = col(i, 2 * p + 1);
-            if (c1 == c0 + 1)
-                v[p] = x[c0 / 2];
-            else
-                v[p] = __builtin_amdgcn_perm(x[c1 / 2], x[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
-        }
+    __device__ __forceinline__ V frag(const uint32_t *w, int f) const {
+        const u32x4 v = {pair(w, f, 0), pair(w, f, 1), pair(w, f, 2), pair(w, f, 3)};
         return __builtin_bit_cast(V, v);
     }
 };
@@ -221,228 +244,297 @@ __device__ __forceinline__ void transpose_frags(V f[4]) {
     }
 }
 
+// A unit's words through a buffer descriptor: an offset past the descriptor's
+// size reads nothing and gives zeros.
 template <int b>
-__device__ __forceinline__ void load_unit(const uint32_t *p, uint32_t *w) {
+__device__ __forceinline__ void load_unit(__amdgpu_buffer_rsrc_t p, uint32_t at, uint32_t base, uint32_t *w) {
     if constexpr (b == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x, w[1] = v.y;
+        const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(p, at, base, 0);
+        w[0] = v[0], w[1] = v[1];
     } else if constexpr (b == 3) {
-        const uint3 v = *reinterpret_cast<const uint3 *>(p);  // 4-byte aligned: a row of 32 n codes is 12 n bytes
-        w[0] = v.x, w[1] = v.y, w[2] = v.z;
+        const u32x3 v = __builtin_amdgcn_raw_buffer_load_b96(p, at, base, 0);
+        w[0] = v[0], w[1] = v[1], w[2] = v[2];
     } else {
 #pragma unroll
         for (int i = 0; i < b / 4; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + 4 * i);
-            w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(p, at + 16 * i, base, 0);
+            w[4 * i] = v[0], w[4 * i + 1] = v[1], w[4 * i + 2] = v[2], w[4 * i + 3] = v[3];
         }
     }
 }
 
-// How a workgroup of kFewWaves waves shares a product: 2^lg waves (slices) split
-// K between them on each of kFewWaves >> lg row tiles.
-constexpr int kFewWaves = 8;
-constexpr int kFewThreads = kFewWaves * kWave;
-constexpr int kFewOccupancy = 4;             // waves per SIMD, which the kernels' registers allow
-constexpr int kFewResident = 256 * 4 * kFewOccupancy;  // waves of the chip at once
-// x is staged in LDS in chunks, a unit of a row per thread, two buffers.
-constexpr int kXPad = 8;  // values after each staged row: sixteen rows start in different banks
+// Prepared x: M rows of whole quads as pieces of eight 16-bit values in slot
+// order, piece (4 (4 step + u) + f) M + m holding fragment f of unit u of row m;
+// columns past the last unit are zero.  A lane's operand of a matrix instruction
+// is one piece, the rows of a lane row next to each other.  Planes (terms of x)
+// follow each other.
+__host__ __device__ inline int64_t prepared_values(int64_t rows, int units) { return rows * few_quads(units) * kQuad; }
+template <int b>
+__device__ __forceinline__ int64_t prepared_at(int col, int M, int m) {
+    const int s = col_slot<b>(col % kUnit);
+    return ((int64_t)(col / kUnit * 4 + (s >> 3)) * M + m) * 8 + (s & 7);
+}
 
-// Rows of activations: row m of plane p is base + p * plane + row(m) * ld.
+// Where a product finds x.
+enum FewX {
+    kRaw = 0,     // rows in their own order: prepared into LDS
+    kCopied = 1,  // prepared in memory: copied into LDS
+    kDirect = 2   // prepared in memory, too much for LDS: read from there, that is from L2, by every wave
+};
 struct XRows {
     const uint16_t *base;
-    int64_t ld, plane;
-    bool gathered;  // rows are numbered by `row` of lane m, else m itself
+    int64_t ld;     // raw: between rows; prepared: between planes
+    bool gathered;  // raw: rows are numbered by `row` of lane m, else m itself
     int32_t row;
 };
 
-__host__ __device__ inline int ceil_log2(int n) { return n <= 1 ? 0 : 32 - __builtin_clz((unsigned)(n - 1)); }
-// Steps of K that a chunk of `rows` staged rows (P M) holds, at most all of them.
-__host__ __device__ inline int chunk_steps(int rows, int steps) {
-    const int c = (kFewThreads / 4) >> ceil_log2(rows);
-    return c < steps ? c : steps;
-}
-__host__ __device__ inline int staged_ld(int chunk) { return chunk * kStep + kXPad; }
-// LDS bytes of a product of 1 .. max_rows rows of `planes` planes: the staged
-// activations, or the waves' sums after it.
-inline size_t few_lds_bytes(int max_rows, int planes, int units) {
-    const int steps = (units + 3) / 4;
-    size_t bytes = (size_t)kFewWaves * max_rows * kTileRows * 4;
-    for (int m = 1; m <= max_rows; ++m) {
-        const int chunk = chunk_steps(planes * m, steps);
-        const size_t one = (size_t)planes * m * staged_ld(chunk) * 2;
-        bytes = std::max(bytes, chunk < steps ? 2 * one : one);
-    }
-    return bytes;
-}
-
-// Columns [128 c0, 128 (c0 + n)) of the M rows (P planes of them) staged for the
-// matrix cores: row-major, each unit's four fragments in slot order, zeros past
-// the last unit (a step may hold fewer than four).
-template <int b, typename T, int P>
+// The workgroup's x on its way into LDS.
+template <int b, int P, FewX kX>
 struct StageX {
-    typedef typename Vec8<T>::V V;
-    int r, u;             // the thread's staged row (r >= P M: none) and its unit in the chunk
-    const uint16_t *src;  // the row's columns
-    uint4 v[4];
-    __device__ __forceinline__ void init(const XRows &x, int M) {
-        const int lg = 9 - ceil_log2(P * M);  // log2 of the threads per row
-        static_assert(kFewThreads == 512, "threads per row");
-        r = threadIdx.x >> lg;
-        u = threadIdx.x & ((1 << lg) - 1);
-        const int p = P == 1 ? 0 : (r >= M) + (P > 2 && r >= 2 * M), m = r - p * M;
-        const int row = x.gathered ? __shfl(x.row, m) : m;
-        src = x.base + (r < P * M ? p * x.plane + row * x.ld : 0);
-    }
-    __device__ __forceinline__ void load(int M, int c0, int n, int units) {
+    static constexpr int kPieces = kStagedValues / 8 / kFewThreads;
+    u32x4 v[kPieces];
+    int at;  // raw: the thread's unit, as first piece and row
+    __device__ __forceinline__ void load(const XRows &x, const FewShape &w, int M) {
+        if constexpr (kX == kRaw) {  // a thread takes a unit
+            static_assert(kStagedValues / kUnit <= kFewThreads, "a unit per thread");
+            const int per_row = 16 * few_quads(w.units);
+            const int r = w.row_pieces.div(4 * threadIdx.x), u = threadIdx.x - r * per_row;
+            const int row = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
+            at = r < M ? 4 * u * M + r : -1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = make_uint4(0, 0, 0, 0);
-        if (r < P * M && u < 4 * n && 4 * c0 + u < units) {
+            for (int i = 0; i < 4; ++i) v[i] = (u32x4){0, 0, 0, 0};
+            if (r < M && u < w.units) {
+                const u32x4 *src = reinterpret_cast<const u32x4 *>(x.base + row * x.ld + u * kUnit);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = reinterpret_cast<const uint4 *>(src + (4 * c0 + u) * kUnit)[i];
+                for (int i = 0; i < 4; ++i) v[i] = src[i];
+            }
+        }
+        if constexpr (kX == kCopied) {
+            const int pieces = (int)(prepared_values(M, w.units) / 8);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int i = threadIdx.x + k * kFewThreads, p = (i >= pieces) + (P > 2 && i >= 2 * pieces);
+                if (i < P * pieces) v[k] = *reinterpret_cast<const u32x4 *>(x.base + p * x.ld + (int64_t)(i - p * pieces) * 8);
+            }
         }
     }
-    __device__ __forceinline__ void store(uint16_t *xs, int M, int n, int ld) const {
-        if (r >= P * M || u >= 4 * n) return;
-        uint32_t w[16];
+    __device__ __forceinline__ void store(uint16_t *xs, const FewShape &w, int M) const {
+        u32x4 *dst = reinterpret_cast<u32x4 *>(xs);
+        if constexpr (kX == kRaw) {
+            if (at < 0) return;
+            uint32_t t[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * i] = v[i].x, w[4 * i + 1] = v[i].y, w[4 * i + 2] = v[i].z, w[4 * i + 3] = v[i].w;
+            for (int i = 0; i < 16; ++i) t[i] = v[i / 4][i % 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<V *>(xs + r * ld + u * kUnit + 8 * i) = Codes<b, T>::xfrag(w, i);
+            for (int f = 0; f < 4; ++f) {
+                u32x4 o;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    constexpr int apart = b == 4 ? 4 : 8;
+                    const int c0 = slot_col<b>(f, 2 * p), c1 = slot_col<b>(f, 2 * p + 1);
+                    o[p] = c1 == c0 + 1 ? t[c0 / 2]
+                                        : __builtin_amdgcn_perm(t[(c0 + apart) / 2], t[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
+                }
+                dst[at + f * M] = o;
+            }
+        }
+        if constexpr (kX == kCopied) {
+            const int pieces = P * (int)(prepared_values(M, w.units) / 8);
+#pragma unroll
+            for (int k = 0; k < kPieces; ++k) {
+                const int i = threadIdx.x + k * kFewThreads;
+                if (i < pieces) dst[i] = v[k];
+            }
+        }
     }
 };
 
-// The wave's sums for a tile of 16 weight rows over its slice of K, from x
-// staged chunk by chunk; every wave of the workgroup calls it, with the same x.
-// row0: the tile's first row in the stack w, rows: its rows there.  kSplit:
-// groups end inside a step, so the fragments of the four lane rows are
-// transposed to make each matrix instruction cover one unit, and the fold with
-// the scale runs per unit; otherwise it runs per step.
-//
-// The weights stream through registers: a body of S steps is loaded while the
-// one before it is computed, so a wave keeps S to 2S KB (4 bits) in flight.
-// Scales and zeros come with it: without kSplit lane row kb reads those of step
-// kb of the body and the rows trade them (spread4), one load for four steps.
-template <int b, typename T, int P, bool kSplit>
-__device__ __forceinline__ floatx4 few_product(const PackedDev &w, int64_t row0, int rows, const XRows &x, int M,
-                                               int slice, int lg, uint16_t *lds) {
-    typedef typename Vec8<T>::V V;
-    typedef Codes<b, T> C;
-    constexpr int S = b == 8 || (kSplit && P > 1) ? 2 : 4;
-    constexpr int NS = kSplit ? S : 1;
-    const int lane = threadIdx.x % kWave, kb = lane >> 4;
-    const int units = w.units, steps = (units + 3) / 4;
-    const int chunk = chunk_steps(P * M, steps), ld = staged_ld(chunk);
-    const int rl = std::min(lane & 15, rows - 1);
-    const uint32_t *wp = w.packed + row0 * w.words + (int64_t)rl * w.words;
-    const float *sp = w.scales + row0 * w.groups + rl * w.groups, *zp = w.zeros + row0 * w.groups + rl * w.groups;
-    const SmallDiv by = w.by;
-    struct Body {
-        uint32_t w[S][b];
-        float s[NS], z[NS];
-    } nxt, cur;
-    auto load = [&](Body &d, int step) {
+// Scales and zero constants of groups [ga, ga + n) of the workgroup's rows into
+// LDS, entry row * ld + group, ld odd so that sixteen rows lie in different
+// banks.  Row i of the workgroup: row i % 16 of tile i / 16; tile t is that of
+// wave t << lg.  (Read where they are used, a few bytes a row at a time, the
+// requests at L2 cost 7 of 33 us at 28672 x 8192 with groups of 128, and half
+// the time with groups of 64.)
+template <int b, typename T, int kMats>
+struct StageGroups {
+    static constexpr int kBatch = 8;  // loads of a thread before its first store
+    const FewMat *mats;
+    int64_t row0;
+    int rows, groups;            // from row0 to the matrix's end; groups per row
+    int count, ga, n, ld;        // rows of the workgroup; the phase's groups
+    int lgn, chunks, total;
+    float s[kBatch], z[kBatch];
+
+    __device__ __forceinline__ void init(int first, int last) {
+        ga = first;
+        n = last - first + 1;
+        ld = n | 1;
+        lgn = std::min(ceil_log2(n), 6);  // a load covers 64 >> lgn rows
+        chunks = (n + kWave - 1) / kWave;
+        total = ((count << lgn) + kFewThreads - 1) / kFewThreads * chunks;
+    }
+    __device__ __forceinline__ bool place(int t, int &r, int &g) const {
+        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+        const int q = chunks == 1 ? t : t / chunks;
+        r = ((q * kFewWaves + wave) << (6 - lgn)) + (lane >> lgn);
+        g = (t - q * chunks) * kWave + (lane & ((1 << lgn) - 1));
+        return t < total && r < count && g < n;
+    }
+    __device__ __forceinline__ void load(int t0) {
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-            const int u = std::min(4 * (step + j) + kb, units - 1);  // past the end: loaded again, not used
-            load_unit<b>(wp + u * b, d.w[j]);
-            if constexpr (kSplit) {
-                const uint32_t gi = by.div(u);
-                d.s[j] = sp[gi], d.z[j] = zp[gi];
+        for (int k = 0; k < kBatch; ++k) {
+            int r, g;
+            if (place(t0 + k, r, g)) {
+                const int t = r / kTileRows;
+                const FewMat &a = mats[kMats > 1 ? t % kMats : 0];
+                const int64_t at = (row0 + std::min(t / kMats * kTileRows + r % kTileRows, rows - 1)) * groups + ga + g;
+                s[k] = a.scales[at];
+                z[k] = a.zeros[at];
             }
         }
-        if constexpr (!kSplit) {
-            const uint32_t gi = by.div(std::min(step + (kb & (S - 1)), steps - 1));
-            d.s[0] = sp[gi], d.z[0] = zp[gi];
+    }
+    __device__ __forceinline__ void store(uint2 *entries, int t0) const {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            int r, g;
+            if (place(t0 + k, r, g)) entries[r * ld + g] = make_uint2(__float_as_uint(s[k]), Codes<b, T>::constant(z[k]));
+        }
+    }
+};
+
+// The workgroup's product: the calling wave's sums for its tile and slice.
+// mats[t % kMats]: the matrix of the workgroup's tile t, whose rows are those of
+// row tile t / kMats; row0: the first row of row tile 0 in the stack, rows: from
+// there to the matrix's end (at least 1).  Every wave of the workgroup calls it.
+//
+// Weights stream through two sets of registers, one computed while the other is
+// loaded (4 to 8 KB of a wave in flight at 4 bits).  Past the wave's slice they
+// are not read and count as zero codes with the scale of an existing group; x is
+// zero past the last unit, so such a step is left out only to save time.
+template <int b, typename T, int P, int kMats, bool kSplit, FewX kX>
+__device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShape &w, int64_t row0, int rows, const XRows &x,
+                                               int M, int wave, unsigned char *smem) {
+    typedef typename Vec8<T>::V V;
+    typedef Codes<b, T> C;
+    const int lane = threadIdx.x % kWave, kb = lane >> 4, lg = w.lg;
+    const int units = w.units, quads = few_quads(units);
+    const int tile = wave >> lg, slice = wave & ((1 << lg) - 1), tiles = kFewWaves >> lg;
+    const int m = std::min(lane & 15, M - 1);
+    uint2 *entries = reinterpret_cast<uint2 *>(smem + kSumsBytes);
+    uint16_t *xs = reinterpret_cast<uint16_t *>(entries + kEntries);
+    const FewMat &mat = mats[kMats > 1 ? tile % kMats : 0];
+    const int t0 = std::min(tile / kMats * kTileRows, rows - 1), tr = std::min(kTileRows, rows - t0), rl = std::min(lane & 15, tr - 1);
+    const uint32_t bytes = 4u * tr * w.words, wo = 4u * (rl * w.words + kb * b);
+    const auto wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t *>(mat.packed + (row0 + t0) * w.words), 0, bytes, 0x00020000);
+    // bytes of prepared x: the lane's first piece, between its pieces of a step, between planes
+    const char *xb = reinterpret_cast<const char *>(kX == kDirect ? x.base : xs);
+    const uint32_t xlane = 16u * ((kSplit ? kb : 4 * kb) * M + m), xnext = (kSplit ? 64u : 16u) * M;
+    const uint32_t xplane = 2u * (uint32_t)(kX == kDirect ? x.ld : prepared_values(M, units));
+
+    constexpr int kS = b == 8 ? 2 : 4;  // steps of a set of registers
+    uint32_t wa[kS][b], wb[kS][b];
+    auto load = [&](uint32_t (*dst)[b], int set, int end) {
+#pragma unroll
+        for (int j = 0; j < kS; ++j) {
+            const int u = 4 * (kS * set + j) + kb;
+            load_unit<b>(wr, set < end && u < units ? wo : bytes, 16u * b * (kS * set + j), dst[j]);
         }
     };
     floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    StageX<b, T, P> stage;
-    stage.init(x, M);
-    stage.load(M, 0, chunk, units);
-    int s = slice * chunk >> lg, end = (slice + 1) * chunk >> lg;  // of the first chunk
-    load(nxt, s);
-    stage.store(lds, M, chunk, ld);
-    __syncthreads();
-    uint16_t *buf = lds, *other = lds + P * M * ld;
     C codes;
-    const int m = std::min(lane & 15, M - 1);
-    for (int c0 = 0; c0 < steps; c0 += chunk) {
-        const int c1 = c0 + chunk, n1 = std::min(chunk, steps - c1);  // the next chunk, if n1 > 0
-        if (n1 > 0) stage.load(M, c1, n1, units);
-        const int next = c1 + (slice * n1 >> lg);
-        const uint16_t *xl = buf + m * ld + kb * (kSplit ? 8 : kUnit);
-        if (s >= end) load(nxt, next);  // fewer steps than slices: nothing here for this wave
-        for (; s < end; s += S) {
-            cur = nxt;
-            load(nxt, s + S < end ? s + S : next);
-            float sc[4], zc[4];
-            if constexpr (!kSplit) {
-                spread4(cur.s[0], sc);
-                spread4(cur.z[0], zc);
-            }
+    StageX<b, P, kX> stage;
+    stage.load(x, w, M);
+    StageGroups<b, T, kMats> groups;
+    groups.mats = mats;
+    groups.row0 = row0;
+    groups.rows = rows;
+    groups.groups = w.groups;
+    groups.count = tiles * kTileRows;
+    auto phase = [&](int q0, auto first) {
+        const int nq = std::min(w.phase, quads - q0);
+        const int qs = q0 + (slice * nq >> lg), qe = q0 + ((slice + 1) * nq >> lg);
+        // the phase's groups: of its first and last column
+        const int ga = w.by.div(kSplit ? 16 * q0 : 4 * q0);
+        const int gb = w.by.div(kSplit ? std::min(16 * (q0 + nq), units) - 1 : std::min(4 * (q0 + nq), few_steps(units)) - 1);
+        if constexpr (!first) __syncthreads();  // the phase before is done with its entries
+        // loads return in order: what the barrier waits for goes before the weights
+        groups.init(ga, gb);
+        groups.load(0);
+        const int hs = qs * 4 / kS, he = qe * 4 / kS;
+        load(wa, hs, he);
+        load(wb, hs + 1, he);
+        if constexpr (first) stage.store(xs, w, M);
+        groups.store(entries, 0);
+        for (int t = groups.kBatch; t < groups.total; t += groups.kBatch) {
+            groups.load(t);
+            groups.store(entries, t);
+        }
+        __syncthreads();
+        const uint2 *el = entries + (tile * kTileRows + (lane & 15)) * groups.ld - ga;
+        auto set = [&](uint32_t (*wq)[b], int h) {
 #pragma unroll
-            for (int j = 0; j < S; ++j) {
-                if (s + j >= end) break;
-                V xf[P][4];
+            for (int j = 0; j < kS; ++j) {
+                const int step = kS * h + j;
+                if (4 * step >= units) break;  // the last quad's steps past the end
+                V xf[P][4], wf[4];
+                uint32_t at = xlane + 256u * M * step;
+                asm volatile("" : "+v"(at));  // one address a step: an induction variable each would fill the registers
 #pragma unroll
                 for (int p = 0; p < P; ++p)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        xf[p][i] = *reinterpret_cast<const V *>(xl + p * M * ld + (s + j - c0) * kStep + i * (kSplit ? kUnit : 8));
-                V wf[4];
+                    for (int i = 0; i < 4; ++i) xf[p][i] = *reinterpret_cast<const V *>(xb + (at + p * xplane + i * xnext));
                 if constexpr (kSplit) {
-                    if constexpr (!C::kOffset) codes.set_zero(cur.z[j]);
+                    if constexpr (!C::kOffset) codes.set(el[w.by.div(std::min(4 * step + kb, units - 1))].y);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) wf[i] = codes.frag(cur.w[j], i);
-                    spread4(cur.s[j], sc);
-                    if constexpr (C::kOffset) spread4(cur.z[j], zc);
+                    for (int i = 0; i < 4; ++i) wf[i] = codes.frag(wq[j], i);
                     transpose_frags(wf);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        const uint2 e = el[w.by.div(std::min(4 * step + i, units - 1))];
                         floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if constexpr (C::kOffset) codes.set_zero(zc[i]);
+                        if constexpr (C::kOffset) codes.set(e.y);
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
                             if constexpr (C::kOffset) g = Vec8<T>::mma(xf[p][i], codes.zero_frag(), g);
                             g = Vec8<T>::mma(xf[p][i], wf[i], g);
                         }
 #pragma unroll
-                        for (int t = 0; t < 4; ++t) acc[t] = fmaf(sc[i], g[t], acc[t]);
+                        for (int t = 0; t < 4; ++t) acc[t] = fmaf(__uint_as_float(e.x), g[t], acc[t]);
                     }
                 } else {
-                    codes.set_zero(zc[j]);
-                    floatx4 g = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint2 e = el[w.by.div(step)];
+                    codes.set(e.y);
+                    floatx4 g[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};  // two chains: half the latency
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        wf[i] = codes.frag(cur.w[j], i);
+                        wf[i] = codes.frag(wq[j], i);
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
-                            if constexpr (C::kOffset) g = Vec8<T>::mma(xf[p][i], codes.zero_frag(), g);
-                            g = Vec8<T>::mma(xf[p][i], wf[i], g);
+                            if constexpr (C::kOffset) g[i & 1] = Vec8<T>::mma(xf[p][i], codes.zero_frag(), g[i & 1]);
+                            g[i & 1] = Vec8<T>::mma(xf[p][i], wf[i], g[i & 1]);
                         }
                     }
 #pragma unroll
-                    for (int t = 0; t < 4; ++t) acc[t] = fmaf(sc[j], g[t], acc[t]);
+                    for (int t = 0; t < 4; ++t) acc[t] = fmaf(__uint_as_float(e.x), g[0][t] + g[1][t], acc[t]);
                 }
             }
+        };
+        for (int h = hs; h < he; h += 2) {
+            set(wa, h);
+            load(wa, h + 2, he);
+            if (h + 1 >= he) break;
+            set(wb, h + 1);
+            load(wb, h + 3, he);
         }
-        if (n1 > 0) {
-            stage.store(other, M, n1, ld);
-            __syncthreads();  // the next chunk is staged; this one's buffer is written again a barrier later
-            uint16_t *t = buf;
-            buf = other;
-            other = t;
-            s = next;
-            end = c1 + ((slice + 1) * n1 >> lg);
-        }
-    }
+    };
+    phase(0, std::true_type());
+    for (int q0 = w.phase; q0 < quads; q0 += w.phase) phase(q0, std::false_type());
     return acc;
 }
 
 // The waves' sums through LDS: after it, sums[(wave * M + m) * 16 + row] of the workgroup.
 __device__ __forceinline__ void few_share(float *sums, int wave, const floatx4 &acc, int M) {
     const int lane = threadIdx.x % kWave;
-    __syncthreads();  // the staged activations are no longer read
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const int m = 4 * (lane >> 4) + t;
@@ -452,16 +544,16 @@ __device__ __forceinline__ void few_share(float *sums, int wave, const floatx4 &
 }
 // Sum over the 2^lg waves from `wave` on of row c of their tile and token m.
 __device__ __forceinline__ float few_sum(const float *sums, int wave, int lg, int M, int m, int c) {
-    float v = 0.0f;
-    for (int k = 0; k < 1 << lg; ++k) v += sums[((wave + k) * M + m) * kTileRows + c];
+    float t[kFewWaves];
+#pragma unroll
+    for (int k = 0; k < kFewWaves; ++k) t[k] = sums[((wave + (k & ((1 << lg) - 1))) * M + m) * kTileRows + c];
+    float v = t[0];
+#pragma unroll
+    for (int k = 1; k < kFewWaves; ++k) v += k >> lg ? 0.0f : t[k];
     return v;
 }
 // The wave's number in the workgroup, known to be the same in all its lanes.
 __device__ __forceinline__ int few_wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); }
-
-// log2 of the waves that split K for one row tile, at most `most`: as many as
-// `tiles` tiles leave room for on the chip at once while a wave keeps a body of steps.
-int few_slices(int64_t tiles, int units, int most);
 
 // Rounding of a result to the output's type, to nearest even.
 __device__ __forceinline__ void store_as(void *y, int64_t i, gptq_dtype dt, float v) {

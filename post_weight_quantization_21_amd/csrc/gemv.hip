@@ -13,30 +13,29 @@ namespace gptq {
 namespace {
 
 struct GemvArgs {
-    PackedDev w[2];
+    FewMat w[2];
+    FewShape shape;
+    int M;
     const uint16_t *x;
     int64_t ldx;
-    int M, lg;
     const float *bias;
     void *y;
     int64_t ldy;
     gptq_dtype y_dt;
 };
 
-// Gated: waves of the even tiles take the gate's rows, those of the odd ones up's.
-template <int b, typename T, bool kGated, bool kSplit>
+// Gated: the even tiles are the gate's rows, the odd ones up's.
+template <int b, typename T, bool kGated, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     constexpr int R = kGated ? 2 : 1, LR = kGated ? 1 : 0;
-    const int wave = few_wave(), lg = a.lg;
+    const int wave = few_wave(), lg = a.shape.lg;
     const int lt = 3 - lg - LR;  // log2 of the row tiles
-    const int tile = wave >> lg;
-    const int64_t r0 = (int64_t)blockIdx.x * kTileRows << lt, d_out = a.w[0].d_out;
-    const int64_t rt = std::min(r0 + (tile >> LR) * kTileRows, d_out - 1);
-    const XRows x = {a.x, a.ldx, 0, false, 0};
-    const floatx4 acc = few_product<b, T, 1, kSplit>(kGated && (tile & 1) ? a.w[R - 1] : a.w[0], rt, (int)std::min<int64_t>(kTileRows, d_out - rt),
-                                                     x, a.M, wave & ((1 << lg) - 1), lg, reinterpret_cast<uint16_t *>(smem));
+    const int64_t r0 = (int64_t)blockIdx.x * kTileRows << lt, d_out = a.shape.d_out;
+    const XRows x = {a.x, a.ldx, false, 0};
     float *sums = reinterpret_cast<float *>(smem);
+    const floatx4 acc = few_product<b, T, 1, R, kSplit, kX>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
+                                                            a.M, wave, smem);
     few_share(sums, wave, acc, a.M);
     for (int n = threadIdx.x; n < a.M * kTileRows << lt; n += kFewThreads) {
         const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
@@ -51,97 +50,118 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvAr
     }
 }
 
-// The activations in packed column order: Xg[m][k] = X[m][kperm[k]].
-__global__ __launch_bounds__(256) void gather_kernel(const uint16_t *__restrict__ X, int64_t ldx, int64_t d_in,
-                                                     const int32_t *__restrict__ kperm, uint16_t *__restrict__ Xg) {
-    const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (k >= d_in) return;
-    int64_t c = kperm[k];
-    c = c < 0 ? 0 : (c >= d_in ? d_in - 1 : c);
-    Xg[blockIdx.y * d_in + k] = X[blockIdx.y * ldx + c];
+// x prepared in memory, its columns in packed order: a thread per value.
+template <int b>
+__global__ __launch_bounds__(256) void prepare_kernel(const uint16_t *__restrict__ X, int64_t ldx, int d_in,
+                                                      const int32_t *__restrict__ kperm, uint16_t *__restrict__ out) {
+    const int k = blockIdx.x * 256 + threadIdx.x, M = gridDim.y, m = blockIdx.y;  // k: column of whole quads
+    if (k >= few_quads(d_in / kUnit) * kQuad) return;
+    uint16_t v = 0;
+    if (k < d_in) {
+        int c = kperm ? kperm[k] : k;
+        c = c < 0 ? 0 : (c >= d_in ? d_in - 1 : c);
+        v = X[m * ldx + c];
+    }
+    out[prepared_at<b>(k, M, m)] = v;
 }
 
-template <int b, typename T>
-void launch_gemv(const GemvArgs &a, bool gated, hipStream_t s) {
-    const dim3 grid((unsigned)ceil_div(a.w[0].d_out, kTileRows * ((kFewWaves >> a.lg) / (gated ? 2 : 1))));
-    const size_t lds = few_lds_bytes(a.M, 1, a.w[0].units);
-    if (gated) {
-        if (a.w[0].split)
-            gemv_kernel<b, T, true, true><<<grid, kFewThreads, lds, s>>>(a);
+template <int b, typename T, bool kGated, bool kSplit>
+void launch_gemv(const GemvArgs &a, FewX x, hipStream_t s) {
+    const dim3 grid((unsigned)ceil_div(a.shape.d_out, kTileRows * ((kFewWaves >> a.shape.lg) / (kGated ? 2 : 1))));
+    const size_t lds = few_lds_bytes(x == kDirect ? 0 : a.M, a.shape.units);
+    switch (x) {
+    case kRaw: gemv_kernel<b, T, kGated, kSplit, kRaw><<<grid, kFewThreads, lds, s>>>(a); break;
+    case kCopied: gemv_kernel<b, T, kGated, kSplit, kCopied><<<grid, kFewThreads, lds, s>>>(a); break;
+    case kDirect: gemv_kernel<b, T, kGated, kSplit, kDirect><<<grid, kFewThreads, lds, s>>>(a); break;
+    }
+}
+
+template <int b>
+hipError_t launch_gemv_bits(GemvArgs a, gptq_dtype x_dt, const gptq_packed &w, bool gated, void *ws, hipStream_t s) {
+    const bool fits = few_staged(a.M, a.shape.units);
+    const FewX x = !fits ? kDirect : (w.kperm ? kCopied : kRaw);
+    if (x != kRaw) {
+        prepare_kernel<b><<<dim3((unsigned)(few_quads(a.shape.units) * kQuad / 256), (unsigned)a.M), 256, 0, s>>>(
+            a.x, a.ldx, (int)w.d_in, w.kperm, static_cast<uint16_t *>(ws));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        a.x = static_cast<const uint16_t *>(ws);
+    }
+    const bool split = few_split(w);
+    if (x_dt == GPTQ_DT_BF16) {
+        if (gated)
+            split ? launch_gemv<b, __bf16, true, true>(a, x, s) : launch_gemv<b, __bf16, true, false>(a, x, s);
         else
-            gemv_kernel<b, T, true, false><<<grid, kFewThreads, lds, s>>>(a);
+            split ? launch_gemv<b, __bf16, false, true>(a, x, s) : launch_gemv<b, __bf16, false, false>(a, x, s);
     } else {
-        if (a.w[0].split)
-            gemv_kernel<b, T, false, true><<<grid, kFewThreads, lds, s>>>(a);
+        if (gated)
+            split ? launch_gemv<b, _Float16, true, true>(a, x, s) : launch_gemv<b, _Float16, true, false>(a, x, s);
         else
-            gemv_kernel<b, T, false, false><<<grid, kFewThreads, lds, s>>>(a);
+            split ? launch_gemv<b, _Float16, false, true>(a, x, s) : launch_gemv<b, _Float16, false, false>(a, x, s);
     }
-}
-
-template <typename T>
-void launch_gemv_bits(const GemvArgs &a, int bits, bool gated, hipStream_t s) {
-    switch (bits) {
-    case 2: return launch_gemv<2, T>(a, gated, s);
-    case 3: return launch_gemv<3, T>(a, gated, s);
-    case 4: return launch_gemv<4, T>(a, gated, s);
-    default: return launch_gemv<8, T>(a, gated, s);
-    }
+    return hipGetLastError();
 }
 
 }  // namespace
 
-PackedDev packed_dev(const gptq_packed &w) {
-    PackedDev d;
-    d.packed = w.packed;
-    d.scales = w.scales;
-    d.zeros = w.zeros;
+FewMat few_mat(const gptq_packed &w) { return {w.packed, w.scales, w.zeros}; }
+
+bool few_split(const gptq_packed &w) { return w.group_size != 0 && w.group_size != w.d_in && w.group_size % kStep != 0; }
+
+FewShape few_shape(const gptq_packed &w, int64_t tiles, int most) {
+    FewShape d;
+    const int64_t g = w.group_size > 0 ? w.group_size : w.d_in;
     d.d_out = (int32_t)w.d_out;
     d.words = (int32_t)(w.d_in / kUnit * w.bits);
-    const int64_t g = w.group_size > 0 ? w.group_size : w.d_in;
     d.groups = (int32_t)(w.d_in / g);
     d.units = (int32_t)(w.d_in / kUnit);
-    d.split = d.groups > 1 && g % kStep != 0;
     // one group per row: any divisor above the number of steps
-    d.by = small_div((uint32_t)(d.groups == 1 ? d.units + 1 : (d.split ? g / kUnit : g / kStep)));
+    d.by = small_div((uint32_t)(few_split(w) ? g / kUnit : (d.groups == 1 ? d.units + 1 : g / kStep)));
+    d.row_pieces = small_div((uint32_t)(64 * few_quads(d.units)));
+    // As many slices as leave the tiles room on the chip at once, with a quad
+    // each at least; more where a workgroup's rows have more entries than LDS.
+    const int quads = few_quads(d.units);
+    d.lg = 0;
+    while (2 << d.lg <= most &&
+           (((tiles << (d.lg + 1)) <= kFewResident && 2 << d.lg <= quads) || (kFewWaves >> d.lg) * kTileRows * (d.groups | 1) > kEntries))
+        ++d.lg;
+    // quads of a phase: at most ceil(512 quads / g) + 1 groups, an odd number of entries a row
+    const int64_t room = kEntries / ((kFewWaves >> d.lg) * kTileRows);
+    d.phase = quads;
+    if ((d.groups | 1) > room) d.phase = (int32_t)std::max<int64_t>(1, (room - 3) * g / kQuad);
     return d;
 }
 
-int few_slices(int64_t tiles, int units, int most) {
-    const int steps = (units + 3) / 4;
-    int lg = 0;
-    while (2 << lg <= most && (tiles << (lg + 1)) <= kFewResident && (4 << lg) < steps) ++lg;
-    return lg;
+size_t few_lds_bytes(int rows, int units) {
+    size_t values = 0;  // up to kStagedValues, by whole rows
+    while (rows > 0 && !few_staged(rows, units)) --rows;
+    values = (size_t)prepared_values(rows, units);
+    return kSumsBytes + kEntries * sizeof(uint2) + values * 2;
 }
 
-size_t gemv_ws_bytes(int64_t M, int64_t d_in) { return align_up((size_t)M * (size_t)d_in * 2, 256); }
+size_t gemv_ws_bytes(int64_t M, int64_t d_in) { return align_up((size_t)prepared_values(M, (int)(d_in / kUnit)) * 2, 256); }
+bool gemv_needs_ws(int64_t M, const gptq_packed &w) { return w.kperm || !few_staged((int)M, (int)(w.d_in / kUnit)); }
 
 hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,
                     const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws, hipStream_t s) {
     GemvArgs a;
-    a.w[0] = packed_dev(w);
-    a.w[1] = packed_dev(up ? *up : w);
+    a.w[0] = few_mat(w);
+    a.w[1] = few_mat(up ? *up : w);
+    const int64_t tiles = ceil_div(w.d_out, kTileRows);
+    a.shape = up ? few_shape(w, 2 * tiles, kFewWaves / 2) : few_shape(w, tiles, kFewWaves);
+    a.M = (int)M;
     a.x = static_cast<const uint16_t *>(X);
     a.ldx = ldx;
-    a.M = (int)M;
-    a.lg = up ? few_slices(2 * ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves / 2)
-              : few_slices(ceil_div(w.d_out, kTileRows), a.w[0].units, kFewWaves);
     a.bias = bias;
     a.y = Y;
     a.ldy = ldy;
     a.y_dt = y_dt;
-    if (w.kperm) {
-        gather_kernel<<<dim3((unsigned)ceil_div(w.d_in, 256), (unsigned)M), 256, 0, s>>>(
-            static_cast<const uint16_t *>(X), ldx, w.d_in, w.kperm, static_cast<uint16_t *>(ws));
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        a.x = static_cast<const uint16_t *>(ws);
-        a.ldx = w.d_in;
+    switch (w.bits) {
+    case 2: return launch_gemv_bits<2>(a, x_dt, w, up, ws, s);
+    case 3: return launch_gemv_bits<3>(a, x_dt, w, up, ws, s);
+    case 4: return launch_gemv_bits<4>(a, x_dt, w, up, ws, s);
+    default: return launch_gemv_bits<8>(a, x_dt, w, up, ws, s);
     }
-    if (x_dt == GPTQ_DT_BF16)
-        launch_gemv_bits<__bf16>(a, w.bits, up != nullptr, s);
-    else
-        launch_gemv_bits<_Float16>(a, w.bits, up != nullptr, s);
-    return hipGetLastError();
 }
 
 }  // namespace gptq

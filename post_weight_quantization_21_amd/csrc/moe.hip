@@ -249,67 +249,92 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
     }
 }
 
-// Rows of activations in an expert's packed column order: out[p][k] =
-// in[token of p or p][kperm[expert][k]], plane by plane.
-__global__ __launch_bounds__(256) void gather_pairs_kernel(const uint16_t *__restrict__ in, int64_t ld, int by_token,
-                                                           int64_t plane, const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
-                                                           int d, uint16_t *__restrict__ out) {
+// Prepared x of an expert's pairs starts at its first pair's row: value
+// start * (whole quads of columns).  One workgroup row per expert.
+template <int b>
+__global__ __launch_bounds__(256) void prepare_pairs_kernel(const uint16_t *__restrict__ X, int64_t ldx, int d,
+                                                            const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
+                                                            uint16_t *__restrict__ out) {
     const Expert &e = lists->expert[blockIdx.y];
-    const int k = blockIdx.x * 256 + threadIdx.x;
-    if (k >= d) return;
-    in += blockIdx.z * plane;
-    out += blockIdx.z * plane;
-    if (e.count == 0) return;
-    int c = kperm[(int64_t)e.expert * d + k];
+    const int k = blockIdx.x * 256 + threadIdx.x, n = e.count;
+    if (n == 0) return;
+    int c = k < d ? (kperm ? kperm[(int64_t)e.expert * d + k] : k) : 0;
     c = c < 0 ? 0 : (c >= d ? d - 1 : c);
-    for (int i = 0; i < e.count; ++i)
-        out[(int64_t)(e.start + i) * d + k] = in[(by_token ? e.token[i] : e.start + i) * ld + c];
+    out += prepared_values(e.start, d / kUnit);
+    for (int m = 0; m < n; ++m) out[prepared_at<b>(k, n, m)] = k < d ? X[e.token[m] * ldx + c] : 0;
+}
+
+// Prepared h with its columns in the packed order of the down product.
+template <int b>
+__global__ __launch_bounds__(256) void permute_pairs_kernel(const uint16_t *__restrict__ h, int64_t plane, int ff,
+                                                            const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
+                                                            uint16_t *__restrict__ out) {
+    const Expert &e = lists->expert[blockIdx.y];
+    const int k = blockIdx.x * 256 + threadIdx.x, n = e.count;
+    if (n == 0) return;
+    int c = k < ff ? kperm[(int64_t)e.expert * ff + k] : 0;
+    c = c < 0 ? 0 : (c >= ff ? ff - 1 : c);
+    const int64_t base = blockIdx.z * plane + prepared_values(e.start, ff / kUnit);
+    for (int m = 0; m < n; ++m) out[base + prepared_at<b>(k, n, m)] = k < ff ? h[base + prepared_at<b>(c, n, m)] : 0;
 }
 
 struct GateUpArgs {
-    PackedDev w[2];
-    const uint16_t *x;  // rows by token, or by pair (ldx = d) when gathered
+    FewMat w[2];
+    FewShape shape;
+    const uint16_t *x;  // rows by token, or prepared by pair
     int64_t ldx;
-    int by_pair, lg, planes;
+    int planes;
     const Lists *lists;
     __bf16 *h;
     int64_t h_plane;
 };
 
-template <int b, typename T, bool kSplit>
+template <int b, typename T, bool kSplit, bool kRawX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(GateUpArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const Expert &e = a.lists->expert[blockIdx.y];
     const int token = e.token[threadIdx.x & (kMoeMaxTokens - 1)];
-    const int start = e.start, count = e.count, wave = few_wave(), lg = a.lg;
+    const int start = e.start, count = e.count, wave = few_wave(), lg = a.shape.lg;
     if (count == 0) return;
     const int lt = 2 - lg;  // log2 of the row tiles
-    const int tile = wave >> lg;
-    const int ff = a.w[0].d_out, r0 = blockIdx.x * kTileRows << lt, rt = std::min(r0 + (tile >> 1) * kTileRows, ff - 1);
-    const XRows x = {a.by_pair ? a.x + start * a.ldx : a.x, a.ldx, 0, !a.by_pair, token};
-    const floatx4 acc = few_product<b, T, 1, kSplit>(tile & 1 ? a.w[1] : a.w[0], (int64_t)e.expert * ff + rt, std::min(kTileRows, ff - rt), x,
-                                                     count, wave & ((1 << lg) - 1), lg, reinterpret_cast<uint16_t *>(smem));
+    const int ff = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
+    const int64_t row = (int64_t)e.expert * ff + r0;
+    floatx4 acc;
+    if constexpr (kRawX) {
+        const XRows x = {a.x, a.ldx, true, token};
+        acc = few_product<b, T, 1, 2, kSplit, kRaw>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
+    } else {
+        const XRows x = {a.x + prepared_values(start, a.shape.units), 0, false, 0};
+        acc = few_staged(count, a.shape.units) ? few_product<b, T, 1, 2, kSplit, kCopied>(a.w, a.shape, row, ff - r0, x, count, wave, smem)
+                                               : few_product<b, T, 1, 2, kSplit, kDirect>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
+    }
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
+    __bf16 *h = a.h + prepared_values(start, ff / kUnit);
     for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
         const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
         if (r0 + c >= ff) continue;
         const int w0 = (c >> 4) << (1 + lg);
-        float h = silu_mul(few_sum(sums, w0, lg, count, m, c & 15), few_sum(sums, w0 + (1 << lg), lg, count, m, c & 15));
-        __bf16 *dst = a.h + (int64_t)(start + m) * ff + r0 + c;
+        float v = silu_mul(few_sum(sums, w0, lg, count, m, c & 15), few_sum(sums, w0 + (1 << lg), lg, count, m, c & 15));
+        __bf16 *dst = h + prepared_at<b>(r0 + c, count, m);
         for (int p = 0; p < a.planes; ++p) {
-            const __bf16 t = (__bf16)h;
+            const __bf16 t = (__bf16)v;
             dst[p * a.h_plane] = t;
-            h -= (float)t;  // exact
+            v -= (float)t;  // exact
         }
+    }
+    if (r0 + (kTileRows << lt) >= ff) {  // the rest of h's last step counts as zero
+        const int rest = few_steps(ff / kUnit) * kStep - ff;
+        for (int n = threadIdx.x; n < count * rest; n += kFewThreads)
+            for (int p = 0; p < a.planes; ++p) h[p * a.h_plane + prepared_at<b>(ff + n % rest, count, n / rest)] = (__bf16)0.0f;
     }
 }
 
 struct DownArgs {
-    PackedDev w;
-    const uint16_t *h;  // planes of rows by pair
+    FewMat w;
+    FewShape shape;
+    const uint16_t *h;  // prepared, planes of rows by pair
     int64_t h_plane;
-    int lg;
     const Lists *lists;
     float *part;  // rows by pair
 };
@@ -318,14 +343,15 @@ template <int b, int P, bool kSplit>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const Expert &e = a.lists->expert[blockIdx.y];
-    const int start = e.start, count = e.count, wave = few_wave(), lg = a.lg;
+    const int start = e.start, count = e.count, wave = few_wave(), lg = a.shape.lg;
     if (count == 0) return;
-    const int lt = 3 - lg, tile = wave >> lg;
-    const int d = a.w.d_out, r0 = blockIdx.x * kTileRows << lt, rt = std::min(r0 + tile * kTileRows, d - 1);
-    const int64_t ff = a.w.units * kUnit;
-    const XRows x = {a.h + start * ff, ff, a.h_plane, false, 0};
-    const floatx4 acc = few_product<b, __bf16, P, kSplit>(a.w, (int64_t)e.expert * d + rt, std::min(kTileRows, d - rt), x, count,
-                                                          wave & ((1 << lg) - 1), lg, reinterpret_cast<uint16_t *>(smem));
+    const int lt = 3 - lg;
+    const int d = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
+    const int64_t row = (int64_t)e.expert * d + r0;
+    const XRows x = {a.h + prepared_values(start, a.shape.units), a.h_plane, false, 0};
+    const floatx4 acc = few_staged(P * count, a.shape.units)
+                            ? few_product<b, __bf16, P, 1, kSplit, kCopied>(&a.w, a.shape, row, d - r0, x, count, wave, smem)
+                            : few_product<b, __bf16, P, 1, kSplit, kDirect>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
     for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
@@ -356,14 +382,15 @@ struct Layout {
 };
 Layout layout(int64_t T, int64_t d, int64_t d_ff, int n_experts, int top_k) {
     const size_t pairs = (size_t)T * top_k;
+    const size_t xv = prepared_values((int64_t)pairs, (int)(d / kUnit)), hv = prepared_values((int64_t)pairs, (int)(d_ff / kUnit));
     Layout l;
     l.logits = 0;
     l.lists = align_up((size_t)T * n_experts * sizeof(double), 256);
     l.h = l.lists + align_up(sizeof(Lists), 256);
-    l.part = l.h + align_up(kMaxPlanes * pairs * d_ff * 2, 256);
+    l.part = l.h + align_up(kMaxPlanes * hv * 2, 256);
     l.xg = l.part + align_up(pairs * d * 4, 256);
-    l.hg = l.xg + align_up(pairs * d * 2, 256);
-    l.bytes = l.hg + align_up(kMaxPlanes * pairs * d_ff * 2, 256);
+    l.hg = l.xg + align_up(xv * 2, 256);
+    l.bytes = l.hg + align_up(kMaxPlanes * hv * 2, 256);
     return l;
 }
 
@@ -382,12 +409,19 @@ struct MoeCall {
     char *ws;
 };
 
-template <int b, int P>
-void launch_down(const DownArgs &w, dim3 grid, size_t lds, hipStream_t s) {
-    if (w.w.split)
-        down_kernel<b, P, true><<<grid, kFewThreads, lds, s>>>(w);
+template <int b, typename T, bool kSplit>
+void launch_gate_up(const GateUpArgs &g, bool raw, dim3 grid, size_t lds, hipStream_t s) {
+    if (raw)
+        gate_up_kernel<b, T, kSplit, true><<<grid, kFewThreads, lds, s>>>(g);
     else
-        down_kernel<b, P, false><<<grid, kFewThreads, lds, s>>>(w);
+        gate_up_kernel<b, T, kSplit, false><<<grid, kFewThreads, lds, s>>>(g);
+}
+template <int b, bool kSplit>
+void launch_down(const DownArgs &w, int planes, dim3 grid, size_t lds, hipStream_t s) {
+    if (planes == 3)
+        down_kernel<b, 3, kSplit><<<grid, kFewThreads, lds, s>>>(w);
+    else
+        down_kernel<b, 2, kSplit><<<grid, kFewThreads, lds, s>>>(w);
 }
 
 template <int b, typename T>
@@ -398,50 +432,49 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     // experts that `pairs` independent choices would hit, which the work is spread for
     const double busy = c.n_experts * (1.0 - std::pow(1.0 - 1.0 / c.n_experts, (double)pairs));
     GateUpArgs g;
-    g.w[0] = packed_dev(*c.gate);
-    g.w[1] = packed_dev(*c.up);
+    const int64_t pair_tiles = ceil_div(ff, kTileRows);
+    g.w[0] = few_mat(*c.gate);
+    g.w[1] = few_mat(*c.up);
+    g.shape = few_shape(*c.gate, (int64_t)(2 * busy * pair_tiles), kFewWaves / 2);
     g.x = static_cast<const uint16_t *>(c.X);
     g.ldx = c.ldx;
-    g.by_pair = 0;
     g.lists = lists;
     g.h = reinterpret_cast<__bf16 *>(c.ws + l.h);
-    g.h_plane = pairs * ff;
+    g.h_plane = prepared_values(pairs, (int)(ff / kUnit));
     g.planes = c.y_dt == GPTQ_DT_F32 ? 3 : 2;
-    if (c.gate->kperm) {
+    const bool raw = !c.gate->kperm && few_staged((int)c.T, g.shape.units);
+    if (!raw) {
         uint16_t *xg = reinterpret_cast<uint16_t *>(c.ws + l.xg);
-        gather_pairs_kernel<<<dim3((unsigned)ceil_div(d, 256), slots), 256, 0, s>>>(g.x, c.ldx, 1, 0, lists, c.gate->kperm, (int)d, xg);
+        prepare_pairs_kernel<b><<<dim3((unsigned)(few_quads(g.shape.units) * kQuad / 256), slots), 256, 0, s>>>(g.x, c.ldx, (int)d, lists,
+                                                                                                               c.gate->kperm, xg);
         g.x = xg;
-        g.ldx = d;
-        g.by_pair = 1;
     }
-    const int64_t gu_tiles = ceil_div(ff, kTileRows);
-    g.lg = few_slices((int64_t)(2 * busy * gu_tiles), g.w[0].units, kFewWaves / 2);
-    const dim3 grid((unsigned)ceil_div(gu_tiles, (kFewWaves >> g.lg) / 2), slots);
-    const size_t lds = few_lds_bytes((int)c.T, 1, g.w[0].units);
-    if (g.w[0].split)
-        gate_up_kernel<b, T, true><<<grid, kFewThreads, lds, s>>>(g);
+    const dim3 grid((unsigned)ceil_div(pair_tiles, (kFewWaves >> g.shape.lg) / 2), slots);
+    const size_t lds = few_lds_bytes((int)c.T, g.shape.units);
+    if (few_split(*c.gate))
+        launch_gate_up<b, T, true>(g, raw, grid, lds, s);
     else
-        gate_up_kernel<b, T, false><<<grid, kFewThreads, lds, s>>>(g);
+        launch_gate_up<b, T, false>(g, raw, grid, lds, s);
     DownArgs w;
-    w.w = packed_dev(*c.down);
+    const int64_t tiles = ceil_div(d, kTileRows);
+    w.w = few_mat(*c.down);
+    w.shape = few_shape(*c.down, (int64_t)(busy * tiles), kFewWaves);
     w.h = reinterpret_cast<const uint16_t *>(g.h);
     w.h_plane = g.h_plane;
     w.lists = lists;
     w.part = reinterpret_cast<float *>(c.ws + l.part);
     if (c.down->kperm) {
         uint16_t *hg = reinterpret_cast<uint16_t *>(c.ws + l.hg);
-        gather_pairs_kernel<<<dim3((unsigned)ceil_div(ff, 256), slots, g.planes), 256, 0, s>>>(w.h, ff, 0, w.h_plane, lists,
-                                                                                               c.down->kperm, (int)ff, hg);
+        permute_pairs_kernel<b><<<dim3((unsigned)(few_quads(w.shape.units) * kQuad / 256), slots, g.planes), 256, 0, s>>>(
+            w.h, w.h_plane, (int)ff, lists, c.down->kperm, hg);
         w.h = hg;
     }
-    const int64_t tiles = ceil_div(d, kTileRows);
-    w.lg = few_slices((int64_t)(busy * tiles), w.w.units, kFewWaves);
-    const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves >> w.lg), slots);
-    const size_t dlds = few_lds_bytes((int)c.T, g.planes, w.w.units);
-    if (g.planes == 3)
-        launch_down<b, 3>(w, dgrid, dlds, s);
+    const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves >> w.shape.lg), slots);
+    const size_t dlds = few_lds_bytes(g.planes * (int)c.T, w.shape.units);
+    if (few_split(*c.down))
+        launch_down<b, true>(w, g.planes, dgrid, dlds, s);
     else
-        launch_down<b, 2>(w, dgrid, dlds, s);
+        launch_down<b, false>(w, g.planes, dgrid, dlds, s);
     combine_kernel<<<dim3((unsigned)ceil_div(d, 256), (unsigned)c.T), 256, 0, s>>>(w.part, lists, (int)d, c.Y, c.ldy, c.y_dt);
 }
 
