@@ -427,8 +427,7 @@ typedef struct {
  *   bias    [d_out] fp32 or NULL.
  *   Y, H    fp16, bf16 or fp32 [M][ldy] out, ldy >= d_out; not X's memory.
  *   ws      scratch of gptq_workspace_bytes(GPTQ_OP_GEMV, 0, d_in, M, NULL), used
- *           (and needed) only with a kperm, or when M times d_in rounded up to a
- *           multiple of 512 is above 16384; 16-byte aligned.
+ *           (and needed) only with a kperm; 16-byte aligned.
  * Sums are fp32 over exact products of the integers q - z (bf16 X with 2-4
  * bits: 2^bits + q, less (2^bits + z) times the sum of x) with x; the scale
  * multiplies a group's sum; the result is rounded once.  Deterministic.  A

@@ -492,8 +492,7 @@ def _few_ws(ws, device):
 
 def _gemv_ws(ws, w, M, device):
     if ws is None:
-        # needed with a column order, and where the activations exceed what the kernels stage (gptq_gemv)
-        if w.kperm is None and M * (-(-w.d_in // 512) * 512) <= 16384:
+        if w.kperm is None:  # not used
             return None, 0
         ws = _workspace(workspace_bytes(OP_GEMV, w.d_out, w.d_in, M), device)
     return _few_ws(ws, device)

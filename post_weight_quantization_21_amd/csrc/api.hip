@@ -110,7 +110,7 @@ gptq_status run_gemv_checked(const void *X, gptq_dtype x_dt, int64_t M, int64_t 
     if (st != GPTQ_OK) return st;
     if (bias && !aligned(bias, 4)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned bias", fn);
     if (M == 0) return GPTQ_OK;
-    const size_t need = gptq::gemv_needs_ws(M, *w) ? gptq::gemv_ws_bytes(M, w->d_in) : 0;
+    const size_t need = w->kperm ? gptq::gemv_ws_bytes(M, w->d_in) : 0;
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
     if (need > 0 && !aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);

@@ -120,7 +120,6 @@ hipError_t run_w4a16(const void *X, int64_t M, int64_t d_in, int64_t ldx, const 
 // Packed layers for a few tokens (gemv.hip, moe.hip)
 // ---------------------------------------------------------------------------
 size_t gemv_ws_bytes(int64_t M, int64_t d_in);
-bool gemv_needs_ws(int64_t M, const gptq_packed &w);
 // up: NULL for the plain product, else the second matrix of the gated one.
 hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,
                     const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws, hipStream_t s);

@@ -25,7 +25,6 @@
 #pragma once
 
 #include <algorithm>
-#include <type_traits>
 
 #include "common.h"
 
@@ -51,15 +50,14 @@ constexpr int kFewThreads = kFewWaves * kWave;
 constexpr int kFewOccupancy = 4;                       // waves per SIMD, which the kernels' registers allow
 constexpr int kFewResident = 256 * 4 * kFewOccupancy;  // waves of the chip at once
 
-// LDS of a workgroup, two of which share a compute unit's 160 KB: the waves'
-// sums, the scales and zero constants of its rows, and x where it fits.
-constexpr int kStagedValues = 16384;  // of x
-constexpr int kEntries = 4096;        // of (scale, zero constant), 8 bytes
+// LDS of a workgroup: the waves' sums, then, for a phase of quads, the scales and
+// zero constants of its rows and x.  Two workgroups share a compute unit's 160
+// KB; one takes most of it where there are no more workgroups than compute units.
 constexpr int kSumsBytes = kFewWaves * kFewRows * kTileRows * 4;
+constexpr int kLdsShared = 80 * 1024, kLdsAlone = 156 * 1024;
 
 __host__ __device__ inline int few_steps(int units) { return (units + 3) / 4; }
 __host__ __device__ inline int few_quads(int units) { return (units + 15) / 16; }
-__host__ __device__ inline bool few_staged(int rows, int units) { return rows * few_quads(units) * kQuad <= kStagedValues; }
 __host__ __device__ inline int ceil_log2(int n) { return n <= 1 ? 0 : 32 - __builtin_clz((unsigned)(n - 1)); }
 
 // Exact quotients n / d of small numbers: n, d < 2^15 (units and steps of a row).
@@ -79,18 +77,24 @@ struct FewShape {
     int32_t d_out, words, groups;  // rows, words per row, groups per row
     int32_t units;                 // units per row (d_in / 32)
     int32_t lg;                    // log2 of the slices
-    int32_t phase;                 // quads whose scales fit in LDS
+    int32_t lds, quad_entries;     // LDS bytes; bytes of a quad's entries
     SmallDiv by;                   // steps per group, or units per group where groups end inside a step
-    SmallDiv row_pieces;           // prepared 16-byte pieces per row of x
 };
 FewMat few_mat(const gptq_packed &w);  // gemv.hip
-// tiles: row tiles that share the chip; most: slices at most.
-FewShape few_shape(const gptq_packed &w, int64_t tiles, int most);
+// tiles: row tiles that share the chip; most: slices at most; rows: of x (all
+// its planes) as expected, and at most.
+FewShape few_shape(const gptq_packed &w, double tiles, int most, int rows, int max_rows);
 // Groups end inside a step: the fragments are transposed so that a matrix
 // instruction covers one unit, and the fold with the scale runs per unit.
 bool few_split(const gptq_packed &w);
-// LDS bytes for up to `rows` staged rows of x.
-size_t few_lds_bytes(int rows, int units);
+
+// LDS bytes that a phase does not grow: the sums and the entries' odd row ends.
+__host__ __device__ inline int few_fixed(int lg) { return kSumsBytes + (kFewWaves >> lg) * kTileRows * 3 * 8; }
+// Quads of a phase: as many as fit.
+__host__ __device__ inline int few_phase(const FewShape &w, int rows) {
+    const int q = (w.lds - few_fixed(w.lg)) / (rows * kQuad * 2 + w.quad_entries), quads = few_quads(w.units);
+    return q < quads ? q : quads;
+}
 
 __device__ __forceinline__ void swap32(uint32_t &a, uint32_t &b) {  // a's upper half with b's lower half
     const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
@@ -275,12 +279,7 @@ __device__ __forceinline__ int64_t prepared_at(int col, int M, int m) {
     return ((int64_t)(col / kUnit * 4 + (s >> 3)) * M + m) * 8 + (s & 7);
 }
 
-// Where a product finds x.
-enum FewX {
-    kRaw = 0,     // rows in their own order: prepared into LDS
-    kCopied = 1,  // prepared in memory: copied into LDS
-    kDirect = 2   // prepared in memory, too much for LDS: read from there, that is from L2, by every wave
-};
+// Activations of a product: rows as they are, or prepared in memory.
 struct XRows {
     const uint16_t *base;
     int64_t ld;     // raw: between rows; prepared: between planes
@@ -288,62 +287,75 @@ struct XRows {
     int32_t row;
 };
 
-// The workgroup's x on its way into LDS.
-template <int b, int P, FewX kX>
+// A phase's x on its way into LDS, in batches of two units a thread.
+template <int b, int P, bool kRaw>
 struct StageX {
-    static constexpr int kPieces = kStagedValues / 8 / kFewThreads;
-    u32x4 v[kPieces];
-    int at;  // raw: the thread's unit, as first piece and row
-    __device__ __forceinline__ void load(const XRows &x, const FewShape &w, int M) {
-        if constexpr (kX == kRaw) {  // a thread takes a unit
-            static_assert(kStagedValues / kUnit <= kFewThreads, "a unit per thread");
-            const int per_row = 16 * few_quads(w.units);
-            const int r = w.row_pieces.div(4 * threadIdx.x), u = threadIdx.x - r * per_row;
-            const int row = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
-            at = r < M ? 4 * u * M + r : -1;
+    static constexpr int kUnits = 2;
+    u32x4 v[4 * kUnits];
+    uint32_t magic;  // raw: of the division by the units of a row
+    int per_row, items, first, total;
+    __device__ __forceinline__ void init(int M, int units, int q0, int nq) {
+        per_row = 16 * nq;
+        magic = 0xFFFFFFFFu / (uint32_t)per_row + 1;
+        items = P * M * per_row;  // units
+        first = 16 * q0;
+        total = (items + kUnits * kFewThreads - 1) / (kUnits * kFewThreads);
+    }
+    // Raw: unit i of the phase is unit u of row r.  Prepared: unit i is pieces 4 i .. of the phase, plane by plane.
+    __device__ __forceinline__ void load(const XRows &x, int M, int units, int batch) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (u32x4){0, 0, 0, 0};
-            if (r < M && u < w.units) {
-                const u32x4 *src = reinterpret_cast<const u32x4 *>(x.base + row * x.ld + u * kUnit);
+        for (int k = 0; k < kUnits; ++k) {
+            if constexpr (kRaw) {
+                const int i = threadIdx.x + (kUnits * batch + k) * kFewThreads;
+                const int r = __umulhi(i, magic), u = first + i - r * per_row;
+                const int row = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = src[i];
-            }
-        }
-        if constexpr (kX == kCopied) {
-            const int pieces = (int)(prepared_values(M, w.units) / 8);
+                for (int j = 0; j < 4; ++j) v[4 * k + j] = (u32x4){0, 0, 0, 0};
+                if (i < items && u < units) {
+                    const u32x4 *src = reinterpret_cast<const u32x4 *>(x.base + row * x.ld + u * kUnit);
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const int i = threadIdx.x + k * kFewThreads, p = (i >= pieces) + (P > 2 && i >= 2 * pieces);
-                if (i < P * pieces) v[k] = *reinterpret_cast<const u32x4 *>(x.base + p * x.ld + (int64_t)(i - p * pieces) * 8);
+                    for (int j = 0; j < 4; ++j) v[4 * k + j] = src[j];
+                }
+            } else {
+                const int plane = 4 * M * per_row;  // pieces
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads, p = (i >= plane) + (P > 2 && i >= 2 * plane);
+                    v[4 * k + j] = (u32x4){0, 0, 0, 0};  // (left alone, it would be kept through the phase before)
+                    if (i < 4 * items) v[4 * k + j] = *reinterpret_cast<const u32x4 *>(x.base + p * x.ld + ((int64_t)4 * first * M + i - p * plane) * 8);
+                }
             }
         }
     }
-    __device__ __forceinline__ void store(uint16_t *xs, const FewShape &w, int M) const {
+    __device__ __forceinline__ void store(uint16_t *xs, int M, int batch) const {
         u32x4 *dst = reinterpret_cast<u32x4 *>(xs);
-        if constexpr (kX == kRaw) {
-            if (at < 0) return;
-            uint32_t t[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) t[i] = v[i / 4][i % 4];
+        for (int k = 0; k < kUnits; ++k) {
+            if constexpr (kRaw) {
+                const int i = threadIdx.x + (kUnits * batch + k) * kFewThreads;
+                const int r = __umulhi(i, magic), u = i - r * per_row;
+                if (i >= items) continue;
+                uint32_t t[16];
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
-                u32x4 o;
+                for (int j = 0; j < 16; ++j) t[j] = v[4 * k + j / 4][j % 4];
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    constexpr int apart = b == 4 ? 4 : 8;
-                    const int c0 = slot_col<b>(f, 2 * p), c1 = slot_col<b>(f, 2 * p + 1);
-                    o[p] = c1 == c0 + 1 ? t[c0 / 2]
-                                        : __builtin_amdgcn_perm(t[(c0 + apart) / 2], t[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
+                for (int f = 0; f < 4; ++f) {
+                    u32x4 o;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        constexpr int apart = b == 4 ? 4 : 8;
+                        const int c0 = slot_col<b>(f, 2 * p), c1 = slot_col<b>(f, 2 * p + 1);
+                        o[p] = c1 == c0 + 1 ? t[c0 / 2]
+                                            : __builtin_amdgcn_perm(t[(c0 + apart) / 2], t[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
+                    }
+                    dst[(4 * u + f) * M + r] = o;
                 }
-                dst[at + f * M] = o;
-            }
-        }
-        if constexpr (kX == kCopied) {
-            const int pieces = P * (int)(prepared_values(M, w.units) / 8);
+            } else {
 #pragma unroll
-            for (int k = 0; k < kPieces; ++k) {
-                const int i = threadIdx.x + k * kFewThreads;
-                if (i < pieces) dst[i] = v[k];
+                for (int j = 0; j < 4; ++j) {
+                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads;
+                    if (i < 4 * items) dst[i] = v[4 * k + j];
+                }
             }
         }
     }
@@ -358,46 +370,40 @@ struct StageX {
 template <int b, typename T, int kMats>
 struct StageGroups {
     static constexpr int kBatch = 8;  // loads of a thread before its first store
-    const FewMat *mats;
-    int64_t row0;
-    int rows, groups;            // from row0 to the matrix's end; groups per row
-    int count, ga, n, ld;        // rows of the workgroup; the phase's groups
-    int lgn, chunks, total;
+    const char *sb[kMats], *zb[kMats];  // of row tile 0
+    int rows, groups;                   // from row tile 0 to the matrix's end; groups per row
+    int ga, n, ld, items, total;        // the phase's groups; entries of a matrix, loads of a thread
+    uint32_t magic;                     // of the division by n
     float s[kBatch], z[kBatch];
 
-    __device__ __forceinline__ void init(int first, int last) {
+    __device__ __forceinline__ void init(int first, int last, int count) {
         ga = first;
         n = last - first + 1;
         ld = n | 1;
-        lgn = std::min(ceil_log2(n), 6);  // a load covers 64 >> lgn rows
-        chunks = (n + kWave - 1) / kWave;
-        total = ((count << lgn) + kFewThreads - 1) / kFewThreads * chunks;
+        magic = n > 1 ? 0xFFFFFFFFu / (uint32_t)n + 1 : 0;
+        items = count / kMats * n;
+        total = (items + kFewThreads - 1) / kFewThreads * kMats;
     }
-    __device__ __forceinline__ bool place(int t, int &r, int &g) const {
-        const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-        const int q = chunks == 1 ? t : t / chunks;
-        r = ((q * kFewWaves + wave) << (6 - lgn)) + (lane >> lgn);
-        g = (t - q * chunks) * kWave + (lane & ((1 << lgn) - 1));
-        return t < total && r < count && g < n;
-    }
+    __device__ __forceinline__ int row_of(int i) const { return magic ? __umulhi(i, magic) : i; }
     __device__ __forceinline__ void load(int t0) {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            int r, g;
-            if (place(t0 + k, r, g)) {
-                const int t = r / kTileRows;
-                const FewMat &a = mats[kMats > 1 ? t % kMats : 0];
-                const int64_t at = (row0 + std::min(t / kMats * kTileRows + r % kTileRows, rows - 1)) * groups + ga + g;
-                s[k] = a.scales[at];
-                z[k] = a.zeros[at];
-            }
+            s[k] = z[k] = 0.0f;
+            if (t0 + k >= total) continue;
+            const int i = threadIdx.x + (t0 + k) / kMats * kFewThreads, r = row_of(i);
+            if (i >= items) continue;
+            const uint32_t at = 4u * (std::min(r, rows - 1) * groups + ga + i - r * n);
+            s[k] = *reinterpret_cast<const float *>(sb[k % kMats] + at);
+            z[k] = *reinterpret_cast<const float *>(zb[k % kMats] + at);
         }
     }
     __device__ __forceinline__ void store(uint2 *entries, int t0) const {
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            int r, g;
-            if (place(t0 + k, r, g)) entries[r * ld + g] = make_uint2(__float_as_uint(s[k]), Codes<b, T>::constant(z[k]));
+            if (t0 + k >= total) continue;
+            const int i = threadIdx.x + (t0 + k) / kMats * kFewThreads, r = row_of(i);
+            const int row = kMats > 1 ? (r >> 4) * 32 + k % kMats * 16 + (r & 15) : r;  // of the workgroup
+            if (i < items) entries[row * ld + i - r * n] = make_uint2(__float_as_uint(s[k]), Codes<b, T>::constant(z[k]));
         }
     }
 };
@@ -407,29 +413,28 @@ struct StageGroups {
 // row tile t / kMats; row0: the first row of row tile 0 in the stack, rows: from
 // there to the matrix's end (at least 1).  Every wave of the workgroup calls it.
 //
-// Weights stream through two sets of registers, one computed while the other is
-// loaded (4 to 8 KB of a wave in flight at 4 bits).  Past the wave's slice they
-// are not read and count as zero codes with the scale of an existing group; x is
-// zero past the last unit, so such a step is left out only to save time.
-template <int b, typename T, int P, int kMats, bool kSplit, FewX kX>
+// K runs in phases whose x and entries fit in LDS (mostly one); in a phase the
+// waves of a tile take equal runs of quads.  Weights stream through two sets of
+// registers, one computed while the other is loaded (4 to 8 KB of a wave in
+// flight at 4 bits); past the wave's run nothing is read.  x is zero past the
+// last unit.
+template <int b, typename T, int P, int kMats, bool kSplit, bool kRaw>
 __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShape &w, int64_t row0, int rows, const XRows &x,
                                                int M, int wave, unsigned char *smem) {
     typedef typename Vec8<T>::V V;
     typedef Codes<b, T> C;
     const int lane = threadIdx.x % kWave, kb = lane >> 4, lg = w.lg;
-    const int units = w.units, quads = few_quads(units);
+    const int units = w.units, quads = few_quads(units), phase_quads = few_phase(w, P * M);
     const int tile = wave >> lg, slice = wave & ((1 << lg) - 1), tiles = kFewWaves >> lg;
     const int m = std::min(lane & 15, M - 1);
-    uint2 *entries = reinterpret_cast<uint2 *>(smem + kSumsBytes);
-    uint16_t *xs = reinterpret_cast<uint16_t *>(entries + kEntries);
+    uint16_t *xs = reinterpret_cast<uint16_t *>(smem + kSumsBytes);
+    uint2 *entries = reinterpret_cast<uint2 *>(smem + kSumsBytes + phase_quads * P * M * kQuad * 2);
     const FewMat &mat = mats[kMats > 1 ? tile % kMats : 0];
     const int t0 = std::min(tile / kMats * kTileRows, rows - 1), tr = std::min(kTileRows, rows - t0), rl = std::min(lane & 15, tr - 1);
     const uint32_t bytes = 4u * tr * w.words, wo = 4u * (rl * w.words + kb * b);
     const auto wr = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint32_t *>(mat.packed + (row0 + t0) * w.words), 0, bytes, 0x00020000);
-    // bytes of prepared x: the lane's first piece, between its pieces of a step, between planes
-    const char *xb = reinterpret_cast<const char *>(kX == kDirect ? x.base : xs);
+    // bytes of prepared x in LDS: the lane's first piece, between its pieces of a step
     const uint32_t xlane = 16u * ((kSplit ? kb : 4 * kb) * M + m), xnext = (kSplit ? 64u : 16u) * M;
-    const uint32_t xplane = 2u * (uint32_t)(kX == kDirect ? x.ld : prepared_values(M, units));
 
     constexpr int kS = b == 8 ? 2 : 4;  // steps of a set of registers
     uint32_t wa[kS][b], wb[kS][b];
@@ -442,42 +447,51 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
     };
     floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     C codes;
-    StageX<b, P, kX> stage;
-    stage.load(x, w, M);
+    StageX<b, P, kRaw> stage;
     StageGroups<b, T, kMats> groups;
-    groups.mats = mats;
-    groups.row0 = row0;
+#pragma unroll
+    for (int k = 0; k < kMats; ++k) {
+        groups.sb[k] = reinterpret_cast<const char *>(mats[k].scales + row0 * w.groups);
+        groups.zb[k] = reinterpret_cast<const char *>(mats[k].zeros + row0 * w.groups);
+    }
     groups.rows = rows;
     groups.groups = w.groups;
-    groups.count = tiles * kTileRows;
-    auto phase = [&](int q0, auto first) {
-        const int nq = std::min(w.phase, quads - q0);
+    for (int q0 = 0; q0 < quads; q0 += phase_quads) {
+        const int nq = std::min(phase_quads, quads - q0);
         const int qs = q0 + (slice * nq >> lg), qe = q0 + ((slice + 1) * nq >> lg);
+        const int hs = qs * 4 / kS, he = qe * 4 / kS;
         // the phase's groups: of its first and last column
         const int ga = w.by.div(kSplit ? 16 * q0 : 4 * q0);
         const int gb = w.by.div(kSplit ? std::min(16 * (q0 + nq), units) - 1 : std::min(4 * (q0 + nq), few_steps(units)) - 1);
-        if constexpr (!first) __syncthreads();  // the phase before is done with its entries
+        if (q0 > 0) __syncthreads();  // the phase before is done with LDS
         // loads return in order: what the barrier waits for goes before the weights
-        groups.init(ga, gb);
+        stage.init(M, units, q0, nq);
+        stage.load(x, M, units, 0);
+        groups.init(ga, gb, tiles * kTileRows);
         groups.load(0);
-        const int hs = qs * 4 / kS, he = qe * 4 / kS;
         load(wa, hs, he);
-        load(wb, hs + 1, he);
-        if constexpr (first) stage.store(xs, w, M);
+        stage.store(xs, M, 0);
         groups.store(entries, 0);
+        for (int t = 1; t < stage.total; ++t) {
+            stage.load(x, M, units, t);
+            stage.store(xs, M, t);
+        }
         for (int t = groups.kBatch; t < groups.total; t += groups.kBatch) {
             groups.load(t);
             groups.store(entries, t);
         }
+        load(wb, hs + 1, he);
         __syncthreads();
         const uint2 *el = entries + (tile * kTileRows + (lane & 15)) * groups.ld - ga;
+        const char *xb = reinterpret_cast<const char *>(xs);
+        const uint32_t xplane = 1024u * nq * M;
         auto set = [&](uint32_t (*wq)[b], int h) {
 #pragma unroll
             for (int j = 0; j < kS; ++j) {
                 const int step = kS * h + j;
                 if (4 * step >= units) break;  // the last quad's steps past the end
                 V xf[P][4], wf[4];
-                uint32_t at = xlane + 256u * M * step;
+                uint32_t at = xlane + 256u * M * (step - 4 * q0);
                 asm volatile("" : "+v"(at));  // one address a step: an induction variable each would fill the registers
 #pragma unroll
                 for (int p = 0; p < P; ++p)
@@ -526,9 +540,7 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
             set(wb, h + 1);
             load(wb, h + 3, he);
         }
-    };
-    phase(0, std::true_type());
-    for (int q0 = w.phase; q0 < quads; q0 += w.phase) phase(q0, std::false_type());
+    }
     return acc;
 }
 

@@ -25,7 +25,7 @@ struct GemvArgs {
 };
 
 // Gated: the even tiles are the gate's rows, the odd ones up's.
-template <int b, typename T, bool kGated, bool kSplit, FewX kX>
+template <int b, typename T, bool kGated, bool kSplit, bool kRaw>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     constexpr int R = kGated ? 2 : 1, LR = kGated ? 1 : 0;
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvAr
     const int64_t r0 = (int64_t)blockIdx.x * kTileRows << lt, d_out = a.shape.d_out;
     const XRows x = {a.x, a.ldx, false, 0};
     float *sums = reinterpret_cast<float *>(smem);
-    const floatx4 acc = few_product<b, T, 1, R, kSplit, kX>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
+    const floatx4 acc = few_product<b, T, 1, R, kSplit, kRaw>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
                                                             a.M, wave, smem);
     few_share(sums, wave, acc, a.M);
     for (int n = threadIdx.x; n < a.M * kTileRows << lt; n += kFewThreads) {
@@ -58,7 +58,7 @@ __global__ __launch_bounds__(256) void prepare_kernel(const uint16_t *__restrict
     if (k >= few_quads(d_in / kUnit) * kQuad) return;
     uint16_t v = 0;
     if (k < d_in) {
-        int c = kperm ? kperm[k] : k;
+        int c = kperm[k];
         c = c < 0 ? 0 : (c >= d_in ? d_in - 1 : c);
         v = X[m * ldx + c];
     }
@@ -66,21 +66,18 @@ __global__ __launch_bounds__(256) void prepare_kernel(const uint16_t *__restrict
 }
 
 template <int b, typename T, bool kGated, bool kSplit>
-void launch_gemv(const GemvArgs &a, FewX x, hipStream_t s) {
+void launch_gemv(const GemvArgs &a, bool raw, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(a.shape.d_out, kTileRows * ((kFewWaves >> a.shape.lg) / (kGated ? 2 : 1))));
-    const size_t lds = few_lds_bytes(x == kDirect ? 0 : a.M, a.shape.units);
-    switch (x) {
-    case kRaw: gemv_kernel<b, T, kGated, kSplit, kRaw><<<grid, kFewThreads, lds, s>>>(a); break;
-    case kCopied: gemv_kernel<b, T, kGated, kSplit, kCopied><<<grid, kFewThreads, lds, s>>>(a); break;
-    case kDirect: gemv_kernel<b, T, kGated, kSplit, kDirect><<<grid, kFewThreads, lds, s>>>(a); break;
-    }
+    if (raw)
+        gemv_kernel<b, T, kGated, kSplit, true><<<grid, kFewThreads, a.shape.lds, s>>>(a);
+    else
+        gemv_kernel<b, T, kGated, kSplit, false><<<grid, kFewThreads, a.shape.lds, s>>>(a);
 }
 
 template <int b>
 hipError_t launch_gemv_bits(GemvArgs a, gptq_dtype x_dt, const gptq_packed &w, bool gated, void *ws, hipStream_t s) {
-    const bool fits = few_staged(a.M, a.shape.units);
-    const FewX x = !fits ? kDirect : (w.kperm ? kCopied : kRaw);
-    if (x != kRaw) {
+    const bool x = !w.kperm;  // raw
+    if (!x) {
         prepare_kernel<b><<<dim3((unsigned)(few_quads(a.shape.units) * kQuad / 256), (unsigned)a.M), 256, 0, s>>>(
             a.x, a.ldx, (int)w.d_in, w.kperm, static_cast<uint16_t *>(ws));
         const hipError_t e = hipGetLastError();
@@ -108,7 +105,7 @@ FewMat few_mat(const gptq_packed &w) { return {w.packed, w.scales, w.zeros}; }
 
 bool few_split(const gptq_packed &w) { return w.group_size != 0 && w.group_size != w.d_in && w.group_size % kStep != 0; }
 
-FewShape few_shape(const gptq_packed &w, int64_t tiles, int most) {
+FewShape few_shape(const gptq_packed &w, double tiles, int most, int rows, int max_rows) {
     FewShape d;
     const int64_t g = w.group_size > 0 ? w.group_size : w.d_in;
     d.d_out = (int32_t)w.d_out;
@@ -117,39 +114,31 @@ FewShape few_shape(const gptq_packed &w, int64_t tiles, int most) {
     d.units = (int32_t)(w.d_in / kUnit);
     // one group per row: any divisor above the number of steps
     d.by = small_div((uint32_t)(few_split(w) ? g / kUnit : (d.groups == 1 ? d.units + 1 : g / kStep)));
-    d.row_pieces = small_div((uint32_t)(64 * few_quads(d.units)));
-    // As many slices as leave the tiles room on the chip at once, with a quad
-    // each at least; more where a workgroup's rows have more entries than LDS.
+    // As many slices as leave the tiles room on the chip at once, and a phase of a quad each at least.
     const int quads = few_quads(d.units);
     d.lg = 0;
-    while (2 << d.lg <= most &&
-           (((tiles << (d.lg + 1)) <= kFewResident && 2 << d.lg <= quads) || (kFewWaves >> d.lg) * kTileRows * (d.groups | 1) > kEntries))
-        ++d.lg;
-    // quads of a phase: at most ceil(512 quads / g) + 1 groups, an odd number of entries a row
-    const int64_t room = kEntries / ((kFewWaves >> d.lg) * kTileRows);
-    d.phase = quads;
-    if ((d.groups | 1) > room) d.phase = (int32_t)std::max<int64_t>(1, (room - 3) * g / kQuad);
-    return d;
-}
-
-size_t few_lds_bytes(int rows, int units) {
-    size_t values = 0;  // up to kStagedValues, by whole rows
-    while (rows > 0 && !few_staged(rows, units)) --rows;
-    values = (size_t)prepared_values(rows, units);
-    return kSumsBytes + kEntries * sizeof(uint2) + values * 2;
+    while (2 << d.lg <= most && tiles * (2 << d.lg) <= kFewResident && 2 << d.lg <= quads) ++d.lg;
+    for (;; --d.lg) {
+        const int per_wg = (kFewWaves >> d.lg) * kTileRows;  // rows of weights
+        const bool alone = tiles * (1 << d.lg) <= 256 * kFewWaves;
+        d.quad_entries = (int32_t)ceil_div((int64_t)per_wg * kQuad * 8, g);
+        if (d.groups == 1) d.quad_entries = 0;
+        const int64_t all = few_fixed(d.lg) + (int64_t)quads * ((int64_t)max_rows * kQuad * 2 + d.quad_entries);
+        d.lds = (int32_t)std::min<int64_t>(all, alone ? kLdsAlone : kLdsShared);
+        if (d.lg == 0 || few_phase(d, rows) >= 1 << d.lg) return d;
+    }
 }
 
 size_t gemv_ws_bytes(int64_t M, int64_t d_in) { return align_up((size_t)prepared_values(M, (int)(d_in / kUnit)) * 2, 256); }
-bool gemv_needs_ws(int64_t M, const gptq_packed &w) { return w.kperm || !few_staged((int)M, (int)(w.d_in / kUnit)); }
 
 hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,
                     const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws, hipStream_t s) {
     GemvArgs a;
     a.w[0] = few_mat(w);
     a.w[1] = few_mat(up ? *up : w);
-    const int64_t tiles = ceil_div(w.d_out, kTileRows);
-    a.shape = up ? few_shape(w, 2 * tiles, kFewWaves / 2) : few_shape(w, tiles, kFewWaves);
+    const double tiles = (double)ceil_div(w.d_out, kTileRows);
     a.M = (int)M;
+    a.shape = up ? few_shape(w, 2 * tiles, kFewWaves / 2, a.M, a.M) : few_shape(w, tiles, kFewWaves, a.M, a.M);
     a.x = static_cast<const uint16_t *>(X);
     a.ldx = ldx;
     a.bias = bias;

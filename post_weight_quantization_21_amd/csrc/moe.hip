@@ -258,7 +258,7 @@ __global__ __launch_bounds__(256) void prepare_pairs_kernel(const uint16_t *__re
     const Expert &e = lists->expert[blockIdx.y];
     const int k = blockIdx.x * 256 + threadIdx.x, n = e.count;
     if (n == 0) return;
-    int c = k < d ? (kperm ? kperm[(int64_t)e.expert * d + k] : k) : 0;
+    int c = k < d ? kperm[(int64_t)e.expert * d + k] : 0;
     c = c < 0 ? 0 : (c >= d ? d - 1 : c);
     out += prepared_values(e.start, d / kUnit);
     for (int m = 0; m < n; ++m) out[prepared_at<b>(k, n, m)] = k < d ? X[e.token[m] * ldx + c] : 0;
@@ -289,7 +289,7 @@ struct GateUpArgs {
     int64_t h_plane;
 };
 
-template <int b, typename T, bool kSplit, bool kRawX>
+template <int b, typename T, bool kSplit, bool kRaw>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(GateUpArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const Expert &e = a.lists->expert[blockIdx.y];
@@ -299,15 +299,8 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(Gat
     const int lt = 2 - lg;  // log2 of the row tiles
     const int ff = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * ff + r0;
-    floatx4 acc;
-    if constexpr (kRawX) {
-        const XRows x = {a.x, a.ldx, true, token};
-        acc = few_product<b, T, 1, 2, kSplit, kRaw>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
-    } else {
-        const XRows x = {a.x + prepared_values(start, a.shape.units), 0, false, 0};
-        acc = few_staged(count, a.shape.units) ? few_product<b, T, 1, 2, kSplit, kCopied>(a.w, a.shape, row, ff - r0, x, count, wave, smem)
-                                               : few_product<b, T, 1, 2, kSplit, kDirect>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
-    }
+    const XRows x = {kRaw ? a.x : a.x + prepared_values(start, a.shape.units), kRaw ? a.ldx : 0, kRaw, token};
+    const floatx4 acc = few_product<b, T, 1, 2, kSplit, kRaw>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
     __bf16 *h = a.h + prepared_values(start, ff / kUnit);
@@ -349,9 +342,7 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownAr
     const int d = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * d + r0;
     const XRows x = {a.h + prepared_values(start, a.shape.units), a.h_plane, false, 0};
-    const floatx4 acc = few_staged(P * count, a.shape.units)
-                            ? few_product<b, __bf16, P, 1, kSplit, kCopied>(&a.w, a.shape, row, d - r0, x, count, wave, smem)
-                            : few_product<b, __bf16, P, 1, kSplit, kDirect>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
+    const floatx4 acc = few_product<b, __bf16, P, 1, kSplit, false>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
     for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
@@ -410,18 +401,18 @@ struct MoeCall {
 };
 
 template <int b, typename T, bool kSplit>
-void launch_gate_up(const GateUpArgs &g, bool raw, dim3 grid, size_t lds, hipStream_t s) {
+void launch_gate_up(const GateUpArgs &g, bool raw, dim3 grid, hipStream_t s) {
     if (raw)
-        gate_up_kernel<b, T, kSplit, true><<<grid, kFewThreads, lds, s>>>(g);
+        gate_up_kernel<b, T, kSplit, true><<<grid, kFewThreads, g.shape.lds, s>>>(g);
     else
-        gate_up_kernel<b, T, kSplit, false><<<grid, kFewThreads, lds, s>>>(g);
+        gate_up_kernel<b, T, kSplit, false><<<grid, kFewThreads, g.shape.lds, s>>>(g);
 }
 template <int b, bool kSplit>
-void launch_down(const DownArgs &w, int planes, dim3 grid, size_t lds, hipStream_t s) {
+void launch_down(const DownArgs &w, int planes, dim3 grid, hipStream_t s) {
     if (planes == 3)
-        down_kernel<b, 3, kSplit><<<grid, kFewThreads, lds, s>>>(w);
+        down_kernel<b, 3, kSplit><<<grid, kFewThreads, w.shape.lds, s>>>(w);
     else
-        down_kernel<b, 2, kSplit><<<grid, kFewThreads, lds, s>>>(w);
+        down_kernel<b, 2, kSplit><<<grid, kFewThreads, w.shape.lds, s>>>(w);
 }
 
 template <int b, typename T>
@@ -431,18 +422,19 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     const unsigned slots = (unsigned)std::min<int64_t>(c.n_experts, pairs);
     // experts that `pairs` independent choices would hit, which the work is spread for
     const double busy = c.n_experts * (1.0 - std::pow(1.0 - 1.0 / c.n_experts, (double)pairs));
+    const int rows = (int)std::ceil(pairs / busy);  // tokens of an expert
     GateUpArgs g;
     const int64_t pair_tiles = ceil_div(ff, kTileRows);
     g.w[0] = few_mat(*c.gate);
     g.w[1] = few_mat(*c.up);
-    g.shape = few_shape(*c.gate, (int64_t)(2 * busy * pair_tiles), kFewWaves / 2);
+    g.shape = few_shape(*c.gate, 2 * busy * pair_tiles, kFewWaves / 2, rows, (int)c.T);
     g.x = static_cast<const uint16_t *>(c.X);
     g.ldx = c.ldx;
     g.lists = lists;
     g.h = reinterpret_cast<__bf16 *>(c.ws + l.h);
     g.h_plane = prepared_values(pairs, (int)(ff / kUnit));
     g.planes = c.y_dt == GPTQ_DT_F32 ? 3 : 2;
-    const bool raw = !c.gate->kperm && few_staged((int)c.T, g.shape.units);
+    const bool raw = !c.gate->kperm;
     if (!raw) {
         uint16_t *xg = reinterpret_cast<uint16_t *>(c.ws + l.xg);
         prepare_pairs_kernel<b><<<dim3((unsigned)(few_quads(g.shape.units) * kQuad / 256), slots), 256, 0, s>>>(g.x, c.ldx, (int)d, lists,
@@ -450,15 +442,14 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
         g.x = xg;
     }
     const dim3 grid((unsigned)ceil_div(pair_tiles, (kFewWaves >> g.shape.lg) / 2), slots);
-    const size_t lds = few_lds_bytes((int)c.T, g.shape.units);
     if (few_split(*c.gate))
-        launch_gate_up<b, T, true>(g, raw, grid, lds, s);
+        launch_gate_up<b, T, true>(g, raw, grid, s);
     else
-        launch_gate_up<b, T, false>(g, raw, grid, lds, s);
+        launch_gate_up<b, T, false>(g, raw, grid, s);
     DownArgs w;
     const int64_t tiles = ceil_div(d, kTileRows);
     w.w = few_mat(*c.down);
-    w.shape = few_shape(*c.down, (int64_t)(busy * tiles), kFewWaves);
+    w.shape = few_shape(*c.down, busy * tiles, kFewWaves, g.planes * rows, g.planes * (int)c.T);
     w.h = reinterpret_cast<const uint16_t *>(g.h);
     w.h_plane = g.h_plane;
     w.lists = lists;
@@ -470,11 +461,10 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
         w.h = hg;
     }
     const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves >> w.shape.lg), slots);
-    const size_t dlds = few_lds_bytes(g.planes * (int)c.T, w.shape.units);
     if (few_split(*c.down))
-        launch_down<b, true>(w, g.planes, dgrid, dlds, s);
+        launch_down<b, true>(w, g.planes, dgrid, s);
     else
-        launch_down<b, false>(w, g.planes, dgrid, dlds, s);
+        launch_down<b, false>(w, g.planes, dgrid, s);
     combine_kernel<<<dim3((unsigned)ceil_div(d, 256), (unsigned)c.T), 256, 0, s>>>(w.part, lists, (int)d, c.Y, c.ldy, c.y_dt);
 }
 
