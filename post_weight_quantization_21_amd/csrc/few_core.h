@@ -287,10 +287,10 @@ struct XRows {
     int32_t row;
 };
 
-// A phase's x on its way into LDS, in batches of two units a thread.
+// A phase's x on its way into LDS, in batches of kUnits units a thread.
 template <int b, int P, bool kRaw>
 struct StageX {
-    static constexpr int kUnits = 2;
+    static constexpr int kUnits = 1;
     u32x4 v[4 * kUnits];
     uint32_t magic;  // raw: of the division by the units of a row
     int per_row, items, first, total;
