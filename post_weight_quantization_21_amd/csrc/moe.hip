@@ -111,20 +111,41 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
 }
 
+// exp(a - b) in fp32, the difference's rounding put back to first order.
+__device__ __forceinline__ float exp_diff(double a, double b) {
+    const double d = a - b;
+    const float hi = (float)d, e = expf(hi);
+    return d > -100.0 ? fmaf(e, (float)(d - hi), e) : e;  // (also an infinite difference)
+}
+template <int ctrl, int rows>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false));
+}
+__device__ __forceinline__ float wave_sum_f(float v) {  // as wave_max
+    v = dpp_add<0x111, 0xf>(v);
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);
+    v = dpp_add<0x143, 0xc>(v);
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// kPer: logits of a lane, n_experts <= 64 kPer.
+template <int kPer>
 __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__ logits, int n_tok, int n_experts,
                                                       int top_k, int renormalize, int slots, int32_t *ids, float *weights,
                                                       Lists *lists) {
-    __shared__ int32_t sel[kMoeMaxTokens][kMoeMaxTopK];
-    __shared__ float wsel[kMoeMaxTokens][kMoeMaxTopK];
+    __shared__ float weight_in[kMoeMaxTokens][kMoeMaxExperts];  // of a token's chosen experts
     __shared__ uint32_t tokens_of[kMoeMaxExperts];  // bit t: token t chose the expert
     __shared__ uint32_t wave_sum[kMoeMaxExperts / kWave];
     __shared__ uint8_t token_of[kMaxPairs];
     __shared__ float weight_of[kMaxPairs];
     const int tid = threadIdx.x, wave = few_wave(), lane = tid % kWave;
-    constexpr int kPer = kMoeMaxExperts / kWave;
     if (tid < kMoeMaxExperts) tokens_of[tid] = 0;
+    int e = -1;  // lane j < top_k: the token's j-th choice
+    bool chosen = false;
     if (wave < n_tok) {
-        int e = -1;
         float w = 0.0f;
         if (!logits) {
             if (lane < top_k) {
@@ -137,64 +158,52 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const int c = lane + kWave * i;
-                v[i] = 0.0;
-                key[i] = 0;
-                if (kWave * i < n_experts && c < n_experts) {
-                    v[i] = logits[(int64_t)wave * n_experts + c];
-                    key[i] = rank_key(v[i], c);
-                }
+                v[i] = c < n_experts ? logits[(int64_t)wave * n_experts + c] : -INFINITY;
+                key[i] = c < n_experts ? rank_key(v[i], c) : 0;
             }
-            uint64_t any_nan = 0;
-            double top = -INFINITY;
             for (int j = 0; j < top_k; ++j) {
                 uint64_t best = key[0];
 #pragma unroll
-                for (int i = 1; i < kPer; ++i)
-                    if (kWave * i < n_experts) best = key[i] > best ? key[i] : best;
+                for (int i = 1; i < kPer; ++i) best = key[i] > best ? key[i] : best;
                 best = wave_max(best);
-                const int be = 511 - (int)(best & 511);
-                if (lane == j) e = be;
+                if (lane == j) e = 511 - (int)(best & 511);
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    if (key[i] == best) key[i] = 0;
+                for (int i = 0; i < kPer; ++i) key[i] = key[i] == best ? 0 : key[i];
             }
             // softmax: the first choice holds the largest logit
-            const int e0 = __builtin_amdgcn_readfirstlane(e);
+            uint64_t any_nan = 0;
+            double mine = 0.0;  // lane j < top_k: its chosen logit
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (kWave * i < n_experts) {
-                    if (e0 >> 6 == i) top = __shfl(v[i], e0 & 63);
-                    any_nan |= __ballot(v[i] != v[i]);
-                }
-            double sum = 0.0, mine = 0.0;  // lane j < top_k: its chosen logit
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (kWave * i < n_experts) {
-                    if (lane + kWave * i < n_experts) sum += exp(v[i] - top);
-                    const double c = __shfl(v[i], e & 63);
-                    if (e >> 6 == i) mine = c;
-                }
-            for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
-            if (any_nan) sum = NAN;  // as the sum over the softmax would be
-            double p = lane < top_k ? exp(mine - top) / sum : 0.0, chosen = p;
-            if (renormalize) {
-                for (int o = kMoeMaxTopK / 2; o > 0; o >>= 1) chosen += __shfl_xor(chosen, o);
-                p /= chosen;
+            for (int i = 0; i < kPer; ++i) {
+                const double c = __shfl(v[i], e & 63);
+                if (e >> 6 == i) mine = c;
+                any_nan |= __ballot(v[i] != v[i]);
             }
-            w = (float)p;
+            const double top = __shfl(mine, 0);
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + kWave * i < n_experts) sum += exp_diff(v[i], top);
+            sum = wave_sum_f(sum);
+            const float p = lane < top_k ? exp_diff(mine, top) : 0.0f;
+            w = p / (renormalize ? wave_sum_f(p) : sum);
+            if (any_nan) w = NAN;  // as the softmax's sum is
         }
-        if (lane < top_k) {
-            sel[wave][lane] = e;
-            wsel[wave][lane] = w;
+        float total_w = 0.0f;  // a caller may name an expert twice
+        for (int j = 0; j < top_k; ++j) {
+            const int ej = __builtin_amdgcn_readlane(e, j);
+            const float wj = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(w), j));
+            total_w += ej == e ? wj : 0.0f;
+        }
+        chosen = lane < top_k && (unsigned)e < (unsigned)n_experts;
+        if (chosen) weight_in[wave][e] = total_w;
+        if (logits && lane < top_k) {
+            if (ids) ids[wave * top_k + lane] = e;
+            if (weights) weights[wave * top_k + lane] = w;
         }
     }
     __syncthreads();
-    if (wave < n_tok && lane < top_k) {
-        const int e = sel[wave][lane];
-        if ((unsigned)e < (unsigned)n_experts) atomicOr(&tokens_of[e], 1u << wave);
-        if (logits && ids) ids[wave * top_k + lane] = e;
-        if (logits && weights) weights[wave * top_k + lane] = wsel[wave][lane];
-    }
+    if (chosen) atomicOr(&tokens_of[e], 1u << wave);
     __syncthreads();
     // positions by a prefix sum over the experts: chosen experts in the high half, pairs in the low one
     const uint32_t mask = tid < kMoeMaxExperts ? tokens_of[tid] : 0;
@@ -221,12 +230,9 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
         x.count = __popc(mask);
         for (uint32_t m = mask; m; m &= m - 1, ++p, ++n) {
             const int t = __ffs(m) - 1;
-            float w = 0.0f;
-            for (int j = 0; j < top_k; ++j)
-                if (sel[t][j] == tid) w += wsel[t][j];
             x.token[n] = t;
             token_of[p] = (uint8_t)t;
-            weight_of[p] = w;
+            weight_of[p] = weight_in[t][tid];
         }
     }
     if (tid >= (int)(total >> 16) && tid < slots) lists->expert[tid].count = 0;
@@ -480,9 +486,9 @@ void launch_moe(const MoeCall &c, const Layout &l, hipStream_t s) {
         else
             router_kernel<T, T><<<grid, 256, 0, s>>>(x, c.ldx, (int)c.T, static_cast<const T *>(c.router), d, c.n_experts, logits);
     }
-    choose_kernel<<<1, 1024, 0, s>>>(logits, (int)c.T, c.n_experts, c.top_k, c.renormalize,
-                                     (int)std::min<int64_t>(c.n_experts, c.T * c.top_k), c.ids, c.weights,
-                                     reinterpret_cast<Lists *>(c.ws + l.lists));
+    auto choose = c.n_experts <= 64 ? choose_kernel<1> : (c.n_experts <= 128 ? choose_kernel<2> : (c.n_experts <= 256 ? choose_kernel<4> : choose_kernel<8>));
+    choose<<<1, 1024, 0, s>>>(logits, (int)c.T, c.n_experts, c.top_k, c.renormalize, (int)std::min<int64_t>(c.n_experts, c.T * c.top_k),
+                              c.ids, c.weights, reinterpret_cast<Lists *>(c.ws + l.lists));
     switch (c.gate->bits) {
     case 2: return launch_experts<2, T>(c, l, s);
     case 3: return launch_experts<3, T>(c, l, s);

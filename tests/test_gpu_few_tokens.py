@@ -196,7 +196,9 @@ def test_moe_layer(oracle_mod, T, d, ff, E, k, bits, group, dt, out, perm, renor
     Y2, _, _ = gq.moe_layer(X, *dw, ids=gi, weights=gw, out_dtype=_dt(out))
     torch.cuda.synchronize()
     assert np.array_equal(host(gi), ids)
-    assert (np.abs(host(gw) - weights) <= 2.0 ** -24 * 1.01 * weights + 1e-30).all()
+    # fp32 softmax of fp64 logits: numerator and terms within 2 ulp of exp and 1 of its correction, at most 14
+    # additions of positive terms in the sum, 4 more of chosen ones when renormalized, one division: below 32 u
+    assert (np.abs(host(gw) - weights) <= 32 * fr.U * weights + 1e-30).all()
     want, bound = fr.moe(x, *hw, ids, weights, out)
     _check(Y, want, bound, "moe")
     assert torch.equal(Y, Y2)  # the same routing handed in gives the same bits
