@@ -65,6 +65,12 @@ GEMV = [
     (1, 128, 11008, 4, 128, "bf16", "bf16", False, False),  # 86 groups
     (8, 64, 8192, 4, 64, "fp16", "fp16", True, False),
     (1, 40, 28672, 4, 32, "bf16", "fp32", False, False),   # 896 groups per row
+    (16, 4300, 8192, 4, 128, "bf16", "fp32", False, False),  # several phases, two workgroups to a compute unit
+    (16, 70, 8192, 3, 0, "fp16", "fp32", False, False),    # several phases, one workgroup
+    (9, 33, 20480, 4, 32, "fp16", "bf16", True, False),    # ... of prepared activations and many groups
+    (1, 20, 98336, 2, 32, "bf16", "fp32", False, False),   # a row too long for one phase; its last quad holds a unit
+    (2, 5000, 544, 8, 32, "fp16", "fp16", False, False),  # two quads, the second of one unit
+    (1, 70000, 64, 4, 64, "bf16", "bf16", False, True),    # many rows
 ]
 
 
@@ -180,6 +186,8 @@ MOE = [
     (4, 512, 384, 6, 2, 2, 128, "bf16", "bf16", False, True, "bf16"),
     (2, 64, 48 * 32, 3, 2, 4, 32, "bf16", "fp32", False, True, "bf16"),  # long second product
     (9, 64, 64, 512, 16, 4, 64, "fp16", "fp32", False, False, "fp32"),   # the most experts
+    (16, 4096, 96, 3, 2, 4, 32, "bf16", "bf16", False, True, "fp32"),    # phases of the first products
+    (16, 64, 5120, 3, 2, 4, 64, "fp16", "fp32", True, True, "fp16"),    # ... and of the second, in three pieces
 ]
 
 
@@ -338,3 +346,62 @@ def test_few_tokens_serve_the_pass_output(oracle_mod):
     both = [dict(w, **{k: np.stack([w[k], w[k]]) for k in ("q", "scales", "zeros", "kperm")}) for w in host_w]
     y, dy = fr.moe(x, *both, np.tile(np.arange(2), (M, 1)), np.full((M, 2), 0.5), "fp32")
     _check(Ym, y, dy, "the same as two equal experts")
+
+
+def test_few_tokens_two_calls_at_once(oracle_mod):
+    """Calls on two streams that overlap, each with a workspace of its own, give what they give alone."""
+    torch = torch_mod()
+    rng = np.random.default_rng(13)
+    E, d, ff = 16, 512, 384
+    _, dw = _experts(rng, oracle_mod, E, d, ff, 4, 32, True)
+    R = cuda(rng.standard_normal((E, d)).astype(np.float32))
+    xs = [_acts(rng, t, d, "bf16")[0] for t in (3, 16)]
+    alone = [gq.moe_layer(x, *dw, router=R, top_k=4) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(gq.moe_layer(xs[i], *dw, router=R, top_k=4))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(r, alone[i]))
+
+
+def test_few_tokens_python_checks(oracle_mod):
+    torch = torch_mod()
+    rng = np.random.default_rng(14)
+    w = fr.make_packed(rng, oracle_mod, 24, 64, 4, 32)
+    p, sc, ze = cuda(w["packed"].view(np.int32)), cuda(w["scales"]), cuda(w["zeros"])
+    dw = gq.packed_weight(p, sc, ze, 4, 32)
+    assert (dw.d_out, dw.d_in, dw.stack) == (24, 64, None)
+    for bad in (lambda: gq.packed_weight(p, sc, ze, 4, 48), lambda: gq.packed_weight(p, sc, ze, 5, 32),
+                lambda: gq.packed_weight(p, sc[:, :1].contiguous(), ze, 4, 32), lambda: gq.packed_weight(p, sc, ze, 3, 32),
+                lambda: gq.packed_weight(p, sc, ze, 4, 32, kperm=torch.zeros(63, dtype=torch.int32, device="cuda"))):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        gq.packed_weight(p, sc.double(), ze, 4, 32)
+    X = torch.zeros(2, 64, dtype=torch.float16, device="cuda")
+    for bad in (lambda: gq.gemv(X.float(), dw), lambda: gq.gemv(X, dw, Y=torch.empty(2, 24, dtype=torch.float64, device="cuda")),
+                lambda: gq.gemv(X, dw, Y=torch.empty(2, 24, device="cuda"), out_dtype=torch.float16)):
+        with pytest.raises(TypeError):
+            bad()
+    stack = gq.packed_weight(p[None], sc[None], ze[None], 4, 32)
+    for bad in (lambda: gq.gemv(X.cpu(), dw), lambda: gq.gemv(X[:, :32], dw), lambda: gq.gemv(X, stack),
+                lambda: gq.gemv(X, dw, Y=torch.empty(2, 23, dtype=torch.float16, device="cuda")),
+                lambda: gq.gemv(X, dw, bias=torch.zeros(24, dtype=torch.float16, device="cuda")),
+                lambda: gq.gemv_gated(X, dw, stack), lambda: gq.moe_layer(X, dw, dw, dw, router=X, top_k=1),
+                lambda: gq.moe_layer(X, stack, stack, stack), lambda: gq.moe_layer(X, stack, stack, stack, router=X[:1]),
+                lambda: gq.moe_layer(X, stack, stack, stack, router=X[:1], top_k=2)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(gq.GptqError) as ei:  # 17 tokens
+        gq.gemv(torch.zeros(17, 64, dtype=torch.float16, device="cuda"), dw)
+    assert ei.value.status == gq.ERR_UNSUPPORTED
+    odd = torch.zeros(2 * 64 + 1, dtype=torch.float16, device="cuda")[1:].view(2, 64)
+    with pytest.raises(gq.GptqError) as ei:  # not 16-byte aligned
+        gq.gemv(odd, dw)
+    assert ei.value.status == gq.ERR_INVALID_ARG
