@@ -248,8 +248,9 @@ __device__ __forceinline__ void transpose_frags(V f[4]) {
     }
 }
 
-// A unit's words through a buffer descriptor: an offset past the descriptor's
-// size reads nothing and gives zeros.
+// A unit's words through a buffer descriptor: `at` not below the descriptor's
+// size reads nothing and gives zeros, whether or not the hardware counts the
+// scalar offset `base` in, as long as base alone is no more than that size.
 template <int b>
 __device__ __forceinline__ void load_unit(__amdgpu_buffer_rsrc_t p, uint32_t at, uint32_t base, uint32_t *w) {
     if constexpr (b == 2) {
@@ -442,7 +443,7 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
 #pragma unroll
         for (int j = 0; j < kS; ++j) {
             const int u = 4 * (kS * set + j) + kb;
-            load_unit<b>(wr, set < end && u < units ? wo : bytes, 16u * b * (kS * set + j), dst[j]);
+            load_unit<b>(wr, set < end && u < units ? wo : bytes, std::min(16u * b * (kS * set + j), bytes), dst[j]);
         }
     };
     floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};

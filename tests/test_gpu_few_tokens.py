@@ -71,6 +71,8 @@ GEMV = [
     (1, 20, 98336, 2, 32, "bf16", "fp32", False, False),   # a row too long for one phase; its last quad holds a unit
     (2, 5000, 544, 8, 32, "fp16", "fp16", False, False),  # two quads, the second of one unit
     (1, 70000, 64, 4, 64, "bf16", "bf16", False, True),    # many rows
+    (1, 1, 32, 2, 32, "fp16", "fp32", False, False),       # one row, whose sets of steps reach past its end
+    (3, 129, 608, 8, 32, "bf16", "fp32", False, False),    # ... as the last tile's only row
 ]
 
 
