@@ -405,7 +405,7 @@ typedef struct {
     const float *scales;
     const float *zeros;   /* integers in 0 .. 2^bits - 1, as the quantizer stores them */
     const int32_t *kperm; /* the perm the codes were packed with, or NULL */
-    int64_t d_out, d_in;  /* d_in a multiple of 32, at most 2^20; d_out at most 2^30 */
+    int64_t d_out, d_in;  /* d_in a multiple of 32, at most 2^20; d_out at most 2^28 */
     int32_t bits;         /* 2, 3, 4 or 8 */
     int32_t group_size;   /* a multiple of 32 that divides d_in, or 0 */
 } gptq_packed;

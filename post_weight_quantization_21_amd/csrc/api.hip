@@ -71,8 +71,8 @@ gptq_status check_packed(const gptq_packed *w, const char *fn, const char *name)
         return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: bits must be 2, 3, 4 or 8", fn, name);
     if (w->d_in % 32 != 0 || w->group_size % 32 != 0)
         return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: d_in and group_size must be multiples of 32", fn, name);
-    if (w->d_in > ((int64_t)1 << 20) || w->d_out > ((int64_t)1 << 30))
-        return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: d_in above 2^20 or d_out above 2^30", fn, name);
+    if (w->d_in > ((int64_t)1 << 20) || w->d_out > ((int64_t)1 << 28))  // 2^28 rows: 2^31 threads of one launch
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: %s: d_in above 2^20 or d_out above 2^28", fn, name);
     if (!w->packed || !w->scales || !w->zeros) return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: NULL pointer", fn, name);
     if (!aligned(w->packed) || !aligned(w->scales, 4) || !aligned(w->zeros, 4) || (w->kperm && !aligned(w->kperm, 4)))
         return fail(GPTQ_ERR_INVALID_ARG, "%s: %s: packed must be 16-byte aligned, the other pointers 4-byte aligned", fn, name);

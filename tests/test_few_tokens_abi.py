@@ -45,7 +45,7 @@ def message():
     (packed(group=16), gq.ERR_UNSUPPORTED, b"multiples of 32"),
     (packed(d_in=48, group=0), gq.ERR_UNSUPPORTED, b"multiples of 32"),
     (packed(d_in=(1 << 20) + 32, group=32), gq.ERR_UNSUPPORTED, b"2^20"),
-    (packed(d_out=(1 << 30) + 1), gq.ERR_UNSUPPORTED, b"2^30"),
+    (packed(d_out=(1 << 28) + 1), gq.ERR_UNSUPPORTED, b"2^28"),
     (packed(at=None), gq.ERR_INVALID_ARG, b"NULL"),
     (packed(scales=None), gq.ERR_INVALID_ARG, b"NULL"),
     (packed(zeros=None), gq.ERR_INVALID_ARG, b"NULL"),
