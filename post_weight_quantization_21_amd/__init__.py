@@ -465,14 +465,17 @@ def _few_result(X, Y, rows, d_out, out_dtype, device, torch, dtypes):
     return Y, dt
 
 
-def _few_launch(fn, device, stream, torch, *args):
-    """fn(*args, stream) with the weights' device current, on `stream` or that device's current stream."""
-    if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(device.index)
-    elif stream.device != device:
+def _few_on(stream, device, torch):
+    """`stream` as the current stream: the call's result and workspace then come from, and go back to, the memory that
+    this stream orders.  (From the caller's, either could still be in use there, or be handed out again too early.)"""
+    if stream.device != device:
         raise ValueError("the stream must be on the weights' device")
-    else:
-        raw = stream.cuda_stream
+    return torch.cuda.stream(stream)
+
+
+def _few_launch(fn, device, torch, *args):
+    """fn(*args, stream) with the weights' device current, on that device's current stream."""
+    raw = torch._C._cuda_getCurrentRawStream(device.index)
     if torch.cuda.current_device() == device.index:
         status = fn(*args, raw)
     else:
@@ -507,6 +510,9 @@ def gemv(X, w: PackedWeight, bias=None, Y=None, out_dtype=None, ws=None, stream=
     """Y = X' W_hat^T (+ bias) for at most 16 tokens: X fp16 or bf16 [M][d_in], w a packed layer of 2, 3, 4 or 8 bits,
     bias fp32 [d_out]; Y [M][d_out] in X's type, or in out_dtype (fp16, bf16, fp32)."""
     torch, lib, act, res = _few_init()
+    if stream is not None:
+        with _few_on(stream, w.device, torch):
+            return gemv(X, w, bias, Y, out_dtype, ws)
     if w.stack is not None:
         raise ValueError("gemv takes a single layer, not a stack")
     dev, d_in, d_out, M = w.device, w.d_in, w.d_out, X.shape[0]
@@ -516,7 +522,7 @@ def gemv(X, w: PackedWeight, bias=None, Y=None, out_dtype=None, ws=None, stream=
                              or not bias.is_contiguous()):
         raise ValueError(f"bias must be a contiguous float32 [{d_out}] on the weights' device")
     wp, wn = _gemv_ws(ws, w, M, dev)
-    _few_launch(lib.gptq_gemv, dev, stream, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), w.ref,
+    _few_launch(lib.gptq_gemv, dev, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), w.ref,
                 None if bias is None else bias.data_ptr(), Y.data_ptr(), yd, _pitch(Y, M, d_out), wp, wn)
     return Y
 
@@ -525,6 +531,9 @@ def gemv_gated(X, gate: PackedWeight, up: PackedWeight, H=None, out_dtype=None, 
     """H = silu(X' W_gate^T) * (X' W_up^T), the first half of a gated MLP, for at most 16 tokens; types as in gemv.
     gate and up share one column order (the same kperm tensor), as they share their inputs."""
     torch, lib, act, res = _few_init()
+    if stream is not None:
+        with _few_on(stream, gate.device, torch):
+            return gemv_gated(X, gate, up, H, out_dtype, ws)
     if gate.stack is not None or up.stack is not None:
         raise ValueError("gemv_gated takes single layers, not stacks")
     dev, d_in, d_ff, M = gate.device, gate.d_in, gate.d_out, X.shape[0]
@@ -533,7 +542,7 @@ def gemv_gated(X, gate: PackedWeight, up: PackedWeight, H=None, out_dtype=None, 
     xd = _few_check_x(X, d_in, dev, act)
     H, hd = _few_result(X, H, M, d_ff, out_dtype, dev, torch, res)
     wp, wn = _gemv_ws(ws, gate, M, dev)
-    _few_launch(lib.gptq_gemv_gated, dev, stream, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), gate.ref, up.ref,
+    _few_launch(lib.gptq_gemv_gated, dev, torch, X.data_ptr(), xd, M, _pitch(X, M, d_in), gate.ref, up.ref,
                 H.data_ptr(), hd, _pitch(H, M, d_ff), wp, wn)
     return H
 
@@ -550,6 +559,9 @@ def moe_layer(X, gate: PackedWeight, up: PackedWeight, down: PackedWeight, route
     X fp16 or bf16 [T][d].  With a router ([E][d], fp32 or X's type) it chooses top_k experts per token; without one,
     ids (int32 [T][top_k]) and weights (fp32 [T][top_k]) are the caller's routing.  Returns (Y, ids, weights)."""
     torch, lib, act, res = _few_init()
+    if stream is not None:
+        with _few_on(stream, gate.device, torch):
+            return moe_layer(X, gate, up, down, router, top_k, renormalize, ids, weights, Y, out_dtype, ws)
     E, dev, d, T = gate.stack, gate.device, gate.d_in, X.shape[0]
     if E is None or up.stack != E or down.stack != E:
         raise ValueError("gate, up and down must be stacks of the same number of experts")
@@ -562,7 +574,7 @@ def moe_layer(X, gate: PackedWeight, up: PackedWeight, down: PackedWeight, route
         if ids is None or weights is None:
             raise ValueError("without a router, ids and weights are needed")
         if top_k is None:
-            top_k = ids.shape[1]
+            top_k = ids.shape[-1] if ids.dim() else 0
     else:
         if top_k is None:
             raise ValueError("a router needs top_k")
@@ -586,7 +598,7 @@ def moe_layer(X, gate: PackedWeight, up: PackedWeight, down: PackedWeight, route
     if ws is None:
         ws = _workspace(moe_workspace_bytes(T, d, gate.d_out, E, top_k), dev)
     wp, wn = _few_ws(ws, dev)
-    _few_launch(lib.gptq_moe_layer, dev, stream, torch, X.data_ptr(), xd, T, _pitch(X, T, d), rp, rd, E, top_k,
+    _few_launch(lib.gptq_moe_layer, dev, torch, X.data_ptr(), xd, T, _pitch(X, T, d), rp, rd, E, top_k,
                 1 if renormalize else 0, gate.ref, up.ref, down.ref, ids.data_ptr(), weights.data_ptr(), Y.data_ptr(), yd,
                 _pitch(Y, T, d), wp, wn)
     return Y, ids, weights

@@ -1,12 +1,14 @@
 """The few-token products in fp64, with the error bounds their GPU tests use.
 
 Bounds.  A sum of n fp32 terms accumulated in any order is off by at most
-n u sum|terms| (u = 2^-24, one rounding per addition; products of a 16-bit
-float and a small integer are exact in fp32).  bf16 activations with 2-4 bits
-sum (2^b + q) x and -(2^b + z) x as separate terms, so the terms are larger
-than (q - z) x; the scale multiplies a group's sum (one rounding each, counted
-with the groups).  The result is rounded once to its type: half an ulp, or half
-the smallest subnormal.
+n u sum|terms| (u = 2^-24, one rounding per addition; 2u where the matrix cores'
+own additions may cut off instead; products of a 16-bit float and a small
+integer are exact in fp32).  The kernels sum at most 128 columns before the
+scale multiplies the sum: 4 matrix instructions of 33 additions per plane of x,
+and as many again for bf16 activations with 2-4 bits, which sum (2^b + q) x and
+-(2^b + z) x as separate terms, larger than (q - z) x.  The scaled sums, one per
+32 columns or more, are then added, and the sums of eight waves.  The result is
+rounded once to its type: half an ulp, or half the smallest subnormal.
 """
 from __future__ import annotations
 
@@ -49,10 +51,11 @@ def product(x, w, e=None, dx=None, planes=1):
         x = x[:, order]
         dx = None if dx is None else dx[:, order]
     W, A = matrix(w, e)
-    n = 2 * planes * x.shape[1] + 2 * w["scales"].shape[-1] + 32  # both terms of a code, a group's scale, the waves' sums
-    bound = n * U * (np.abs(x) @ A.T)
+    per_fold = 2 * 2 * planes * min(4, x.shape[1] // 32) * 33 * U * 1.01  # (the planes of x add up to a little more than |x|)
+    folds = (x.shape[1] // 32 + 16) * U
+    bound = np.abs(x) @ (per_fold * A + folds * np.abs(W)).T
     if dx is not None:
-        bound = bound + dx @ (np.abs(W) + n * U * A).T
+        bound = bound + dx @ (np.abs(W) * (1 + folds) + per_fold * A).T
     return x @ W.T, bound
 
 

@@ -97,6 +97,22 @@ def test_gemv(oracle_mod, M, d_out, d_in, bits, group, dt, out, perm, bias):
     assert torch.equal(Y, Y2)  # the same bits again
 
 
+@pytest.mark.parametrize("M,d_out,d_in,bits,group,dt,out,perm,bias", GEMV)
+def test_gemv_integers(oracle_mod, M, d_out, d_in, bits, group, dt, out, perm, bias):
+    """Small integers and scales of 1/2, 1 and 2: every sum is exact in fp32, so every term counts once, to the bit."""
+    log(f"gemv of integers M={M} {d_out}x{d_in} {bits} bits g={group} {dt} perm={perm}")
+    rng = np.random.default_rng(M * 999 + d_in + bits)
+    w = fr.make_packed(rng, oracle_mod, d_out, d_in, bits, group, perm)
+    w["scales"] = rng.choice(np.array([0.5, 1.0, 2.0], dtype=np.float32), size=w["scales"].shape)
+    top = 2 if bits == 8 else 4
+    x = rng.integers(-top, top + 1, size=(M, d_in)).astype(np.float64)
+    X = cuda(x.astype(np.float32)).to(_dt(dt))
+    want = fr.product(x, w)[0]
+    assert (np.abs(x) @ np.abs(fr.matrix(w)[1]).T).max() < 2 ** 23  # in steps of a half: below 2^24 of them
+    Y = host(gq.gemv(X, _dev(w), out_dtype=_dt("fp32"))).astype(np.float64)
+    assert np.array_equal(Y, want)
+
+
 @pytest.mark.parametrize("M,d_out,d_in,bits,group,dt,out,perm", [
     (1, 16, 128, 4, 128, "bf16", "bf16", False),
     (3, 35, 160, 4, 32, "fp16", "fp32", True),
@@ -370,6 +386,78 @@ def test_few_tokens_two_calls_at_once(oracle_mod):
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, alone[i]))
+
+
+def test_few_tokens_memory_of_another_stream(oracle_mod):
+    """A call on a stream that is busy: its result and workspace must not be the caller's memory, which the caller's
+    own stream fills meanwhile."""
+    torch = torch_mod()
+    rng = np.random.default_rng(15)
+    d, M = 512, 5
+    w = _dev(fr.make_packed(rng, oracle_mod, d, d, 4, 64, True))  # a column order: the call needs a workspace
+    x = _acts(rng, M, d, "bf16")[0]
+    want, want_h = gq.gemv(x, w), gq.gemv_gated(x, w, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for call, expect in ((lambda: gq.gemv(x, w, stream=side), want), (lambda: gq.gemv_gated(x, w, w, stream=side), want_h)):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        y = call()
+        junk = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda")
+                for n in 8 * [gq.workspace_bytes(gq.OP_GEMV, d, d, M)] + 8 * [M * d * 2]]
+        torch.cuda.synchronize()
+        assert torch.equal(y, expect) and all(bool((j == 0x55).all()) for j in junk)
+
+
+def _random_stack(gen, n, d_out, d_in, bits, g):
+    """A packed stack of random codes made on the device, its scales about those of unit rows."""
+    torch = torch_mod()
+    words = torch.randint(-2**31, 2**31 - 1, (n, d_out, d_in * bits // 32), dtype=torch.int32, device="cuda", generator=gen)
+    scales = torch.rand((n, d_out, d_in // g), device="cuda", generator=gen).add_(0.2).mul_(2.0 * d_in ** -0.5 / 2 ** bits)
+    zeros = torch.randint(0, 2 ** bits, (n, d_out, d_in // g), dtype=torch.uint8, device="cuda", generator=gen).float()
+    return words, scales, zeros
+
+
+def _host_layers(words, scales, zeros, bits, g):
+    """Layers of the above (or rows of one) as the 64-bit formulas take them."""
+    p = host(words).view(np.uint32)
+    k = np.arange(p.shape[-1] * 32 // bits)
+    q = (p[..., k * bits // 32] >> (k * bits % 32).astype(np.uint32)) & np.uint32(2 ** bits - 1)
+    return dict(q=q, scales=host(scales), zeros=host(zeros), kperm=None, bits=bits, group=g)
+
+
+def test_gemv_past_4_gib():
+    """A layer whose codes, and whose scales, take more than 2^32 bytes: rows at both ends and in between."""
+    torch = torch_mod()
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(16)
+    d_out, d_in, g = (1 << 22) + 40, 8192, 32
+    words, scales, zeros = (t[0] for t in _random_stack(gen, 1, d_out, d_in, 2, g))
+    assert words.numel() * 4 > 1 << 32 and scales.numel() * 4 > 1 << 32
+    x = torch.randn(2, d_in, device="cuda", generator=gen).bfloat16()
+    y = gq.gemv(x, gq.packed_weight(words, scales, zeros, 2, g), out_dtype=torch.float32)
+    rows = torch.tensor([*range(40), *range(d_out // 2, d_out // 2 + 40), *range(d_out - 60, d_out)], device="cuda")
+    v, bound = fr.product(host(x.float()).astype(np.float64), _host_layers(words[rows], scales[rows], zeros[rows], 2, g))
+    _check(y[:, rows], v, fr.rounded(v, bound, "fp32"), "rows of a layer past 4 GiB")
+
+
+def test_moe_past_4_gib():
+    """Stacks of more than 2^32 bytes each: a token of the last expert, and one of the first."""
+    torch = torch_mod()
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB of device memory")
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    E, d, ff, g = 512, 4096, 4224, 128
+    stacks = [_random_stack(gen, E, *shape, 4, g) for shape in ((ff, d), (ff, d), (d, ff))]
+    assert all(s[0].numel() * 4 > 1 << 32 for s in stacks)
+    x = torch.randn(2, d, device="cuda", generator=gen).half()
+    ids = torch.tensor([[E - 1], [0]], dtype=torch.int32, device="cuda")
+    weights = torch.tensor([[1.0], [0.5]], device="cuda")
+    got = gq.moe_layer(x, *(gq.packed_weight(*t, 4, g) for t in stacks), ids=ids, weights=weights, out_dtype=torch.float32)[0]
+    two = [_host_layers(*(t[[0, E - 1]] for t in s), 4, g) for s in stacks]
+    y, bound = fr.moe(host(x.float()).astype(np.float64), *two, np.array([[1], [0]]), host(weights), "fp32")
+    _check(got, y, bound, "experts of stacks past 4 GiB")
 
 
 def test_few_tokens_python_checks(oracle_mod):
