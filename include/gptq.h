@@ -427,7 +427,8 @@ typedef struct {
  *   bias    [d_out] fp32 or NULL.
  *   Y, H    fp16, bf16 or fp32 [M][ldy] out, ldy >= d_out; not X's memory.
  *   ws      scratch of gptq_workspace_bytes(GPTQ_OP_GEMV, 0, d_in, M, NULL), used
- *           (and needed) only with a kperm; 16-byte aligned.
+ *           (and needed) only with a kperm and M * d_in > GPTQ_GEMV_GATHERS, below
+ *           which the kernel gathers X itself; 16-byte aligned.
  * Sums are fp32 over exact products of the integers q - z (bf16 X with 2-4
  * bits: 2^bits + q, less (2^bits + z) times the sum of x) with x; the scale
  * multiplies a group's sum; the result is rounded once.  Deterministic.  A
@@ -436,6 +437,7 @@ typedef struct {
  * M == 0 is a no-op.  GPTQ_ERR_UNSUPPORTED for other bits, M, group sizes or
  * sizes than the above (more tokens: gptq_w4a16_gemm).
  */
+#define GPTQ_GEMV_GATHERS 4096
 GPTQ_API gptq_status gptq_gemv(const void *X, gptq_dtype x_dtype, int64_t M, int64_t ldx, const gptq_packed *w,
                                const float *bias, void *Y, gptq_dtype y_dtype, int64_t ldy, void *ws, size_t ws_bytes,
                                hipStream_t stream);

@@ -21,6 +21,7 @@ OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = 0, -1, -2, -3, -4
 DT_F32, DT_BF16, DT_F16 = 0, 1, 2
 OP_HESSIAN, OP_PREPARE, OP_QUANTIZE, OP_LOSS, OP_W4A16, OP_HESSIAN_TOKENS, OP_SMOOTH, OP_AWQ = 0, 1, 2, 3, 4, 5, 6, 7
 OP_CALIBRATE, OP_GEMV = 8, 10
+GEMV_GATHERS = 4096  # with M * d_in up to this, gemv and gemv_gated need no workspace under a column order
 
 EXPORTED = (
     "gptq_hessian_accumulate", "gptq_prepare_hinv", "gptq_quantize_layer", "gptq_rtn_quantize",
@@ -495,7 +496,7 @@ def _few_ws(ws, device):
 
 def _gemv_ws(ws, w, M, device):
     if ws is None:
-        if w.kperm is None:  # not used
+        if w.kperm is None or M * w.d_in <= GEMV_GATHERS:  # not used
             return None, 0
         ws = _workspace(workspace_bytes(OP_GEMV, w.d_out, w.d_in, M), device)
     return _few_ws(ws, device)

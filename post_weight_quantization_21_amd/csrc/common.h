@@ -119,6 +119,7 @@ hipError_t run_w4a16(const void *X, int64_t M, int64_t d_in, int64_t ldx, const 
 // ---------------------------------------------------------------------------
 // Packed layers for a few tokens (gemv.hip, moe.hip)
 // ---------------------------------------------------------------------------
+bool gemv_prepares(int64_t M, int64_t d_in);  // a kperm's gather runs as a kernel of its own
 size_t gemv_ws_bytes(int64_t M, int64_t d_in);
 // up: NULL for the plain product, else the second matrix of the gated one.
 hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,

@@ -280,16 +280,19 @@ __device__ __forceinline__ int64_t prepared_at(int col, int M, int m) {
     return ((int64_t)(col / kUnit * 4 + (s >> 3)) * M + m) * 8 + (s & 7);
 }
 
-// Activations of a product: rows as they are, or prepared in memory.
+// Activations of a product: rows as they are, rows whose columns are read in
+// packed order, or prepared in memory.
+enum FewX { kRawX, kOrderedX, kPreparedX };
 struct XRows {
     const uint16_t *base;
-    int64_t ld;     // raw: between rows; prepared: between planes
-    bool gathered;  // raw: rows are numbered by `row` of lane m, else m itself
+    int64_t ld;            // between rows; prepared: between planes
+    bool gathered;         // raw: rows are numbered by `row` of lane m, else m itself
     int32_t row;
+    const int32_t *order;  // ordered: x's column of each packed one
 };
 
 // A phase's x on its way into LDS, in batches of kUnits units a thread.
-template <int b, int P, bool kRaw>
+template <int b, int P, FewX kX>
 struct StageX {
     static constexpr int kUnits = 1;
     u32x4 v[4 * kUnits];
@@ -303,10 +306,11 @@ struct StageX {
         total = (items + kUnits * kFewThreads - 1) / (kUnits * kFewThreads);
     }
     // Raw: unit i of the phase is unit u of row r.  Prepared: unit i is pieces 4 i .. of the phase, plane by plane.
+    // Ordered: pieces as prepared, each gathered value by value.
     __device__ __forceinline__ void load(const XRows &x, int M, int units, int batch) {
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
-            if constexpr (kRaw) {
+            if constexpr (kX == kRawX) {
                 const int i = threadIdx.x + (kUnits * batch + k) * kFewThreads;
                 const int r = __umulhi(i, magic), u = first + i - r * per_row;
                 const int row = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
@@ -316,6 +320,21 @@ struct StageX {
                     const u32x4 *src = reinterpret_cast<const u32x4 *>(x.base + row * x.ld + u * kUnit);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[4 * k + j] = src[j];
+                }
+            } else if constexpr (kX == kOrderedX) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads, piece = (int)((uint32_t)i / (uint32_t)M);
+                    const int u = first + (piece >> 2), f = piece & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
+                    v[4 * k + j] = (u32x4){0, 0, 0, 0};
+                    if (i < 4 * items && u < units) {
+                        const uint16_t *row = x.base + (i - piece * M) * x.ld;
+                        const int32_t *at = x.order + u * kUnit + f0;
+                        uint32_t h[8];
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) h[n] = row[std::min(std::max(at[slot_col<b>(0, n)], 0), units * kUnit - 1)];
+                        v[4 * k + j] = (u32x4){h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
+                    }
                 }
             } else {
                 const int plane = 4 * M * per_row;  // pieces
@@ -332,7 +351,7 @@ struct StageX {
         u32x4 *dst = reinterpret_cast<u32x4 *>(xs);
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
-            if constexpr (kRaw) {
+            if constexpr (kX == kRawX) {
                 const int i = threadIdx.x + (kUnits * batch + k) * kFewThreads;
                 const int r = __umulhi(i, magic), u = i - r * per_row;
                 if (i >= items) continue;
@@ -419,7 +438,7 @@ struct StageGroups {
 // registers, one computed while the other is loaded (4 to 8 KB of a wave in
 // flight at 4 bits); past the wave's run nothing is read.  x is zero past the
 // last unit.
-template <int b, typename T, int P, int kMats, bool kSplit, bool kRaw>
+template <int b, typename T, int P, int kMats, bool kSplit, FewX kX>
 __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShape &w, int64_t row0, int rows, const XRows &x,
                                                int M, int wave, unsigned char *smem) {
     typedef typename Vec8<T>::V V;
@@ -448,7 +467,7 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
     };
     floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     C codes;
-    StageX<b, P, kRaw> stage;
+    StageX<b, P, kX> stage;
     StageGroups<b, T, kMats> groups;
 #pragma unroll
     for (int k = 0; k < kMats; ++k) {

@@ -18,6 +18,7 @@ struct GemvArgs {
     int M;
     const uint16_t *x;
     int64_t ldx;
+    const int32_t *order;
     const float *bias;
     void *y;
     int64_t ldy;
@@ -25,16 +26,16 @@ struct GemvArgs {
 };
 
 // Gated: the even tiles are the gate's rows, the odd ones up's.
-template <int b, typename T, bool kGated, bool kSplit, bool kRaw>
+template <int b, typename T, bool kGated, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     constexpr int R = kGated ? 2 : 1, LR = kGated ? 1 : 0;
     const int wave = few_wave(), lg = a.shape.lg;
     const int lt = 3 - lg - LR;  // log2 of the row tiles
     const int64_t r0 = (int64_t)blockIdx.x * kTileRows << lt, d_out = a.shape.d_out;
-    const XRows x = {a.x, a.ldx, false, 0};
+    const XRows x = {a.x, a.ldx, false, 0, a.order};
     float *sums = reinterpret_cast<float *>(smem);
-    const floatx4 acc = few_product<b, T, 1, R, kSplit, kRaw>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
+    const floatx4 acc = few_product<b, T, 1, R, kSplit, kX>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
                                                             a.M, wave, smem);
     few_share(sums, wave, acc, a.M);
     for (int n = threadIdx.x; n < a.M * kTileRows << lt; n += kFewThreads) {
@@ -66,18 +67,17 @@ __global__ __launch_bounds__(256) void prepare_kernel(const uint16_t *__restrict
 }
 
 template <int b, typename T, bool kGated, bool kSplit>
-void launch_gemv(const GemvArgs &a, bool raw, hipStream_t s) {
+void launch_gemv(const GemvArgs &a, FewX x, hipStream_t s) {
     const dim3 grid((unsigned)ceil_div(a.shape.d_out, kTileRows * ((kFewWaves >> a.shape.lg) / (kGated ? 2 : 1))));
-    if (raw)
-        gemv_kernel<b, T, kGated, kSplit, true><<<grid, kFewThreads, a.shape.lds, s>>>(a);
-    else
-        gemv_kernel<b, T, kGated, kSplit, false><<<grid, kFewThreads, a.shape.lds, s>>>(a);
+    auto kernel = x == kRawX ? gemv_kernel<b, T, kGated, kSplit, kRawX>
+                             : (x == kOrderedX ? gemv_kernel<b, T, kGated, kSplit, kOrderedX> : gemv_kernel<b, T, kGated, kSplit, kPreparedX>);
+    kernel<<<grid, kFewThreads, a.shape.lds, s>>>(a);
 }
 
 template <int b>
 hipError_t launch_gemv_bits(GemvArgs a, gptq_dtype x_dt, const gptq_packed &w, bool gated, void *ws, hipStream_t s) {
-    const bool x = !w.kperm;  // raw
-    if (!x) {
+    const FewX x = !w.kperm ? kRawX : (gemv_prepares(a.M, w.d_in) ? kPreparedX : kOrderedX);
+    if (x == kPreparedX) {
         prepare_kernel<b><<<dim3((unsigned)(few_quads(a.shape.units) * kQuad / 256), (unsigned)a.M), 256, 0, s>>>(
             a.x, a.ldx, (int)w.d_in, w.kperm, static_cast<uint16_t *>(ws));
         const hipError_t e = hipGetLastError();
@@ -129,7 +129,15 @@ FewShape few_shape(const gptq_packed &w, double tiles, int most, int rows, int m
     }
 }
 
-size_t gemv_ws_bytes(int64_t M, int64_t d_in) { return align_up((size_t)prepared_values(M, (int)(d_in / kUnit)) * 2, 256); }
+// Up to eight values a thread the product's own gather costs less than a launch
+// and a pass through memory: one token of 4096 x 4096 takes 6.9 us against 8.1,
+// two of them 8.3 against 8.4, but four 11.6 against 8.6 and one token of 8192 x
+// 8192 18.6 against 15.5, since every workgroup gathers all of x.
+bool gemv_prepares(int64_t M, int64_t d_in) { return M * d_in > GPTQ_GEMV_GATHERS; }
+
+size_t gemv_ws_bytes(int64_t M, int64_t d_in) {
+    return gemv_prepares(M, d_in) ? align_up((size_t)prepared_values(M, (int)(d_in / kUnit)) * 2, 256) : 0;
+}
 
 hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed &w, const gptq_packed *up,
                     const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws, hipStream_t s) {
@@ -141,6 +149,7 @@ hipError_t run_gemv(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, cons
     a.shape = up ? few_shape(w, 2 * tiles, kFewWaves / 2, a.M, a.M) : few_shape(w, tiles, kFewWaves, a.M, a.M);
     a.x = static_cast<const uint16_t *>(X);
     a.ldx = ldx;
+    a.order = w.kperm;
     a.bias = bias;
     a.y = Y;
     a.ldy = ldy;

@@ -295,7 +295,7 @@ struct GateUpArgs {
     int64_t h_plane;
 };
 
-template <int b, typename T, bool kSplit, bool kRaw>
+template <int b, typename T, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(GateUpArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const Expert &e = a.lists->expert[blockIdx.y];
@@ -305,8 +305,9 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(Gat
     const int lt = 2 - lg;  // log2 of the row tiles
     const int ff = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * ff + r0;
-    const XRows x = {kRaw ? a.x : a.x + prepared_values(start, a.shape.units), kRaw ? a.ldx : 0, kRaw, token};
-    const floatx4 acc = few_product<b, T, 1, 2, kSplit, kRaw>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
+    constexpr bool raw = kX == kRawX;
+    const XRows x = {raw ? a.x : a.x + prepared_values(start, a.shape.units), raw ? a.ldx : 0, raw, token, nullptr};
+    const floatx4 acc = few_product<b, T, 1, 2, kSplit, kX>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
     __bf16 *h = a.h + prepared_values(start, ff / kUnit);
@@ -347,8 +348,8 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownAr
     const int lt = 3 - lg;
     const int d = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * d + r0;
-    const XRows x = {a.h + prepared_values(start, a.shape.units), a.h_plane, false, 0};
-    const floatx4 acc = few_product<b, __bf16, P, 1, kSplit, false>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
+    const XRows x = {a.h + prepared_values(start, a.shape.units), a.h_plane, false, 0, nullptr};
+    const floatx4 acc = few_product<b, __bf16, P, 1, kSplit, kPreparedX>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
     for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
@@ -409,9 +410,9 @@ struct MoeCall {
 template <int b, typename T, bool kSplit>
 void launch_gate_up(const GateUpArgs &g, bool raw, dim3 grid, hipStream_t s) {
     if (raw)
-        gate_up_kernel<b, T, kSplit, true><<<grid, kFewThreads, g.shape.lds, s>>>(g);
+        gate_up_kernel<b, T, kSplit, kRawX><<<grid, kFewThreads, g.shape.lds, s>>>(g);
     else
-        gate_up_kernel<b, T, kSplit, false><<<grid, kFewThreads, g.shape.lds, s>>>(g);
+        gate_up_kernel<b, T, kSplit, kPreparedX><<<grid, kFewThreads, g.shape.lds, s>>>(g);
 }
 template <int b, bool kSplit>
 void launch_down(const DownArgs &w, int planes, dim3 grid, hipStream_t s) {

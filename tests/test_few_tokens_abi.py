@@ -75,13 +75,15 @@ def test_gemv_arguments_refused(kw, status):
 
 
 def test_gemv_workspace():
-    need = gq.workspace_bytes(gq.OP_GEMV, 64, 128, 3)
-    assert need >= 3 * 512 * 2  # whole quads of columns
-    ordered = packed(kperm=P)
-    assert gemv(ordered, M=3, ws_bytes=need - 1) == gq.ERR_WORKSPACE
-    assert gemv(ordered, M=3, ws=None) == gq.ERR_WORKSPACE
-    assert gemv(ordered, M=3, ws=P + 8) == gq.ERR_INVALID_ARG
-    assert gated(ordered, ordered, M=3, ws_bytes=need - 1) == gq.ERR_WORKSPACE
+    need = gq.workspace_bytes(gq.OP_GEMV, 64, 4128, 3)
+    assert need >= 3 * 4608 * 2  # whole quads of columns
+    ordered = packed(d_in=4128, group=0, kperm=P)
+    assert gemv(ordered, M=3, ldx=4128, ws_bytes=need - 1) == gq.ERR_WORKSPACE
+    assert gemv(ordered, M=3, ldx=4128, ws=None) == gq.ERR_WORKSPACE
+    assert gemv(ordered, M=3, ldx=4128, ws=P + 8) == gq.ERR_INVALID_ARG
+    assert gated(ordered, ordered, M=3, ldx=4128, ws_bytes=need - 1) == gq.ERR_WORKSPACE
+    for m, d in ((1, gq.GEMV_GATHERS), (16, gq.GEMV_GATHERS // 16)):  # the largest without one, and one unit more
+        assert gq.workspace_bytes(gq.OP_GEMV, 64, d, m) == 0 < gq.workspace_bytes(gq.OP_GEMV, 64, d + 32, m)
     with pytest.raises(gq.GptqError) as ei:
         gq.workspace_bytes(9, 1, 1)  # the number between the operations stays free
     assert ei.value.status == gq.ERR_INVALID_ARG

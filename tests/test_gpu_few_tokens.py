@@ -71,6 +71,12 @@ GEMV = [
     (1, 20, 98336, 2, 32, "bf16", "fp32", False, False),   # a row too long for one phase; its last quad holds a unit
     (2, 5000, 544, 8, 32, "fp16", "fp16", False, False),  # two quads, the second of one unit
     (1, 70000, 64, 4, 64, "bf16", "bf16", False, True),    # many rows
+    (1, 70, 736, 2, 32, "bf16", "fp32", True, False),      # a column order gathered by the product itself: each bits
+    (16, 20, 224, 2, 0, "fp16", "fp32", True, False),
+    (1, 64, 4096, 8, 128, "bf16", "fp32", True, False),
+    (2, 40, 2048, 4, 128, "fp16", "fp32", True, False),
+    (3, 40, 1312, 3, 32, "bf16", "fp32", True, False),
+    (1, 40, 4128, 4, 32, "fp16", "fp32", True, False),     # ... and one unit too long for it
     (1, 1, 32, 2, 32, "fp16", "fp32", False, False),       # one row, whose sets of steps reach past its end
     (3, 129, 608, 8, 32, "bf16", "fp32", False, False),    # ... as the last tile's only row
 ]
