@@ -286,7 +286,7 @@ enum FewX { kRawX, kOrderedX, kPreparedX };
 struct XRows {
     const uint16_t *base;
     int64_t ld;            // between rows; prepared: between planes
-    bool gathered;         // raw: rows are numbered by `row` of lane m, else m itself
+    bool gathered;         // raw and ordered: rows are numbered by `row` of lane m, else m itself
     int32_t row;
     const int32_t *order;  // ordered: x's column of each packed one
 };
@@ -326,9 +326,10 @@ struct StageX {
                 for (int j = 0; j < 4; ++j) {
                     const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads, piece = (int)((uint32_t)i / (uint32_t)M);
                     const int u = first + (piece >> 2), f = piece & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
+                    const int r = i - piece * M, m = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
                     v[4 * k + j] = (u32x4){0, 0, 0, 0};
                     if (i < 4 * items && u < units) {
-                        const uint16_t *row = x.base + (i - piece * M) * x.ld;
+                        const uint16_t *row = x.base + m * x.ld;
                         const int32_t *at = x.order + u * kUnit + f0;
                         uint32_t h[8];
 #pragma unroll

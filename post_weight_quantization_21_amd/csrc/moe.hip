@@ -289,6 +289,7 @@ struct GateUpArgs {
     FewShape shape;
     const uint16_t *x;  // rows by token, or prepared by pair
     int64_t ldx;
+    const int32_t *order;  // ordered: of every expert
     int planes;
     const Lists *lists;
     __bf16 *h;
@@ -305,8 +306,9 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(Gat
     const int lt = 2 - lg;  // log2 of the row tiles
     const int ff = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * ff + r0;
-    constexpr bool raw = kX == kRawX;
-    const XRows x = {raw ? a.x : a.x + prepared_values(start, a.shape.units), raw ? a.ldx : 0, raw, token, nullptr};
+    constexpr bool rows = kX != kPreparedX;
+    const XRows x = {rows ? a.x : a.x + prepared_values(start, a.shape.units), rows ? a.ldx : 0, rows, token,
+                     kX == kOrderedX ? a.order + (int64_t)e.expert * a.shape.units * kUnit : nullptr};
     const floatx4 acc = few_product<b, T, 1, 2, kSplit, kX>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
@@ -408,11 +410,10 @@ struct MoeCall {
 };
 
 template <int b, typename T, bool kSplit>
-void launch_gate_up(const GateUpArgs &g, bool raw, dim3 grid, hipStream_t s) {
-    if (raw)
-        gate_up_kernel<b, T, kSplit, kRawX><<<grid, kFewThreads, g.shape.lds, s>>>(g);
-    else
-        gate_up_kernel<b, T, kSplit, kPreparedX><<<grid, kFewThreads, g.shape.lds, s>>>(g);
+void launch_gate_up(const GateUpArgs &g, FewX x, dim3 grid, hipStream_t s) {
+    auto kernel = x == kRawX ? gate_up_kernel<b, T, kSplit, kRawX>
+                             : (x == kOrderedX ? gate_up_kernel<b, T, kSplit, kOrderedX> : gate_up_kernel<b, T, kSplit, kPreparedX>);
+    kernel<<<grid, kFewThreads, g.shape.lds, s>>>(g);
 }
 template <int b, bool kSplit>
 void launch_down(const DownArgs &w, int planes, dim3 grid, hipStream_t s) {
@@ -441,8 +442,11 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     g.h = reinterpret_cast<__bf16 *>(c.ws + l.h);
     g.h_plane = prepared_values(pairs, (int)(ff / kUnit));
     g.planes = c.y_dt == GPTQ_DT_F32 ? 3 : 2;
-    const bool raw = !c.gate->kperm;
-    if (!raw) {
+    // gathered by the products up to the same size as in gemv.hip: one token of 64 experts x 1408 x 2048 takes 30.4 us
+    // against 31.7 through a kernel of its own
+    g.order = c.gate->kperm;
+    const FewX x = !c.gate->kperm ? kRawX : (gemv_prepares(rows, d) ? kPreparedX : kOrderedX);
+    if (x == kPreparedX) {
         uint16_t *xg = reinterpret_cast<uint16_t *>(c.ws + l.xg);
         prepare_pairs_kernel<b><<<dim3((unsigned)(few_quads(g.shape.units) * kQuad / 256), slots), 256, 0, s>>>(g.x, c.ldx, (int)d, lists,
                                                                                                                c.gate->kperm, xg);
@@ -450,9 +454,9 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     }
     const dim3 grid((unsigned)ceil_div(pair_tiles, (kFewWaves >> g.shape.lg) / 2), slots);
     if (few_split(*c.gate))
-        launch_gate_up<b, T, true>(g, raw, grid, s);
+        launch_gate_up<b, T, true>(g, x, grid, s);
     else
-        launch_gate_up<b, T, false>(g, raw, grid, s);
+        launch_gate_up<b, T, false>(g, x, grid, s);
     DownArgs w;
     const int64_t tiles = ceil_div(d, kTileRows);
     w.w = few_mat(*c.down);

@@ -212,6 +212,9 @@ MOE = [
     (9, 64, 64, 512, 16, 4, 64, "fp16", "fp32", False, False, "fp32"),   # the most experts
     (16, 4096, 96, 3, 2, 4, 32, "bf16", "bf16", False, True, "fp32"),    # phases of the first products
     (16, 64, 5120, 3, 2, 4, 64, "fp16", "fp32", True, True, "fp16"),    # ... and of the second, in three pieces
+    (16, 1024, 96, 3, 2, 2, 32, "bf16", "bf16", True, False, "fp32"),   # a column order too large for the product's own gather
+    (1, 4096, 64, 4, 2, 8, 64, "fp16", "fp32", True, True, "fp32"),    # ... and the largest it takes
+    (16, 512, 64, 40, 2, 3, 32, "bf16", "fp32", True, True, "bf16"),
 ]
 
 
