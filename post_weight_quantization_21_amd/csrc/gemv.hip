@@ -118,15 +118,27 @@ FewShape few_shape(const gptq_packed &w, double tiles, int most, int rows, int m
     const int quads = few_quads(d.units);
     d.lg = 0;
     while (2 << d.lg <= most && tiles * (2 << d.lg) <= kFewResident && 2 << d.lg <= quads) ++d.lg;
-    for (;; --d.lg) {
-        const int per_wg = (kFewWaves >> d.lg) * kTileRows;  // rows of weights
-        const bool alone = tiles * (1 << d.lg) <= 256 * kFewWaves;
+    auto plan = [&](int lg) {  // the phase of lg
+        d.lg = lg;
+        const int per_wg = (kFewWaves >> lg) * kTileRows;  // rows of weights
+        const bool alone = tiles * (1 << lg) <= 256 * kFewWaves;
         d.quad_entries = (int32_t)ceil_div((int64_t)per_wg * kQuad * 8, g);
         if (d.groups == 1) d.quad_entries = 0;
-        const int64_t all = few_fixed(d.lg) + (int64_t)quads * ((int64_t)max_rows * kQuad * 2 + d.quad_entries);
+        const int64_t all = few_fixed(lg) + (int64_t)quads * ((int64_t)max_rows * kQuad * 2 + d.quad_entries);
         d.lds = (int32_t)std::min<int64_t>(all, alone ? kLdsAlone : kLdsShared);
-        if (d.lg == 0 || few_phase(d, rows) >= 1 << d.lg) return d;
+        return few_phase(d, rows);
+    };
+    int lg = d.lg, phase = plan(lg);
+    while (lg > 0 && phase < 1 << lg) phase = plan(--lg);
+    // Half the slices where that takes fewer phases (the workgroups, no more than compute units then, have the larger
+    // LDS) and x fills most of a phase: 8 tokens of 8192 x 8192 in 17.2 us instead of 20.3, 16 of 28672 x 8192 in 50.4
+    // instead of 55.2.  With x no more than twice the entries it loses: 4 of 28672 x 8192 39.9 us instead of 38.1,
+    // 2 of 8192 x 28672 in groups of 32 75.6 instead of 63.9.
+    if (lg > 0 && phase < quads) {
+        const int lower = plan(lg - 1);
+        if (ceil_div(quads, lower) >= ceil_div(quads, phase) || rows * kQuad * 2 < 3 * d.quad_entries) plan(lg);
     }
+    return d;
 }
 
 // Up to eight values a thread the product's own gather costs less than a launch

@@ -66,6 +66,7 @@ GEMV = [
     (8, 64, 8192, 4, 64, "fp16", "fp16", True, False),
     (1, 40, 28672, 4, 32, "bf16", "fp32", False, False),   # 896 groups per row
     (16, 4300, 8192, 4, 128, "bf16", "fp32", False, False),  # several phases, two workgroups to a compute unit
+    (8, 4200, 8192, 4, 128, "fp16", "fp32", False, False), # fewer slices for fewer phases
     (16, 70, 8192, 3, 0, "fp16", "fp32", False, False),    # several phases, one workgroup
     (9, 33, 20480, 4, 32, "fp16", "bf16", True, False),    # ... of prepared activations and many groups
     (1, 20, 98336, 2, 32, "bf16", "fp32", False, False),   # a row too long for one phase; its last quad holds a unit
