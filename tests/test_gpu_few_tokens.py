@@ -284,6 +284,51 @@ def test_moe_router_ties_and_nan(oracle_mod):
     assert not (host(ids) == 3).any() and torch.isnan(w).all()
 
 
+def test_moe_non_finite_token_stays_in_its_row(oracle_mod):
+    """A token with a NaN or an infinity shares experts with the others and changes nothing of theirs."""
+    torch = torch_mod()
+    rng = np.random.default_rng(18)
+    E, d, ff, T, k = 4, 256, 96, 6, 3
+    _, dw = _experts(rng, oracle_mod, E, d, ff, 4, 32, False)
+    R = cuda(rng.standard_normal((E, d)).astype(np.float32))
+    X, _ = _acts(rng, T, d, "bf16")
+    good = gq.moe_layer(X, *dw, router=R, top_k=k)
+    bad = X.clone()
+    bad[1, 7], bad[4, 200] = float("nan"), float("inf")
+    Y, ids, w = gq.moe_layer(bad, *dw, router=R, top_k=k)
+    same = [0, 2, 3, 5]
+    assert torch.equal(ids[same], good[1][same]) and torch.equal(w[same], good[2][same])
+    assert not torch.isfinite(Y[1]).any() and not torch.isfinite(Y[4]).any()
+    assert torch.isnan(w[1]).all() and ids[1].tolist() == [0, 1, 2]  # NaN logits tie
+    # the other tokens' rows: their experts hold the same pairs or others, in rows of their own
+    assert torch.isfinite(Y[same]).all() and torch.equal(Y[same], good[0][same])
+
+
+@pytest.mark.parametrize("M,d", [(1, 512), (16, 512)])  # gathered by the product, and by a kernel of its own
+def test_few_tokens_order_entries_are_clamped(oracle_mod, M, d):
+    torch = torch_mod()
+    rng = np.random.default_rng(19)
+    w = fr.make_packed(rng, oracle_mod, 40, d, 4, 64, True)
+    w["kperm"][[3, 100]] = (-5, d + 7)
+    clamped = dict(w, kperm=np.clip(w["kperm"], 0, d - 1))
+    X, _ = _acts(rng, M, d, "bf16")
+    a, b = _dev(w), _dev(clamped)
+    assert torch.equal(gq.gemv(X, a), gq.gemv(X, b)) and torch.equal(gq.gemv_gated(X, a, a), gq.gemv_gated(X, b, b))
+    E = 3
+    stacks = [fr.make_packed(rng, oracle_mod, *s, 4, 32, True, n=E) for s in ((d, d), (d, d), (d, d))]
+    stacks[1]["kperm"] = stacks[0]["kperm"]
+    ids = torch.arange(M, dtype=torch.int32, device="cuda").remainder(E).view(M, 1)
+    weights = torch.ones(M, 1, device="cuda")
+    for s in (stacks[0], stacks[2]):
+        s["kperm"][0, 9], s["kperm"][2, 31] = d, -1
+    got = []
+    for f in (lambda k: k, lambda k: np.clip(k, 0, d - 1)):
+        gate, down = (_dev(dict(s, kperm=f(s["kperm"]))) for s in (stacks[0], stacks[2]))
+        up = gq.packed_weight(cuda(stacks[1]["packed"].view(np.int32)), cuda(stacks[1]["scales"]), cuda(stacks[1]["zeros"]), 4, 32, kperm=gate.kperm)
+        got.append(gq.moe_layer(X, gate, up, down, ids=ids, weights=weights)[0])
+    assert torch.equal(*got)
+
+
 def test_few_tokens_no_moe_tokens(oracle_mod):
     torch = torch_mod()
     rng = np.random.default_rng(10)
