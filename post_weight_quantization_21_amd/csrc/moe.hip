@@ -18,6 +18,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "expert_load.h"
 #include "few_core.h"
 
 namespace gptq {
@@ -443,24 +444,22 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     const int64_t d = c.gate->d_in, ff = c.gate->d_out, pairs = c.T * c.top_k;
     Lists *lists = reinterpret_cast<Lists *>(c.ws + l.lists);
     const unsigned slots = (unsigned)std::min<int64_t>(c.n_experts, pairs);
-    // experts that `pairs` independent choices would hit, which the work is spread for
-    const double busy = c.n_experts * (1.0 - std::pow(1.0 - 1.0 / c.n_experts, (double)pairs));
-    const int rows = (int)std::ceil(pairs / busy);  // tokens of an expert
+    const ExpertLoad load = expert_load(c.T, c.n_experts, c.top_k);
     GateUpArgs g;
     const int64_t pair_tiles = ceil_div(ff, kTileRows);
     g.w[0] = few_mat(*c.gate);
     g.w[1] = few_mat(*c.up);
-    g.shape = few_shape(*c.gate, 2 * busy * pair_tiles, kFewWaves / 2, rows, (int)c.T);
+    g.shape = few_shape(*c.gate, 2 * load.experts * pair_tiles, kFewWaves / 2, load.rows, (int)c.T);
     g.x = static_cast<const uint16_t *>(c.X);
     g.ldx = c.ldx;
     g.lists = lists;
     g.h = reinterpret_cast<__bf16 *>(c.ws + l.h);
     g.h_plane = prepared_values(pairs, (int)(ff / kUnit));
     g.planes = c.y_dt == GPTQ_DT_F32 ? 3 : 2;
-    // gathered by the products up to the same size as in gemv.hip: one token of 64 experts x 1408 x 2048 takes 30.4 us
-    // against 31.7 through a kernel of its own
+    // gathered by the products up to the same size as in gemv.hip, with an expert's rows for M: one token of 64 experts x
+    // 1408 x 2048 takes 30.4 us against 31.7 through a kernel of its own
     g.order = c.gate->kperm;
-    const FewX x = !c.gate->kperm ? kRawX : (gemv_prepares(rows, d) ? kPreparedX : kOrderedX);
+    const FewX x = !c.gate->kperm ? kRawX : (gemv_prepares(load.rows, d) ? kPreparedX : kOrderedX);
     if (x == kPreparedX) {
         uint16_t *xg = reinterpret_cast<uint16_t *>(c.ws + l.xg);
         prepare_pairs_kernel<b><<<dim3((unsigned)(few_quads(g.shape.units) * kQuad / 256), slots), 256, 0, s>>>(g.x, c.ldx, (int)d, lists,
@@ -475,7 +474,7 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     DownArgs w;
     const int64_t tiles = ceil_div(d, kTileRows);
     w.w = few_mat(*c.down);
-    w.shape = few_shape(*c.down, busy * tiles, kFewWaves, g.planes * rows, g.planes * (int)c.T);
+    w.shape = few_shape(*c.down, load.experts * tiles, kFewWaves, g.planes * load.rows, g.planes * (int)c.T);
     w.h = reinterpret_cast<const uint16_t *>(g.h);
     w.h_plane = g.h_plane;
     w.lists = lists;

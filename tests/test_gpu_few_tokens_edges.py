@@ -1,0 +1,53 @@
+"""The few-token products (gemv, gemv_gated, moe_layer) at the borders of their paths, types and memory."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import few_ref as fr
+import post_weight_quantization_21_amd as gq
+from gpu_util import cuda, host, log, torch_mod
+from test_gpu_few_tokens import _acts, _check, _dt, _experts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    torch = torch_mod()
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    gq.load_library()
+
+
+def _launches(call):
+    """The number of kernels that a call launches: the nodes of a graph it is captured into."""
+    torch = torch_mod()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph, stream=side):
+        call()
+    n = ctypes.c_size_t(0)
+    get = gq.load_library().hipGraphGetNodes
+    get.argtypes = [ctypes.c_void_p, ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t)]
+    assert get(graph.raw_cuda_graph(), None, ctypes.byref(n)) == 0
+    return n.value
+
+
+# One token's experts have one row each: up to GEMV_GATHERS columns the first products gather the order themselves.
+@pytest.mark.parametrize("d,E,k,launches", [(gq.GEMV_GATHERS, 4, 2, 6), (gq.GEMV_GATHERS + 32, 4, 2, 7), (2080, 9, 8, 6), (2080, 3, 3, 6)])
+def test_moe_one_token_in_a_column_order(oracle_mod, d, E, k, launches):
+    torch = torch_mod()
+    log(f"moe of one token in a column order: d={d} E={E} k={k}")
+    rng = np.random.default_rng(d + k)
+    hw, dw = _experts(rng, oracle_mod, E, d, 64, 4, 32, True)
+    X, x = _acts(rng, 1, d, "bf16")
+    R = cuda((rng.standard_normal((E, d)) * (2 / np.sqrt(d))).astype(np.float32))
+    ids, weights = fr.route(x, host(R).astype(np.float64), k, True)
+    Y, gi, _ = gq.moe_layer(X, *dw, router=R, top_k=k, out_dtype=torch.float32)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(gi), ids)
+    want, bound = fr.moe(x, *hw, ids, weights, "fp32")
+    _check(Y, want, bound, "moe")
+    assert _launches(lambda: gq.moe_layer(X, *dw, router=R, top_k=k, out_dtype=torch.float32)) == launches
