@@ -465,7 +465,8 @@ GPTQ_API gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t 
  *   gate, up  stacks of n_experts layers [d_ff][d]; down: [d][d_ff].  gate and up
  *           agree as in gptq_gemv_gated.  All three have the same bits.
  *   ids     [T][top_k] int32 and weights [T][top_k] fp32: outputs (either may be
- *           NULL) with a router, inputs without.  As inputs, an id outside
+ *           NULL) with a router, inputs without.  The softmax is in fp64, a
+ *           weight is rounded once.  As inputs, an id outside
  *           0 .. n_experts - 1 adds nothing (padding), and one that a token
  *           names twice counts with the sum of its weights.
  *   Y       fp16, bf16 or fp32 [T][ldy] out, ldy >= d; not X's memory.

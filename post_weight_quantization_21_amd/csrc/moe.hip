@@ -115,24 +115,23 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v) {
            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63);
 }
 
-// exp(a - b) in fp32, the difference's rounding put back to first order.
-__device__ __forceinline__ float exp_diff(double a, double b) {
-    const double d = a - b;
-    const float hi = (float)d, e = expf(hi);
-    return d > -100.0 ? fmaf(e, (float)(d - hi), e) : e;  // (also an infinite difference)
-}
 template <int ctrl, int rows>
-__device__ __forceinline__ float dpp_add(float v) {
-    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), ctrl, rows, 0xf, false));
+__device__ __forceinline__ double dpp_add(double v) {
+    const uint64_t k = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)k, ctrl, rows, 0xf, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(k >> 32), ctrl, rows, 0xf, false);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
-__device__ __forceinline__ float wave_sum_f(float v) {  // as wave_max
+__device__ __forceinline__ double wave_sum_d(double v) {  // as wave_max
     v = dpp_add<0x111, 0xf>(v);
     v = dpp_add<0x112, 0xf>(v);
     v = dpp_add<0x114, 0xf>(v);
     v = dpp_add<0x118, 0xf>(v);
     v = dpp_add<0x142, 0xa>(v);
     v = dpp_add<0x143, 0xc>(v);
-    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+    const uint64_t k = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(k >> 32), 63) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)k, 63));
 }
 
 // kPer: logits of a lane, n_experts <= 64 kPer.  One workgroup, since the numbering
@@ -176,7 +175,7 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) key[i] = key[i] == best ? 0 : key[i];
             }
-            // softmax: the first choice holds the largest logit
+            // softmax in fp64, each weight rounded once: the first choice holds the largest logit
             uint64_t any_nan = 0;
             double mine = 0.0;  // lane j < top_k: its chosen logit
 #pragma unroll
@@ -185,14 +184,15 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
                 if (e >> 6 == i) mine = c;
                 any_nan |= __ballot(v[i] != v[i]);
             }
-            const double top = __shfl(mine, 0);
-            float sum = 0.0f;
+            const double top = __shfl(mine, 0), p = lane < top_k ? exp(mine - top) : 0.0;
+            double sum = p;
+            if (!renormalize) {
+                sum = 0.0;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (lane + kWave * i < n_experts) sum += exp_diff(v[i], top);
-            sum = wave_sum_f(sum);
-            const float p = lane < top_k ? exp_diff(mine, top) : 0.0f;
-            w = p / (renormalize ? wave_sum_f(p) : sum);
+                for (int i = 0; i < kPer; ++i)
+                    if (lane + kWave * i < n_experts) sum += exp(v[i] - top);
+            }
+            w = (float)(p / wave_sum_d(sum));
             if (any_nan) w = NAN;  // as the softmax's sum is
         }
         float total_w = 0.0f;  // a caller may name an expert twice

@@ -7,7 +7,7 @@ import pytest
 import few_ref as fr
 import post_weight_quantization_21_amd as gq
 from gpu_util import cuda, host, log, torch_mod
-from test_gpu_few_tokens import _acts, _check, _dt, _experts
+from test_gpu_few_tokens import _acts, _check, _dev, _dt, _experts
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,23 @@ def test_moe_one_token_in_a_column_order(oracle_mod, d, E, k, launches):
     want, bound = fr.moe(x, *hw, ids, weights, "fp32")
     _check(Y, want, bound, "moe")
     assert _launches(lambda: gq.moe_layer(X, *dw, router=R, top_k=k, out_dtype=torch.float32)) == launches
+
+
+@pytest.mark.parametrize("T,E,k,renorm", [(1, 64, 6, True), (16, 128, 8, True), (16, 128, 8, False), (7, 512, 16, False), (16, 300, 16, True),
+                                          (5, 3, 3, False), (16, 1, 1, True), (16, 1, 1, False), (9, 65, 1, False)])
+def test_moe_weights_are_rounded_once(oracle_mod, T, E, k, renorm):
+    """The softmax is in fp64: a weight is its value rounded to fp32 (half a step; the fp64 sums of 64 products, of at
+    most 512 exponentials and of logits of at most 30 are far below the other hundredth)."""
+    torch = torch_mod()
+    log(f"moe weights T={T} E={E} k={k} renorm={renorm}")
+    rng = np.random.default_rng(T + E + k)
+    _, dw = _experts(rng, oracle_mod, E, 64, 32, 4, 32, False)
+    X, x = _acts(rng, T, 64, "bf16")
+    R = cuda((rng.standard_normal((E, 64)) * 0.4).astype(np.float32))
+    ids, weights = fr.route(x, host(R).astype(np.float64), k, renorm)
+    _, gi, gw = gq.moe_layer(X, *dw, router=R, top_k=k, renormalize=renorm)
+    torch.cuda.synchronize()
+    assert np.array_equal(host(gi), ids)
+    ratio = np.abs(host(gw).astype(np.float64) - weights) / (1.01 * fr.U * weights)
+    log(f"  worst error over the bound {ratio.max():.3f}")
+    assert (ratio <= 1).all()
