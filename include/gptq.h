@@ -459,9 +459,8 @@ GPTQ_API gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t 
  *           multiple of 8.
  *   router  [n_experts][d] in router_dtype (fp32, or X's type), 16-byte aligned;
  *           its products are summed in fp64, since a rounding could change the
- *           choice; logits equal to 43 bits are a tie.  A NaN logit ranks below
- *           every number and makes the token's weights NaN.  NULL: the caller
- *           routes, and ids and weights are inputs.
+ *           choice.  A NaN logit ranks below every number and makes the token's
+ *           weights NaN.  NULL: the caller routes, and ids and weights are inputs.
  *   gate, up  stacks of n_experts layers [d_ff][d]; down: [d][d_ff].  gate and up
  *           agree as in gptq_gemv_gated.  All three have the same bits.
  *   ids     [T][top_k] int32 and weights [T][top_k] fp32: outputs (either may be

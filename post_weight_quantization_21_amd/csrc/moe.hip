@@ -87,13 +87,11 @@ __global__ __launch_bounds__(256) void router_kernel(const T *__restrict__ X, in
         logits[(int64_t)(t0 + t) * n_experts + e] = part[0][t] + part[1][t] + part[2][t] + part[3][t];
 }
 
-// A logit's rank as an unsigned key: ascending with the logit to 43 significant
-// bits, then descending with the expert's index; a NaN lies below every number.
-__device__ __forceinline__ uint64_t rank_key(double v, int e) {
-    uint64_t k = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
-    k = k >> 63 ? ~k : k | (1ull << 63);
-    if (v != v) k = 1ull << 9;  // above "no candidate", which is 0
-    return (k & ~511ull) | (511 - e);
+// A logit's rank as an unsigned key, ascending with the logit; a NaN lies below
+// every number, and above "no candidate", which is 0.
+__device__ __forceinline__ uint64_t rank_key(double v) {
+    const uint64_t k = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
+    return v != v ? 1 : (k >> 63 ? ~k : k | (1ull << 63));
 }
 template <int ctrl, int rows>
 __device__ __forceinline__ uint64_t dpp_max(uint64_t v) {
@@ -164,16 +162,22 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
             for (int i = 0; i < kPer; ++i) {
                 const int c = lane + kWave * i;
                 v[i] = c < n_experts ? logits[(int64_t)wave * n_experts + c] : -INFINITY;
-                key[i] = c < n_experts ? rank_key(v[i], c) : 0;
+                key[i] = c < n_experts ? rank_key(v[i]) : 0;
             }
             for (int j = 0; j < top_k; ++j) {
                 uint64_t best = key[0];
 #pragma unroll
                 for (int i = 1; i < kPer; ++i) best = key[i] > best ? key[i] : best;
                 best = wave_max(best);
-                if (lane == j) e = 511 - (int)(best & 511);
+                int first = 0;  // the lowest index that holds it: registers go before lanes
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) key[i] = key[i] == best ? 0 : key[i];
+                for (int i = kPer - 1; i >= 0; --i) {
+                    const uint64_t at = __ballot(key[i] == best);
+                    if (at) first = kWave * i + __builtin_ctzll(at);
+                }
+                if (lane == j) e = first;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) key[i] = lane + kWave * i == first ? 0 : key[i];
             }
             // softmax in fp64, each weight rounded once: the first choice holds the largest logit
             uint64_t any_nan = 0;

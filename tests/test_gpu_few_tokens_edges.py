@@ -71,3 +71,23 @@ def test_moe_weights_are_rounded_once(oracle_mod, T, E, k, renorm):
     ratio = np.abs(host(gw).astype(np.float64) - weights) / (1.01 * fr.U * weights)
     log(f"  worst error over the bound {ratio.max():.3f}")
     assert (ratio <= 1).all()
+
+
+@pytest.mark.parametrize("E,low,high", [(2, 0, 1), (64, 3, 60), (300, 5, 299), (512, 130, 448)])
+def test_moe_router_ranks_by_every_bit(oracle_mod, E, low, high):
+    """Logits of 1 and 1 + 2^-48, both exact in the router's fp64 sum: the larger comes first whatever its index."""
+    torch = torch_mod()
+    rng = np.random.default_rng(E)
+    _, dw = _experts(rng, oracle_mod, E, 64, 32, 4, 32, False)
+    X = torch.zeros(1, 64, dtype=torch.bfloat16, device="cuda")
+    X[0, 0], X[0, 1] = 1.0, 2.0 ** -24
+    for first, second in ((high, low), (low, high)):
+        R = torch.full((E, 64), -1.0, device="cuda")
+        R[[low, high], 0] = 1.0
+        R[[low, high], 1] = 0.0
+        R[first, 1] = 2.0 ** -24
+        _, ids, _ = gq.moe_layer(X, *dw, router=R, top_k=2)
+        assert ids[0].tolist() == [first, second]
+    R[first, 1] = 0.0  # equal: the lower index first
+    _, ids, _ = gq.moe_layer(X, *dw, router=R, top_k=2)
+    assert ids[0].tolist() == [low, high]
