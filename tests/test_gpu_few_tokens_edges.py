@@ -91,3 +91,22 @@ def test_moe_router_ranks_by_every_bit(oracle_mod, E, low, high):
     R[first, 1] = 0.0  # equal: the lower index first
     _, ids, _ = gq.moe_layer(X, *dw, router=R, top_k=2)
     assert ids[0].tolist() == [low, high]
+
+
+# (M, d_out, d_in, bits, group, out): a value per token as large as bf16 holds (8 bits: 2^119), whose sums the
+# definition leaves finite
+@pytest.mark.parametrize("M,d_out,d_in,bits,group,out", [
+    (1, 40, 160, 2, 32, "fp32"), (3, 40, 512, 2, 128, "bf16"), (2, 33, 160, 3, 0, "fp32"), (16, 20, 640, 3, 32, "bf16"),
+    (1, 40, 160, 4, 32, "bf16"), (16, 70, 1024, 4, 128, "fp32"), (2, 40, 160, 8, 32, "fp32"), (5, 40, 1024, 8, 128, "bf16")])
+def test_gemv_of_the_largest_bf16_activations(oracle_mod, M, d_out, d_in, bits, group, out):
+    torch = torch_mod()
+    log(f"gemv of large activations M={M} {d_out}x{d_in} {bits} bits g={group} -> {out}")
+    rng = np.random.default_rng(d_in + bits)
+    w = fr.make_packed(rng, oracle_mod, d_out, d_in, bits, group)
+    X, _ = _acts(rng, M, d_in, "bf16")
+    for m in range(M):
+        X[m, int(rng.integers(d_in))] = float(rng.choice([-1, 1])) * (2.0 ** 119 if bits == 8 else torch.finfo(torch.bfloat16).max)
+    x = host(X.float()).astype(np.float64)
+    want, bound = fr.product(x, w)
+    assert np.abs(want).max() < 2.0 ** 127
+    _check(gq.gemv(X, _dev(w), out_dtype=_dt(out)), want, fr.rounded(want, bound, out), "large activations")
