@@ -604,6 +604,14 @@ __device__ __forceinline__ void store_as(void *y, int64_t i, gptq_dtype dt, floa
         static_cast<_Float16 *>(y)[i] = (_Float16)v;
 }
 
-__device__ __forceinline__ float silu_mul(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// silu(g) u.  Below -80 exp(-g) nears fp32's end (and passes it at -88.7) while u
+// may bring the result back: exp(g) in two halves, and 1 + exp(g) is 1.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+    if (g < -80.0f) {
+        const float e = expf(0.5f * g);
+        return g * e * (e * u);
+    }
+    return g / (1.0f + expf(-g)) * u;
+}
 
 }  // namespace gptq

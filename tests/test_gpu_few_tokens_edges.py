@@ -110,3 +110,27 @@ def test_gemv_of_the_largest_bf16_activations(oracle_mod, M, d_out, d_in, bits, 
     want, bound = fr.product(x, w)
     assert np.abs(want).max() < 2.0 ** 127
     _check(gq.gemv(X, _dev(w), out_dtype=_dt(out)), want, fr.rounded(want, bound, out), "large activations")
+
+
+def test_gated_of_very_negative_gates(oracle_mod):
+    """silu(g) u where exp(-g) is past fp32's range, and silu(g) alone near or below its smallest numbers: g from -86
+    to -200, u of 2^100."""
+    torch = torch_mod()
+    d_out, d_in, U0 = 115, 32, 2.0 ** 100
+    gate, up = (dict(q=np.full((d_out, d_in), 0, dtype=np.uint8), scales=np.ones((d_out, 1), dtype=np.float32),
+                     zeros=np.zeros((d_out, 1), dtype=np.float32), kperm=None, bits=8, group=0) for _ in range(2))
+    gate["q"][:, 1] = 86 + np.arange(d_out)  # times x = -1
+    up["q"][:, 0] = 1
+    up["scales"][:] = U0
+    for w in (gate, up):
+        w["packed"] = oracle_mod.pack_codes(w["q"], 8)
+    for dt in ("bf16", "fp16"):
+        X = torch.zeros(2, d_in, dtype=_dt(dt), device="cuda")
+        X[:, 0], X[:, 1], X[1, 0] = 1.0, -1.0, -1.0
+        H = host(gq.gemv_gated(X, _dev(gate), _dev(up), out_dtype=torch.float32)).astype(np.float64)
+        g = -(86.0 + np.arange(d_out))
+        want = g * np.exp(g) / (1 + np.exp(g)) * U0 * np.array([[1.0], [-1.0]])
+        # the sums are exact; two exponentials, three products: 8 ulp of fp32 as for the ordinary values
+        bound = 16 * fr.U * np.abs(want) + 2.0 ** -149
+        log(f"  worst err/bound {(np.abs(H - want) / bound).max():.3g}")
+        assert (np.abs(H - want) <= bound).all()
