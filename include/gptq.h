@@ -425,7 +425,8 @@ typedef struct {
  *   w       the layer.  gate and up agree in d_out, d_in, bits, group_size and
  *           kperm (they see the same inputs, hence one Hessian and one order).
  *   bias    [d_out] fp32 or NULL.
- *   Y, H    fp16, bf16 or fp32 [M][ldy] out, ldy >= d_out; not X's memory.
+ *   Y, H    fp16, bf16 or fp32 [M][ldy] out, ldy >= d_out; no element may be X's
+ *           memory (GPTQ_ERR_INVALID_ARG).
  *   ws      scratch of gptq_workspace_bytes(GPTQ_OP_GEMV, 0, d_in, M, NULL), used
  *           (and needed) only with a kperm and M * d_in > GPTQ_GEMV_GATHERS, below
  *           which the kernel gathers X itself; 16-byte aligned.
@@ -471,7 +472,7 @@ GPTQ_API gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t 
  *           weight is rounded once.  As inputs, an id outside
  *           0 .. n_experts - 1 adds nothing (padding), and one that a token
  *           names twice counts with the sum of its weights.
- *   Y       fp16, bf16 or fp32 [T][ldy] out, ldy >= d; not X's memory.
+ *   Y       fp16, bf16 or fp32 [T][ldy] out, ldy >= d, apart from X as above.
  *   ws      scratch of gptq_moe_workspace_bytes(), 16-byte aligned.
  * 1 <= top_k <= min(n_experts, 16), n_experts <= 512.  h passes between the two
  * products with 16 significant bits (24 for an fp32 Y), in bf16 pieces; every

@@ -509,7 +509,7 @@ def _pitch(t, rows, cols):
 
 def gemv(X, w: PackedWeight, bias=None, Y=None, out_dtype=None, ws=None, stream=None):
     """Y = X' W_hat^T (+ bias) for at most 16 tokens: X fp16 or bf16 [M][d_in], w a packed layer of 2, 3, 4 or 8 bits,
-    bias fp32 [d_out]; Y [M][d_out] in X's type, or in out_dtype (fp16, bf16, fp32)."""
+    bias fp32 [d_out]; Y [M][d_out], apart from X, in X's type or in out_dtype (fp16, bf16, fp32)."""
     torch, lib, act, res = _few_init()
     if stream is not None:
         with _few_on(stream, w.device, torch):

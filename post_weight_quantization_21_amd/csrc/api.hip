@@ -101,6 +101,26 @@ gptq_status check_few(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, in
     return GPTQ_OK;
 }
 
+// Whether any two of n rows of bytes, at a and at b, share one.
+bool rows_overlap(const void *a, int64_t a_pitch, int64_t a_row, const void *b, int64_t b_pitch, int64_t b_row, int64_t n) {
+    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+    if (a0 + (n - 1) * a_pitch + a_row <= b0 || b0 + (n - 1) * b_pitch + b_row <= a0) return false;
+    for (int64_t i = 0; i < n; ++i)
+        for (int64_t j = 0; j < n; ++j) {
+            const uintptr_t r = a0 + i * a_pitch, t = b0 + j * b_pitch;
+            if (r < t + b_row && t < r + a_row) return true;
+        }
+    return false;
+}
+
+// The workgroups read X while others write Y.
+gptq_status check_apart(const void *X, int64_t M, int64_t ldx, int64_t d_in, const void *Y, gptq_dtype y_dt, int64_t ldy,
+                        int64_t d_out, const char *fn) {
+    const int64_t y = y_dt == GPTQ_DT_F32 ? 4 : 2;
+    if (rows_overlap(X, 2 * ldx, 2 * d_in, Y, y * ldy, y * d_out, M)) return fail(GPTQ_ERR_INVALID_ARG, "%s: X and the result overlap", fn);
+    return GPTQ_OK;
+}
+
 gptq_status run_gemv_checked(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed *w,
                              const gptq_packed *up, const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws,
                              size_t ws_bytes, hipStream_t stream, const char *fn) {
@@ -114,6 +134,8 @@ gptq_status run_gemv_checked(const void *X, gptq_dtype x_dt, int64_t M, int64_t 
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
     if (need > 0 && !aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    st = check_apart(X, M, ldx, w->d_in, Y, y_dt, ldy, w->d_out, fn);
+    if (st != GPTQ_OK) return st;
     return hip_status(gptq::run_gemv(X, x_dt, M, ldx, *w, up, bias, Y, y_dt, ldy, ws, stream), fn);
 }
 
@@ -505,6 +527,8 @@ gptq_status gptq_moe_layer(const void *X, gptq_dtype x_dtype, int64_t T, int64_t
     if (!ws || ws_bytes < need)
         return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
     if (!aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    st = check_apart(X, T, ldx, gate->d_in, Y, y_dtype, ldy, gate->d_in, fn);
+    if (st != GPTQ_OK) return st;
     return hip_status(gptq::run_moe(X, x_dtype, T, ldx, router, router_dtype, n_experts, top_k, renormalize ? 1 : 0, *gate,
                                     *up, *down, ids, weights, Y, y_dtype, ldy, ws, stream),
                       fn);

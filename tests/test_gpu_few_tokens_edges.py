@@ -134,3 +134,27 @@ def test_gated_of_very_negative_gates(oracle_mod):
         bound = 16 * fr.U * np.abs(want) + 2.0 ** -149
         log(f"  worst err/bound {(np.abs(H - want) / bound).max():.3g}")
         assert (np.abs(H - want) <= bound).all()
+
+
+def test_few_tokens_results_between_the_rows_of_x(oracle_mod):
+    """X and the results as columns of one tensor, next to each other but apart: allowed, and X stays as it was."""
+    torch = torch_mod()
+    rng = np.random.default_rng(21)
+    d, M, E = 128, 5, 4
+    w = _dev(fr.make_packed(rng, oracle_mod, d, d, 4, 32))
+    _, dw = _experts(rng, oracle_mod, E, d, d, 4, 32, False)
+    X, _ = _acts(rng, M, d, "bf16")
+    ids = torch.arange(M, dtype=torch.int32, device="cuda").remainder(E).view(M, 1)
+    weights = torch.ones(M, 1, device="cuda")
+    buf = torch.zeros(M, 4 * d, dtype=torch.bfloat16, device="cuda")
+    x, y, h, z = buf.split(d, dim=1)
+    x.copy_(X)
+    gq.gemv(x, w, Y=y)
+    gq.gemv_gated(x, w, w, H=h)
+    gq.moe_layer(x, *dw, ids=ids, weights=weights, Y=z)
+    assert torch.equal(x, X) and torch.equal(y, gq.gemv(X, w)) and torch.equal(h, gq.gemv_gated(X, w, w))
+    assert torch.equal(z, gq.moe_layer(X, *dw, ids=ids, weights=weights)[0])
+    for call in (lambda: gq.gemv(X, w, Y=X), lambda: gq.gemv_gated(X, w, w, H=X), lambda: gq.moe_layer(X, *dw, ids=ids, weights=weights, Y=X)):
+        with pytest.raises(gq.GptqError) as ei:
+            call()
+        assert ei.value.status == gq.ERR_INVALID_ARG
