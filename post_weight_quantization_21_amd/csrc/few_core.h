@@ -277,8 +277,7 @@ __device__ __forceinline__ void load_unit(__amdgpu_buffer_rsrc_t p, uint32_t at,
 // Prepared x: M rows of whole quads as pieces of eight 16-bit values in slot
 // order, piece (4 (4 step + u) + f) M + m holding fragment f of unit u of row m;
 // columns past the last unit are zero.  A lane's operand of a matrix instruction
-// is one piece, the rows of a lane row next to each other.  Planes (terms of x)
-// follow each other.
+// is one piece, the rows of a lane row next to each other.
 __host__ __device__ inline int64_t prepared_values(int64_t rows, int units) { return rows * few_quads(units) * kQuad; }
 template <int b>
 __device__ __forceinline__ int64_t prepared_at(int col, int M, int m) {
@@ -287,18 +286,21 @@ __device__ __forceinline__ int64_t prepared_at(int col, int M, int m) {
 }
 
 // Activations of a product: rows as they are, rows whose columns are read in
-// packed order, or prepared in memory.
-enum FewX { kRawX, kOrderedX, kPreparedX };
+// packed order, prepared in memory, or fp32 rows, which become two planes of fp16
+// that follow each other in LDS: each value times its row's power of two rounded
+// to fp16, and the rest rounded to fp16.
+enum FewX { kRawX, kOrderedX, kPreparedX, kFloatX };
 struct XRows {
-    const uint16_t *base;
-    int64_t ld;            // between rows; prepared: between planes
+    const void *base;
+    int64_t ld;            // between rows (not prepared)
     bool gathered;         // raw and ordered: rows are numbered by `row` of lane m, else m itself
     int32_t row;
     const int32_t *order;  // ordered: x's column of each packed one
+    float scale;           // fp32: the power of two of row m in lane m
 };
 
-// A phase's x on its way into LDS, in batches of kUnits units a thread.
-template <int b, int P, FewX kX>
+// A phase's x on its way into LDS, in batches of kUnits units a thread (fp32: half as many).
+template <int b, FewX kX>
 struct StageX {
     static constexpr int kUnits = 1;
     u32x4 v[4 * kUnits];
@@ -306,14 +308,15 @@ struct StageX {
     int per_row, items, first, total;
     __device__ __forceinline__ void init(int M, int units, int q0, int nq) {
         per_row = 16 * nq;
-        magic = 0xFFFFFFFFu / (uint32_t)per_row + 1;
-        items = P * M * per_row;  // units
+        magic = 0xFFFFFFFFu / (uint32_t)(kX == kFloatX ? 4 * per_row : per_row) + 1;
+        items = M * per_row;  // units
         first = 16 * q0;
-        total = (items + kUnits * kFewThreads - 1) / (kUnits * kFewThreads);
+        total = ((kX == kFloatX ? 2 * items : items) + kUnits * kFewThreads - 1) / (kUnits * kFewThreads);
     }
     // Raw: unit i of the phase is unit u of row r.  Prepared: unit i is pieces 4 i .. of the phase, plane by plane.
-    // Ordered: pieces as prepared, each gathered value by value.
+    // Ordered: pieces as prepared, each gathered value by value.  fp32: piece i, two a thread, is piece p of row r.
     __device__ __forceinline__ void load(const XRows &x, int M, int units, int batch) {
+        const uint16_t *base = static_cast<const uint16_t *>(x.base);
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
             if constexpr (kX == kRawX) {
@@ -323,7 +326,7 @@ struct StageX {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[4 * k + j] = (u32x4){0, 0, 0, 0};
                 if (i < items && u < units) {
-                    const u32x4 *src = reinterpret_cast<const u32x4 *>(x.base + row * x.ld + u * kUnit);
+                    const u32x4 *src = reinterpret_cast<const u32x4 *>(base + row * x.ld + u * kUnit);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[4 * k + j] = src[j];
                 }
@@ -335,7 +338,7 @@ struct StageX {
                     const int r = i - piece * M, m = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
                     v[4 * k + j] = (u32x4){0, 0, 0, 0};
                     if (i < 4 * items && u < units) {
-                        const uint16_t *row = x.base + m * x.ld;
+                        const uint16_t *row = base + m * x.ld;
                         const int32_t *at = x.order + u * kUnit + f0;
                         uint32_t h[8];
 #pragma unroll
@@ -343,18 +346,29 @@ struct StageX {
                         v[4 * k + j] = (u32x4){h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
                     }
                 }
+            } else if constexpr (kX == kFloatX) {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    const int i = threadIdx.x + (2 * (kUnits * batch + k) + j / 2) * kFewThreads, r = __umulhi(i, magic), p = i - r * 4 * per_row;
+                    const int u = first + (p >> 2), f = p & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
+                    v[4 * k + j] = v[4 * k + j + 1] = (u32x4){0, 0, 0, 0};
+                    if (i < 4 * items && u < units) {
+                        const float *src = static_cast<const float *>(x.base) + r * x.ld + u * kUnit + f0;
+                        v[4 * k + j] = *reinterpret_cast<const u32x4 *>(src);  // the piece's two runs of four columns
+                        v[4 * k + j + 1] = *reinterpret_cast<const u32x4 *>(src + (b == 2 ? 8 : 4));
+                    }
+                }
             } else {
-                const int plane = 4 * M * per_row;  // pieces
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads, p = (i >= plane) + (P > 2 && i >= 2 * plane);
+                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads;
                     v[4 * k + j] = (u32x4){0, 0, 0, 0};  // (left alone, it would be kept through the phase before)
-                    if (i < 4 * items) v[4 * k + j] = *reinterpret_cast<const u32x4 *>(x.base + p * x.ld + ((int64_t)4 * first * M + i - p * plane) * 8);
+                    if (i < 4 * items) v[4 * k + j] = *reinterpret_cast<const u32x4 *>(base + ((int64_t)4 * first * M + i) * 8);
                 }
             }
         }
     }
-    __device__ __forceinline__ void store(uint16_t *xs, int M, int batch) const {
+    __device__ __forceinline__ void store(uint16_t *xs, const XRows &x, int M, int batch) const {
         u32x4 *dst = reinterpret_cast<u32x4 *>(xs);
 #pragma unroll
         for (int k = 0; k < kUnits; ++k) {
@@ -376,6 +390,23 @@ struct StageX {
                                             : __builtin_amdgcn_perm(t[(c0 + apart) / 2], t[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
                     }
                     dst[(4 * u + f) * M + r] = o;
+                }
+            } else if constexpr (kX == kFloatX) {
+#pragma unroll
+                for (int j = 0; j < 4; j += 2) {
+                    const int i = threadIdx.x + (2 * (kUnits * batch + k) + j / 2) * kFewThreads, r = __umulhi(i, magic), p = i - r * 4 * per_row;
+                    const float scale = __shfl(x.scale, r & (kWave - 1));
+                    if (i >= 4 * items) continue;
+                    _Float16 hi[8], lo[8];
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) {
+                        const int c = slot_col<b>(0, n), run = c >= (b == 2 ? 8 : 4);
+                        const float a = __uint_as_float(v[4 * k + j + run][c & 3]) * scale;
+                        hi[n] = (_Float16)a;
+                        lo[n] = (_Float16)(a - (float)hi[n]);
+                    }
+                    dst[p * M + r] = __builtin_bit_cast(u32x4, (f16x8){hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]});
+                    dst[4 * items + p * M + r] = __builtin_bit_cast(u32x4, (f16x8){lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]});
                 }
             } else {
 #pragma unroll
@@ -445,11 +476,12 @@ struct StageGroups {
 // registers, one computed while the other is loaded (4 to 8 KB of a wave in
 // flight at 4 bits); past the wave's run nothing is read.  x is zero past the
 // last unit.
-template <int b, typename T, int P, int kMats, bool kSplit, FewX kX>
+template <int b, typename T, int kMats, bool kSplit, FewX kX>
 __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShape &w, int64_t row0, int rows, const XRows &x,
                                                int M, int wave, unsigned char *smem) {
     typedef typename Vec8<T>::V V;
     typedef Codes<b, T> C;
+    constexpr int P = kX == kFloatX ? 2 : 1;  // planes of x
     const int lane = threadIdx.x % kWave, kb = lane >> 4, lg = w.lg;
     const int units = w.units, quads = few_quads(units), phase_quads = few_phase(w, P * M);
     const int tile = wave >> lg, slice = wave & ((1 << lg) - 1), tiles = kFewWaves >> lg;
@@ -474,7 +506,7 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
     };
     floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
     C codes;
-    StageX<b, P, kX> stage;
+    StageX<b, kX> stage;
     StageGroups<b, T, kMats> groups;
 #pragma unroll
     for (int k = 0; k < kMats; ++k) {
@@ -497,11 +529,11 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
         groups.init(ga, gb, tiles * kTileRows);
         groups.load(0);
         load(wa, hs, he);
-        stage.store(xs, M, 0);
+        stage.store(xs, x, M, 0);
         groups.store(entries, 0);
         for (int t = 1; t < stage.total; ++t) {
             stage.load(x, M, units, t);
-            stage.store(xs, M, t);
+            stage.store(xs, x, M, t);
         }
         for (int t = groups.kBatch; t < groups.total; t += groups.kBatch) {
             groups.load(t);

@@ -38,9 +38,9 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvAr
     const int wave = few_wave(), lg = a.shape.lg;
     const int lt = 3 - lg - LR;  // log2 of the row tiles
     const int64_t r0 = (int64_t)blockIdx.x * kTileRows << lt, d_out = a.shape.d_out;
-    const XRows x = {a.x, a.ldx, false, 0, a.order};
+    const XRows x = {a.x, a.ldx, false, 0, a.order, 0.0f};
     float *sums = reinterpret_cast<float *>(smem);
-    const floatx4 acc = few_product<b, T, 1, R, kSplit, kX>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
+    const floatx4 acc = few_product<b, T, R, kSplit, kX>(a.w, a.shape, r0, (int)std::min<int64_t>(d_out - r0, kTileRows * kFewWaves), x,
                                                             a.M, wave, smem);
     few_share(sums, wave, acc, a.M);
     for (int n = threadIdx.x; n < a.M * kTileRows << lt; n += kFewThreads) {

@@ -10,11 +10,12 @@
 //   down:    the same for the second product, whose rows by pair are left in fp32
 //   combine: Y[t] = the sum of the token's pairs, expert by expert, weighted
 //
-// h = silu(gate) * up between the products is a sum of bf16 values, two for a
-// 16-bit result and three for an fp32 one (16 and 24 significant bits): each is
-// an operand plane of the down product, whose weights are exact in bf16 up to a
-// constant, so nothing of h is lost that the result could show.  One bf16 or fp16
-// value per h costs 1.5 times the error of the final rounding.
+// h = silu(gate) * up passes between the products in fp32.  The second one, whose
+// weights q - z are exact in fp16, takes it as two fp16 values of 11 bits and a
+// sign each, after a power of two per row has brought the row's largest to 2^14 ..
+// 2^15: a value loses at most 2^-24 of itself, or 2^-40 of its row's largest.  (A
+// sum of two bf16 values, 2^-17, was the same in error against 64 bits for 16-bit
+// results, but twice as many of them fell to the other side of their rounding.)
 #include <algorithm>
 #include <cmath>
 
@@ -39,6 +40,9 @@ struct Token {  // a token's pairs, ascending
 struct Lists {
     Token token[kMoeMaxTokens];
     Expert expert[kMaxPairs];
+    // of a pair's h: the largest magnitude, as fp32 bits; a line each, as the atomics on one line wait for each other (32
+    // pairs of 14336 values side by side: 142 us instead of 115)
+    uint32_t top[kMaxPairs][32];
 };
 
 template <typename T>
@@ -146,6 +150,7 @@ __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__
     __shared__ float weight_of[kMaxPairs];
     const int tid = threadIdx.x, wave = few_wave(), lane = tid % kWave;
     if (tid < kMoeMaxExperts) tokens_of[tid] = 0;
+    if (tid < kMaxPairs) lists->top[tid][0] = 0;
     int e = -1;  // lane j < top_k: the token's j-th choice
     bool chosen = false;
     if (wave < n_tok) {
@@ -280,18 +285,15 @@ __global__ __launch_bounds__(256) void prepare_pairs_kernel(const uint16_t *__re
     for (int m = 0; m < n; ++m) out[prepared_at<b>(k, n, m)] = k < d ? X[e.token[m] * ldx + c] : 0;
 }
 
-// Prepared h with its columns in the packed order of the down product.
-template <int b>
-__global__ __launch_bounds__(256) void permute_pairs_kernel(const uint16_t *__restrict__ h, int64_t plane, int ff,
-                                                            const Lists *__restrict__ lists, const int32_t *__restrict__ kperm,
-                                                            uint16_t *__restrict__ out) {
+// h with its columns in the packed order of the down product.
+__global__ __launch_bounds__(256) void permute_pairs_kernel(const float *__restrict__ h, int ff, const Lists *__restrict__ lists,
+                                                            const int32_t *__restrict__ kperm, float *__restrict__ out) {
     const Expert &e = lists->expert[blockIdx.y];
     const int k = blockIdx.x * 256 + threadIdx.x, n = e.count;
-    if (n == 0) return;
-    int c = k < ff ? kperm[(int64_t)e.expert * ff + k] : 0;
+    if (n == 0 || k >= ff) return;
+    int c = kperm[(int64_t)e.expert * ff + k];
     c = c < 0 ? 0 : (c >= ff ? ff - 1 : c);
-    const int64_t base = blockIdx.z * plane + prepared_values(e.start, ff / kUnit);
-    for (int m = 0; m < n; ++m) out[base + prepared_at<b>(k, n, m)] = k < ff ? h[base + prepared_at<b>(c, n, m)] : 0;
+    for (int m = 0; m < n; ++m) out[(int64_t)(e.start + m) * ff + k] = h[(int64_t)(e.start + m) * ff + c];
 }
 
 struct GateUpArgs {
@@ -300,10 +302,8 @@ struct GateUpArgs {
     const uint16_t *x;  // rows by token, or prepared by pair
     int64_t ldx;
     const int32_t *order;  // ordered: of every expert
-    int planes;
-    const Lists *lists;
-    __bf16 *h;
-    int64_t h_plane;
+    Lists *lists;
+    float *h;  // rows by pair
 };
 
 // 13 us for 6 experts of 1408 x 2048 in 4 bits (19 MB), 37 us for the ~82 that 16
@@ -320,61 +320,61 @@ __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(Gat
     const int ff = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * ff + r0;
     constexpr bool rows = kX != kPreparedX;
-    const XRows x = {rows ? a.x : a.x + prepared_values(start, a.shape.units), rows ? a.ldx : 0, rows, token,
-                     kX == kOrderedX ? a.order + (int64_t)e.expert * a.shape.units * kUnit : nullptr};
-    const floatx4 acc = few_product<b, T, 1, 2, kSplit, kX>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
+    const XRows x = {rows ? a.x : a.x + prepared_values(start, a.shape.units), a.ldx, rows, token,
+                     kX == kOrderedX ? a.order + (int64_t)e.expert * a.shape.units * kUnit : nullptr, 0.0f};
+    const floatx4 acc = few_product<b, T, 2, kSplit, kX>(a.w, a.shape, row, ff - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
-    __bf16 *h = a.h + prepared_values(start, ff / kUnit);
     for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
-        const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
-        if (r0 + c >= ff) continue;
+        const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);  // (m is one in 16 << lt <= 64 lanes)
         const int w0 = (c >> 4) << (1 + lg);
-        float v = silu_mul(few_sum(sums, w0, lg, count, m, c & 15), few_sum(sums, w0 + (1 << lg), lg, count, m, c & 15));
-        __bf16 *dst = h + prepared_at<b>(r0 + c, count, m);
-        for (int p = 0; p < a.planes; ++p) {
-            const __bf16 t = (__bf16)v;
-            dst[p * a.h_plane] = t;
-            v -= (float)t;  // exact
+        const float v = silu_mul(few_sum(sums, w0, lg, count, m, c & 15), few_sum(sums, w0 + (1 << lg), lg, count, m, c & 15));
+        uint32_t most = 0;
+        if (r0 + c < ff) {
+            a.h[(int64_t)(start + m) * ff + r0 + c] = v;
+            most = __float_as_uint(v) & 0x7FFFFFFFu;
         }
-    }
-    if (r0 + (kTileRows << lt) >= ff) {  // the rest of h's last step counts as zero
-        const int rest = few_steps(ff / kUnit) * kStep - ff;
-        for (int n = threadIdx.x; n < count * rest; n += kFewThreads)
-            for (int p = 0; p < a.planes; ++p) h[p * a.h_plane + prepared_at<b>(ff + n % rest, count, n / rest)] = (__bf16)0.0f;
+        for (int o = 8 << lt; o > 0; o >>= 1) most = std::max(most, (uint32_t)__shfl_xor((int)most, o));
+        if (c == 0) atomicMax(a.lists->top[start + m], most);  // a maximum, whatever the order
     }
 }
 
 struct DownArgs {
     FewMat w;
     FewShape shape;
-    const uint16_t *h;  // prepared, planes of rows by pair
-    int64_t h_plane;
+    const float *h;  // rows by pair
     const Lists *lists;
     float *part;  // rows by pair
 };
 
-// P matrix instructions per fragment of weights (two where the constant is one of
-// its own), as the weights are unpacked once for all planes.  8 us, 28 us and 64-71
-// us for the experts of gate_up_kernel's figures: half their bytes in 60-85% of
-// the time, for h has P planes and K is d_ff.  Adding a token's pairs here, by the
-// last workgroup to arrive, took 35 and 200 us: the fence before its count.
-template <int b, int P, bool kSplit>
+// The exponent that brings a row's largest magnitude (fp32 bits) to 2^14 .. 2^15,
+// or a smaller row up by as much as fp32 has.
+__device__ __forceinline__ int row_exponent(uint32_t top) { return std::min(126, 127 + 14 - (int)(top >> 23)); }
+__device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Two matrix instructions per fragment of weights, which are unpacked once for both
+// planes of h.  7.2 us, 26 us and 60 us for the experts of gate_up_kernel's figures:
+// half their bytes in 55-70% of the time, for h has two planes and K is d_ff.  Adding
+// a token's pairs here, by the last workgroup to arrive, took 35 and 200 us: the
+// fence before its count.
+template <int b, bool kSplit>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     const Expert &e = a.lists->expert[blockIdx.y];
     const int start = e.start, count = e.count, wave = few_wave(), lg = a.shape.lg;
     if (count == 0) return;
     const int lt = 3 - lg;
-    const int d = a.shape.d_out, r0 = blockIdx.x * kTileRows << lt;
+    const int d = a.shape.d_out, ff = a.shape.units * kUnit, r0 = blockIdx.x * kTileRows << lt;
     const int64_t row = (int64_t)e.expert * d + r0;
-    const XRows x = {a.h + prepared_values(start, a.shape.units), a.h_plane, false, 0, nullptr};
-    const floatx4 acc = few_product<b, __bf16, P, 1, kSplit, kPreparedX>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
+    const float scale = power_of_2(row_exponent(a.lists->top[start + std::min((int)(threadIdx.x & (kMoeMaxTokens - 1)), count - 1)][0]));
+    const XRows x = {a.h + (int64_t)start * ff, ff, false, 0, nullptr, scale};
+    const floatx4 acc = few_product<b, _Float16, 1, kSplit, kFloatX>(&a.w, a.shape, row, d - r0, x, count, wave, smem);
     float *sums = reinterpret_cast<float *>(smem);
     few_share(sums, wave, acc, count);
     for (int n = threadIdx.x; n < count * kTileRows << lt; n += kFewThreads) {
         const int m = n >> (4 + lt), c = n & ((kTileRows << lt) - 1);
-        if (r0 + c < d) a.part[(int64_t)(start + m) * d + r0 + c] = few_sum(sums, (c >> 4) << lg, lg, count, m, c & 15);
+        const float back = power_of_2(-row_exponent(a.lists->top[start + m][0]));
+        if (r0 + c < d) a.part[(int64_t)(start + m) * d + r0 + c] = few_sum(sums, (c >> 4) << lg, lg, count, m, c & 15) * back;
     }
 }
 
@@ -396,21 +396,19 @@ __global__ __launch_bounds__(256) void combine_kernel(const float *__restrict__ 
     store_as(y, blockIdx.y * ldy + c, y_dt, y0);
 }
 
-constexpr int kMaxPlanes = 3;
 struct Layout {
     size_t logits, lists, h, part, xg, hg, bytes;
 };
 Layout layout(int64_t T, int64_t d, int64_t d_ff, int n_experts, int top_k) {
-    const size_t pairs = (size_t)T * top_k;
-    const size_t xv = prepared_values((int64_t)pairs, (int)(d / kUnit)), hv = prepared_values((int64_t)pairs, (int)(d_ff / kUnit));
+    const size_t pairs = (size_t)T * top_k, hb = align_up(pairs * d_ff * 4, 256);
     Layout l;
     l.logits = 0;
     l.lists = align_up((size_t)T * n_experts * sizeof(double), 256);
     l.h = l.lists + align_up(sizeof(Lists), 256);
-    l.part = l.h + align_up(kMaxPlanes * hv * 2, 256);
+    l.part = l.h + hb;
     l.xg = l.part + align_up(pairs * d * 4, 256);
-    l.hg = l.xg + align_up(xv * 2, 256);
-    l.bytes = l.hg + align_up(kMaxPlanes * hv * 2, 256);
+    l.hg = l.xg + align_up((size_t)prepared_values((int64_t)pairs, (int)(d / kUnit)) * 2, 256);
+    l.bytes = l.hg + hb;
     return l;
 }
 
@@ -435,14 +433,6 @@ void launch_gate_up(const GateUpArgs &g, FewX x, dim3 grid, hipStream_t s) {
                              : (x == kOrderedX ? gate_up_kernel<b, T, kSplit, kOrderedX> : gate_up_kernel<b, T, kSplit, kPreparedX>);
     kernel<<<grid, kFewThreads, g.shape.lds, s>>>(g);
 }
-template <int b, bool kSplit>
-void launch_down(const DownArgs &w, int planes, dim3 grid, hipStream_t s) {
-    if (planes == 3)
-        down_kernel<b, 3, kSplit><<<grid, kFewThreads, w.shape.lds, s>>>(w);
-    else
-        down_kernel<b, 2, kSplit><<<grid, kFewThreads, w.shape.lds, s>>>(w);
-}
-
 template <int b, typename T>
 void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     const int64_t d = c.gate->d_in, ff = c.gate->d_out, pairs = c.T * c.top_k;
@@ -457,9 +447,7 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     g.x = static_cast<const uint16_t *>(c.X);
     g.ldx = c.ldx;
     g.lists = lists;
-    g.h = reinterpret_cast<__bf16 *>(c.ws + l.h);
-    g.h_plane = prepared_values(pairs, (int)(ff / kUnit));
-    g.planes = c.y_dt == GPTQ_DT_F32 ? 3 : 2;
+    g.h = reinterpret_cast<float *>(c.ws + l.h);
     // gathered by the products up to the same size as in gemv.hip, with an expert's rows for M: one token of 64 experts x
     // 1408 x 2048 takes 30.4 us against 31.7 through a kernel of its own
     g.order = c.gate->kperm;
@@ -478,22 +466,17 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     DownArgs w;
     const int64_t tiles = ceil_div(d, kTileRows);
     w.w = few_mat(*c.down);
-    w.shape = few_shape(*c.down, load.experts * tiles, kFewWaves, g.planes * load.rows, g.planes * (int)c.T);
-    w.h = reinterpret_cast<const uint16_t *>(g.h);
-    w.h_plane = g.h_plane;
+    w.shape = few_shape(*c.down, load.experts * tiles, kFewWaves, 2 * load.rows, 2 * (int)c.T);
+    w.h = g.h;
     w.lists = lists;
     w.part = reinterpret_cast<float *>(c.ws + l.part);
     if (c.down->kperm) {
-        uint16_t *hg = reinterpret_cast<uint16_t *>(c.ws + l.hg);
-        permute_pairs_kernel<b><<<dim3((unsigned)(few_quads(w.shape.units) * kQuad / 256), slots, g.planes), 256, 0, s>>>(
-            w.h, w.h_plane, (int)ff, lists, c.down->kperm, hg);
+        float *hg = reinterpret_cast<float *>(c.ws + l.hg);
+        permute_pairs_kernel<<<dim3((unsigned)ceil_div(ff, 256), slots), 256, 0, s>>>(g.h, (int)ff, lists, c.down->kperm, hg);
         w.h = hg;
     }
-    const dim3 dgrid((unsigned)ceil_div(tiles, kFewWaves >> w.shape.lg), slots);
-    if (few_split(*c.down))
-        launch_down<b, true>(w, g.planes, dgrid, s);
-    else
-        launch_down<b, false>(w, g.planes, dgrid, s);
+    auto down = few_split(*c.down) ? down_kernel<b, true> : down_kernel<b, false>;
+    down<<<dim3((unsigned)ceil_div(tiles, kFewWaves >> w.shape.lg), slots), kFewThreads, w.shape.lds, s>>>(w);
     combine_kernel<<<dim3((unsigned)ceil_div(d, 256), (unsigned)c.T), 256, 0, s>>>(w.part, lists, (int)d, c.Y, c.ldy, c.y_dt);
 }
 

@@ -46,3 +46,19 @@ def test_integers_of_16_bits_for_16_bit_results(oracle_mod):
     x = fx.acts(rng, 6, 128)
     _, n_pieces = fx.moe(x, gate, up, down, rng.integers(0, 2, size=(6, 1)), np.ones((6, 1)))
     assert n_pieces == 2
+
+
+@pytest.mark.parametrize("out", ["bf16", "fp16"])
+def test_pieces_of_h_show_in_16_bit_results(oracle_mod, out):
+    """Two bf16 values for h change roundings of the cases with 16-bit results; three do not."""
+    torch = pytest.importorskip("torch")
+    dt = {"bf16": torch.bfloat16, "fp16": torch.float16}[out]
+    rng = np.random.default_rng(16 + 4096 + 640 + 3)
+    gate, up, down = fx.experts(rng, oracle_mod, 2, 4096, 640, 3, 32, False, True)
+    if out == "fp16":
+        down["scales"] = down["scales"] / np.float32(512)
+    x = fx.acts(rng, 16, 4096)
+    h = _hidden(x, gate, up, 0)
+    y = [torch.from_numpy(fr.product(fx.pieces(h, n), down, 0)[0].astype(np.float32)).to(dt) for n in (2, 3)]
+    want = torch.from_numpy(fr.product(h, down, 0)[0].astype(np.float32)).to(dt)
+    assert not torch.equal(y[0], want) and torch.equal(y[1], want)

@@ -95,3 +95,47 @@ def test_moe_of_integers(oracle_mod, T, d, ff, E, k, bits, group, dt, out, perm)
     got, _, _ = gq.moe_layer(cuda(x.astype(np.float32)).to(_dt(dt)), *_pair(gate, up), _dev(down), ids=cuda(ids), weights=cuda(weights),
                              out_dtype=_dt(out))
     _equal(got, want, out)
+
+
+# h of more than 17 bits with 16-bit results: enough of them for a rounding to fall to the other side
+@pytest.mark.parametrize("T,d,ff,E,k,bits,group,dt,out,perm", [
+    (16, 4096, 640, 2, 2, 3, 32, "bf16", "bf16", False),
+    (16, 4096, 640, 2, 2, 8, 128, "fp16", "fp16", True),
+    (16, 4096, 1152, 2, 1, 2, 64, "bf16", "fp16", True),
+])
+def test_moe_of_large_integers_with_16_bit_results(oracle_mod, T, d, ff, E, k, bits, group, dt, out, perm):
+    log(f"moe of large integers T={T} d={d} ff={ff} E={E} k={k} {bits} bits g={group} {dt}->{out} perm={perm}")
+    rng = np.random.default_rng(T + d + ff + bits)
+    gate, up, down = fx.experts(rng, oracle_mod, E, d, ff, bits, group, perm, True)
+    if out == "fp16":
+        down["scales"] = down["scales"] / np.float32(512)
+    x = fx.acts(rng, T, d)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    weights = rng.choice(np.array([1.0, 2.0], dtype=np.float32), size=ids.shape)
+    want, pieces = fx.moe(x, gate, up, down, ids, weights.astype(np.float64))
+    assert pieces == 3
+    got, _, _ = gq.moe_layer(cuda(x.astype(np.float32)).to(_dt(dt)), *_pair(gate, up), _dev(down), ids=cuda(ids), weights=cuda(weights),
+                             out_dtype=_dt(out))
+    _equal(got, want, out)
+
+
+@pytest.mark.parametrize("bits,dt", [(4, "bf16"), (8, "fp16")])
+def test_moe_rows_of_every_size(oracle_mod, bits, dt):
+    """Each token's h is scaled by a power of two of its own: up matrices of 2^-60 to 2^60, tokens whose h is zero."""
+    torch = torch_mod()
+    rng = np.random.default_rng(bits)
+    E, T, d, ff = 3, 9, 128, 640
+    gate, up, down = fx.experts(rng, oracle_mod, E, d, ff, bits, 32, False, True)
+    x = fx.acts(rng, T, d)
+    ids = np.arange(T, dtype=np.int32).reshape(T, 1) % E
+    weights = np.ones((T, 1), dtype=np.float32)
+    want, _ = fx.moe(x, gate, up, down, ids, weights.astype(np.float64))
+    X = cuda(x.astype(np.float32)).to(_dt(dt))
+    for exps in ((-60, 0, 60), (60, -100, 3), (-126 + 40, 80, 0)):
+        scaled = dict(up, scales=up["scales"] * np.float32(2) ** np.array(exps, dtype=np.float32)[:, None, None])
+        got = gq.moe_layer(X, *_pair(gate, scaled), _dev(down), ids=cuda(ids), weights=cuda(weights), out_dtype=torch.float32)[0]
+        _equal(got, want * 2.0 ** np.array(exps, dtype=np.float64)[ids], "fp32")
+    X[4] = 0
+    got = gq.moe_layer(X, *_pair(gate, up), _dev(down), ids=cuda(ids), weights=cuda(weights), out_dtype=torch.float32)[0]
+    want[4] = 0
+    _equal(got, want, "fp32")
