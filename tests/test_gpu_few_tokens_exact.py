@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 import few_exact as fx
+import few_ref as fr
 import post_weight_quantization_21_amd as gq
 from gpu_util import cuda, host, log, torch_mod
 from test_gpu_few_tokens import _dev, _dt
@@ -139,3 +140,28 @@ def test_moe_rows_of_every_size(oracle_mod, bits, dt):
     got = gq.moe_layer(X, *_pair(gate, up), _dev(down), ids=cuda(ids), weights=cuda(weights), out_dtype=torch.float32)[0]
     want[4] = 0
     _equal(got, want, "fp32")
+
+
+@pytest.mark.parametrize("bits", [2, 3, 4, 8])
+def test_moe_small_hidden_values_beside_large_ones(oracle_mod, bits):
+    """One hidden value of 2^20 units that the second product does not use (its codes are the zero point), beside values
+    from 2^-20 to 2^20 of its units: what a value loses is at most 2^-24 of itself or 2^-39 of the largest."""
+    torch = torch_mod()
+    rng = np.random.default_rng(bits)
+    d, ff = 64, 64
+    gate, up = fx.gate_and_up(rng, oracle_mod, (1, ff, d), bits, 32, False, False)
+    up["scales"] = up["scales"] * (2.0 ** np.concatenate([[20], rng.integers(-20, 12, size=ff - 1)])).astype(np.float32)[None, :, None]
+    x = fx.acts(rng, 3, d)
+    h = np.stack([fr.product(x, gate, 0)[0], fr.product(x, up, 0)[0]]).prod(axis=0)
+    # the second product picks one hidden value per row: row k is value k, and the large one is used by no row but its own
+    down = dict(q=np.zeros((1, ff, ff), dtype=np.uint8), scales=np.ones((1, ff, 2), dtype=np.float32), zeros=np.ones((1, ff, 2), dtype=np.float32),
+                kperm=None, bits=bits, group=32)
+    down["q"][:] = 1
+    down["q"][0, np.arange(ff), np.arange(ff)] = 2
+    fx.pack(down, oracle_mod)
+    got = gq.moe_layer(cuda(x.astype(np.float32)).bfloat16(), *_pair(gate, up), _dev(down), ids=torch.zeros(3, 1, dtype=torch.int32, device="cuda"),
+                       weights=torch.ones(3, 1, device="cuda"), out_dtype=torch.float32)[0]
+    err = np.abs(got.cpu().numpy().astype(np.float64) - h)
+    bound = np.maximum(2.0 ** -24 * np.abs(h), 2.0 ** -39 * np.abs(h).max(axis=1, keepdims=True))
+    log(f"  worst error / bound {np.max(err / np.maximum(bound, 1e-300)):.3f}")
+    assert (err <= bound).all()
