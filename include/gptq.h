@@ -475,7 +475,7 @@ GPTQ_API gptq_status gptq_gemv_gated(const void *X, gptq_dtype x_dtype, int64_t 
  *   Y       fp16, bf16 or fp32 [T][ldy] out, ldy >= d, apart from X as above.
  *   ws      scratch of gptq_moe_workspace_bytes(), 16-byte aligned.
  * 1 <= top_k <= min(n_experts, 16), n_experts <= 512.  h passes between the two
- * products in fp32; the second one reads it to 2^-24 of a value, or 2^-40 of the
+ * products in fp32; the second one reads it to 2^-24 of a value, or 2^-39 of the
  * largest of its token's and expert's.  Every sum is fp32 (the router's fp64), the
  * result is rounded once.  Deterministic.
  * T == 0 is a no-op.

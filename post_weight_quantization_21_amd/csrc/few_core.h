@@ -299,121 +299,114 @@ struct XRows {
     float scale;           // fp32: the power of two of row m in lane m
 };
 
-// A phase's x on its way into LDS, in batches of kUnits units a thread (fp32: half as many).
+// A phase's x on its way into LDS, in batches of a unit a thread (fp32: half of one).
 template <int b, FewX kX>
 struct StageX {
-    static constexpr int kUnits = 1;
-    u32x4 v[4 * kUnits];
-    uint32_t magic;  // raw: of the division by the units of a row
-    int per_row, items, first, total;
+    u32x4 v[4];
+    uint32_t magic;                    // raw: of the division by the units of a row; fp32: by its pieces
+    int per_row, items, first, total;  // units of a row and of all in the phase, its first unit, batches
     __device__ __forceinline__ void init(int M, int units, int q0, int nq) {
         per_row = 16 * nq;
         magic = 0xFFFFFFFFu / (uint32_t)(kX == kFloatX ? 4 * per_row : per_row) + 1;
         items = M * per_row;  // units
         first = 16 * q0;
-        total = ((kX == kFloatX ? 2 * items : items) + kUnits * kFewThreads - 1) / (kUnits * kFewThreads);
+        total = ((kX == kFloatX ? 2 * items : items) + kFewThreads - 1) / kFewThreads;
     }
-    // Raw: unit i of the phase is unit u of row r.  Prepared: unit i is pieces 4 i .. of the phase, plane by plane.
-    // Ordered: pieces as prepared, each gathered value by value.  fp32: piece i, two a thread, is piece p of row r.
+    // Raw: unit i of the phase is unit u of row r.  Prepared: piece i of the phase, four a thread.  Ordered: pieces as
+    // prepared, each gathered value by value.  fp32: piece i, two a thread, is piece p of row r.
     __device__ __forceinline__ void load(const XRows &x, int M, int units, int batch) {
         const uint16_t *base = static_cast<const uint16_t *>(x.base);
+        if constexpr (kX == kRawX) {
+            const int i = threadIdx.x + batch * kFewThreads;
+            const int r = __umulhi(i, magic), u = first + i - r * per_row;
+            const int row = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            if constexpr (kX == kRawX) {
-                const int i = threadIdx.x + (kUnits * batch + k) * kFewThreads;
-                const int r = __umulhi(i, magic), u = first + i - r * per_row;
-                const int row = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
+            for (int j = 0; j < 4; ++j) v[j] = (u32x4){0, 0, 0, 0};
+            if (i < items && u < units) {
+                const u32x4 *src = reinterpret_cast<const u32x4 *>(base + row * x.ld + u * kUnit);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * k + j] = (u32x4){0, 0, 0, 0};
-                if (i < items && u < units) {
-                    const u32x4 *src = reinterpret_cast<const u32x4 *>(base + row * x.ld + u * kUnit);
+                for (int j = 0; j < 4; ++j) v[j] = src[j];
+            }
+        } else if constexpr (kX == kOrderedX) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[4 * k + j] = src[j];
+            for (int j = 0; j < 4; ++j) {
+                const int i = threadIdx.x + (4 * batch + j) * kFewThreads, piece = (int)((uint32_t)i / (uint32_t)M);
+                const int u = first + (piece >> 2), f = piece & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
+                const int r = i - piece * M, m = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
+                v[j] = (u32x4){0, 0, 0, 0};
+                if (i < 4 * items && u < units) {
+                    const uint16_t *row = base + m * x.ld;
+                    const int32_t *at = x.order + u * kUnit + f0;
+                    uint32_t h[8];
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) h[n] = row[std::min(std::max(at[slot_col<b>(0, n)], 0), units * kUnit - 1)];
+                    v[j] = (u32x4){h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
                 }
-            } else if constexpr (kX == kOrderedX) {
+            }
+        } else if constexpr (kX == kFloatX) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads, piece = (int)((uint32_t)i / (uint32_t)M);
-                    const int u = first + (piece >> 2), f = piece & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
-                    const int r = i - piece * M, m = x.gathered ? __shfl(x.row, r & (kWave - 1)) : r;
-                    v[4 * k + j] = (u32x4){0, 0, 0, 0};
-                    if (i < 4 * items && u < units) {
-                        const uint16_t *row = base + m * x.ld;
-                        const int32_t *at = x.order + u * kUnit + f0;
-                        uint32_t h[8];
-#pragma unroll
-                        for (int n = 0; n < 8; ++n) h[n] = row[std::min(std::max(at[slot_col<b>(0, n)], 0), units * kUnit - 1)];
-                        v[4 * k + j] = (u32x4){h[0] | h[1] << 16, h[2] | h[3] << 16, h[4] | h[5] << 16, h[6] | h[7] << 16};
-                    }
+            for (int j = 0; j < 4; j += 2) {
+                const int i = threadIdx.x + (2 * batch + j / 2) * kFewThreads, r = __umulhi(i, magic), p = i - r * 4 * per_row;
+                const int u = first + (p >> 2), f = p & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
+                v[j] = v[j + 1] = (u32x4){0, 0, 0, 0};
+                if (i < 4 * items && u < units) {
+                    const float *src = static_cast<const float *>(x.base) + r * x.ld + u * kUnit + f0;
+                    v[j] = *reinterpret_cast<const u32x4 *>(src);  // the piece's two runs of four columns
+                    v[j + 1] = *reinterpret_cast<const u32x4 *>(src + (b == 2 ? 8 : 4));
                 }
-            } else if constexpr (kX == kFloatX) {
+            }
+        } else {
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    const int i = threadIdx.x + (2 * (kUnits * batch + k) + j / 2) * kFewThreads, r = __umulhi(i, magic), p = i - r * 4 * per_row;
-                    const int u = first + (p >> 2), f = p & 3, f0 = b == 2 ? 16 * (f >> 1) + 4 * (f & 1) : 8 * f;
-                    v[4 * k + j] = v[4 * k + j + 1] = (u32x4){0, 0, 0, 0};
-                    if (i < 4 * items && u < units) {
-                        const float *src = static_cast<const float *>(x.base) + r * x.ld + u * kUnit + f0;
-                        v[4 * k + j] = *reinterpret_cast<const u32x4 *>(src);  // the piece's two runs of four columns
-                        v[4 * k + j + 1] = *reinterpret_cast<const u32x4 *>(src + (b == 2 ? 8 : 4));
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads;
-                    v[4 * k + j] = (u32x4){0, 0, 0, 0};  // (left alone, it would be kept through the phase before)
-                    if (i < 4 * items) v[4 * k + j] = *reinterpret_cast<const u32x4 *>(base + ((int64_t)4 * first * M + i) * 8);
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int i = threadIdx.x + (4 * batch + j) * kFewThreads;
+                v[j] = (u32x4){0, 0, 0, 0};  // (left alone, it would be kept through the phase before)
+                if (i < 4 * items) v[j] = *reinterpret_cast<const u32x4 *>(base + ((int64_t)4 * first * M + i) * 8);
             }
         }
     }
     __device__ __forceinline__ void store(uint16_t *xs, const XRows &x, int M, int batch) const {
         u32x4 *dst = reinterpret_cast<u32x4 *>(xs);
+        if constexpr (kX == kRawX) {
+            const int i = threadIdx.x + batch * kFewThreads;
+            const int r = __umulhi(i, magic), u = i - r * per_row;
+            if (i >= items) return;
+            uint32_t t[16];
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            if constexpr (kX == kRawX) {
-                const int i = threadIdx.x + (kUnits * batch + k) * kFewThreads;
-                const int r = __umulhi(i, magic), u = i - r * per_row;
-                if (i >= items) continue;
-                uint32_t t[16];
+            for (int j = 0; j < 16; ++j) t[j] = v[j / 4][j % 4];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) t[j] = v[4 * k + j / 4][j % 4];
+            for (int f = 0; f < 4; ++f) {
+                u32x4 o;
 #pragma unroll
-                for (int f = 0; f < 4; ++f) {
-                    u32x4 o;
-#pragma unroll
-                    for (int p = 0; p < 4; ++p) {
-                        constexpr int apart = b == 4 ? 4 : 8;
-                        const int c0 = slot_col<b>(f, 2 * p), c1 = slot_col<b>(f, 2 * p + 1);
-                        o[p] = c1 == c0 + 1 ? t[c0 / 2]
-                                            : __builtin_amdgcn_perm(t[(c0 + apart) / 2], t[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
-                    }
-                    dst[(4 * u + f) * M + r] = o;
+                for (int p = 0; p < 4; ++p) {
+                    constexpr int apart = b == 4 ? 4 : 8;
+                    const int c0 = slot_col<b>(f, 2 * p), c1 = slot_col<b>(f, 2 * p + 1);
+                    o[p] = c1 == c0 + 1 ? t[c0 / 2]
+                                        : __builtin_amdgcn_perm(t[(c0 + apart) / 2], t[c0 / 2], c0 & 1 ? 0x07060302u : 0x05040100u);
                 }
-            } else if constexpr (kX == kFloatX) {
+                dst[(4 * u + f) * M + r] = o;
+            }
+        } else if constexpr (kX == kFloatX) {
 #pragma unroll
-                for (int j = 0; j < 4; j += 2) {
-                    const int i = threadIdx.x + (2 * (kUnits * batch + k) + j / 2) * kFewThreads, r = __umulhi(i, magic), p = i - r * 4 * per_row;
-                    const float scale = __shfl(x.scale, r & (kWave - 1));
-                    if (i >= 4 * items) continue;
-                    _Float16 hi[8], lo[8];
+            for (int j = 0; j < 4; j += 2) {
+                const int i = threadIdx.x + (2 * batch + j / 2) * kFewThreads, r = __umulhi(i, magic), p = i - r * 4 * per_row;
+                const float scale = __shfl(x.scale, r & (kWave - 1));
+                if (i >= 4 * items) continue;
+                _Float16 hi[8], lo[8];
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        const int c = slot_col<b>(0, n), run = c >= (b == 2 ? 8 : 4);
-                        const float a = __uint_as_float(v[4 * k + j + run][c & 3]) * scale;
-                        hi[n] = (_Float16)a;
-                        lo[n] = (_Float16)(a - (float)hi[n]);
-                    }
-                    dst[p * M + r] = __builtin_bit_cast(u32x4, (f16x8){hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]});
-                    dst[4 * items + p * M + r] = __builtin_bit_cast(u32x4, (f16x8){lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]});
+                for (int n = 0; n < 8; ++n) {
+                    const int c = slot_col<b>(0, n), run = c >= (b == 2 ? 8 : 4);
+                    const float a = __uint_as_float(v[j + run][c & 3]) * scale;
+                    hi[n] = (_Float16)a;
+                    lo[n] = (_Float16)(a - (float)hi[n]);
                 }
-            } else {
+                dst[p * M + r] = __builtin_bit_cast(u32x4, (f16x8){hi[0], hi[1], hi[2], hi[3], hi[4], hi[5], hi[6], hi[7]});
+                dst[4 * items + p * M + r] = __builtin_bit_cast(u32x4, (f16x8){lo[0], lo[1], lo[2], lo[3], lo[4], lo[5], lo[6], lo[7]});
+            }
+        } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = threadIdx.x + (4 * (kUnits * batch + k) + j) * kFewThreads;
-                    if (i < 4 * items) dst[i] = v[4 * k + j];
-                }
+            for (int j = 0; j < 4; ++j) {
+                const int i = threadIdx.x + (4 * batch + j) * kFewThreads;
+                if (i < 4 * items) dst[i] = v[j];
             }
         }
     }

@@ -13,7 +13,7 @@
 // h = silu(gate) * up passes between the products in fp32.  The second one, whose
 // weights q - z are exact in fp16, takes it as two fp16 values of 11 bits and a
 // sign each, after a power of two per row has brought the row's largest to 2^14 ..
-// 2^15: a value loses at most 2^-24 of itself, or 2^-40 of its row's largest.  (A
+// 2^15: a value loses at most 2^-24 of itself, or 2^-39 of its row's largest.  (A
 // sum of two bf16 values, 2^-17, was the same in error against 64 bits for 16-bit
 // results, but twice as many of them fell to the other side of their rounding.)
 #include <algorithm>
