@@ -383,7 +383,9 @@ GPTQ_API gptq_status gptq_pack_codes(const uint8_t *codes, int64_t d_out, int64_
  *   ws      scratch of gptq_workspace_bytes(GPTQ_OP_W4A16, d_out, d_in, M, NULL).
  * Products are exact (integer weights times fp16 on fp16 matrix cores); sums
  * are fp32, added over K splits in a fixed order (deterministic).  g must be
- * a multiple of 32 (else GPTQ_ERR_UNSUPPORTED); packed 16-byte aligned.
+ * a multiple of 32 (else GPTQ_ERR_UNSUPPORTED); packed 16-byte aligned.  For up
+ * to 16 rows gptq_gemv, below, is faster (one row of 28672 x 8192: 33 us against
+ * 40) and takes bf16 and 2, 3 and 8 bits too.
  */
 GPTQ_API gptq_status gptq_w4a16_gemm(const void *X, gptq_dtype x_dtype, int64_t M, int64_t d_in, int64_t ldx,
                                      const int32_t *kperm, const uint32_t *packed, const float *scales,

@@ -369,7 +369,7 @@ def pack_codes(codes, bits: int, packed=None, perm=None, stream=None):
 
 
 def w4a16_gemm(X, packed, scales, zeros, group_size: int, d_out: int, kperm=None, Y=None, ws=None, stream=None):
-    """Y = X' W_hat^T with fp16 X [M][d_in] and 4-bit packed weights; Y fp32 [M][d_out]."""
+    """Y = X' W_hat^T with fp16 X [M][d_in] and 4-bit packed weights; Y fp32 [M][d_out].  Up to 16 rows gemv is faster."""
     import torch
     _need_cuda(packed, scales, zeros, kperm, Y)
     if not X.is_cuda:

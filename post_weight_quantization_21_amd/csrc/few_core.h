@@ -16,12 +16,14 @@
 // The result has its weight row in the lane's column (D[4 kb + i][r], i = 0..3,
 // m = 4 kb + i), so scale and zero are one value per lane.
 //
-// What bounds it: the instructions that unpack (measured at 28672 x 8192, one
-// token: 67 vector instructions per step of 16 x 128 codes kept a compute unit
-// at 8 bytes a clock; 36-40 of them are the unpacking itself).  Hence scales and
-// zero constants come ready from LDS, weights through buffer loads with scalar
-// offsets, and two quads of registers take turns without copies.  The matrix
-// cores are a quarter busy, for one token as for sixteen, so all M run on them.
+// What bounds it: start and staging where the layer is small, its bytes where it is
+// large, and beside them the instructions that unpack: one token of 28672 x 8192
+// issues 75 vector instructions per step of 16 x 128 codes (36-40 unpack), which
+// keep the vector units busy for 0.38 of the time, and eight gated tokens in groups
+// of 64 issue 115 for 0.55 of it (counters).  Hence scales and zero constants come
+// ready from LDS, weights through buffer loads with scalar offsets, and two quads of
+// registers take turns without copies.  The matrix cores are busy for 0.03 to 0.16
+// of the time, so all M run on them.
 #pragma once
 
 #include <algorithm>

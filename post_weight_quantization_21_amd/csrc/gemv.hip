@@ -26,11 +26,12 @@ struct GemvArgs {
 };
 
 // Gated: the even tiles are the gate's rows, the odd ones up's.
-// Bound by the weights' bytes where they are many: one token of 28672 x 8192 in 4
-// bits (132 MB) takes 31-32 us, 4.1 TB/s; gated, eight tokens of 28672 x 8192 in
-// groups of 64 (294 MB) 87-95 us, 3.1-3.4 TB/s, where unpacking, transposing and
-// folding bind.  By start and staging where they are few: 5.3 us for 1024 x 4096,
-// 23.5 us for sixteen tokens of 8192 x 8192 in 3 bits (256 KB of x per workgroup).
+// Cold weights, between calls.  Bound by the weights' bytes where they are many: one
+// token of 28672 x 8192 in 4 bits (132 MB) takes 32.5 us, 4.1 TB/s; gated, eight
+// tokens of 28672 x 8192 in groups of 64 (294 MB) 92-93 us, 3.2 TB/s, where
+// unpacking, transposing and folding bind.  By start and staging where they are few:
+// 6.1 us for 1024 x 4096, 23.9 us for sixteen tokens of 8192 x 8192 in 3 bits (256 KB
+// of x per workgroup).
 template <int b, typename T, bool kGated, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gemv_kernel(GemvArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];

@@ -137,7 +137,7 @@ __device__ __forceinline__ double wave_sum_d(double v) {  // as wave_max
 }
 
 // kPer: logits of a lane, n_experts <= 64 kPer.  One workgroup, since the numbering
-// needs every token's choice: 3.9 us for one token's 6 of 64, 7.9 for 16 tokens' 8
+// needs every token's choice: 4.1 us for one token's 6 of 64, 8.2 for 16 tokens' 8
 // of 128 (its rounds of maxima are dependent, 18 steps each).
 template <int kPer>
 __global__ __launch_bounds__(1024) void choose_kernel(const double *__restrict__ logits, int n_tok, int n_experts,
@@ -306,9 +306,10 @@ struct GateUpArgs {
     float *h;  // rows by pair
 };
 
-// 13 us for 6 experts of 1408 x 2048 in 4 bits (19 MB), 37 us for the ~82 that 16
-// tokens choose of 128 x 768 x 2048 (146 MB, 3.9 TB/s), 80-87 us for ~5.5 of 14336 x
-// 4096 (361 MB, 4.1-4.5 TB/s): a workgroup's start and staging per 128 rows or fewer, then the bytes.
+// Cold weights: 14 us for 6 experts of 1408 x 2048 in 4 bits (19 MB), 38 us for the
+// ~82 that 16 tokens choose of 128 x 768 x 2048 (146 MB, 3.8 TB/s), 87 us for ~5.5 of
+// 14336 x 4096 (361 MB, 4.1 TB/s): a workgroup's start and staging per 128 rows or
+// fewer, then the bytes.
 template <int b, typename T, bool kSplit, FewX kX>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void gate_up_kernel(GateUpArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -353,10 +354,10 @@ __device__ __forceinline__ int row_exponent(uint32_t top) { return std::min(126,
 __device__ __forceinline__ float power_of_2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 // Two matrix instructions per fragment of weights, which are unpacked once for both
-// planes of h.  7.2 us, 26 us and 60 us for the experts of gate_up_kernel's figures:
-// half their bytes in 55-70% of the time, for h has two planes and K is d_ff.  Adding
-// a token's pairs here, by the last workgroup to arrive, took 35 and 200 us: the
-// fence before its count.
+// planes of h.  8 us, 26 us and 62 us for the experts of gate_up_kernel's figures:
+// half their bytes in 57-70% of the time, for h has two planes and K is d_ff.  Adding
+// a token's pairs here, by the last workgroup to arrive, took 35 us instead of 8 and
+// 200 instead of 28: the fence before its count.
 template <int b, bool kSplit>
 __global__ __launch_bounds__(kFewThreads, kFewOccupancy) void down_kernel(DownArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
@@ -449,7 +450,7 @@ void launch_experts(const MoeCall &c, const Layout &l, hipStream_t s) {
     g.lists = lists;
     g.h = reinterpret_cast<float *>(c.ws + l.h);
     // gathered by the products up to the same size as in gemv.hip, with an expert's rows for M: one token of 64 experts x
-    // 1408 x 2048 takes 30.4 us against 31.7 through a kernel of its own
+    // 1408 x 2048 takes 30.4 us against 31.7 through a kernel of its own, of 1408 x 4096 39.4 against 39.8
     g.order = c.gate->kperm;
     const FewX x = !c.gate->kperm ? kRawX : (gemv_prepares(load.rows, d) ? kPreparedX : kOrderedX);
     if (x == kPreparedX) {
