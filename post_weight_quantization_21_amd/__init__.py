@@ -466,11 +466,17 @@ def _few_result(X, Y, rows, d_out, out_dtype, device, torch, dtypes):
     return Y, dt
 
 
-def _few_on(stream, device, torch):
+def _few_on(stream, device, torch, layers, *tensors):
     """`stream` as the current stream: the call's result and workspace then come from, and go back to, the memory that
-    this stream orders.  (From the caller's, either could still be in use there, or be handed out again too early.)"""
+    this stream orders.  (From the caller's, either could still be in use there, or be handed out again too early.)  What
+    the caller gives may be dropped when the call returns: its memory is not handed out before this stream is done."""
     if stream.device != device:
         raise ValueError("the stream must be on the weights' device")
+    for w in layers:
+        tensors += (w.packed, w.scales, w.zeros, w.kperm)
+    for t in tensors:
+        if t is not None and t.is_cuda:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -512,7 +518,7 @@ def gemv(X, w: PackedWeight, bias=None, Y=None, out_dtype=None, ws=None, stream=
     bias fp32 [d_out]; Y [M][d_out], apart from X, in X's type or in out_dtype (fp16, bf16, fp32)."""
     torch, lib, act, res = _few_init()
     if stream is not None:
-        with _few_on(stream, w.device, torch):
+        with _few_on(stream, w.device, torch, (w,), X, bias, Y, ws):
             return gemv(X, w, bias, Y, out_dtype, ws)
     if w.stack is not None:
         raise ValueError("gemv takes a single layer, not a stack")
@@ -533,7 +539,7 @@ def gemv_gated(X, gate: PackedWeight, up: PackedWeight, H=None, out_dtype=None, 
     gate and up share one column order (the same kperm tensor), as they share their inputs."""
     torch, lib, act, res = _few_init()
     if stream is not None:
-        with _few_on(stream, gate.device, torch):
+        with _few_on(stream, gate.device, torch, (gate, up), X, H, ws):
             return gemv_gated(X, gate, up, H, out_dtype, ws)
     if gate.stack is not None or up.stack is not None:
         raise ValueError("gemv_gated takes single layers, not stacks")
@@ -561,7 +567,7 @@ def moe_layer(X, gate: PackedWeight, up: PackedWeight, down: PackedWeight, route
     ids (int32 [T][top_k]) and weights (fp32 [T][top_k]) are the caller's routing.  Returns (Y, ids, weights)."""
     torch, lib, act, res = _few_init()
     if stream is not None:
-        with _few_on(stream, gate.device, torch):
+        with _few_on(stream, gate.device, torch, (gate, up, down), X, router, ids, weights, Y, ws):
             return moe_layer(X, gate, up, down, router, top_k, renormalize, ids, weights, Y, out_dtype, ws)
     E, dev, d, T = gate.stack, gate.device, gate.d_in, X.shape[0]
     if E is None or up.stack != E or down.stack != E:

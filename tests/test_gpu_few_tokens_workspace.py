@@ -96,3 +96,48 @@ def test_two_graphs(layers, given):
             torch.cuda.synchronize()
             assert torch.equal(graphs[0][3], want[i]) and torch.equal(graphs[1][3], want[j]), name
             assert torch.equal(eager, want[(i + 1) % 4]), name
+
+
+def test_inputs_dropped_on_return(layers):
+    """What a call on another, busy stream reads may be dropped at once: its memory is not handed out again before."""
+    torch = torch_mod()
+    x = _acts(np.random.default_rng(35), M, D, "bf16")[0]
+    for name, call, size in layers:
+        expect = call(x)
+        side = torch.cuda.Stream()
+        x_copy, ws = x.clone(), torch.empty(size, dtype=torch.uint8, device="cuda")
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        y = call(x_copy, ws=ws, stream=side)
+        at = {x_copy.data_ptr(), ws.data_ptr()}
+        del x_copy, ws
+        junk = [torch.full((n,), 0x55, dtype=torch.uint8, device="cuda") for n in 4 * [size] + 4 * [M * D * 2]]
+        assert not at & {j.data_ptr() for j in junk}, name
+        torch.cuda.synchronize()
+        assert torch.equal(y, expect), name
+
+
+def test_stream_named_inside_a_capture(layers):
+    """A captured call that names the capturing stream, its input dropped inside the capture."""
+    torch = torch_mod()
+    rng = np.random.default_rng(36)
+    inputs = [_acts(rng, M, D, "bf16")[0] for _ in range(3)]
+    for name, call, size in layers:
+        want = [call(x * 2) for x in inputs]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        buf = inputs[0].clone()
+        call(buf, stream=side)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            x = buf * 2
+            out = call(x, stream=side)
+            del x
+        for i in (0, 2, 1, 1):
+            buf.copy_(inputs[i])
+            g.replay()
+            eager = call(inputs[i] * 2)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[i]) and torch.equal(eager, want[i]), name
