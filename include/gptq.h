@@ -437,9 +437,9 @@ typedef struct {
  * multiplies a group's sum; the result is rounded once.  Deterministic.  bf16 X:
  * a sum may overflow, and its result be no number, where the magnitudes of a
  * token's values in 128 columns (from a multiple of 128 on) add up to 2^128 (8
- * bits: 2^120) or more, or a scale is 2^120 or more.  A token whose activations
- * are not all finite gets results that are not finite or NaN, in its own row
- * only.  Out-of-range kperm entries are clamped.
+ * bits: 2^120) or more.  A token whose activations are not all finite gets
+ * results that are not finite or NaN, in its own row only.  Out-of-range kperm
+ * entries are clamped.
  * M == 0 is a no-op.  GPTQ_ERR_UNSUPPORTED for other bits, M, group sizes or
  * sizes than the above (more tokens: gptq_w4a16_gemm).
  */

@@ -159,9 +159,9 @@ __device__ __forceinline__ uint32_t code_at(const uint32_t *w, int c) {
 // with one more matrix instruction per fragment, whose B operand is the constant
 // -(2^b + z); only the fp32 sums round.  Eight-bit codes fill bf16's significand,
 // so they go through fp32: q - z is an integer of at most 255 and exact in bf16.
-// bf16's 2^b + q and 2^b + z are held less an exponent, below 1, and the scale is
-// kScaled times larger: x may be as large as fp32 itself holds, and products with
-// 2^b + q would leave fp32 where the result does not.  (Of eight bits, whose x may
+// bf16's 2^b + q and 2^b + z are held less an exponent, below 1, and the sums are
+// multiplied by kScaled at the end: x may be as large as fp32 itself holds, and
+// products with 2^b + q would leave fp32 where the result does not.  (Of eight bits, whose x may
 // be 2^8 times smaller, that multiply-add with a literal instead of a subtraction
 // takes 13.2 us instead of 11.4 for seven tokens of 5003 x 2720.)
 template <int b, typename T>
@@ -169,7 +169,7 @@ struct Codes {
     typedef typename Vec8<T>::V V;
     static constexpr bool kF16 = __is_same(T, _Float16);
     static constexpr bool kOffset = !kF16 && b < 8;  // fragments hold 2^b + q
-    static constexpr float kScaled = kOffset ? (float)(2 << b) : 1.0f;  // a power of two: nothing rounds
+    static constexpr float kScaled = 2 << b;  // a power of two: nothing rounds
     uint32_t magic;
     uint32_t zc;  // constant(z)
     f16x2 z2;     // fp16, two bits: 256 + z, 16 + z
@@ -183,7 +183,7 @@ struct Codes {
     __device__ __forceinline__ static uint32_t constant(float z) {
         if constexpr (kF16) return __builtin_bit_cast(uint32_t, (f16x2){(_Float16)(1024.0f + z), (_Float16)(64.0f + z)});
         if constexpr (!kOffset) return __float_as_uint(z);
-        const __bf16 v = (__bf16)(-((float)(1 << b) + z) / kScaled);
+        const __bf16 v = (__bf16)fmaf(z, -1.0f / kScaled, -0.5f);
         return __builtin_bit_cast(uint32_t, (bf16x2){v, v});
     }
     __device__ __forceinline__ void set(uint32_t c) {
@@ -456,7 +456,7 @@ struct StageGroups {
             if (t0 + k >= total) continue;
             const int i = threadIdx.x + (t0 + k) / kMats * kFewThreads, r = row_of(i);
             const int row = kMats > 1 ? (r >> 4) * 32 + k % kMats * 16 + (r & 15) : r;  // of the workgroup
-            if (i < items) entries[row * ld + i - r * n] = make_uint2(__float_as_uint(s[k] * Codes<b, T>::kScaled), Codes<b, T>::constant(z[k]));
+            if (i < items) entries[row * ld + i - r * n] = make_uint2(__float_as_uint(s[k]), Codes<b, T>::constant(z[k]));
         }
     }
 };
@@ -594,6 +594,10 @@ __device__ __forceinline__ floatx4 few_product(const FewMat *mats, const FewShap
             set(wb, h + 1);
             load(wb, h + 3, he);
         }
+    }
+    if constexpr (C::kOffset) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[t] *= C::kScaled;
     }
     return acc;
 }
