@@ -491,6 +491,123 @@ GPTQ_API gptq_status gptq_moe_workspace_bytes(int64_t T, int64_t d, int64_t d_ff
                                               size_t *out);
 
 /*
+ * A key/value cache held in 4 bits (page "量化方法族：GPTQ、AWQ、SmoothQuant、FP8、
+ * LLM.int8()、KV-cache", §3.6: the cache is quantized to hold longer texts; the grids
+ * are the integer ones above), beside the few-token products: what a decoding step
+ * reads between them.
+ *
+ * A pool of pages of `page` tokens; a sequence's row of a table names its pages, and
+ * token i of it is at place i % page of page table[i / page].  Per page and kv head:
+ *   k       [page][head_dim/8] words: word b head_dim/32 + t (b = 0..3) holds dims 32 t + 8 b
+ *           + e, the code of dim e at bits 4 (e / 2 + 4 (e % 2))
+ *   v       [page/8][head_dim/4][8] 16-bit units: unit 16 u + m of token 8 i + r holds
+ *           dims 64 u + 16 j + m, their codes at bits 4 j (j = 0..3)
+ *   k_grid, v_grid  [groups][page] words: the scale s as bf16 in the upper half, 8 - z as
+ *           fp16 in the lower; groups of group_size consecutive dims (0: one per head)
+ *   weight  [page] fp32: the attention weights that the token got, added up
+ * each with the pages and heads in front: [n_pages][n_heads][...].  A value is s (q - z).
+ * The struct lives on the host and is read during the call; its pointers are device
+ * pointers, 16-byte aligned.
+ *
+ * lens [n_seq] int32 are the sequences' lengths in tokens, the new ones among them: a
+ * decoding step raises them once and hands the same lens to each layer's append and
+ * attention.  A length below 0 counts as 0, one above the table (or max_len) as that.  A
+ * table entry that is not a page of the pool is read and written nowhere: its tokens are
+ * not stored, not attended to, and of no weight.
+ * Pages may be shared between sequences (a common beginning) as long as nothing is
+ * written there: appended to, or given weights.
+ */
+typedef struct {
+    uint32_t *k;
+    uint16_t *v;
+    uint32_t *k_grid, *v_grid;
+    float *weight;      /* or NULL: no weights are kept */
+    int64_t n_pages;    /* at most 2^31 - 1 */
+    int32_t n_heads;    /* kv heads, at most 65535 */
+    int32_t head_dim;   /* 64, 128, 192 or 256 */
+    int32_t page;       /* a power of two, 16 .. 2^20 */
+    int32_t group_size; /* 32, 64, 128 or head_dim (0), a divisor of head_dim */
+    int32_t symmetric;  /* 1: symmetric grids, 0: asymmetric ones */
+} gptq_kv_cache;
+
+/*
+ * New tokens' keys and values into the cache.
+ *   K, V    fp16 or bf16 [T][ldk], [T][ldv]: n_heads x head_dim values a row, both 16-byte
+ *           aligned, ldk and ldv multiples of 8 and >= n_heads * head_dim.
+ *   offs    [n_seq + 1] int32, rising from 0, or NULL: sequence b's new tokens are rows
+ *           offs[b] .. offs[b+1] - 1; NULL: T / n_seq rows each (T a multiple of n_seq).
+ *           They take the last places below lens[b]; tokens that would come before
+ *           place 0 are padding and stored nowhere, and so are rows from offs[n_seq] on.
+ *   table   [n_seq][width] int32; width * page at most 2^30.
+ *   K_out, V_out  [T][ldko], [T][ldvo] in K's type, or NULL: the values that the cache now
+ *           holds for these tokens, rounded once.  Aligned as K, and apart from K, V and
+ *           each other (or the same memory as K and V, row by row).  Rows from offs[n_seq]
+ *           on are left as they were.
+ * A group's grid is the one above with 4 bits, but its scale is rounded to bf16 before
+ * zero and codes are chosen with it.  A group with a value that is not finite, or a
+ * spread beyond fp32, gets a scale that is no number: what attends to it is no number.
+ * The new tokens' weights are set to 0.  T * n_heads at most 2^26.
+ */
+GPTQ_API gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv, gptq_dtype dtype, int64_t T,
+                                    const int32_t *offs, const gptq_kv_cache *cache, const int32_t *table, int64_t width,
+                                    const int32_t *lens, int64_t n_seq, void *K_out, int64_t ldko, void *V_out,
+                                    int64_t ldvo, hipStream_t stream);
+
+/*
+ * Attention of every sequence's last n tokens over the cache, themselves included:
+ *   O[b][i][h] = sum_t p_t v_t,  p = softmax_t(scale Q[b][i][h] . k_t),
+ * over the tokens t < lens[b] - n + 1 + i, with the keys and values of kv head
+ * h / (q_heads / n_heads).  A row that sees nothing (lens[b] = 0, or padding on the left
+ * where lens[b] < n) is 0.
+ *   Q       fp16 or bf16 [n_seq * n][ldq], q_heads x head_dim values a row, 16-byte aligned,
+ *           ldq a multiple of 8; 1 <= n <= 16, q_heads a multiple of n_heads, at most 256
+ *           times it.
+ *   O       [n_seq * n][ldo] in Q's type, 2-byte aligned, no element in Q's memory.
+ *   scale   finite and > 0 (usually head_dim^-1/2).
+ *   max_len lengths above it count as it; at most width * page.  It sets the launch's
+ *           size: the closer to the longest sequence, the better.
+ *   accumulate, decay  with accumulate, weight_t of each kv head becomes decay * weight_t
+ *           + the sum of p_t over i and the heads of its group (decay in [0, 1]; 0 does
+ *           not read the old one).  Needs weight; pages then belong to one sequence.
+ *   ws      scratch of gptq_kv_attention_workspace_bytes(), 16-byte aligned; the same
+ *           sizes, n_seq no larger and max_len no larger need no more.
+ * Products with the keys are exact (integers q - 8 times Q in fp16 or, from bf16, to
+ * 2^-40 of a row's largest value); sums and softmax are fp32; p s_v enters the second
+ * product in fp16 (2^-11 of each term) and the result is rounded once.  Deterministic.  A
+ * query that is not finite makes its own row not finite or NaN, and the weights of what
+ * it sees.  n_seq * n_heads * ceil(n q_heads / n_heads / 16) at most 2^20.
+ */
+GPTQ_API gptq_status gptq_kv_attention(const void *Q, gptq_dtype dtype, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq,
+                                       const gptq_kv_cache *cache, const int32_t *table, int64_t width, const int32_t *lens,
+                                       int64_t max_len, float scale, int32_t accumulate, float decay, void *O, int64_t ldo,
+                                       void *ws, size_t ws_bytes, hipStream_t stream);
+GPTQ_API gptq_status gptq_kv_attention_workspace_bytes(const gptq_kv_cache *cache, int64_t n_seq, int64_t n, int64_t q_heads,
+                                                       int64_t max_len, size_t *out);
+
+/*
+ * Eviction: of every sequence and kv head, min(lens[b], budget) tokens are kept: the last
+ * min(recent, that many), and of the others the heaviest by accumulated weight (ties to
+ * the lower place; NaN below every number).  Their codes, grids and weights are copied, in
+ * order, to places 0, 1, ... of the pages that `to` names; the cache as `table` names it
+ * stays as it was, so its pages may be shared, and are the caller's to reuse afterwards.
+ *   to       [n_seq][to_width] int32 pages, to_width * page >= budget; none of them is a
+ *            page that `table` names below a length, or named twice.  Entries that are
+ *            not pages of the pool are not written.
+ *   budget   >= 1; 0 <= recent <= budget.  n_seq * n_heads * budget at most 2^27.
+ *   kept     [n_seq][n_heads][budget] int32 out: the places that the kept tokens had, -1
+ *            behind the last.
+ *   new_lens [n_seq] int32 out or NULL: min(lens[b], budget); not lens itself.
+ *   max_len  lengths above it count as it; at most width * page.
+ *   ws       scratch of gptq_kv_evict_workspace_bytes() (may be NULL when 0), 16-byte aligned.
+ */
+GPTQ_API gptq_status gptq_kv_evict(const gptq_kv_cache *cache, const int32_t *table, int64_t width, const int32_t *lens,
+                                   int64_t n_seq, int64_t max_len, const int32_t *to, int64_t to_width, int64_t budget,
+                                   int64_t recent, int32_t *kept, int32_t *new_lens, void *ws, size_t ws_bytes,
+                                   hipStream_t stream);
+GPTQ_API gptq_status gptq_kv_evict_workspace_bytes(const gptq_kv_cache *cache, int64_t n_seq, int64_t max_len, int64_t budget,
+                                                   size_t *out);
+
+/*
  * Kernel timing for benchmarks (off by default).  While enabled, the column
  * pass records a pair of HIP events around each of its kernel launches of the
  * kinds below, on the stream the kernel runs on:

@@ -31,6 +31,7 @@ EXPORTED = (
     "gptq_quantize_layer_noalloc", "gptq_timing_enable", "gptq_timing_read",
     "gptq_linear_forward", "gptq_calibrate_hessian", "gptq_calibrate_chunk_tokens",
     "gptq_gemv", "gptq_gemv_gated", "gptq_moe_layer", "gptq_moe_workspace_bytes",
+    "gptq_kv_append", "gptq_kv_attention", "gptq_kv_attention_workspace_bytes", "gptq_kv_evict", "gptq_kv_evict_workspace_bytes",
 )
 TIMED_LAZY, TIMED_BATCH, TIMED_LAZY_SPLIT = 0, 1, 2
 NOALLOC_SCRATCH_BYTES = 64 << 20  # GPTQ_NOALLOC_SCRATCH_BYTES
@@ -56,6 +57,14 @@ class Packed(ctypes.Structure):
                 ("bits", ctypes.c_int32), ("group_size", ctypes.c_int32)]
 
 
+class KVCacheStruct(ctypes.Structure):
+    """Mirror of ``gptq_kv_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_grid", ctypes.c_void_p), ("v_grid", ctypes.c_void_p),
+                ("weight", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("n_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page", ctypes.c_int32), ("group_size", ctypes.c_int32),
+                ("symmetric", ctypes.c_int32)]
+
+
 # gptq_grid: when the quantization grids are fitted
 GRIDS = {"dynamic": 0, "static": 1, "tensor": 2}
 
@@ -78,7 +87,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise ImportError(f"{path} is missing: build it with `python -m post_weight_quantization_21_amd.build`")
     lib = ctypes.CDLL(path)
     vp, i64, i32, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
-    cfgp, pkp = ctypes.POINTER(Config), ctypes.POINTER(Packed)
+    cfgp, pkp, kvp, szp = (ctypes.POINTER(t) for t in (Config, Packed, KVCacheStruct, sz))
+    f32 = ctypes.c_float
     sig = {
         "gptq_hessian_accumulate": [vp, vp, vp, i32, i64, i64, i64, vp, sz, vp],
         "gptq_prepare_hinv": [vp, vp, i64, cfgp, vp, vp, vp, vp, sz, vp],
@@ -101,6 +111,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "gptq_gemv_gated": [vp, i32, i64, i64, pkp, pkp, vp, i32, i64, vp, sz, vp],
         "gptq_moe_layer": [vp, i32, i64, i64, vp, i32, i32, i32, i32, pkp, pkp, pkp, vp, vp, vp, i32, i64, vp, sz, vp],
         "gptq_moe_workspace_bytes": [i64, i64, i64, i32, i32, ctypes.POINTER(sz)],
+        "gptq_kv_append": [vp, i64, vp, i64, i32, i64, vp, kvp, vp, i64, vp, i64, vp, i64, vp, i64, vp],
+        "gptq_kv_attention": [vp, i32, i64, i64, i64, i64, kvp, vp, i64, vp, i64, f32, i32, f32, vp, i64, vp, sz, vp],
+        "gptq_kv_attention_workspace_bytes": [kvp, i64, i64, i64, i64, szp],
+        "gptq_kv_evict": [kvp, vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, vp, sz, vp],
+        "gptq_kv_evict_workspace_bytes": [kvp, i64, i64, i64, szp],
         "gptq_timing_enable": [i32],
         "gptq_timing_read": [i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(i64), ctypes.POINTER(ctypes.c_double)],
         "gptq_status_string": [ctypes.c_int],
@@ -609,6 +624,198 @@ def moe_layer(X, gate: PackedWeight, up: PackedWeight, down: PackedWeight, route
                 1 if renormalize else 0, gate.ref, up.ref, down.ref, ids.data_ptr(), weights.data_ptr(), Y.data_ptr(), yd,
                 _pitch(Y, T, d), wp, wn)
     return Y, ids, weights
+
+
+class KVCache:
+    """A pool of pages of a 4-bit key/value cache for ``kv_append``, ``kv_attention`` and ``kv_evict``: the tensors and
+    their ``gptq_kv_cache``.  It keeps the tensors alive."""
+    __slots__ = ("k", "v", "k_grid", "v_grid", "weight", "n_pages", "n_heads", "head_dim", "page", "group_size", "symmetric",
+                 "device", "c", "ref", "tensors")
+
+    def __init__(self, k, v, k_grid, v_grid, weight, group_size, symmetric):
+        import torch
+        tensors = (k, v, k_grid, v_grid, weight)
+        _need_cuda(*tensors)
+        if k.dtype != torch.int32 or v.dtype != torch.int16 or k_grid.dtype != torch.int32 or v_grid.dtype != torch.int32 or \
+                (weight is not None and weight.dtype != torch.float32):
+            raise TypeError("k and the grids must be int32, v int16, weight float32")
+        if any(t.device != k.device for t in tensors if t is not None):
+            raise ValueError("the tensors of a cache must be on one device")
+        if k.dim() != 4 or k.numel() == 0:
+            raise ValueError("k must be [pages][heads][page][head_dim / 8]")
+        pages, heads, page, words = k.shape
+        dim = 8 * words
+        group = group_size or dim
+        if group < 0 or dim % group:
+            raise ValueError("group_size must divide head_dim (0: one group per head)")
+        if tuple(v.shape) != (pages, heads, page // 8, dim // 4, 8):
+            raise ValueError(f"v must be {[pages, heads, page // 8, dim // 4, 8]}")
+        if any(tuple(t.shape) != (pages, heads, dim // group, page) for t in (k_grid, v_grid)):
+            raise ValueError(f"k_grid and v_grid must be {[pages, heads, dim // group, page]}")
+        if weight is not None and tuple(weight.shape) != (pages, heads, page):
+            raise ValueError(f"weight must be {[pages, heads, page]}")
+        self.k, self.v, self.k_grid, self.v_grid, self.weight, self.device = *tensors, k.device
+        self.n_pages, self.n_heads, self.page, self.head_dim = pages, heads, page, dim
+        self.group_size, self.symmetric, self.tensors = group, bool(symmetric), tensors
+        self.c = KVCacheStruct(k.data_ptr(), v.data_ptr(), k_grid.data_ptr(), v_grid.data_ptr(),
+                               None if weight is None else weight.data_ptr(), pages, heads, dim, page, group, int(self.symmetric))
+        self.ref = ctypes.byref(self.c)
+
+
+def kv_cache(k, v, k_grid, v_grid, weight=None, group_size: int = 0, symmetric: bool = False) -> KVCache:
+    """A cache in given tensors: k int32 [pages][heads][page][head_dim/8], v int16 [pages][heads][page/8][head_dim/4][8],
+    k_grid and v_grid int32 [pages][heads][groups][page], weight fp32 [pages][heads][page] or None (layout: ``gptq.h``)."""
+    return KVCache(k, v, k_grid, v_grid, weight, int(group_size), symmetric)
+
+
+def kv_cache_empty(n_pages: int, n_heads: int, head_dim: int, page: int = 64, group_size: int = 0, symmetric: bool = False,
+                   weights: bool = False, device=None) -> KVCache:
+    """A cache with nothing in it, on the current device or `device`; with `weights` it can accumulate attention weights."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    groups = head_dim // (group_size or head_dim)
+
+    def new(dtype, *shape):
+        return torch.empty(n_pages, n_heads, *shape, dtype=dtype, device=dev)
+    return KVCache(new(torch.int32, page, head_dim // 8), new(torch.int16, page // 8, head_dim // 4, 8),
+                   new(torch.int32, groups, page), new(torch.int32, groups, page),
+                   new(torch.float32, page) if weights else None, int(group_size), symmetric)
+
+
+def _kv_ints(t, shape, device, name, torch):
+    if t.device != device or t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or \
+            any(n is not None and m != n for m, n in zip(t.shape, shape)):
+        raise ValueError(f"{name} must be a contiguous int32 {['any' if n is None else n for n in shape]} on the cache's device")
+    return t
+
+
+def _kv_rows(X, heads, dim, device, dtypes, name):
+    """Pitch and type of [..., heads, dim] whose rows (all leading dimensions) lie at one pitch."""
+    dt = dtypes.get(X.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be float16 or bfloat16")
+    if X.device != device or X.dim() < 3 or tuple(X.shape[-2:]) != (heads, dim) or X.stride(-1) != 1 or \
+            (heads > 1 and X.stride(-2) != dim):
+        raise ValueError(f"{name} must be [...][{heads}][{dim}] on the cache's device, contiguous within a token")
+    ld, rows = heads * dim, 1
+    for i in range(X.dim() - 3, -1, -1):
+        if X.shape[i] > 1:
+            if rows == 1:
+                ld = X.stride(i)
+            elif X.stride(i) != rows * ld:
+                raise ValueError(f"the tokens of {name} must lie at one pitch")
+        rows *= X.shape[i]
+    return ld, dt
+
+
+def kv_append(K, V, cache: KVCache, table, lens, offs=None, values=False, K_out=None, V_out=None, stream=None):
+    """Keys and values of new tokens (fp16 or bf16 [T][heads][head_dim]) into the last places below lens (int32 [n_seq], the
+    new tokens among them) of the pages that table (int32 [n_seq][width]) names.  offs (int32 [n_seq + 1]): sequence b's rows
+    are offs[b] .. offs[b+1] - 1; without it each has T / n_seq.  With values (or K_out, V_out) it returns what the cache
+    now holds for them, (K_out, V_out) in K's type."""
+    torch, lib, act, _ = _few_init()
+    if stream is not None:
+        with _few_on(stream, cache.device, torch, (), *cache.tensors, K, V, table, lens, offs, K_out, V_out):
+            return kv_append(K, V, cache, table, lens, offs, values, K_out, V_out)
+    dev, heads, dim = cache.device, cache.n_heads, cache.head_dim
+    if K.dim() != 3 or K.shape != V.shape or K.dtype != V.dtype:
+        raise ValueError("K and V must be [tokens][heads][head_dim] of one type")
+    ldk, dt = _kv_rows(K, heads, dim, dev, act, "K")
+    ldv, _ = _kv_rows(V, heads, dim, dev, act, "V")
+    T, n_seq = K.shape[0], lens.shape[0]
+    _kv_ints(lens, (n_seq,), dev, "lens", torch)
+    _kv_ints(table, (n_seq, None), dev, "table", torch)
+    if offs is not None:
+        _kv_ints(offs, (n_seq + 1,), dev, "offs", torch)
+    if values:
+        K_out = torch.empty((T, heads, dim), dtype=K.dtype, device=dev) if K_out is None else K_out
+        V_out = torch.empty((T, heads, dim), dtype=K.dtype, device=dev) if V_out is None else V_out
+    outs = []
+    for out, name in ((K_out, "K_out"), (V_out, "V_out")):
+        if out is None:
+            outs += [None, 0]
+            continue
+        if out.shape != K.shape or out.dtype != K.dtype:
+            raise ValueError(f"{name} must have K's shape and type")
+        outs += [out.data_ptr(), _kv_rows(out, heads, dim, dev, act, name)[0]]
+    _few_launch(lib.gptq_kv_append, dev, torch, K.data_ptr(), ldk, V.data_ptr(), ldv, dt, T,
+                None if offs is None else offs.data_ptr(), cache.ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n_seq, *outs)
+    return (K_out, V_out) if K_out is not None or V_out is not None else None
+
+
+def kv_attention_workspace_bytes(cache: KVCache, n_seq: int, n: int, q_heads: int, max_len: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gptq_kv_attention_workspace_bytes(cache.ref, n_seq, n, q_heads, max_len, ctypes.byref(out)))
+    return int(out.value)
+
+
+def kv_attention(Q, cache: KVCache, table, lens, scale=None, max_len=None, decay=None, O=None, ws=None, stream=None):
+    """Attention of every sequence's last n <= 16 tokens over its cached tokens: Q fp16 or bf16 [n_seq][n][q_heads][head_dim],
+    table and lens as in kv_append; scale defaults to head_dim^-1/2, max_len (no length is longer) to what the table holds.
+    With decay (0 .. 1) the cache's weights become decay * weight + what each token got.  Returns O, in Q's shape and type."""
+    torch, lib, act, _ = _few_init()
+    if stream is not None:
+        with _few_on(stream, cache.device, torch, (), *cache.tensors, Q, table, lens, O, ws):
+            return kv_attention(Q, cache, table, lens, scale, max_len, decay, O, ws)
+    dev, dim = cache.device, cache.head_dim
+    if Q.dim() != 4:
+        raise ValueError("Q must be [sequences][tokens][heads][head_dim]")
+    n_seq, n, q_heads, _ = Q.shape
+    ldq, dt = _kv_rows(Q, q_heads, dim, dev, act, "Q")
+    _kv_ints(lens, (n_seq,), dev, "lens", torch)
+    _kv_ints(table, (n_seq, None), dev, "table", torch)
+    if O is None:
+        O = torch.empty((n_seq, n, q_heads, dim), dtype=Q.dtype, device=dev)
+    elif O.shape != Q.shape or O.dtype != Q.dtype:
+        raise ValueError("O must have Q's shape and type")
+    ldo, _ = _kv_rows(O, q_heads, dim, dev, act, "O")
+    if max_len is None:
+        max_len = table.shape[1] * cache.page
+    if ws is None:
+        ws = _workspace(kv_attention_workspace_bytes(cache, n_seq, n, q_heads, max_len), dev)
+    wp, wn = _few_ws(ws, dev)
+    _few_launch(lib.gptq_kv_attention, dev, torch, Q.data_ptr(), dt, n_seq, n, q_heads, ldq, cache.ref, table.data_ptr(),
+                table.shape[1], lens.data_ptr(), max_len, dim ** -0.5 if scale is None else scale, 0 if decay is None else 1,
+                0.0 if decay is None else decay, O.data_ptr(), ldo, wp, wn)
+    return O
+
+
+def kv_evict_workspace_bytes(cache: KVCache, n_seq: int, max_len: int, budget: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check(load_library().gptq_kv_evict_workspace_bytes(cache.ref, n_seq, max_len, budget, ctypes.byref(out)))
+    return int(out.value)
+
+
+def kv_evict(cache: KVCache, table, lens, to, budget: int, recent: int = 0, max_len=None, kept=None, new_lens=None, ws=None,
+             stream=None):
+    """Of every sequence and head the last `recent` tokens and the heaviest others, `budget` in all, are copied in order to the
+    pages that `to` (int32 [n_seq][width]) names, which are none of table's.  Returns (kept, new_lens): int32
+    [n_seq][heads][budget], the places that the kept tokens had (-1 behind the last), and int32 [n_seq], min(lens, budget)."""
+    torch, lib, _, _ = _few_init()
+    if stream is not None:
+        with _few_on(stream, cache.device, torch, (), *cache.tensors, table, lens, to, kept, new_lens, ws):
+            return kv_evict(cache, table, lens, to, budget, recent, max_len, kept, new_lens, ws)
+    dev, n_seq = cache.device, lens.shape[0]
+    _kv_ints(lens, (n_seq,), dev, "lens", torch)
+    _kv_ints(table, (n_seq, None), dev, "table", torch)
+    _kv_ints(to, (n_seq, None), dev, "to", torch)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    if kept is None:
+        kept = torch.empty((n_seq, cache.n_heads, budget), dtype=torch.int32, device=dev)
+    if new_lens is None:
+        new_lens = torch.empty((n_seq,), dtype=torch.int32, device=dev)
+    _kv_ints(kept, (n_seq, cache.n_heads, budget), dev, "kept", torch)
+    _kv_ints(new_lens, (n_seq,), dev, "new_lens", torch)
+    if max_len is None:
+        max_len = table.shape[1] * cache.page
+    if ws is None:
+        need = kv_evict_workspace_bytes(cache, n_seq, max_len, budget)
+        ws = _workspace(need, dev) if need else None
+    wp, wn = _few_ws(ws, dev)
+    _few_launch(lib.gptq_kv_evict, dev, torch, cache.ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n_seq, max_len,
+                to.data_ptr(), to.shape[1], budget, recent, kept.data_ptr(), new_lens.data_ptr(), wp, wn)
+    return kept, new_lens
 
 
 @dataclass

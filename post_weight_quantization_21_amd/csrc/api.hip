@@ -121,6 +121,71 @@ gptq_status check_apart(const void *X, int64_t M, int64_t ldx, int64_t d_in, con
     return GPTQ_OK;
 }
 
+// The same for many rows of one kind: rows next to each other (or columns of one tensor) take no loop.
+bool many_overlap(const void *a, int64_t a_pitch, int64_t a_row, const void *b, int64_t b_pitch, int64_t b_row, int64_t n) {
+    const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+    if ((n - 1) * a_pitch + a_row <= d || (n - 1) * b_pitch + b_row <= -d) return false;
+    // row i of a and row j of b share a byte where -b_row < d + j b_pitch - i a_pitch < a_row
+    for (int64_t i = 0; i < n; ++i) {
+        const int64_t at = i * a_pitch - d;  // the first j with at - b_row < j b_pitch
+        const int64_t j = at - b_row < 0 ? 0 : (at - b_row) / b_pitch + 1;
+        if (j < n && j * b_pitch < at + a_row) return true;
+        if (a_pitch == b_pitch && j > 0) return false;  // a later row lies to its neighbours as this one does
+    }
+    return false;
+}
+
+constexpr int64_t kKvTokens = (int64_t)1 << 30;  // of a table
+
+gptq_status check_kv(const gptq_kv_cache *c, const char *fn) {
+    if (!c) return fail(GPTQ_ERR_INVALID_ARG, "%s: cache is NULL", fn);
+    if (c->n_pages <= 0 || c->n_heads <= 0 || c->head_dim <= 0 || c->page <= 0)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: cache: sizes must be > 0", fn);
+    if (c->group_size < 0 || (c->group_size > 0 && c->head_dim % c->group_size != 0))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: cache: group_size does not divide head_dim", fn);
+    if (c->symmetric != 0 && c->symmetric != 1) return fail(GPTQ_ERR_INVALID_ARG, "%s: cache: symmetric must be 0 or 1", fn);
+    if (c->head_dim % 64 != 0 || c->head_dim > 256) return fail(GPTQ_ERR_UNSUPPORTED, "%s: cache: head_dim must be 64, 128, 192 or 256", fn);
+    if (c->group_size != 0 && c->group_size != c->head_dim && c->group_size != 32 && c->group_size != 64 && c->group_size != 128)
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: cache: group_size must be 32, 64, 128 or head_dim", fn);
+    if ((c->page & (c->page - 1)) != 0 || c->page < 16 || c->page > (1 << 20))
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: cache: page must be a power of two, 16 .. 2^20", fn);
+    if (c->n_pages > 0x7FFFFFFF || c->n_heads > 65535) return fail(GPTQ_ERR_UNSUPPORTED, "%s: cache: too many pages or heads", fn);
+    if (!c->k || !c->v || !c->k_grid || !c->v_grid) return fail(GPTQ_ERR_INVALID_ARG, "%s: cache: NULL pointer", fn);
+    if (!aligned(c->k) || !aligned(c->v) || !aligned(c->k_grid) || !aligned(c->v_grid) || !aligned(c->weight))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: cache: pointers must be 16-byte aligned", fn);
+    return GPTQ_OK;
+}
+
+// The sequences of a call, and the longest length that counts.
+gptq_status check_seqs(const gptq_kv_cache *c, const int32_t *table, int64_t width, const int32_t *lens, int64_t n_seq, int64_t max_len,
+                       const char *fn) {
+    if (n_seq < 0 || width <= 0 || max_len < 0) return fail(GPTQ_ERR_INVALID_ARG, "%s: bad sizes", fn);
+    if (n_seq > 65535 || width > kKvTokens / c->page) return fail(GPTQ_ERR_UNSUPPORTED, "%s: more than 65535 sequences or 2^30 tokens of one", fn);
+    if (max_len > width * c->page) return fail(GPTQ_ERR_INVALID_ARG, "%s: max_len is more than the table holds", fn);
+    if (n_seq > 0 && (!table || !lens)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (!aligned(table, 4) || !aligned(lens, 4)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    return GPTQ_OK;
+}
+
+gptq_status check_kv_queries(const gptq_kv_cache *c, int64_t n_seq, int64_t n, int64_t q_heads, int64_t max_len, const char *fn) {
+    if (n_seq < 0 || max_len < 0 || n <= 0 || q_heads <= 0 || q_heads % c->n_heads != 0)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: bad sizes (q_heads must be a multiple of n_heads)", fn);
+    if (n > 16 || q_heads / c->n_heads > 256) return fail(GPTQ_ERR_UNSUPPORTED, "%s: at most 16 tokens, and 256 query heads on one", fn);
+    const int64_t tiles = gptq::ceil_div(n * (q_heads / c->n_heads), 16);
+    if (n_seq > 65535 || max_len > kKvTokens || n_seq * c->n_heads * tiles > ((int64_t)1 << 20) ||
+        n_seq * gptq::ceil_div(max_len, 32) > ((int64_t)1 << 30))
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: too many sequences, heads and queries at once", fn);
+    return GPTQ_OK;
+}
+
+gptq_status check_kv_budget(const gptq_kv_cache *c, int64_t n_seq, int64_t max_len, int64_t budget, const char *fn) {
+    if (n_seq < 0 || max_len < 0 || budget < 1) return fail(GPTQ_ERR_INVALID_ARG, "%s: bad sizes", fn);
+    if (n_seq > 65535 || max_len > kKvTokens || budget > kKvTokens || n_seq * c->n_heads > ((int64_t)1 << 20) ||
+        n_seq * c->n_heads * budget > ((int64_t)1 << 27))
+        return fail(GPTQ_ERR_UNSUPPORTED, "%s: too many sequences, heads and kept tokens at once", fn);
+    return GPTQ_OK;
+}
+
 gptq_status run_gemv_checked(const void *X, gptq_dtype x_dt, int64_t M, int64_t ldx, const gptq_packed *w,
                              const gptq_packed *up, const float *bias, void *Y, gptq_dtype y_dt, int64_t ldy, void *ws,
                              size_t ws_bytes, hipStream_t stream, const char *fn) {
@@ -531,6 +596,111 @@ gptq_status gptq_moe_layer(const void *X, gptq_dtype x_dtype, int64_t T, int64_t
     if (st != GPTQ_OK) return st;
     return hip_status(gptq::run_moe(X, x_dtype, T, ldx, router, router_dtype, n_experts, top_k, renormalize ? 1 : 0, *gate,
                                     *up, *down, ids, weights, Y, y_dtype, ldy, ws, stream),
+                      fn);
+}
+
+gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv, gptq_dtype dtype, int64_t T, const int32_t *offs,
+                           const gptq_kv_cache *cache, const int32_t *table, int64_t width, const int32_t *lens, int64_t n_seq,
+                           void *K_out, int64_t ldko, void *V_out, int64_t ldvo, hipStream_t stream) {
+    const char *fn = "gptq_kv_append";
+    gptq_status st = check_kv(cache, fn);
+    if (st == GPTQ_OK) st = check_seqs(cache, table, width, lens, n_seq, 0, fn);
+    if (st != GPTQ_OK) return st;
+    const int64_t row = (int64_t)cache->n_heads * cache->head_dim;
+    if (!few_dtype(dtype)) return fail(GPTQ_ERR_INVALID_ARG, "%s: keys and values must be fp16 or bf16", fn);
+    if (T < 0 || (!offs && T > 0 && (n_seq == 0 || T % n_seq != 0)))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: T must be a multiple of n_seq where there are no offsets", fn);
+    if (T > ((int64_t)1 << 26) / cache->n_heads) return fail(GPTQ_ERR_UNSUPPORTED, "%s: T * n_heads above 2^26", fn);
+    if (T > 0 && (!K || !V)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (ldk < row || ldv < row || (K_out && ldko < row) || (V_out && ldvo < row))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: leading dimension too small", fn);
+    if (!aligned(K) || !aligned(V) || ldk % 8 != 0 || ldv % 8 != 0 || (K_out && (!aligned(K_out) || ldko % 8 != 0)) ||
+        (V_out && (!aligned(V_out) || ldvo % 8 != 0)))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: K, V and the results must be 16-byte aligned, their pitches multiples of 8", fn);
+    if (offs && !aligned(offs, 4)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned offsets", fn);
+    if (T == 0 || n_seq == 0) return GPTQ_OK;
+    // a thread writes the values that it read, after reading them
+    const bool same_k = K_out == K && ldko == ldk, same_v = V_out == V && ldvo == ldv;
+    if ((K_out && ((!same_k && many_overlap(K, 2 * ldk, 2 * row, K_out, 2 * ldko, 2 * row, T)) ||
+                   many_overlap(V, 2 * ldv, 2 * row, K_out, 2 * ldko, 2 * row, T))) ||
+        (V_out && ((!same_v && many_overlap(V, 2 * ldv, 2 * row, V_out, 2 * ldvo, 2 * row, T)) ||
+                   many_overlap(K, 2 * ldk, 2 * row, V_out, 2 * ldvo, 2 * row, T))) ||
+        (K_out && V_out && many_overlap(K_out, 2 * ldko, 2 * row, V_out, 2 * ldvo, 2 * row, T)))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: K, V and the results overlap", fn);
+    return hip_status(gptq::run_kv_append(K, ldk, V, ldv, dtype, T, offs, *cache, table, width, lens, n_seq, K_out, ldko, V_out, ldvo, stream),
+                      fn);
+}
+
+gptq_status gptq_kv_attention_workspace_bytes(const gptq_kv_cache *cache, int64_t n_seq, int64_t n, int64_t q_heads, int64_t max_len,
+                                              size_t *out) {
+    const char *fn = "gptq_kv_attention_workspace_bytes";
+    if (!out) return fail(GPTQ_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    gptq_status st = check_kv(cache, fn);
+    if (st == GPTQ_OK) st = check_kv_queries(cache, n_seq, n, q_heads, max_len, fn);
+    if (st != GPTQ_OK) return st;
+    *out = gptq::kv_attention_ws_bytes(*cache, n_seq, n, q_heads, max_len);
+    return GPTQ_OK;
+}
+
+gptq_status gptq_kv_attention(const void *Q, gptq_dtype dtype, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq,
+                              const gptq_kv_cache *cache, const int32_t *table, int64_t width, const int32_t *lens, int64_t max_len,
+                              float scale, int32_t accumulate, float decay, void *O, int64_t ldo, void *ws, size_t ws_bytes,
+                              hipStream_t stream) {
+    const char *fn = "gptq_kv_attention";
+    gptq_status st = check_kv(cache, fn);
+    if (st == GPTQ_OK) st = check_seqs(cache, table, width, lens, n_seq, max_len, fn);
+    if (st == GPTQ_OK) st = check_kv_queries(cache, n_seq, n, q_heads, max_len, fn);
+    if (st != GPTQ_OK) return st;
+    const int64_t row = q_heads * cache->head_dim;
+    if (!few_dtype(dtype)) return fail(GPTQ_ERR_INVALID_ARG, "%s: queries must be fp16 or bf16", fn);
+    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(GPTQ_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
+    if (accumulate && !(decay >= 0.0f && decay <= 1.0f)) return fail(GPTQ_ERR_INVALID_ARG, "%s: decay outside [0, 1]", fn);
+    if (accumulate && !cache->weight) return fail(GPTQ_ERR_INVALID_ARG, "%s: the cache keeps no weights", fn);
+    if (n_seq > 0 && (!Q || !O)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (ldq < row || ldo < row) return fail(GPTQ_ERR_INVALID_ARG, "%s: leading dimension too small", fn);
+    if (!aligned(Q) || ldq % 8 != 0 || !aligned(O, 2))
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: Q must be 16-byte aligned with ldq a multiple of 8, O 2-byte aligned", fn);
+    if (n_seq == 0) return GPTQ_OK;
+    const size_t need = gptq::kv_attention_ws_bytes(*cache, n_seq, n, q_heads, max_len);
+    if (!ws || ws_bytes < need) return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
+    if (!aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    if (many_overlap(Q, 2 * ldq, 2 * row, O, 2 * ldo, 2 * row, n_seq * n)) return fail(GPTQ_ERR_INVALID_ARG, "%s: Q and the result overlap", fn);
+    return hip_status(gptq::run_kv_attention(Q, dtype, n_seq, n, q_heads, ldq, *cache, table, width, lens, max_len, scale, accumulate != 0,
+                                             decay, O, ldo, ws, stream),
+                      fn);
+}
+
+gptq_status gptq_kv_evict_workspace_bytes(const gptq_kv_cache *cache, int64_t n_seq, int64_t max_len, int64_t budget, size_t *out) {
+    const char *fn = "gptq_kv_evict_workspace_bytes";
+    if (!out) return fail(GPTQ_ERR_INVALID_ARG, "%s: out is NULL", fn);
+    gptq_status st = check_kv(cache, fn);
+    if (st == GPTQ_OK) st = check_kv_budget(cache, n_seq, max_len, budget, fn);
+    if (st != GPTQ_OK) return st;
+    *out = gptq::kv_evict_ws_bytes(*cache, n_seq, max_len, budget);
+    return GPTQ_OK;
+}
+
+gptq_status gptq_kv_evict(const gptq_kv_cache *cache, const int32_t *table, int64_t width, const int32_t *lens, int64_t n_seq,
+                          int64_t max_len, const int32_t *to, int64_t to_width, int64_t budget, int64_t recent, int32_t *kept,
+                          int32_t *new_lens, void *ws, size_t ws_bytes, hipStream_t stream) {
+    const char *fn = "gptq_kv_evict";
+    gptq_status st = check_kv(cache, fn);
+    if (st == GPTQ_OK) st = check_seqs(cache, table, width, lens, n_seq, max_len, fn);
+    if (st == GPTQ_OK) st = check_kv_budget(cache, n_seq, max_len, budget, fn);
+    if (st != GPTQ_OK) return st;
+    if (recent < 0 || recent > budget) return fail(GPTQ_ERR_INVALID_ARG, "%s: recent outside 0 .. budget", fn);
+    if (to_width <= 0 || to_width > kKvTokens / cache->page || to_width * cache->page < budget)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: the pages to fill do not hold the budget", fn);
+    if (!cache->weight) return fail(GPTQ_ERR_INVALID_ARG, "%s: the cache keeps no weights", fn);
+    if (n_seq > 0 && (!to || !kept)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);
+    if (!aligned(to, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+    if (new_lens && new_lens == lens) return fail(GPTQ_ERR_INVALID_ARG, "%s: new_lens is lens", fn);
+    if (n_seq == 0) return GPTQ_OK;
+    const size_t need = gptq::kv_evict_ws_bytes(*cache, n_seq, max_len, budget);
+    if (need > 0 && (!ws || ws_bytes < need))
+        return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
+    if (need > 0 && !aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    return hip_status(gptq::run_kv_evict(*cache, table, width, lens, n_seq, max_len, to, to_width, budget, recent, kept, new_lens, ws, stream),
                       fn);
 }
 

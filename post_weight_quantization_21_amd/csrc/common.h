@@ -132,6 +132,22 @@ hipError_t run_moe(const void *X, gptq_dtype x_dt, int64_t T, int64_t ldx, const
                    void *ws, hipStream_t s);
 
 // ---------------------------------------------------------------------------
+// 4-bit key/value cache (kv_append.hip, kv_attention.hip, kv_evict.hip)
+// ---------------------------------------------------------------------------
+hipError_t run_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv, gptq_dtype dt, int64_t T, const int32_t *offs,
+                         const gptq_kv_cache &c, const int32_t *table, int64_t width, const int32_t *lens, int64_t n_seq,
+                         void *K_out, int64_t ldko, void *V_out, int64_t ldvo, hipStream_t s);
+size_t kv_attention_ws_bytes(const gptq_kv_cache &c, int64_t n_seq, int64_t n, int64_t q_heads, int64_t max_len);
+// weights: whether the cached tokens' weights are accumulated, with `decay` for the old ones.
+hipError_t run_kv_attention(const void *Q, gptq_dtype dt, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq,
+                            const gptq_kv_cache &c, const int32_t *table, int64_t width, const int32_t *lens, int64_t max_len,
+                            float scale, bool weights, float decay, void *O, int64_t ldo, void *ws, hipStream_t s);
+size_t kv_evict_ws_bytes(const gptq_kv_cache &c, int64_t n_seq, int64_t max_len, int64_t budget);
+hipError_t run_kv_evict(const gptq_kv_cache &c, const int32_t *table, int64_t width, const int32_t *lens, int64_t n_seq,
+                        int64_t max_len, const int32_t *to, int64_t to_width, int64_t budget, int64_t recent, int32_t *kept,
+                        int32_t *new_lens, void *ws, hipStream_t s);
+
+// ---------------------------------------------------------------------------
 // Per-channel scaling before the pass (prepass.hip)
 // ---------------------------------------------------------------------------
 hipError_t run_channel_stats(const void *X, gptq_dtype dt, int64_t d_in, int64_t n_tok, int64_t ldx, float *absmax,

@@ -1,0 +1,138 @@
+"""gptq_kv_append, gptq_kv_attention and gptq_kv_evict: workspace queries and refused calls (no GPU work: every refusal comes
+before anything is launched, and so do calls without sequences or tokens)."""
+import ctypes
+
+import pytest
+
+import post_weight_quantization_21_amd as gq
+
+P = 0x10000000  # made-up aligned addresses, far apart
+FAR = 0x4000000000
+INV, UNS, WS = gq.ERR_INVALID_ARG, gq.ERR_UNSUPPORTED, gq.ERR_WORKSPACE
+
+
+def cache(k=P, v=P, kg=P, vg=P, weight=P, pages=100, heads=2, dim=128, page=64, group=0, sym=0):
+    return gq.KVCacheStruct(k, v, kg, vg, weight, pages, heads, dim, page, group, sym)
+
+
+def ref(c):
+    return None if c is None else ctypes.byref(c)
+
+
+def append(c, K=P, ldk=256, V=2 * P, ldv=256, dt=gq.DT_BF16, T=4, offs=None, table=P, width=8, lens=P, n_seq=2, Ko=None, ldko=256,
+           Vo=None, ldvo=256):
+    return gq.load_library().gptq_kv_append(K, ldk, V, ldv, dt, T, offs, ref(c), table, width, lens, n_seq, Ko, ldko, Vo, ldvo, None)
+
+
+def attention(c, Q=P, dt=gq.DT_F16, n_seq=2, n=1, hq=8, ldq=1024, table=P, width=8, lens=P, max_len=512, scale=0.1, acc=0, decay=0.0,
+              O=2 * P, ldo=1024, ws=FAR, ws_bytes=1 << 40):
+    return gq.load_library().gptq_kv_attention(Q, dt, n_seq, n, hq, ldq, ref(c), table, width, lens, max_len, scale, acc, decay, O, ldo,
+                                               ws, ws_bytes, None)
+
+
+def evict(c, table=P, width=8, lens=P, n_seq=2, max_len=512, to=P, to_width=2, budget=128, recent=16, kept=P, new=2 * P, ws=FAR,
+          ws_bytes=1 << 40):
+    return gq.load_library().gptq_kv_evict(ref(c), table, width, lens, n_seq, max_len, to, to_width, budget, recent, kept, new, ws,
+                                           ws_bytes, None)
+
+
+@pytest.mark.parametrize("c,status,text", [
+    (None, INV, b"NULL"), (cache(k=None), INV, b"NULL"), (cache(v=None), INV, b"NULL"), (cache(kg=None), INV, b"NULL"),
+    (cache(vg=None), INV, b"NULL"), (cache(k=P + 8), INV, b"aligned"), (cache(weight=P + 4), INV, b"aligned"),
+    (cache(pages=0), INV, b"sizes"), (cache(heads=0), INV, b"sizes"), (cache(dim=0), INV, b"sizes"), (cache(page=0), INV, b"sizes"),
+    (cache(group=48), INV, b"group_size"), (cache(group=-32), INV, b"group_size"), (cache(sym=2), INV, b"symmetric"),
+    (cache(dim=96), UNS, b"head_dim"), (cache(dim=320), UNS, b"head_dim"), (cache(group=16), UNS, b"group_size"),
+    (cache(dim=192, group=96), UNS, b"group_size"), (cache(page=48), UNS, b"page"), (cache(page=8), UNS, b"page"),
+    (cache(page=1 << 21), UNS, b"page"), (cache(pages=1 << 31), UNS, b"pages"), (cache(heads=65536), UNS, b"heads"),
+])
+def test_caches_refused(c, status, text):
+    out = ctypes.c_size_t(0)
+    lib = gq.load_library()
+    for call in (lambda: append(c), lambda: attention(c), lambda: evict(c),
+                 lambda: lib.gptq_kv_attention_workspace_bytes(ref(c), 2, 1, 8, 512, ctypes.byref(out)),
+                 lambda: lib.gptq_kv_evict_workspace_bytes(ref(c), 2, 512, 128, ctypes.byref(out))):
+        assert call() == status
+        assert text in lib.gptq_last_error()
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n_seq=-1), INV), (dict(width=0), INV), (dict(table=None), INV), (dict(lens=None), INV), (dict(table=P + 2), INV),
+    (dict(lens=P + 1), INV), (dict(n_seq=65536), UNS), (dict(width=(1 << 24) + 1), UNS),
+])
+def test_sequences_refused(kw, status):
+    assert append(cache(), **{"T": 0, **kw}) == status
+    assert attention(cache(), **kw) == status
+    assert evict(cache(), **kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), INV), (dict(T=3), INV), (dict(T=4, n_seq=0), INV), (dict(T=(1 << 25) + 2), UNS), (dict(dt=gq.DT_F32), INV),
+    (dict(K=None), INV), (dict(V=None), INV), (dict(ldk=248), INV), (dict(ldv=255), INV), (dict(ldk=260), INV), (dict(K=P + 8), INV),
+    (dict(V=P + 2), INV), (dict(Ko=P + 4), INV), (dict(Ko=3 * P, ldko=128), INV), (dict(Vo=3 * P, ldvo=260), INV), (dict(offs=P + 1), INV),
+    (dict(Ko=P + 512, T=2), INV), (dict(Ko=P, ldko=512), INV), (dict(Ko=2 * P), INV),
+    (dict(Vo=P), INV), (dict(Ko=3 * P, Vo=3 * P + 256), INV), (dict(ldk=768, ldv=768, V=P + 512, Ko=P + 1008, ldko=768), INV),
+])
+def test_append_refused(kw, status):
+    assert append(cache(), **kw) == status
+
+
+def test_append_without_tokens():
+    assert append(cache(), T=0) == gq.OK
+    assert append(cache(), T=0, K=None, V=None) == gq.OK
+    assert append(cache(), T=0, n_seq=0, table=None, lens=None) == gq.OK
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=0), INV), (dict(n=17), UNS), (dict(hq=7, ldq=4096, ldo=4096), INV), (dict(hq=0), INV),
+    (dict(hq=514, ldq=1 << 17, ldo=1 << 17), UNS), (dict(dt=gq.DT_F32), INV), (dict(max_len=513), INV), (dict(max_len=-1), INV),
+    (dict(scale=0.0), INV), (dict(scale=-1.0), INV), (dict(scale=float("nan")), INV), (dict(scale=float("inf")), INV),
+    (dict(acc=1, decay=1.5), INV), (dict(acc=1, decay=-0.1), INV), (dict(acc=1, decay=float("nan")), INV), (dict(Q=None), INV),
+    (dict(O=None), INV), (dict(ldq=1016), INV), (dict(ldo=1023), INV), (dict(ldq=1028), INV), (dict(Q=P + 8), INV), (dict(O=P + 1), INV),
+    (dict(ws=None), WS), (dict(ws_bytes=8), WS), (dict(ws=FAR + 8), INV), (dict(O=P), INV), (dict(O=P + 2046), INV),
+    (dict(n_seq=65535, n=16, hq=32, ldq=4096, ldo=4096), UNS),
+])
+def test_attention_refused(kw, status):
+    assert attention(cache(), **kw) == status
+
+
+def test_attention_needs_weights_to_accumulate():
+    assert attention(cache(weight=None), acc=1) == INV
+    assert b"weights" in gq.load_library().gptq_last_error()
+
+
+def test_attention_without_sequences():
+    assert attention(cache(), n_seq=0, Q=None, O=None, table=None, lens=None, ws=None, ws_bytes=0) == gq.OK
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(budget=0), INV), (dict(recent=-1), INV), (dict(recent=129), INV), (dict(to_width=0), INV), (dict(to_width=1), INV),
+    (dict(to=None), INV), (dict(kept=None), INV), (dict(to=P + 2), INV), (dict(kept=P + 1), INV), (dict(new=P + 3), INV),
+    (dict(new=P), INV), (dict(max_len=513), INV), (dict(budget=1 << 27, to_width=1 << 21, n_seq=2), UNS),
+])
+def test_evict_refused(kw, status):
+    assert evict(cache(), **kw) == status
+
+
+def test_evict_needs_weights():
+    assert evict(cache(weight=None)) == INV
+    assert b"weights" in gq.load_library().gptq_last_error()
+    assert evict(cache(), n_seq=0, table=None, lens=None, to=None, kept=None, new=None, ws=None, ws_bytes=0) == gq.OK
+
+
+def test_workspace_grows_with_rows_not_with_length():
+    def need(**kw):
+        a = dict(n_seq=4, n=1, hq=8, max_len=1 << 20, c=cache())
+        a.update(kw)
+        out = ctypes.c_size_t(0)
+        st = gq.load_library().gptq_kv_attention_workspace_bytes(ref(a["c"]), a["n_seq"], a["n"], a["hq"], a["max_len"], ctypes.byref(out))
+        assert st == gq.OK
+        return out.value
+
+    assert need() < 64 << 20
+    assert need(max_len=1 << 24) == need()
+    assert need(max_len=100) <= need(max_len=4096) <= need()
+    assert need(n_seq=2) <= need()
+
+
+def test_struct_matches_the_header():
+    assert ctypes.sizeof(gq.KVCacheStruct) == 6 * 8 + 5 * 4 + 4
