@@ -1,12 +1,12 @@
 // New keys and values into the pages of a 4-bit cache.
 //
 // A group's grid (all decisions binary32, round half to even):
-//   asymmetric  lo = min(min x, 0), hi = max(max x, 0), s = bf16((hi - lo) / 15),
+//   asymmetric  lo = min(min x, 0), hi = max(max x, 0), s = bf16((hi - lo) (1/15)),
 //               z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(x / s + z), 0, 15)
-//   symmetric   s = bf16(max|x| / 7), z = 8, q = clamp(rint(x / s), -7, 7) + 8
-// with s = 1 where it would be 0.  The scale is rounded before the codes are chosen,
-// so its sixteen bits cost no accuracy beyond the last code's (a range may end 0.06
-// of a step past code 15).  A group with a value that is not finite, or whose scale
+//   symmetric   s = bf16(max|x| (1/7)), z = 8, q = clamp(rint(x / s), -7, 7) + 8
+// with s = 1 where it would be 0 (1/15 and 1/7: the nearest binary32).  The scale is
+// rounded before the codes are chosen, so its sixteen bits cost no accuracy beyond the
+// last code's (a range may end 0.06 of a step past code 15).  A group with a value that is not finite, or whose scale
 // is not, is stored with a scale that is no number.
 #include "kv_cache.h"
 
@@ -62,7 +62,7 @@ struct Grid4 {
 __device__ __forceinline__ Grid4 fit4(const Range &r, bool symmetric) {
 #pragma clang fp contract(off)
     Grid4 g;
-    const float s = symmetric ? fmaxf(-r.lo, r.hi) / 7.0f : (r.hi - r.lo) / 15.0f;
+    const float s = symmetric ? fmaxf(-r.lo, r.hi) * (1.0f / 7.0f) : (r.hi - r.lo) * (1.0f / 15.0f);
     g.s = (float)(__bf16)s;
     if (g.s == 0.0f) g.s = 1.0f;
     g.bad = r.bad || !(g.s < __builtin_inff());

@@ -20,10 +20,10 @@ def fit(x: np.ndarray, group: int, symmetric: bool):
     g = x.reshape(*x.shape[:-1], -1, group)
     with np.errstate(all="ignore"):
         if symmetric:
-            s = np.abs(g).max(-1, keepdims=True) / f(7)
+            s = np.abs(g).max(-1, keepdims=True) * (f(1) / f(7))
         else:
             lo, hi = np.minimum(g.min(-1, keepdims=True), f(0)), np.maximum(g.max(-1, keepdims=True), f(0))
-            s = (hi - lo) / f(15)
+            s = (hi - lo) * (f(1) / f(15))
         bad = ~np.isfinite(g).all(-1, keepdims=True)
         s = bf16_round(np.where(np.isfinite(s), s, f(np.inf)))
         s = np.where(s == 0, f(1), s)
