@@ -18,6 +18,7 @@
 // One pass with a running maximum: the sums are rescaled only when a score passes the
 // maximum they are held to by 2^6 (p may then be up to 64, which fp16 and fp32 hold).
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_cache.h"
 
@@ -27,7 +28,7 @@ namespace {
 constexpr int kKvTile = 32;   // tokens of a tile
 constexpr int kKvWaves = 4;   // waves of a workgroup, each with tiles of its own
 constexpr int kKvThreads = kKvWaves * kWave;
-constexpr int kKvLeast = 8;   // tiles of a workgroup at least
+constexpr int kKvLeast = 4;   // tiles of a workgroup at least
 constexpr float kSlack = 6.0f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -38,527 +39,713 @@ struct AttnArgs {
     int64_t ldq;
     uint16_t *o;
     int64_t ldo;
-    float *part;   // [item][head][column][D], unnormalized, relative to the item's maximum
-    float2 *stat;  // [item][head][column]: maximum (of log2) and sum
+    float *part;   // [segment][head][column][D], unnormalized, relative to the segment's maximum
+    float2 *stat;  // [segment][head][column]: maximum (of log2) and sum
+    float2 *last;  // [sequence][head][column]: maximum and 1 / sum over all of a sequence, or NULL
     float scale;   // times log2 e
     float decay;
     int32_t n, group, cols;  // new tokens, query heads of a kv head, n * group
-    int32_t target;  // items wanted over all sequences
-    int32_t bf16, direct, keep_stat;
+    int32_t target;  // workgroups that share the tiles
+    int32_t bf16, direct;
 };
 
 __device__ __forceinline__ float xor_max(float v, int o) { return fmaxf(v, __shfl_xor(v, o)); }
 __device__ __forceinline__ float xor_add(float v, int o) { return v + __shfl_xor(v, o); }
 
-// How the cached tokens are shared out: items of `chunk` tiles, sequence after sequence.
+// The thread's number as a value that nothing is computed from ahead of time: what a rare path derives from it would hold
+// registers over the loops otherwise.
+__device__ __forceinline__ int fresh_thread() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
+// How the cached tokens are shared out: the tiles of all sequences in a row, `chunk` to a
+// workgroup, whose part of one sequence is a segment.  Workgroup x's segment of sequence b
+// has the number x + b.
 struct Share {
-    int b, first, tiles, chunk;  // the item's sequence, its first tile and how many; tiles of a whole item
-    int base, splits, len;       // the sequence's first item, and how many it has
+    int b, start, tiles, len;  // a sequence, its first tile in the row, its tiles and length
 };
 __device__ __forceinline__ int tiles_of(const KvSeqs &s, int b) { return b < s.n ? (s.len(b) + kKvTile - 1) / kKvTile : 0; }
-__device__ __forceinline__ int chunk_of(const AttnArgs &a) {
+__device__ __forceinline__ int wave_sum(int v) {
+    for (int o = 1; o < kWave; o *= 2) v += __shfl_xor(v, o);
+    return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ int total_tiles(const AttnArgs &a) {
     const int lane = threadIdx.x & 63;
     int total = 0;
     for (int b0 = 0; b0 < a.seqs.n; b0 += kWave) total += tiles_of(a.seqs, b0 + lane);
-    for (int o = 1; o < kWave; o *= 2) total += __shfl_xor(total, o);
+    return wave_sum(total);
+}
+__device__ __forceinline__ int chunk_of(const AttnArgs &a, int total) {
     const int c = (total + a.target - 1) / a.target;
     return max(kKvLeast, (c + kKvWaves - 1) / kKvWaves * kKvWaves);
 }
-// The share of item x (b < 0: there is none), or with `seq` the items of sequence x.
-__device__ __forceinline__ Share share_of(const AttnArgs &a, int x, bool seq) {
+// The sequence that tile `at` of the row belongs to, or with `seq` sequence `at`.
+__device__ __forceinline__ Share share_of(const AttnArgs &a, int at, bool seq) {
     const int lane = threadIdx.x & 63;
-    Share s;
-    s.b = -1;
-    s.chunk = chunk_of(a);
+    Share s = {};
     int base = 0;
     for (int b0 = 0; b0 < a.seqs.n; b0 += kWave) {
-        const int tiles = tiles_of(a.seqs, b0 + lane), mine = (tiles + s.chunk - 1) / s.chunk;
-        int sum = mine;
+        const int tiles = tiles_of(a.seqs, b0 + lane);
+        int sum = tiles;
         for (int o = 1; o < kWave; o *= 2) {
             const int v = __shfl_up(sum, o);
             if (lane >= o) sum += v;
         }
-        const int from = base + sum - mine;
-        const uint64_t hit = __ballot(seq ? b0 + lane == x : from <= x && x < from + mine);
+        const int from = base + sum - tiles;
+        const uint64_t hit = __ballot(seq ? b0 + lane == at : from <= at && at < from + tiles);
         if (hit) {
             const int l = __builtin_ctzll(hit);
             s.b = b0 + l;
-            s.base = __shfl(from, l);
-            s.splits = __shfl(mine, l);
-            s.first = (x - s.base) * s.chunk;
-            s.tiles = min(s.chunk, __shfl(tiles, l) - s.first);
+            s.start = __builtin_amdgcn_readlane(from, l);
+            s.tiles = __builtin_amdgcn_readlane(tiles, l);
             s.len = a.seqs.len(s.b);
-            return s;
+            break;
         }
-        base += __shfl(sum, kWave - 1);
+        base += __builtin_amdgcn_readlane(sum, kWave - 1);
     }
     return s;
 }
 
-// The share of this workgroup.
-__device__ __forceinline__ Share my_share(const AttnArgs &a) {
-    if (!a.direct) return share_of(a, blockIdx.x, false);
-    const int b = blockIdx.x, tiles = tiles_of(a.seqs, b);
-    return {b, 0, tiles, tiles, b, 1, a.seqs.len(b)};
-}
+// The pages of a tile: one, or with pages of sixteen tokens one for each half.  -1: there is none.
+struct TilePages {
+    int lo, hi;
+    __device__ __forceinline__ TilePages(const AttnArgs &a, const int32_t *row, int tile, int len) {
+        const int slot = tile * kKvTile;
+        lo = hi = a.seqs.page_of(a.pool, row, slot);
+        if (a.pool.lg_page == 4) hi = slot + 16 < len ? a.seqs.page_of(a.pool, row, slot + 16) : lo;
+    }
+    __device__ __forceinline__ bool missing() const { return (lo | hi) < 0; }
+};
 
+// A wave's 32 cached tokens, as they come from memory.  Lane 16 kb + r holds key row r (token 8 (r / 4) + 4 t + r % 4 of
+// half t), dims of lane row kb; of the values the eight tokens of block kb, dims 64 u + 16 j + r; and of the grids token
+// lane % 32, keys in the lower lanes, values in the upper ones.
 template <int D64, int NG>
-struct Tile {  // a lane's part of 32 cached tokens
+struct Tile {
     static constexpr int D = 64 * D64, KW = D / 32;
     uint32_t k[2][KW];
     u32x4 v[D64];
-    u32x4 kg[NG][2], vg[NG][2];
-    bool there;  // the page of this lane's eight tokens exists
+    uint32_t grid[NG];
 
-    __device__ __forceinline__ void load(const KvPool &pool, const KvSeqs &seqs, const int32_t *row, int tile, int last_block, int h) {
-        const int lane = threadIdx.x & 63, r = lane & 15, kb = lane >> 4, mask = pool.page() - 1;
-        const int bk = min(4 * tile + (r >> 2), last_block), bv = min(4 * tile + kb, last_block);  // blocks of eight tokens
-        const int pk = seqs.page_of(pool, row, 8 * bk), pv = seqs.page_of(pool, row, 8 * bv);
-        there = pv >= 0;
-        const int64_t fk = pool.first(max(pk, 0), h), fv = pool.first(max(pv, 0), h);
-        const int ak = (8 * bk) & mask, av = (8 * bv) & mask;
+    template <typename T>
+    __device__ __forceinline__ static const T *at(const char *base, uint32_t bytes) {
+        return reinterpret_cast<const T *>(base + bytes);
+    }
+    __device__ __forceinline__ void key_words(const char *words, uint32_t off) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t *p = pool.k + (fk + ak + 4 * t + (r & 3)) * (D / 8) + kb * KW;
             if constexpr (KW % 4 == 0) {
 #pragma unroll
                 for (int i = 0; i < KW; i += 4) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(p + i);
+                    const u32x4 w = *at<u32x4>(words, off + 2 * D * t + 4 * i);
                     k[t][i] = w[0], k[t][i + 1] = w[1], k[t][i + 2] = w[2], k[t][i + 3] = w[3];
                 }
             } else {
 #pragma unroll
                 for (int i = 0; i < KW; i += 2) {
-                    const u32x2 w = *reinterpret_cast<const u32x2 *>(p + i);
+                    const u32x2 w = *at<u32x2>(words, off + 2 * D * t + 4 * i);
                     k[t][i] = w[0], k[t][i + 1] = w[1];
                 }
             }
         }
+    }
+    __device__ __forceinline__ void load_keys(const AttnArgs &a, TilePages p, int tile, int h) {
+        const char *k0 = reinterpret_cast<const char *>(a.pool.k);
+        if (a.pool.lg_page > 4) {  // one page: its base is the same for all lanes
+            const int lane = threadIdx.x & 63, r = lane & 15, kb = lane >> 4, row = 8 * (r >> 2) + (r & 3), tok = lane & 31;
+            const char *g0 = reinterpret_cast<const char *>(lane < 32 ? a.pool.k_grid : a.pool.v_grid);
+            const int64_t first = a.pool.first(max(p.lo, 0), h), in = tile * kKvTile & (a.pool.page() - 1);
+            key_words(k0 + (first + in) * (D / 2), row * (D / 2) + kb * KW * 4);
 #pragma unroll
-        for (int u = 0; u < D64; ++u)
-            v[u] = *reinterpret_cast<const u32x4 *>(pool.v + (fv + av) * (D / 4) + (16 * u + r) * 8);
+            for (int g = 0; g < NG; ++g) grid[g] = *at<uint32_t>(g0 + (first * NG + in) * 4, 4 * tok + ((uint32_t)g << (a.pool.lg_page + 2)));
+        } else {
+            const int lane = fresh_thread() & 63, r = lane & 15, kb = lane >> 4, row = 8 * (r >> 2) + (r & 3), tok = lane & 31;
+            const char *g0 = reinterpret_cast<const char *>(lane < 32 ? a.pool.k_grid : a.pool.v_grid);
+            const int64_t fk = a.pool.first(max(r < 8 ? p.lo : p.hi, 0), h), fg = a.pool.first(max(tok < 16 ? p.lo : p.hi, 0), h);
+            key_words(k0 + fk * (D / 2), (row & 15) * (D / 2) + kb * KW * 4);
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
+            for (int g = 0; g < NG; ++g) grid[g] = *at<uint32_t>(g0 + fg * (4 * NG), 4 * (tok & 15) + 64 * g);
+        }
+    }
+    __device__ __forceinline__ void load_values(const AttnArgs &a, TilePages p, int tile, int h) {
+        const char *v0 = reinterpret_cast<const char *>(a.pool.v);
+        if (a.pool.lg_page > 4) {
+            const int lane = threadIdx.x & 63, r = lane & 15, kb = lane >> 4;
+            const int64_t first = a.pool.first(max(p.lo, 0), h), in = tile * kKvTile & (a.pool.page() - 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int64_t at = fv * NG + (int64_t)g * (mask + 1) + av + 4 * t;
-                kg[g][t] = *reinterpret_cast<const u32x4 *>(pool.k_grid + at);
-                vg[g][t] = *reinterpret_cast<const u32x4 *>(pool.v_grid + at);
-            }
+            for (int u = 0; u < D64; ++u) v[u] = *at<u32x4>(v0 + (first + in) * (D / 2), kb * 4 * D + r * 16 + 256 * u);
+        } else {
+            const int lane = fresh_thread() & 63, r = lane & 15, kb = lane >> 4;
+            const int64_t fv = a.pool.first(max(kb < 2 ? p.lo : p.hi, 0), h);
+#pragma unroll
+            for (int u = 0; u < D64; ++u) v[u] = *at<u32x4>(v0 + fv * (D / 2), (kb & 1) * 4 * D + r * 16 + 256 * u);
+        }
     }
 };
 
-// Codes as fp16 q - 8: masked in place they make 1024 + q or, four bits up, 64 + q.
-struct Unpack {
-    uint32_t m0 = 0x64006400u, m1 = 0x54005400u;
-    __device__ __forceinline__ Unpack() { asm volatile("" : "+v"(m0), "+v"(m1)); }  // registers: VOP3 takes no literal
-    __device__ __forceinline__ uint32_t low(uint32_t w) const {
-        const f16x2 h = __builtin_bit_cast(f16x2, (w & 0x000F000Fu) | m0) - (f16x2){(_Float16)1032.0f, (_Float16)1032.0f};
-        return __builtin_bit_cast(uint32_t, h);
-    }
-    __device__ __forceinline__ uint32_t high(uint32_t w) const {
-        const f16x2 h = __builtin_bit_cast(f16x2, (w & 0x00F000F0u) | m1) - (f16x2){(_Float16)72.0f, (_Float16)72.0f};
-        return __builtin_bit_cast(uint32_t, h);
-    }
-    __device__ __forceinline__ f16x8 keys(uint32_t w) const {
-        const u32x4 f = {low(w), high(w), low(w >> 8), high(w >> 8)};
-        return __builtin_bit_cast(f16x8, f);
-    }
-    // Dim j of the four of each unit: eight tokens.
-    __device__ __forceinline__ f16x8 values(const u32x4 &w, int j) const {
-        u32x4 f;
+// The grids of a wave's tile in LDS, token by token: scales in fp32 (of values times the wave's power of two) and -z in
+// fp16.  Written by the lane that holds a token's word, read by the lanes that need eight.
+template <int NG>
+struct TileGrids {
+    float scale[2][NG][kKvTile];
+    uint16_t zero[2][NG][kKvTile];
+
+    __device__ __forceinline__ void put(const uint32_t grid[NG], float vscale, bool gone) {
+        const int lane = threadIdx.x & 63, side = lane >> 5, tok = lane & 31;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t x = j < 2 ? w[i] : w[i] >> 8;
-            f[i] = j & 1 ? high(x) : low(x);
+        for (int g = 0; g < NG; ++g) {
+            const float s = grid_scale_of(grid[g]);
+            const _Float16 c = __builtin_bit_cast(f16x2, grid[g])[0];
+            scale[side][g][tok] = gone ? 0.0f : side ? s * vscale : s;
+            // a column that does not see a token multiplies its zero by p = 0: it must be a number
+            zero[side][g][tok] = __builtin_bit_cast(uint16_t, gone || !(s == s) ? (_Float16)0.0f : c - (_Float16)8.0f);
         }
-        return __builtin_bit_cast(f16x8, f);
+    }
+    // Eight tokens of block kb; t: four of them.
+    __device__ __forceinline__ floatx4 scales(int side, int g, int kb, int t) const {
+        return *reinterpret_cast<const floatx4 *>(&scale[side][g][8 * kb + 4 * t]);
+    }
+    __device__ __forceinline__ f16x8 zeros(int side, int g, int kb) const {
+        return *reinterpret_cast<const f16x8 *>(&zero[side][g][8 * kb]);
     }
 };
+// What the wave has put into LDS is there for its other lanes.
+__device__ __forceinline__ void wave_fence() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Codes as fp16, masked in place: subnormal numbers q 2^-24 or, four bits up, q 2^-20, which the matrix cores take as they
+// are (an instruction a pair; with q - 8 as normal numbers it would be two).
+__device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x000F000Fu; }
+__device__ __forceinline__ uint32_t high(uint32_t w) { return w & 0x00F000F0u; }
+__device__ __forceinline__ f16x8 key_frag(uint32_t w) {  // pairs 0 and 2 are 2^4 smaller: the queries' are 2^4 larger there
+    const uint32_t x = w >> 8;
+    const u32x4 f = {low(w), high(w), low(x), high(x)};
+    return __builtin_bit_cast(f16x8, f);
+}
+// Dims j and j + 1 (j = 0, 2) of the four of each unit, eight tokens.
+__device__ __forceinline__ void value_frags(f16x8 f[2], const u32x4 &w, int j) {
+    u32x4 a, b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = j ? w[i] >> 8 : w[i];
+        a[i] = low(x);
+        b[i] = high(x);
+    }
+    f[0] = __builtin_bit_cast(f16x8, a);
+    f[1] = __builtin_bit_cast(f16x8, b);
+}
+constexpr float kCode = 1.0f / (1 << 24);  // of a code of 1
 
 __device__ __forceinline__ floatx4 mma(f16x8 a, f16x8 b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
-// Sixteen columns of queries as B operands, with their sums per group.
+// Sixteen columns of queries as B operands, times a power of two of their row, with their sums per group.
 template <int D64, int NG>
 struct Queries {
     static constexpr int KW = 2 * D64;
     f16x8 x[KW];
-    float sum[NG];  // of the group's x: what c_k multiplies
-    float scale;    // of S, to log2
+    float sum[NG];  // of the group's x, times kCode
+    float scale;    // of scores, to log2
     int sees;       // slots below this are visible
 
     __device__ __forceinline__ void load(const AttnArgs &a, int b, int h, int len, int col) {
-        const int lane = threadIdx.x & 63, kb = lane >> 4;
+        const int kb = (fresh_thread() & 63) >> 4;
         const bool real = col < a.cols;
         const int i = real ? col / a.group : 0, hq = h * a.group + (real ? col - i * a.group : 0);
         sees = real ? len - a.n + 1 + i : 0;
         const uint16_t *q = a.q + ((int64_t)b * a.n + i) * a.ldq + (int64_t)hq * (64 * D64) + 8 * kb;
         u32x4 w[KW];
+#pragma unroll
+        for (int t = 0; t < KW; ++t) w[t] = real ? *reinterpret_cast<const u32x4 *>(q + 32 * t) : (u32x4){};
+        auto value = [&](int t, int e) {
+            const uint32_t v = w[t][e / 2];
+            return a.bf16 ? __uint_as_float(e & 1 ? v & 0xFFFF0000u : v << 16) : (float)__builtin_bit_cast(f16x2, v)[e & 1];
+        };
         float top = 0.0f;
 #pragma unroll
-        for (int t = 0; t < KW; ++t) {
-            w[t] = real ? *reinterpret_cast<const u32x4 *>(q + 32 * t) : (u32x4){};
-            if (a.bf16) {
+        for (int t = 0; t < KW; ++t)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[t][e] << 16)), fabsf(__uint_as_float(w[t][e] & 0xFFFF0000u))));
-            }
-        }
-        scale = a.scale;
-        if (a.bf16) {
-            // times 2^(15 - e), top < 2^e: fp16's largest binade
-            top = xor_max(xor_max(top, 16), 32);
-            int e = 0;
-            if (top > 0.0f && top < __builtin_inff()) frexpf(top, &e);
-            const int up = 15 - e;
-#pragma unroll
-            for (int t = 0; t < KW; ++t)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const f32x2 f = {ldexpf(__uint_as_float(w[t][j] << 16), up), ldexpf(__uint_as_float(w[t][j] & 0xFFFF0000u), up)};
-                    w[t][j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
-                }
-            scale = ldexpf(scale, -up);
-        }
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(t, e)));
+        top = xor_max(xor_max(top, 16), 32);
+        int e = 0;
+        if (top > 0.0f && top < __builtin_inff()) frexpf(top, &e);
+        const int up = 15 - e;  // top < 2^e: fp16's largest binade
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float s = 0.0f;
 #pragma unroll
             for (int t = g * KW / NG; t < (g + 1) * KW / NG; ++t) {
-                x[t] = __builtin_bit_cast(f16x8, w[t]);
+                u32x4 y;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += (float)x[t][e];
+                for (int j = 0; j < 4; ++j) {  // pair j of the fragment; the odd ones meet codes 2^4 larger
+                    const int d = j & 1 ? up - 4 : up;
+                    const f32x2 f = {ldexpf(value(t, 2 * j), d), ldexpf(value(t, 2 * j + 1), d)};
+                    const f16x2 hf = __builtin_convertvector(f, f16x2);
+                    s += ((float)hf[0] + (float)hf[1]) * (j & 1 ? 16.0f : 1.0f);
+                    y[j] = __builtin_bit_cast(uint32_t, hf);
+                }
+                x[t] = __builtin_bit_cast(f16x8, y);
             }
-            sum[g] = xor_add(xor_add(s, 16), 32);
+            sum[g] = xor_add(xor_add(s, 16), 32) * kCode;
         }
+        scale = ldexpf(a.scale, 24 - up);
     }
 };
 
 __device__ __forceinline__ bool hidden(bool there, int slot, int sees) { return !there || slot >= sees; }
 
-// Scores of the lane's eight tokens in its column, in log2; -inf where hidden.
-template <int D64, int NG>
-__device__ __forceinline__ void scores(float s[8], const Tile<D64, NG> &tile, const f16x8 kf[2][2 * D64], const Queries<D64, NG> &q,
-                                       int slot, bool masked) {
-    constexpr int KW = 2 * D64;
+// Scores of the lane's eight tokens in the columns, in log2 and less the columns' `base`, before any mask.
+template <int D64, int NG, int NT>
+__device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile, const TileGrids<NG> &grids, const Queries<D64, NG> q[NT],
+                                       const float base[NT]) {
+    constexpr int KW = 2 * D64, SG = KW / NG;  // matrix instructions of a group
+    const int kb = (threadIdx.x & 63) >> 4;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        float y[4] = {};
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            floatx4 acc = {};
+            floatx4 acc[NT] = {};
 #pragma unroll
-            for (int w = g * KW / NG; w < (g + 1) * KW / NG; ++w) acc = mma(kf[t][w], q.x[w], acc);
+            for (int w = g * SG; w < (g + 1) * SG; ++w) {
+                const f16x8 kf = key_frag(tile.k[t][w]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t grid = tile.kg[g][t][i];
-                const float v = fmaf(grid_zero_of(grid), q.sum[g], acc[i]), k = grid_scale_of(grid) * q.scale;
-                y[i] = g == 0 ? k * v : fmaf(k, v, y[i]);
+                for (int c = 0; c < NT; ++c) acc[c] = mma(kf, q[c].x[w], acc[c]);
             }
+            const floatx4 scale = grids.scales(0, g, kb, t);
+            const f16x8 zero = grids.zeros(0, g, kb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+                    s[c][4 * t + i] = fmaf(scale[i] * q[c].scale, fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]),
+                                           g == 0 ? -base[c] : s[c][4 * t + i]);
+            __builtin_amdgcn_sched_barrier(0);  // fragments and grids of one group at a time: registers
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * t + i] = y[i];
-    }
-    if (masked) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (hidden(tile.there, slot + i, q.sees)) s[i] = kNegInf;
-    }
 }
 
+// A wave's sums over its tiles of a segment.
 template <int D64, int NG, int NT>
-__global__ __launch_bounds__(kKvThreads) void attention_kernel(AttnArgs a) {
-    constexpr int D = 64 * D64, KW = 2 * D64;
-    extern __shared__ __attribute__((aligned(16))) float smem[];  // [wave][column][D] of one column tile, then (m, l)
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, kb = lane >> 4;
-    const int h = blockIdx.y, col0 = blockIdx.z * (16 * NT);
-    const Share sh = my_share(a);
-    if (sh.b < 0) return;
-    const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
-    const int last_block = (sh.len + 7) / 8 - 1;
-    Queries<D64, NG> q[NT];
-#pragma unroll
-    for (int c = 0; c < NT; ++c) q[c].load(a, sh.b, h, sh.len, col0 + 16 * c + r);
+struct Sums {
+    static constexpr int D = 64 * D64;
+    floatx4 acc[NT][D / 16];                  // of codes: kCode or, in odd dims of a unit, 16 kCode a step
+    float corr[NT][NG], sum[NT], base[NT];    // base: what scores are taken less (0 as long as nothing is seen)
+    float slack[NT];                          // a score above it raises base: kSlack, or anything as long as nothing is seen
+    float vmax, vscale;                       // a power of two above every s_v / 4; 2^6 over it
 
-    floatx4 acc[NT][D / 16] = {};
-    float corr[NT][NG] = {}, sum[NT] = {}, top[NT];
-    for (int c = 0; c < NT; ++c) top[c] = kNegInf;
-    float vmax = 0.0f, vscale = 1.0f;  // a power of two above every s_v / 4, and 2^6 over it
-    const Unpack un;
-    const int clear = sh.len - a.n + 1;  // slots below this are visible to every column
-
-    for (int tile = sh.first + wave; tile < sh.first + sh.tiles; tile += kKvWaves) {
-        Tile<D64, NG> t;
-        t.load(a.pool, a.seqs, row, tile, last_block, h);
-        const int slot = tile * kKvTile + 8 * kb;
-        const bool masked = (tile + 1) * kKvTile > clear || __any(!t.there);
-        f16x8 kf[2][KW];
-#pragma unroll
-        for (int i = 0; i < KW; ++i) kf[0][i] = un.keys(t.k[0][i]), kf[1][i] = un.keys(t.k[1][i]);
-        float p[NT][8];
-        bool high = false;
+    __device__ __forceinline__ Sums() {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-            scores<D64, NG>(p[c], t, kf, q[c], slot, masked);
-            float m = p[c][0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) m = fmaxf(m, p[c][i]);
-            high |= m > top[c] + kSlack;
+            for (int d = 0; d < D / 16; ++d) acc[c][d] = (floatx4){};
+#pragma unroll
+            for (int g = 0; g < NG; ++g) corr[c][g] = 0.0f;
+            sum[c] = base[c] = 0.0f;
+            slack[c] = kNegInf;
         }
-        float sv[NG][8], most = 0.0f;
+        vmax = 0.0f;
+        vscale = 1.0f;
+    }
+    __device__ __forceinline__ void times(int c, float f) {
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
+        for (int g = 0; g < NG; ++g) corr[c][g] *= f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                sv[g][i] = grid_scale_of(t.vg[g][i / 4][i % 4]);
-                if (masked && hidden(t.there, slot + i, sh.len)) sv[g][i] = 0.0f;
-                most = fmaxf(most, sv[g][i]);
-            }
-        if (__any(high || most > 4.0f * vmax)) {
-            const float m4 = xor_max(xor_max(most, 16), 32);
-            float down = 1.0f;
-            if (m4 > vmax) {
-                const float was = vscale;
-                int e;
-                frexpf(m4, &e);
-                e = max(e, -118);  // 2^(6 - e) stays finite
-                vmax = ldexpf(1.0f, e);
-                vscale = ldexpf(1.0f, 6 - e);
-                down = vscale / was;
-            }
+        for (int d = 0; d < D / 16; ++d) acc[c][d] *= f;
+    }
+    // A new power of two for the values' scales, the largest of which is `most` (of the lane's).
+    __device__ __forceinline__ void raise_values(float most) {
+        for (int o = 1; o < kWave; o *= 2) most = xor_max(most, o);
+        const float was = vscale;
+        int e;
+        frexpf(most, &e);
+        e = max(e, -118);  // 2^(6 - e) stays finite
+        vmax = ldexpf(1.0f, e);
+        vscale = ldexpf(1.0f, 6 - e);
 #pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                float m = p[c][0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i) m = fmaxf(m, p[c][i]);
-                m = fmaxf(top[c], xor_max(xor_max(m, 16), 32));
-                const float f = top[c] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top[c] - m);
-                top[c] = m;
-                sum[c] *= f;
-#pragma unroll
-                for (int g = 0; g < NG; ++g) corr[c][g] *= f * down;
-#pragma unroll
-                for (int d = 0; d < D / 16; ++d) acc[c][d] *= f * down;
-            }
-        }
+        for (int c = 0; c < NT; ++c) times(c, vscale / was);
+    }
+    // A new base from the lane's scores.
+    __device__ __forceinline__ void raise(float s[NT][8]) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-            const float base = top[c] == kNegInf ? 0.0f : top[c];
+            float m = s[c][0];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[c][i] = __builtin_amdgcn_exp2f(p[c][i] - base);
-                sum[c] += p[c][i];
-            }
-        }
+            for (int i = 1; i < 8; ++i) m = fmaxf(m, s[c][i]);
+            m = xor_max(xor_max(m, 16), 32);
+            const bool first = slack[c] == kNegInf;
+            if (first ? m > kNegInf : m > 0.0f) {
+                times(c, first ? 1.0f : __builtin_amdgcn_exp2f(-m));  // (of nothing, the first time)
+                sum[c] *= first ? 1.0f : __builtin_amdgcn_exp2f(-m);
+                base[c] += m;
+                slack[c] = kSlack;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            f16x8 pf[NT];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sv[g][i] *= vscale;
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-                float ps[8], z[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ps[i] = p[c][i] * sv[g][i], z[i] = grid_zero_of(t.vg[g][i / 4][i % 4]);
-                if (masked) {  // a hidden token's grid may hold anything
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (hidden(t.there, slot + i, q[c].sees)) ps[i] = z[i] = 0.0f;
-                }
-                u32x4 w;
-#pragma unroll
-                for (int i = 0; i < 8; i += 2)
-                    w[i / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector(((f32x2){ps[i], ps[i + 1]}), f16x2));
-                pf[c] = __builtin_bit_cast(f16x8, w);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) corr[c][g] = fmaf((float)pf[c][i], z[i], corr[c][g]);
-            }
-#pragma unroll
-            for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d) {
-                const f16x8 vf = un.values(t.v[d / 4], d % 4);
-#pragma unroll
-                for (int c = 0; c < NT; ++c) acc[c][d] = mma(vf, pf[c], acc[c][d]);
+                for (int i = 0; i < 8; ++i) s[c][i] -= m;
             }
         }
     }
+    __device__ __forceinline__ float top(int c) const { return slack[c] == kNegInf ? kNegInf : base[c]; }
+};
 
-    // The waves' sums, brought to the largest of their maxima and added in wave order.
+__device__ __forceinline__ int64_t result_at(const AttnArgs &a, int b, int h, int col, int D) {
+    const int tok = col / a.group;
+    return ((int64_t)b * a.n + tok) * a.ldo + (int64_t)(h * a.group + col - tok * a.group) * D;
+}
+__device__ __forceinline__ uint16_t result16(const AttnArgs &a, float y) {
+    return a.bf16 ? __builtin_bit_cast(uint16_t, (__bf16)y) : __builtin_bit_cast(uint16_t, (_Float16)y);
+}
+// How much of a sum relative to `top` counts in one relative to `all`.
+__device__ __forceinline__ float share_in(float top, float all) { return top == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top - all); }
+
+// The waves' sums, brought to the largest of their maxima and added in wave order: the result where the segment is all of
+// its sequence, else its part.
+template <int D64, int NG, int NT>
+__device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG, NT> &s, const Share &sh, bool whole, float *smem, int h, int col0) {
+    constexpr int D = 64 * D64;
+    const int thread = fresh_thread(), lane = thread & 63, wave = thread >> 6, r = lane & 15, kb = lane >> 4;
     float2 *ml = reinterpret_cast<float2 *>(smem + kKvWaves * 16 * D);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
-        const float l = xor_add(xor_add(sum[c], 16), 32);
-        if (c) __syncthreads();
-        if (kb == 0) ml[wave * 16 + r] = make_float2(top[c], l);
+        const float l = xor_add(xor_add(s.sum[c], 16), 32);
+        __syncthreads();  // what the last round left in LDS has been read
+        if (kb == 0) ml[wave * 16 + r] = make_float2(s.top(c), l);
         __syncthreads();
         float m = kNegInf;
         for (int w = 0; w < kKvWaves; ++w) m = fmaxf(m, ml[w * 16 + r].x);
-        const float f = (top[c] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(top[c] - m)) / vscale;
+        const float f = share_in(s.top(c), m) / (s.vscale * kCode);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float k = xor_add(xor_add(corr[c][g], 16), 32);
+            const float k = xor_add(xor_add(s.corr[c][g], 16), 32) * kCode;
 #pragma unroll
-            for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d) {
-                const floatx4 y = (acc[c][d] + k) * f;
-                *reinterpret_cast<floatx4 *>(smem + (wave * 16 + r) * D + 16 * d + 4 * kb) = y;
-            }
+            for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d)
+                *reinterpret_cast<floatx4 *>(smem + (wave * 16 + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f;
         }
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * D; i += kKvThreads) {
+        for (int i = thread; i < 16 * D; i += kKvThreads) {
             const int cc = i / D, d = i % D, col = col0 + 16 * c + cc;
             if (col >= a.cols) break;
             float M = kNegInf, L = 0.0f, o = 0.0f;
             for (int w = 0; w < kKvWaves; ++w) M = fmaxf(M, ml[w * 16 + cc].x);
             for (int w = 0; w < kKvWaves; ++w) {
                 const float2 v = ml[w * 16 + cc];
-                L += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - M);
+                L += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - M);  // (a NaN stays)
                 o += smem[(w * 16 + cc) * D + d];
             }
-            const int64_t at = ((int64_t)blockIdx.x * gridDim.y + h) * a.cols + col;
-            if (sh.splits == 1) {
-                const float y = L == 0.0f ? 0.0f : o / L;
-                const int tok = col / a.group;
-                uint16_t *to = a.o + ((int64_t)sh.b * a.n + tok) * a.ldo + (int64_t)(h * a.group + col - tok * a.group) * D + d;
-                *to = a.bf16 ? __builtin_bit_cast(uint16_t, (__bf16)y) : __builtin_bit_cast(uint16_t, (_Float16)y);
+            if (whole) {
+                a.o[result_at(a, sh.b, h, col, D) + d] = result16(a, L == 0.0f ? 0.0f : o / L);
+                if (d == 0 && a.last) a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col] = make_float2(M, L == 0.0f ? 0.0f : 1.0f / L);
             } else {
+                const int64_t at = ((int64_t)(blockIdx.x + sh.b) * a.pool.heads + h) * a.cols + col;
                 a.part[at * D + d] = o;
+                if (d == 0) a.stat[at] = make_float2(M, L);
             }
-            if (d == 0 && a.keep_stat) a.stat[at] = make_float2(M, L);
         }
     }
 }
 
-// The maximum and sum of a column over its sequence's items, by the 64 lanes of a wave.
-__device__ __forceinline__ float2 joined_stat(const AttnArgs &a, const Share &sh, int h, int col) {
-    const int lane = threadIdx.x & 63;
-    float m = kNegInf, l = 0.0f;
-    for (int x = lane; x < sh.splits; x += kWave) m = fmaxf(m, a.stat[((int64_t)(sh.base + x) * a.pool.heads + h) * a.cols + col].x);
-    for (int o = 1; o < kWave; o *= 2) m = xor_max(m, o);
-    for (int x = lane; x < sh.splits; x += kWave) {
-        const float2 v = a.stat[((int64_t)(sh.base + x) * a.pool.heads + h) * a.cols + col];
-        l += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - m);
+// Waves of a SIMD that the registers of a kernel allow.
+constexpr int occupancy(int D64, int NG, int NT) { return D64 * NT <= 2 ? 4 : 2; }
+
+template <int D64, int NG, int NT>
+__global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_kernel(AttnArgs a) {
+    constexpr int D = 64 * D64;
+    extern __shared__ __attribute__((aligned(16))) float smem[];  // [wave][column][D] of one column tile, then (m, l), then grids
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4;
+    const int h = blockIdx.y, col0 = blockIdx.z * (16 * NT);
+    TileGrids<NG> &grids = reinterpret_cast<TileGrids<NG> *>(smem + kKvWaves * 16 * (D + 2))[wave];
+    int from, to;  // of the row of tiles
+    Share sh;
+    if (a.direct) {  // a sequence to a workgroup
+        sh = {(int)blockIdx.x, 0, tiles_of(a.seqs, blockIdx.x), a.seqs.len(blockIdx.x)};
+        from = 0;
+        to = sh.tiles;
+    } else {
+        const int total = total_tiles(a), chunk = chunk_of(a, total);
+        from = blockIdx.x * chunk;
+        to = min(from + chunk, total);
+        if (from >= to) return;
+        sh = share_of(a, from, false);
     }
-    for (int o = 1; o < kWave; o *= 2) l = xor_add(l, o);
-    return make_float2(m, l);
+    for (;;) {
+        const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
+        const int t0 = from - sh.start, t1 = min(to - sh.start, sh.tiles);  // of the sequence
+        Queries<D64, NG> q[NT];
+#pragma unroll
+        for (int c = 0; c < NT; ++c) q[c].load(a, sh.b, h, sh.len, col0 + 16 * c + r);
+        Sums<D64, NG, NT> sums;
+        const int clear = sh.len - a.n + 1;  // slots below this are visible to every column
+        int tile = t0 + wave;
+        Tile<D64, NG> t;
+        TilePages pages = {a, row, max(min(tile, t1 - 1), 0), sh.len};
+        if (tile < t1) {
+            t.load_keys(a, pages, tile, h);
+            t.load_values(a, pages, tile, h);
+        }
+        // The keys of the next tile are on their way during the second product, its values during the first of the next.
+        while (tile < t1) {
+            const int next = tile + kKvWaves;
+            const TilePages coming = {a, row, min(next, t1 - 1), sh.len};
+            const bool masked = (tile + 1) * kKvTile > clear || pages.missing();
+            const bool gone = masked && hidden(((lane & 16) ? pages.hi : pages.lo) >= 0, tile * kKvTile + (lane & 31), sh.len);
+            float most = 0.0f;
+            if (lane >= 32 && !gone) {
+#pragma unroll
+                for (int g = 0; g < NG; ++g) most = fmaxf(most, grid_scale_of(t.grid[g]));
+            }
+            if (__any(most > 4.0f * sums.vmax)) sums.raise_values(most);
+            grids.put(t.grid, sums.vscale, gone);
+            wave_fence();
+            float p[NT][8];
+            scores<D64, NG, NT>(p, t, grids, q, sums.base);
+            if (next < t1) t.load_keys(a, coming, next, h);
+            const int slot = tile * kKvTile + 8 * kb;
+            const bool there = (kb < 2 ? pages.lo : pages.hi) >= 0;
+            if (masked) {
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (hidden(there, slot + i, q[c].sees)) p[c][i] = kNegInf;
+            }
+            bool high = false;
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                float m = p[c][0];
+#pragma unroll
+                for (int i = 1; i < 8; ++i) m = fmaxf(m, p[c][i]);
+                high |= m > sums.slack[c];
+            }
+            if (__any(high)) sums.raise(p);
+#pragma unroll
+            for (int c = 0; c < NT; ++c)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[c][i] = __builtin_amdgcn_exp2f(p[c][i]);
+                    sums.sum[c] += p[c][i];
+                }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const floatx4 s0 = grids.scales(1, g, kb, 0), s1 = grids.scales(1, g, kb, 1);
+                const f16x8 zero = grids.zeros(1, g, kb);
+                f16x8 pf[NT];
+#pragma unroll
+                for (int c = 0; c < NT; ++c) {
+                    float ps[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ps[i] = p[c][i] * (i < 4 ? s0[i] : s1[i - 4]);
+                    if (masked) {  // a value that this column does not see may be no number
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (hidden(there, slot + i, q[c].sees)) ps[i] = 0.0f;
+                    }
+                    u32x4 w;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f16x2 f = __builtin_convertvector(((f32x2){ps[2 * i], ps[2 * i + 1]}), f16x2);
+                        sums.corr[c][g] = __builtin_amdgcn_fdot2(f, (f16x2){zero[2 * i], zero[2 * i + 1]}, sums.corr[c][g], false);
+                        w[i] = __builtin_bit_cast(uint32_t, f);
+                    }
+                    pf[c] = __builtin_bit_cast(f16x8, w);
+                }
+#pragma unroll
+                for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; d += 2) {
+                    f16x8 vf[2];
+                    value_frags(vf, t.v[d / 4], d % 4);
+#pragma unroll
+                    for (int c = 0; c < NT; ++c) {
+                        sums.acc[c][d] = mma(vf[0], pf[c], sums.acc[c][d]);
+                        sums.acc[c][d + 1] = mma(vf[1], pf[c], sums.acc[c][d + 1]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+            if (next < t1) t.load_values(a, coming, next, h);
+            tile = next;
+            pages = coming;
+        }
+        write_sums<D64, NG, NT>(a, sums, sh, t0 == 0 && t1 == sh.tiles, smem, h, col0);
+        if (from + (t1 - t0) >= to) break;
+        from += t1 - t0;
+        sh = share_of(a, from, false);
+    }
 }
 
-// Sequences of more than one item, or none: a wave per column.
+// Sequences of several segments, or of none: a workgroup per column, whose threads take four dims of every kLanes-th segment.
 template <int D64>
 __global__ __launch_bounds__(kKvThreads) void combine_kernel(AttnArgs a) {
-    constexpr int D = 64 * D64;
-    const int lane = threadIdx.x & 63, h = blockIdx.y, b = blockIdx.x;
-    const int col = blockIdx.z * kKvWaves + (threadIdx.x >> 6);
+    constexpr int D = 64 * D64, kRow = D / 4, kLanes = kKvThreads / kRow, kMost = 1024;  // D = 192: 5 rows, 16 idle threads
+    __shared__ float share[kMost];
+    __shared__ float red[2][kKvWaves];
+    __shared__ floatx4 sums[kKvThreads];
+    const int col = blockIdx.x, h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int chunk = chunk_of(a, total_tiles(a));
     const Share sh = share_of(a, b, true);
-    if (sh.splits == 1 || col >= a.cols) return;
-    const float2 ml = joined_stat(a, sh, h, col);
-    float o[D64] = {};
-    for (int x = 0; x < sh.splits; ++x) {
-        const int64_t at = ((int64_t)(sh.base + x) * a.pool.heads + h) * a.cols + col;
-        const float m = a.stat[at].x;
-        const float f = m == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(m - ml.x);
-#pragma unroll
-        for (int u = 0; u < D64; ++u) o[u] += f * a.part[at * D + 64 * u + lane];
+    const int x0 = sh.start / chunk, n = sh.tiles ? (sh.start + sh.tiles - 1) / chunk - x0 + 1 : 0;
+    if (n == 1) return;
+    const int64_t at0 = ((int64_t)(x0 + b) * a.pool.heads + h) * a.cols + col, step = (int64_t)a.pool.heads * a.cols;
+    float m = kNegInf, l = 0.0f;
+    for (int x = threadIdx.x; x < n; x += kKvThreads) m = fmaxf(m, a.stat[at0 + x * step].x);
+    for (int o = 1; o < kWave; o *= 2) m = xor_max(m, o);
+    if (lane == 0) red[0][wave] = m;
+    __syncthreads();
+    for (int w = 0; w < kKvWaves; ++w) m = fmaxf(m, red[0][w]);
+    for (int x = threadIdx.x; x < n; x += kKvThreads) {
+        const float2 v = a.stat[at0 + x * step];
+        const float f = share_in(v.x, m);
+        share[x] = f;
+        l += v.x == kNegInf ? v.y : v.y * f;
     }
-    const int tok = col / a.group;
-    uint16_t *to = a.o + ((int64_t)b * a.n + tok) * a.ldo + (int64_t)(h * a.group + col - tok * a.group) * D;
-#pragma unroll
-    for (int u = 0; u < D64; ++u) {
-        const float y = ml.y == 0.0f ? 0.0f : o[u] / ml.y;
-        to[64 * u + lane] = a.bf16 ? __builtin_bit_cast(uint16_t, (__bf16)y) : __builtin_bit_cast(uint16_t, (_Float16)y);
+    for (int o = 1; o < kWave; o *= 2) l = xor_add(l, o);
+    if (lane == 0) red[1][wave] = l;
+    __syncthreads();
+    l = 0.0f;
+    for (int w = 0; w < kKvWaves; ++w) l += red[1][w];
+    const int mine = threadIdx.x / kRow, d4 = threadIdx.x % kRow;
+    floatx4 o = {};
+    if (mine < kLanes) {
+#pragma unroll 4
+        for (int x = mine; x < n; x += kLanes) o += share[x] * *reinterpret_cast<const floatx4 *>(a.part + (at0 + x * step) * D + 4 * d4);
     }
+    sums[threadIdx.x] = o;
+    __syncthreads();
+    if (threadIdx.x < kRow) {
+        for (int y = 1; y < kLanes; ++y) o += sums[y * kRow + threadIdx.x];
+        uint16_t *to = a.o + result_at(a, b, h, col, D) + 4 * threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) to[i] = result16(a, l == 0.0f ? 0.0f : o[i] / l);
+    }
+    if (threadIdx.x == 0 && a.last) a.last[((int64_t)b * a.pool.heads + h) * a.cols + col] = make_float2(m, l == 0.0f ? 0.0f : 1.0f / l);
+}
+
+__device__ __forceinline__ float sum16(float v) {  // over a row of sixteen lanes
+    auto turned = [](float x, auto n) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + decltype(n)::value, 0xF, 0xF, true));  // row_ror
+    };
+    v += turned(v, std::integral_constant<int, 8>());
+    v += turned(v, std::integral_constant<int, 4>());
+    v += turned(v, std::integral_constant<int, 2>());
+    return v + turned(v, std::integral_constant<int, 1>());
 }
 
 // weight[token] = decay weight[token] + the sum of p over the columns, once maxima and sums are known.  Only the
 // keys are read again; the same instructions give the same scores.
-template <int D64, int NG>
-__global__ __launch_bounds__(kKvThreads) void weights_kernel(AttnArgs a) {
-    constexpr int KW = 2 * D64;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, r = lane & 15, kb = lane >> 4, h = blockIdx.y;
-    const Share sh = my_share(a);
-    if (sh.b < 0) return;
-    const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
-    const int last_block = (sh.len + 7) / 8 - 1, clear = sh.len - a.n + 1;
-    const Unpack un;
-    for (int col0 = 0; col0 < a.cols; col0 += 16) {
-        Queries<D64, NG> q;
-        q.load(a, sh.b, h, sh.len, col0 + r);
-        float2 ml = make_float2(0.0f, 0.0f);
-        for (int c = 0; c < 16 && col0 + c < a.cols; ++c) {
-            const float2 v = joined_stat(a, sh, h, col0 + c);
-            if (c == r) ml = v;
-        }
-        const float inv = ml.y == 0.0f ? 0.0f : 1.0f / ml.y, base = ml.x == kNegInf ? 0.0f : ml.x;
-        for (int tile = sh.first + wave; tile < sh.first + sh.tiles; tile += kKvWaves) {
+template <int D64, int NG, int NT>
+__global__ __launch_bounds__(kKvThreads, D64 * NT <= 4 ? 4 : 2) void weights_kernel(AttnArgs a) {
+    __shared__ __attribute__((aligned(16))) TileGrids<NG> all_grids[kKvWaves];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4, h = blockIdx.y;
+    TileGrids<NG> &grids = all_grids[wave];
+    const int total = total_tiles(a), chunk = chunk_of(a, total);
+    int from = blockIdx.x * chunk;
+    const int to = min(from + chunk, total);
+    while (from < to) {
+        const Share sh = share_of(a, from, false);
+        const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
+        const int t0 = from - sh.start, t1 = min(to - sh.start, sh.tiles), clear = sh.len - a.n + 1;
+        for (int col0 = 0; col0 < a.cols; col0 += 16 * NT) {
+            Queries<D64, NG> q[NT];
+            float base[NT], inv[NT];
+#pragma unroll
+            for (int c = 0; c < NT; ++c) {
+                const int col = col0 + 16 * c + r;
+                q[c].load(a, sh.b, h, sh.len, col);
+                const float2 v = col < a.cols ? a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col] : make_float2(0.0f, 0.0f);
+                base[c] = v.x == kNegInf ? 0.0f : v.x;
+                inv[c] = v.y;  // 0 where nothing is seen
+            }
+            int tile = t0 + wave;
             Tile<D64, NG> t;
-            t.load(a.pool, a.seqs, row, tile, last_block, h);
-            const int slot = tile * kKvTile + 8 * kb;
-            f16x8 kf[2][KW];
+            TilePages pages = {a, row, min(tile, t1 - 1), sh.len};
+            if (tile < t1) t.load_keys(a, pages, tile, h);
+            while (tile < t1) {
+                const int next = tile + kKvWaves;
+                const TilePages coming = {a, row, min(next, t1 - 1), sh.len};
+                const int slot = tile * kKvTile + 8 * kb, page = kb < 2 ? pages.lo : pages.hi;
+                float p[NT][8], w[8] = {};
+                grids.put(t.grid, 1.0f, false);
+                wave_fence();
+                scores<D64, NG, NT>(p, t, grids, q, base);
+                if (next < t1) t.load_keys(a, coming, next, h);
+                if ((tile + 1) * kKvTile > clear || pages.missing()) {
 #pragma unroll
-            for (int i = 0; i < KW; ++i) kf[0][i] = un.keys(t.k[0][i]), kf[1][i] = un.keys(t.k[1][i]);
-            float p[8];
-            scores<D64, NG>(p, t, kf, q, slot, (tile + 1) * kKvTile > clear || __any(!t.there));
+                    for (int c = 0; c < NT; ++c)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = col0 + r < a.cols ? __builtin_amdgcn_exp2f(p[i] - base) * inv : 0.0f;
-                for (int o = 1; o < 16; o *= 2) p[i] = xor_add(p[i], o);
-            }
-            const int page = slot < sh.len ? a.seqs.page_of(a.pool, row, slot) : -1;
-            if (r == 0 && page >= 0) {
-                float *w = a.pool.weight + a.pool.first(page, h) + (slot & (a.pool.page() - 1));
+                        for (int i = 0; i < 8; ++i)
+                            if (hidden(page >= 0, slot + i, q[c].sees)) p[c][i] = kNegInf;
+                }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (slot + i < sh.len) w[i] = col0 ? w[i] + p[i] : (a.decay == 0.0f ? p[i] : fmaf(a.decay, w[i], p[i]));
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)  // columns that are none see nothing
+                        w[i] += col0 + 16 * c + r < a.cols ? __builtin_amdgcn_exp2f(p[c][i]) * inv[c] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = sum16(w[i]);
+                if (r == 0 && page >= 0) {
+                    float *to = a.pool.weight + a.pool.first(page, h) + (slot & (a.pool.page() - 1));
+                    const float old = col0 ? 1.0f : a.decay;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (slot + i < sh.len) to[i] = old == 0.0f ? w[i] : fmaf(old, to[i], w[i]);
+                }
+                tile = next;
+                pages = coming;
             }
         }
+        from += t1 - t0;
     }
 }
 
 struct Plan {
     int nt, items, target;
     bool direct;
-    size_t part, stat;  // bytes
+    size_t part, stat, last;  // bytes
 };
 Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_len) {
     Plan p;
     p.nt = cols > 16 && c.head_dim <= 128 ? 2 : 1;  // two tiles of larger heads do not fit the registers
     const int64_t tiles = ceil_div(max_len, kKvTile), blocks = c.n_heads * ceil_div(cols, 16 * p.nt);
-    p.target = (int)std::max<int64_t>(1, 1024 / blocks);
-    const int64_t most = std::max<int64_t>(1, ceil_div(tiles, kKvLeast));
-    p.items = (int)std::min<int64_t>(n_seq * most, p.target + n_seq);
-    p.direct = most == 1;
-    const size_t rows = (size_t)p.items * c.n_heads * cols;
-    p.part = p.direct ? 0 : align_up(rows * c.head_dim * 4, 256);
-    p.stat = align_up(rows * 8, 256);
+    // as many workgroups as the chip holds at once, but no more than combine_kernel takes of one sequence
+    p.target = (int)std::min<int64_t>(1000, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, 1, p.nt) / blocks));
+    p.direct = tiles <= kKvLeast;
+    const int64_t all = std::max<int64_t>(1, n_seq * tiles);
+    p.items = (int)(p.direct ? n_seq : std::min<int64_t>(p.target, ceil_div(all, kKvLeast)));
+    const size_t rows = (size_t)c.n_heads * cols, segments = p.direct ? 0 : rows * (p.items + n_seq);
+    p.part = align_up(segments * c.head_dim * 4, 256);
+    p.stat = align_up(segments * 8, 256);
+    p.last = align_up(rows * n_seq * 8, 256);
     return p;
 }
 
-template <int D64, int NG>
-hipError_t launch_attention(const AttnArgs &a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
-    const size_t lds = (size_t)kKvWaves * 16 * (64 * D64 * 4 + 8);
-    const dim3 grid((unsigned)p.items, (unsigned)a.pool.heads, (unsigned)ceil_div(a.cols, 16 * p.nt));
-    bool two = false;
-    if constexpr (D64 <= 2) two = p.nt == 2;
-    if constexpr (D64 <= 2) {
-        if (two) attention_kernel<D64, NG, 2><<<grid, kKvThreads, lds, s>>>(a);
-    }
-    if (!two) attention_kernel<D64, NG, 1><<<grid, kKvThreads, lds, s>>>(a);
+template <int D64, int NG, int NT>
+hipError_t launch_tiles(AttnArgs a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
+    const size_t lds = (size_t)kKvWaves * (16 * (64 * D64 * 4 + 8) + sizeof(TileGrids<NG>));
+    attention_kernel<D64, NG, NT><<<dim3((unsigned)p.items, (unsigned)a.pool.heads, (unsigned)ceil_div(a.cols, 16 * NT)), kKvThreads, lds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (!p.direct) {
-        combine_kernel<D64><<<dim3((unsigned)n_seq, (unsigned)a.pool.heads, (unsigned)ceil_div(a.cols, kKvWaves)), kKvThreads, 0, s>>>(a);
+        combine_kernel<D64><<<dim3((unsigned)a.cols, (unsigned)a.pool.heads, (unsigned)n_seq), kKvThreads, 0, s>>>(a);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (weights) {
-        weights_kernel<D64, NG><<<dim3((unsigned)p.items, (unsigned)a.pool.heads), kKvThreads, 0, s>>>(a);
+        weights_kernel<D64, NG, NT><<<dim3((unsigned)p.items, (unsigned)a.pool.heads), kKvThreads, 0, s>>>(a);
         e = hipGetLastError();
     }
     return e;
+}
+template <int D64, int NG>
+hipError_t launch_attention(const AttnArgs &a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
+    if constexpr (D64 <= 2) {
+        if (p.nt == 2) return launch_tiles<D64, NG, 2>(a, p, n_seq, weights, s);
+    }
+    return launch_tiles<D64, NG, 1>(a, p, n_seq, weights, s);
 }
 
 }  // namespace
 
 size_t kv_attention_ws_bytes(const gptq_kv_cache &c, int64_t n_seq, int64_t n, int64_t q_heads, int64_t max_len) {
     const Plan p = plan_of(c, n_seq, n * (q_heads / c.n_heads), max_len);
-    return p.part + p.stat;
+    return p.part + p.stat + p.last;
 }
 
 hipError_t run_kv_attention(const void *Q, gptq_dtype dt, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq, const gptq_kv_cache &c,
@@ -577,12 +764,12 @@ hipError_t run_kv_attention(const void *Q, gptq_dtype dt, int64_t n_seq, int64_t
     const Plan p = plan_of(c, n_seq, a.cols, max_len);
     a.part = static_cast<float *>(ws);
     a.stat = reinterpret_cast<float2 *>(static_cast<char *>(ws) + p.part);
+    a.last = weights ? reinterpret_cast<float2 *>(static_cast<char *>(ws) + p.part + p.stat) : nullptr;
     a.scale = scale * 1.44269504088896340736f;
     a.decay = decay;
     a.target = p.target;
     a.bf16 = dt == GPTQ_DT_BF16;
     a.direct = p.direct;
-    a.keep_stat = weights || !p.direct;
     const int ng = a.pool.groups;
     switch (c.head_dim / 64) {
     case 1: return ng == 1 ? launch_attention<1, 1>(a, p, (int)n_seq, weights, s) : launch_attention<1, 2>(a, p, (int)n_seq, weights, s);
