@@ -13,6 +13,8 @@
 namespace gptq {
 namespace {
 
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
 struct AppendArgs {
     KvPool pool;
     KvSeqs seqs;
@@ -21,195 +23,247 @@ struct AppendArgs {
     uint16_t *out[2];  // the values as stored, or NULL
     int64_t ld_out[2];
     const int32_t *offs;
-    int64_t T;
+    int64_t T, per;  // tokens; tokens of a sequence where there are no offsets
     int32_t bf16, symmetric;
 };
 
 __device__ __forceinline__ float load16(uint16_t h, bool bf16) {
     return bf16 ? __uint_as_float((uint32_t)h << 16) : (float)__builtin_bit_cast(_Float16, h);
 }
-__device__ __forceinline__ uint16_t store16(float f, bool bf16) {
-    return bf16 ? __builtin_bit_cast(uint16_t, (__bf16)f) : __builtin_bit_cast(uint16_t, (_Float16)f);
+
+// A step of a reduction over neighbouring lanes: the value of the lane's partner.
+template <int kStep>
+__device__ __forceinline__ float partner(float v) {
+    const int x = __float_as_int(v);
+    if constexpr (kStep == 16) {
+        return __shfl_xor(v, 16);
+    } else {  // pairs, quads, halves of eight, halves of a row
+        constexpr int ctrl = kStep == 1 ? 0xB1 : kStep == 2 ? 0x4E : kStep == 4 ? 0x141 : 0x140;
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, x, ctrl, 0xF, 0xF, true));
+    }
 }
 
+// The range of a group, which always holds 0, and the sum of its values: no number if one of them is none.
 struct Range {
-    float lo, hi;
-    bool bad;
-    __device__ __forceinline__ void add(float x) {
-        lo = fminf(lo, x);
-        hi = fmaxf(hi, x);
-        bad |= !(fabsf(x) < __builtin_inff());
-    }
-    __device__ __forceinline__ void add(const Range &r) {
-        lo = fminf(lo, r.lo);
-        hi = fmaxf(hi, r.hi);
-        bad |= r.bad;
-    }
-    template <int W>  // over W neighbouring lanes
+    float lo, hi, sum;
+    template <int kStep, int W>  // over W neighbouring lanes
     __device__ __forceinline__ void reduce() {
-#pragma unroll
-        for (int o = 1; o < W; o *= 2) {
-            const Range r = {__shfl_xor(lo, o), __shfl_xor(hi, o), (bool)__shfl_xor((int)bad, o)};
-            add(r);
+        if constexpr (kStep < W) {
+            lo = fminf(lo, partner<kStep>(lo));
+            hi = fmaxf(hi, partner<kStep>(hi));
+            sum += partner<kStep>(sum);
+            reduce<2 * kStep, W>();
         }
     }
 };
 
+// x / s is the correctly rounded quotient by Markstein's correction, as in quant_grid.h: with r = RN(1 / s) and q = RN(x r),
+// RN(q + (x - q s) r).  |x / s| stays below 16, since s comes from the group's own range; scales outside 2^-100 .. 2^100
+// are brought back by a power of two m, so that no step over- or underflows (where x / s is tiny, it rounds away anyway).
 struct Grid4 {
-    float s, z, qlo, qhi, zadd;
+    float s, m, ss, r, z, lo, hi, zadd;
     bool bad;
+
+    __device__ __forceinline__ Grid4(const Range &g, bool symmetric) {
+#pragma clang fp contract(off)
+        s = symmetric ? fmaxf(-g.lo, g.hi) * (1.0f / 7.0f) : (g.hi - g.lo) * (1.0f / 15.0f);
+        s = (float)(__bf16)s;
+        if (s == 0.0f) s = 1.0f;
+        bad = !(s < __builtin_inff()) || !(g.sum == g.sum);  // an infinite value makes s infinite
+        m = s < 0x1p-100f ? 0x1p100f : s > 0x1p100f ? 0x1p-100f : 1.0f;
+        ss = s * m;
+        r = 1.0f / ss;
+        z = symmetric ? 0.0f : __builtin_amdgcn_fmed3f(rintf(quotient(-g.lo * m)), 0.0f, 15.0f);
+        lo = symmetric ? -7.0f : 0.0f;
+        hi = symmetric ? 7.0f : 15.0f;
+        zadd = symmetric ? 8.0f : 0.0f;
+        if (bad) s = __builtin_nanf("");
+    }
+    __device__ __forceinline__ float quotient(float x) const {
+        const float q = x * r;
+        return fmaf(fmaf(-q, ss, x), r, q);
+    }
+    // The code less zadd of x m, and the value that one stands for.
+    __device__ __forceinline__ float level(float x) const {
+#pragma clang fp contract(off)
+        return __builtin_amdgcn_fmed3f(rintf(quotient(x) + z), lo, hi);
+    }
+    __device__ __forceinline__ float value(float level) const { return s * (level - z); }
+    __device__ __forceinline__ uint32_t word() const {
+        const uint32_t top = bad ? 0x7FC0u : __float_as_uint(s) >> 16;
+        return top << 16 | __builtin_bit_cast(uint16_t, (_Float16)(bad ? 0.0f : 8.0f - (zadd + z)));
+    }
 };
-__device__ __forceinline__ Grid4 fit4(const Range &r, bool symmetric) {
-#pragma clang fp contract(off)
-    Grid4 g;
-    const float s = symmetric ? fmaxf(-r.lo, r.hi) * (1.0f / 7.0f) : (r.hi - r.lo) * (1.0f / 15.0f);
-    g.s = (float)(__bf16)s;
-    if (g.s == 0.0f) g.s = 1.0f;
-    g.bad = r.bad || !(g.s < __builtin_inff());
-    g.z = symmetric ? 0.0f : fminf(fmaxf(rintf(-r.lo / g.s), 0.0f), 15.0f);
-    g.qlo = symmetric ? -7.0f : 0.0f;
-    g.qhi = symmetric ? 7.0f : 15.0f;
-    g.zadd = symmetric ? 8.0f : 0.0f;
-    return g;
-}
-__device__ __forceinline__ uint32_t code4(const Grid4 &g, float x) {
-#pragma clang fp contract(off)
-    const float q = fminf(fmaxf(rintf(x / g.s + g.z), g.qlo), g.qhi) + g.zadd;
-    return g.bad ? 8u : (uint32_t)q;
-}
-__device__ __forceinline__ uint32_t word4(const Grid4 &g) {
-    const uint32_t s = g.bad ? 0x7FC0u : __float_as_uint(g.s) >> 16;
-    const float c = g.bad ? 0.0f : 8.0f - (g.zadd + g.z);
-    return (s << 16) | __builtin_bit_cast(uint16_t, (_Float16)c);
-}
-__device__ __forceinline__ float value4(const Grid4 &g, uint32_t q) {
-    return g.bad ? __builtin_nanf("") : g.s * ((float)q - (g.zadd + g.z));
+
+// Four levels as the codes' sixteen bits, the first lowest (sums below 2^16 are exact).
+__device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, float zadd) {
+    return (uint32_t)fmaf(fmaf(fmaf(d, 16.0f, c), 16.0f, b), 16.0f, fmaf(zadd, 4369.0f, a));
 }
 
-// A thread takes eight values of one token, head and side: of keys a word, eight dims
-// next to each other; of values two units, dims 64 u + 16 j + m, + 1 for j = 0 .. 3.
-template <int D64, int GROUP>
+constexpr int kBlockTokens = 32;  // tokens of a workgroup that stages values
+
+// A workgroup takes tokens of one head and side, a thread eight neighbouring dims of one: a word of keys.  Values: eight
+// lanes hold a set of 64 dims, lane i dims 16 j + 8 (i % 2) .. + 7 with j = i / 2; they trade words so that each has two
+// units of all four j.  Units of neighbouring tokens share sixteen bytes: staged, whole blocks of eight tokens are put
+// together in LDS and stored at once (32768 tokens of 8 heads of 128 values: TIME_STAGED), else each token's two bytes
+// (TIME_PLAIN; but 32 single tokens TIME_SMALL).
+template <int D64, int GROUP, bool kStaged>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
-    constexpr int D = 64 * D64, NG = D / GROUP, kLanes = D64 == 1 ? 8 : (D64 == 2 ? 16 : 32);
-    const bool values = blockIdx.y != 0;
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;  // (token, head)
-    const int i = threadIdx.x % kLanes, heads = a.pool.heads;
-    const int64_t t = row / heads;
-    const int h = (int)(row - t * heads);
-    // the token's sequence and slot
-    int b, slot = -1;
-    if (!a.offs) {
-        const int64_t per = a.T / a.seqs.n;
-        b = (int)(t / per);
-        if (t < a.T) slot = a.seqs.len(b) - (int)((b + 1) * per - t);
-    } else {
-        int lo = 0, hi = a.seqs.n;  // the first sequence that ends behind t
-        while (lo < hi) {
-            const int mid = (lo + hi) / 2;
-            if (a.offs[mid + 1] > t)
-                hi = mid;
-            else
-                lo = mid + 1;
-        }
-        b = lo;
-        if (t < a.T && b < a.seqs.n) slot = a.seqs.len(b) - (int)(a.offs[b + 1] - t);
+    constexpr int D = 64 * D64, NG = D / GROUP, kLanes = D64 == 1 ? 8 : (D64 == 2 ? 16 : 32), kPass = 256 / kLanes;
+    constexpr int kPasses = kStaged ? kBlockTokens / kPass : 1, kTokens = kPass * kPasses, kCols = kTokens + 8;
+    __shared__ int64_t place[kTokens];  // tokens counted over the pool, of the head; -1: stored nowhere, -2: in no sequence
+    __shared__ int whole;               // the slot of the first token where all of them follow it on pages that exist, else -1
+    __shared__ __attribute__((aligned(16))) uint16_t units[kStaged ? D / 4 : 1][kCols];
+    const bool values = blockIdx.z != 0;
+    const int h = blockIdx.y, i = threadIdx.x % kLanes, mask = a.pool.page() - 1;
+    const int64_t t0 = (int64_t)blockIdx.x * kTokens;
+    u32x4 x[kPasses];
+#pragma unroll
+    for (int p = 0; p < kPasses; ++p) {
+        const int64_t t = t0 + p * kPass + threadIdx.x / kLanes;
+        x[p] = (u32x4){};
+        if (t < a.T && i < D / 8) x[p] = *reinterpret_cast<const u32x4 *>(a.x[values] + t * a.ld[values] + h * D + 8 * i);
     }
-    const bool in = t < a.T && b < a.seqs.n, mine = i < D / 8;
-    int page = -1;
-    if (in && slot >= 0 && slot < a.seqs.capacity) page = a.seqs.page_of(a.pool, a.seqs.table + (int64_t)b * a.seqs.width, slot);
-    uint16_t x16[8];
-    Range r[2] = {};
-    const int u = i / 8, m = 2 * (i % 8);
-    if (in && mine) {
-        const uint16_t *x = a.x[values] + t * a.ld[values] + h * D;
-        if (!values) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(x + 8 * i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x16[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t w = *reinterpret_cast<const uint32_t *>(x + 64 * u + 16 * j + m);
-                x16[2 * j] = (uint16_t)w;
-                x16[2 * j + 1] = (uint16_t)(w >> 16);
+    if (threadIdx.x < 64) {  // the first wave finds the tokens' places
+        const int64_t t = t0 + threadIdx.x;
+        int b = a.seqs.n, slot = -1;
+        if (threadIdx.x < kTokens && t < a.T) {
+            if (!a.offs) {
+                b = (int)(t / a.per);
+                slot = a.seqs.len(b) - (int)((int64_t)(b + 1) * a.per - t);
+            } else {
+                int lo = 0, hi = a.seqs.n;  // the first sequence that ends behind t
+                while (lo < hi) {
+                    const int mid = (lo + hi) / 2;
+                    if (a.offs[mid + 1] > t)
+                        hi = mid;
+                    else
+                        lo = mid + 1;
+                }
+                b = lo;
+                if (b < a.seqs.n) slot = a.seqs.len(b) - (int)(a.offs[b + 1] - t);
             }
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) r[values ? e / 4 : 0].add(load16(x16[e], a.bf16));
-    }
-    // The group's range: of keys over the lanes that hold it; of values a group of 32
-    // is half of every lane's share of a set of 64.
-    Grid4 g[2];
-    if (!values) {
-        r[0].template reduce<(GROUP == 32 ? 4 : GROUP == 64 ? 8 : GROUP == 128 ? 16 : 32)>();
-        g[0] = g[1] = fit4(r[0], a.symmetric);
-    } else if constexpr (GROUP == 32) {
-        r[0].template reduce<8>();
-        r[1].template reduce<8>();
-        g[0] = fit4(r[0], a.symmetric);
-        g[1] = fit4(r[1], a.symmetric);
-    } else {
-        r[0].add(r[1]);
-        r[0].template reduce<(GROUP == 64 ? 8 : GROUP == 128 ? 16 : 32)>();
-        g[0] = g[1] = fit4(r[0], a.symmetric);
-    }
-    if (!in || !mine) return;
-    uint32_t q[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q[e] = code4(g[values ? e / 4 : 0], load16(x16[e], a.bf16));
-    if (a.out[values]) {
-        uint16_t *o = a.out[values] + t * a.ld_out[values] + h * D, y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = store16(value4(g[values ? e / 4 : 0], q[e]), a.bf16);
-        if (!values) {
-            u32x4 w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = y[2 * e] | (uint32_t)y[2 * e + 1] << 16;
-            *reinterpret_cast<u32x4 *>(o + 8 * i) = w;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint32_t *>(o + 64 * u + 16 * j + m) = y[2 * j] | (uint32_t)y[2 * j + 1] << 16;
+        int page = -1;
+        if (b < a.seqs.n && slot >= 0 && slot < a.seqs.capacity) page = a.seqs.page_of(a.pool, a.seqs.table + (int64_t)b * a.seqs.width, slot);
+        if (threadIdx.x < kTokens) place[threadIdx.x] = page >= 0 ? a.pool.first(page, h) + (slot & mask) : (b < a.seqs.n ? -1 : -2);
+        if constexpr (kStaged) {
+            const bool same = b == __shfl(b, 0) && page >= 0;
+            const uint64_t all = __ballot(same || threadIdx.x >= kTokens);
+            if (threadIdx.x == 0) whole = ~all ? -1 : slot;
         }
     }
-    if (page < 0) return;
-    const int at = slot & (a.pool.page() - 1);
-    const int64_t first = a.pool.first(page, h);
-    if (!values) {
-        uint32_t w = 0;
+    __syncthreads();
+    const bool wide = kStaged && values && whole >= 0;
+    const int shift = kStaged ? whole & 7 : 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w |= q[e] << (4 * (e / 2 + 4 * (e & 1)));
-        a.pool.k[(first + at) * (D / 8) + (i & 3) * (D / 32) + (i >> 2)] = w;
-        if (8 * i % GROUP == 0) a.pool.k_grid[first * NG + (int64_t)(8 * i / GROUP) * a.pool.page() + at] = word4(g[0]);
-        if (i == 0 && a.pool.weight) a.pool.weight[first + at] = 0.0f;
-    } else {
-        uint16_t *v = a.pool.v + ((first + (at & ~7)) * (D / 4) + (16 * u + m) * 8 + (at & 7));
+    for (int p = 0; p < kPasses; ++p) {
+        const int n = p * kPass + threadIdx.x / kLanes;  // of the workgroup's tokens
+        const int64_t t = t0 + n, at = place[n];
+        float f[8];
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            v[8 * k] = (uint16_t)(q[k] | q[2 + k] << 4 | q[4 + k] << 8 | q[6 + k] << 12);
-        uint32_t *grid = a.pool.v_grid + first * NG + at;
-        if constexpr (GROUP == 32) {
-            if (i % 8 < 2) grid[(int64_t)(2 * u + i % 8) * a.pool.page()] = word4(i % 8 ? g[1] : g[0]);
+        for (int e = 0; e < 8; ++e) {
+            const uint16_t w = (uint16_t)(x[p][e / 2] >> (16 * (e & 1)));
+            f[e] = load16(w, a.bf16);
+        }
+        Range range = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            range.lo = fminf(range.lo, fminf(f[e], f[e + 1]));
+            range.hi = fmaxf(range.hi, fmaxf(f[e], f[e + 1]));
+            range.sum += f[e] + f[e + 1];
+        }
+        range.template reduce<1, (GROUP == 192 ? 32 : GROUP / 8)>();
+        const Grid4 g(range, a.symmetric);
+        if (__any(g.m != 1.0f)) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] *= g.m;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = g.level(f[e]);
+        if (a.out[values] && at > -2 && t < a.T && i < D / 8) {
+            u32x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y0 = g.value(f[2 * e]), y1 = g.value(f[2 * e + 1]);
+                y[e] = a.bf16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(((f32x2){y0, y1}), bf16x2))
+                              : __builtin_bit_cast(uint32_t, __builtin_convertvector(((f32x2){y0, y1}), f16x2));
+            }
+            *reinterpret_cast<u32x4 *>(a.out[values] + t * a.ld_out[values] + h * D + 8 * i) = y;
+        }
+        uint32_t w;
+        if (!values) {  // dim e at bits 4 (e / 2 + 4 (e % 2))
+            w = codes4(f[0], f[2], f[4], f[6], g.zadd) | codes4(f[1], f[3], f[5], f[7], g.zadd) << 16;
+            if (g.bad) w = 0x88888888u;
         } else {
-            if (8 * i % GROUP == 0) grid[(int64_t)(8 * i / GROUP) * a.pool.page()] = word4(g[0]);
+            uint32_t nib = codes4(f[0], f[1], f[2], f[3], g.zadd) | codes4(f[4], f[5], f[6], f[7], g.zadd) << 16;
+            if (g.bad) nib = 0x88888888u;
+            // this lane's units m = 2 (i % 8), + 1: nibbles 2 (i % 4), + 1 of the lanes with their half of the dims
+            const int lane = threadIdx.x & 63, from = (lane & ~7) + (i % 8) / 4, down = 8 * (i % 4);
+            w = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = (uint32_t)__shfl((int)nib, from + 2 * j) >> down;
+                w |= (two & 15u) << (4 * j) | (two & 0xF0u) << (12 + 4 * j);
+            }
+        }
+        if (at < 0 || i >= D / 8) continue;
+        const int64_t first = at & ~(int64_t)mask;
+        const int in = (int)(at & mask), unit = 2 * i;  // 16 u + m of the first of the two units
+        if (8 * i % GROUP == 0) {
+            uint32_t *grid = (values ? a.pool.v_grid : a.pool.k_grid) + first * NG + ((int64_t)(8 * i / GROUP) << a.pool.lg_page);
+            grid[in] = g.word();
+        }
+        if (!values) {
+            a.pool.k[at * (D / 8) + (i & 3) * (D / 32) + (i >> 2)] = w;
+            if (i == 0 && a.pool.weight) a.pool.weight[at] = 0.0f;
+        } else if (wide) {
+            if constexpr (kStaged) {
+                units[unit][n + shift] = (uint16_t)w;
+                units[unit + 1][n + shift] = (uint16_t)(w >> 16);
+            }
+        } else {
+            uint16_t *v = a.pool.v + (at & ~(int64_t)7) * (D / 4) + unit * 8 + (at & 7);
+            v[0] = (uint16_t)w;
+            v[8] = (uint16_t)(w >> 16);
+        }
+    }
+    if constexpr (kStaged) {
+        if (!wide) return;
+        __syncthreads();
+        for (int j = threadIdx.x; j < kCols / 8 * (D / 4); j += 256) {
+            const int c = j / (D / 4) * 8, unit = j % (D / 4);  // columns c .. c + 7 are tokens c - shift ..
+            const int lo = max(c - shift, 0), hi = min(c - shift + 8, kTokens);
+            if (lo >= hi) continue;
+            uint16_t *v = a.pool.v + (place[lo] & ~(int64_t)7) * (D / 4) + unit * 8;
+            if (hi - lo == 8) {
+                *reinterpret_cast<u32x4 *>(v) = *reinterpret_cast<const u32x4 *>(&units[unit][c]);
+            } else {
+                for (int n = lo; n < hi; ++n) v[(n + shift) & 7] = units[unit][n + shift];
+            }
         }
     }
 }
 
+template <int D64, int GROUP>
+void launch_append(const AppendArgs &a, hipStream_t s) {
+    constexpr int kPass = 256 / (D64 == 1 ? 8 : (D64 == 2 ? 16 : 32));
+    // Staged where there are workgroups of 32 tokens for every compute unit.
+    if (ceil_div(a.T, kBlockTokens) * a.pool.heads * 2 >= 512)
+        append_kernel<D64, GROUP, true><<<dim3((unsigned)ceil_div(a.T, kBlockTokens), (unsigned)a.pool.heads, 2), 256, 0, s>>>(a);
+    else
+        append_kernel<D64, GROUP, false><<<dim3((unsigned)ceil_div(a.T, kPass), (unsigned)a.pool.heads, 2), 256, 0, s>>>(a);
+}
 template <int D64>
 hipError_t launch_append(const AppendArgs &a, int group, hipStream_t s) {
-    constexpr int kLanes = D64 == 1 ? 8 : (D64 == 2 ? 16 : 32);
-    const dim3 grid((unsigned)ceil_div(a.T * a.pool.heads, 256 / kLanes), 2);
-    void (*kernel)(AppendArgs) = nullptr;
     if (group == 64 * D64)
-        kernel = append_kernel<D64, 64 * D64>;
+        launch_append<D64, 64 * D64>(a, s);
     else if (group == 32)
-        kernel = append_kernel<D64, 32>;
+        launch_append<D64, 32>(a, s);
     else if (group == 64)
-        kernel = append_kernel<D64, 64>;
+        launch_append<D64, 64>(a, s);
     else if constexpr (D64 == 4)
-        kernel = append_kernel<D64, 128>;
-    kernel<<<grid, 256, 0, s>>>(a);
+        launch_append<D64, 128>(a, s);
     return hipGetLastError();
 }
 
@@ -236,6 +290,7 @@ hipError_t run_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv,
     a.ld_out[1] = ldvo;
     a.offs = offs;
     a.T = T;
+    a.per = T / n_seq;
     a.bf16 = dt == GPTQ_DT_BF16;
     a.symmetric = c.symmetric;
     const int group = c.group_size ? c.group_size : c.head_dim;

@@ -1,6 +1,8 @@
 // Thinning out a 4-bit cache: of every sequence and kv head, the last `recent`
 // tokens and the heaviest others by accumulated weight, `budget` in all, are copied to
 // other pages in slot order.
+#include <algorithm>
+
 #include "kv_cache.h"
 
 namespace gptq {
@@ -23,15 +25,33 @@ __device__ __forceinline__ uint32_t rank_of(float w) {
     const uint32_t u = __float_as_uint(w + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ uint32_t rank_at(const EvictArgs &a, const int32_t *row, int h, int slot) {
+// Of four neighbouring slots from a multiple of four on, which share a page.
+__device__ __forceinline__ u32x4 ranks_at(const EvictArgs &a, const int32_t *row, int h, int slot) {
     const int page = a.seqs.page_of(a.pool, row, slot);
-    return page < 0 ? 0u : rank_of(a.pool.weight[a.pool.first(page, h) + (slot & (a.pool.page() - 1))]);
+    if (page < 0) return (u32x4){};
+    const floatx4 w = *reinterpret_cast<const floatx4 *>(a.pool.weight + a.pool.first(page, h) + (slot & (a.pool.page() - 1)));
+    return (u32x4){rank_of(w[0]), rank_of(w[1]), rank_of(w[2]), rank_of(w[3])};
 }
 
-// The `heavy`-th largest rank of slots below `safe`, digit by digit from the highest (a histogram of 256 each), then
-// the kept slots in order: all above that rank, and of those at it the first ones.
-__global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
-    __shared__ uint32_t hist[256], found[2];
+// The inclusive sum over the lanes up to this one, by DPP row shifts and broadcasts.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+
+// The rank of the `heavy`-th largest of the slots below `safe`, digit by digit from the highest (11, 11 and 10 bits, a
+// histogram of each), then the kept slots in order: all above that rank, and of those at it the first ones.  Ranks stay in
+// LDS where they fit, `in_lds` of them (a multiple of four); a wave walks slots next to each other, so that order is a matter
+// of sums over its lanes.
+constexpr int kBins = 2048, kRanksInLds = 36 * 1024;  // 144 KB
+__global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int in_lds) {
+    extern __shared__ uint32_t ranks[];
+    __shared__ uint32_t hist[kBins], found[2], sums[kSelectWaves];
     __shared__ int counts[2][kSelectWaves];
     const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int32_t *row = a.seqs.table + (int64_t)b * a.seqs.width;
@@ -40,52 +60,84 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a) {
     int32_t *kept = a.kept + ((int64_t)b * a.pool.heads + h) * a.budget;
     for (int i = keep + threadIdx.x; i < a.budget; i += kSelectThreads) kept[i] = -1;
     if (a.new_lens && h == 0 && threadIdx.x == 0) a.new_lens[b] = keep;
-    uint32_t edge = 0;  // the rank of the last that stays; `ties` of those that have it stay
-    int ties = heavy;
-    if (heavy > 0 && heavy < safe) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (threadIdx.x < 256) hist[threadIdx.x] = 0;
-            __syncthreads();
-            for (int i = threadIdx.x; i < safe; i += kSelectThreads) {
-                const uint32_t k = rank_at(a, row, h, i);
-                if (shift == 24 || k >> (shift + 8) == edge >> (shift + 8)) atomicAdd(&hist[k >> shift & 255], 1u);
-            }
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                uint32_t left = ties;
-                int d = 255;
-                while (d > 0 && hist[d] < left) left -= hist[d--];
-                found[0] = d;
-                found[1] = left;
-            }
-            __syncthreads();
-            edge |= found[0] << shift;
-            ties = found[1];
-        }
+    for (int i = threadIdx.x; i < recent; i += kSelectThreads) kept[heavy + i] = safe + i;
+    if (heavy == 0) return;
+    if (heavy == safe) {
+        for (int i = threadIdx.x; i < safe; i += kSelectThreads) kept[i] = i;
+        return;
     }
-    // heavy == safe: every rank is at or above 0, and ties is enough for all of them
-    int above0 = 0, ties0 = 0;  // kept above the edge, and seen at it, before this round
-    for (int i0 = 0; i0 < len; i0 += kSelectThreads) {
-        const int i = i0 + threadIdx.x;
-        bool above = false, at = false;
-        if (i < safe && heavy > 0) {
-            const uint32_t k = rank_at(a, row, h, i);
-            above = k > edge;
-            at = k == edge;
-        } else if (i >= safe && i < len) {
-            above = true;
-        }
-        const uint64_t va = __ballot(above), vt = __ballot(at), below = (1ull << lane) - 1;
-        if (lane == 0) counts[0][wave] = __popcll(va), counts[1][wave] = __popcll(vt);
+    u32x4 *four = reinterpret_cast<u32x4 *>(ranks);
+    auto rank4 = [&](int i) { return i < in_lds ? four[i / 4] : ranks_at(a, row, h, i); };
+    const int stored = min(safe, in_lds);
+#pragma unroll 8
+    for (int i = 4 * threadIdx.x; i < stored; i += 4 * kSelectThreads) four[i / 4] = ranks_at(a, row, h, i);
+    uint32_t edge = 0, ties = heavy;  // the rank of the last that stays; `ties` of those that have it stay
+    for (int shift = 21, bits = 11; shift >= 0;) {
+        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) hist[i] = 0;
         __syncthreads();
-        int na = above0 + __popcll(va & below), nt = ties0 + __popcll(vt & below);
-        for (int w = 0; w < kSelectWaves; ++w) {
-            if (w < wave) na += counts[0][w], nt += counts[1][w];
-            above0 += counts[0][w];
-            ties0 += counts[1][w];
+        const uint32_t digits = (1u << bits) - 1;
+        const int above = shift + bits;
+#pragma unroll 4
+        for (int i = 4 * threadIdx.x; i < safe; i += 4 * kSelectThreads) {
+            const u32x4 k = rank4(i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (i + e < safe && (above == 32 || k[e] >> above == edge >> above)) atomicAdd(&hist[k[e] >> shift & digits], 1u);
         }
-        if (above || (at && nt < ties)) kept[na + min(nt, ties)] = i;
         __syncthreads();
+        // thread i holds bins kBins - 2 i - 1 and - 2: sums from the highest bin down
+        const uint32_t h0 = hist[kBins - 1 - 2 * threadIdx.x], h1 = hist[kBins - 2 - 2 * threadIdx.x];
+        const uint32_t upto = (uint32_t)wave_scan((int)(h0 + h1));
+        if (lane == 63) sums[wave] = upto;
+        __syncthreads();
+        uint32_t before = upto - h0 - h1;
+        for (int w = 0; w < wave; ++w) before += sums[w];
+        if (before < ties && ties <= before + h0)
+            found[0] = kBins - 1 - 2 * threadIdx.x, found[1] = ties - before;
+        else if (before + h0 < ties && ties <= before + h0 + h1)
+            found[0] = kBins - 2 - 2 * threadIdx.x, found[1] = ties - before - h0;
+        __syncthreads();
+        edge |= found[0] << shift;
+        ties = found[1];
+        bits = shift < 11 ? 10 : 11;
+        shift = shift == 21 ? 10 : shift == 10 ? 0 : -1;
+    }
+    // A wave's share of the slots in rounds of 256, four neighbouring ones a lane.
+    const int share = (safe + 4 * kSelectThreads - 1) / (4 * kSelectThreads) * (4 * kWave), i0 = wave * share, i1 = min(i0 + share, safe);
+    int na = 0, nt = 0;
+    for (int i = i0 + 4 * lane; i < i1; i += 4 * kWave) {
+        const u32x4 k = rank4(i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) na += i + e < i1 && k[e] > edge, nt += i + e < i1 && k[e] == edge;
+    }
+    na = wave_scan(na);
+    nt = wave_scan(nt);
+    if (lane == 63) counts[0][wave] = na, counts[1][wave] = nt;
+    __syncthreads();
+    na = nt = 0;
+    for (int w = 0; w < wave; ++w) na += counts[0][w], nt += counts[1][w];
+    for (int j = i0; j < i1; j += 4 * kWave) {
+        const int i = j + 4 * lane;
+        const u32x4 k = i < i1 ? rank4(i) : (u32x4){};
+        bool above[4], at[4];
+        int ma = 0, mt = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            above[e] = i + e < i1 && k[e] > edge;
+            at[e] = i + e < i1 && k[e] == edge;
+            ma += above[e];
+            mt += at[e];
+        }
+        const int sa = wave_scan(ma), st = wave_scan(mt);
+        int pa = na + sa - ma, pt = nt + st - mt;  // before this lane's
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (above[e] || (at[e] && pt < (int)ties)) kept[pa + min(pt, (int)ties)] = i + e;
+            pa += above[e];
+            pt += at[e];
+        }
+        na += __builtin_amdgcn_readlane(sa, 63);
+        nt += __builtin_amdgcn_readlane(st, 63);
     }
 }
 
@@ -169,7 +221,8 @@ hipError_t run_kv_evict(const gptq_kv_cache &c, const int32_t *table, int64_t wi
     a.recent = (int32_t)recent;
     a.kept = kept;
     a.new_lens = new_lens;
-    select_kernel<<<dim3((unsigned)c.n_heads, (unsigned)n_seq), kSelectThreads, 0, s>>>(a);
+    const int in_lds = (int)std::min<int64_t>(align_up(max_len, 4), kRanksInLds);
+    select_kernel<<<dim3((unsigned)c.n_heads, (unsigned)n_seq), kSelectThreads, (size_t)in_lds * 4, s>>>(a, in_lds);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)ceil_div(budget, 32), (unsigned)c.n_heads, (unsigned)n_seq);
