@@ -630,7 +630,7 @@ class KVCache:
     """A pool of pages of a 4-bit key/value cache for ``kv_append``, ``kv_attention`` and ``kv_evict``: the tensors and
     their ``gptq_kv_cache``.  It keeps the tensors alive."""
     __slots__ = ("k", "v", "k_grid", "v_grid", "weight", "n_pages", "n_heads", "head_dim", "page", "group_size", "symmetric",
-                 "device", "c", "ref", "tensors")
+                 "device", "scale", "c", "ref", "tensors")
 
     def __init__(self, k, v, k_grid, v_grid, weight, group_size, symmetric):
         import torch
@@ -656,6 +656,7 @@ class KVCache:
             raise ValueError(f"weight must be {[pages, heads, page]}")
         self.k, self.v, self.k_grid, self.v_grid, self.weight, self.device = *tensors, k.device
         self.n_pages, self.n_heads, self.page, self.head_dim = pages, heads, page, dim
+        self.scale = dim ** -0.5
         self.group_size, self.symmetric, self.tensors = group, bool(symmetric), tensors
         self.c = KVCacheStruct(k.data_ptr(), v.data_ptr(), k_grid.data_ptr(), v_grid.data_ptr(),
                                None if weight is None else weight.data_ptr(), pages, heads, dim, page, group, int(self.symmetric))
@@ -682,22 +683,35 @@ def kv_cache_empty(n_pages: int, n_heads: int, head_dim: int, page: int = 64, gr
                    new(torch.float32, page) if weights else None, int(group_size), symmetric)
 
 
+# The checks below run once per layer and token, so what is common is asked first and the rest only where it fails.
 def _kv_ints(t, shape, device, name, torch):
-    if t.device != device or t.dtype != torch.int32 or t.dim() != len(shape) or not t.is_contiguous() or \
+    """An int32 tensor of this shape (None: any size) next to the cache; its address."""
+    if t.dtype is not torch.int32 or t.device != device or not t.is_contiguous() or t.dim() != len(shape) or \
             any(n is not None and m != n for m, n in zip(t.shape, shape)):
         raise ValueError(f"{name} must be a contiguous int32 {['any' if n is None else n for n in shape]} on the cache's device")
-    return t
+    return t.data_ptr()
 
 
-def _kv_rows(X, heads, dim, device, dtypes, name):
-    """Pitch and type of [..., heads, dim] whose rows (all leading dimensions) lie at one pitch."""
-    dt = dtypes.get(X.dtype)
-    if dt is None:
-        raise TypeError(f"{name} must be float16 or bfloat16")
-    if X.device != device or X.dim() < 3 or tuple(X.shape[-2:]) != (heads, dim) or X.stride(-1) != 1 or \
-            (heads > 1 and X.stride(-2) != dim):
-        raise ValueError(f"{name} must be [...][{heads}][{dim}] on the cache's device, contiguous within a token")
-    ld, rows = heads * dim, 1
+def _kv_seqs(table, lens, device, torch):
+    """Sequences, the table's width, and the addresses of both."""
+    i32 = torch.int32
+    if lens.dtype is not i32 or table.dtype is not i32 or lens.device != device or table.device != device or lens.dim() != 1 or \
+            table.dim() != 2 or not lens.is_contiguous() or not table.is_contiguous() or table.shape[0] != lens.shape[0]:
+        raise ValueError("lens must be a contiguous int32 [sequences] and table [sequences][pages] on the cache's device")
+    n, width = table.shape
+    return n, width, table.data_ptr(), lens.data_ptr()
+
+
+def _kv_pitch(X, heads, dim, device, name):
+    """Elements between the tokens of [..., heads, dim] (all leading dimensions at one pitch)."""
+    if X.device != device or X.shape[-2] != heads or X.shape[-1] != dim:
+        raise ValueError(f"{name} must be [...][{heads}][{dim}] on the cache's device")
+    ld = heads * dim
+    if X.is_contiguous():
+        return ld
+    if X.stride(-1) != 1 or (heads > 1 and X.stride(-2) != dim):
+        raise ValueError(f"{name} must be contiguous within a token")
+    rows = 1
     for i in range(X.dim() - 3, -1, -1):
         if X.shape[i] > 1:
             if rows == 1:
@@ -705,7 +719,7 @@ def _kv_rows(X, heads, dim, device, dtypes, name):
             elif X.stride(i) != rows * ld:
                 raise ValueError(f"the tokens of {name} must lie at one pitch")
         rows *= X.shape[i]
-    return ld, dt
+    return ld
 
 
 def kv_append(K, V, cache: KVCache, table, lens, offs=None, values=False, K_out=None, V_out=None, stream=None):
@@ -717,30 +731,36 @@ def kv_append(K, V, cache: KVCache, table, lens, offs=None, values=False, K_out=
     if stream is not None:
         with _few_on(stream, cache.device, torch, (), *cache.tensors, K, V, table, lens, offs, K_out, V_out):
             return kv_append(K, V, cache, table, lens, offs, values, K_out, V_out)
-    dev, heads, dim = cache.device, cache.n_heads, cache.head_dim
-    if K.dim() != 3 or K.shape != V.shape or K.dtype != V.dtype:
+    dev, heads, dim, dtype, shape = cache.device, cache.n_heads, cache.head_dim, K.dtype, K.shape
+    dt = act.get(dtype)
+    if dt is None:
+        raise TypeError("K must be float16 or bfloat16")
+    if len(shape) != 3 or V.shape != shape or V.dtype is not dtype:
         raise ValueError("K and V must be [tokens][heads][head_dim] of one type")
-    ldk, dt = _kv_rows(K, heads, dim, dev, act, "K")
-    ldv, _ = _kv_rows(V, heads, dim, dev, act, "V")
-    T, n_seq = K.shape[0], lens.shape[0]
-    _kv_ints(lens, (n_seq,), dev, "lens", torch)
-    _kv_ints(table, (n_seq, None), dev, "table", torch)
-    if offs is not None:
-        _kv_ints(offs, (n_seq + 1,), dev, "offs", torch)
-    if values:
-        K_out = torch.empty((T, heads, dim), dtype=K.dtype, device=dev) if K_out is None else K_out
-        V_out = torch.empty((T, heads, dim), dtype=K.dtype, device=dev) if V_out is None else V_out
-    outs = []
-    for out, name in ((K_out, "K_out"), (V_out, "V_out")):
-        if out is None:
-            outs += [None, 0]
-            continue
-        if out.shape != K.shape or out.dtype != K.dtype:
-            raise ValueError(f"{name} must have K's shape and type")
-        outs += [out.data_ptr(), _kv_rows(out, heads, dim, dev, act, name)[0]]
-    _few_launch(lib.gptq_kv_append, dev, torch, K.data_ptr(), ldk, V.data_ptr(), ldv, dt, T,
-                None if offs is None else offs.data_ptr(), cache.ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n_seq, *outs)
-    return (K_out, V_out) if K_out is not None or V_out is not None else None
+    ldk, ldv = _kv_pitch(K, heads, dim, dev, "K"), _kv_pitch(V, heads, dim, dev, "V")
+    n_seq, width, tp, lp = _kv_seqs(table, lens, dev, torch)
+    op = None if offs is None else _kv_ints(offs, (n_seq + 1,), dev, "offs", torch)
+    kp = vp = None
+    ldko = ldvo = heads * dim
+    if K_out is not None:
+        if K_out.shape != shape or K_out.dtype is not dtype:
+            raise ValueError("K_out must have K's shape and type")
+        ldko = _kv_pitch(K_out, heads, dim, dev, "K_out")
+    elif values:
+        K_out = torch.empty(shape, dtype=dtype, device=dev)
+    if V_out is not None:
+        if V_out.shape != shape or V_out.dtype is not dtype:
+            raise ValueError("V_out must have V's shape and type")
+        ldvo = _kv_pitch(V_out, heads, dim, dev, "V_out")
+    elif values:
+        V_out = torch.empty(shape, dtype=dtype, device=dev)
+    if K_out is not None:
+        kp = K_out.data_ptr()
+    if V_out is not None:
+        vp = V_out.data_ptr()
+    _few_launch(lib.gptq_kv_append, dev, torch, K.data_ptr(), ldk, V.data_ptr(), ldv, dt, shape[0], op, cache.ref, tp, width, lp, n_seq,
+                kp, ldko, vp, ldvo)
+    return None if K_out is None and V_out is None else (K_out, V_out)
 
 
 def kv_attention_workspace_bytes(cache: KVCache, n_seq: int, n: int, q_heads: int, max_len: int) -> int:
@@ -757,26 +777,32 @@ def kv_attention(Q, cache: KVCache, table, lens, scale=None, max_len=None, decay
     if stream is not None:
         with _few_on(stream, cache.device, torch, (), *cache.tensors, Q, table, lens, O, ws):
             return kv_attention(Q, cache, table, lens, scale, max_len, decay, O, ws)
-    dev, dim = cache.device, cache.head_dim
-    if Q.dim() != 4:
+    dev, dim, dtype, shape = cache.device, cache.head_dim, Q.dtype, Q.shape
+    dt = act.get(dtype)
+    if dt is None:
+        raise TypeError("Q must be float16 or bfloat16")
+    if len(shape) != 4:
         raise ValueError("Q must be [sequences][tokens][heads][head_dim]")
-    n_seq, n, q_heads, _ = Q.shape
-    ldq, dt = _kv_rows(Q, q_heads, dim, dev, act, "Q")
-    _kv_ints(lens, (n_seq,), dev, "lens", torch)
-    _kv_ints(table, (n_seq, None), dev, "table", torch)
+    rows, n, q_heads, _ = shape
+    ldq = _kv_pitch(Q, q_heads, dim, dev, "Q")
+    n_seq, width, tp, lp = _kv_seqs(table, lens, dev, torch)
+    if rows != n_seq:
+        raise ValueError("Q, table and lens must have the same number of sequences")
     if O is None:
-        O = torch.empty((n_seq, n, q_heads, dim), dtype=Q.dtype, device=dev)
-    elif O.shape != Q.shape or O.dtype != Q.dtype:
-        raise ValueError("O must have Q's shape and type")
-    ldo, _ = _kv_rows(O, q_heads, dim, dev, act, "O")
+        O = torch.empty(shape, dtype=dtype, device=dev)
+        ldo = q_heads * dim
+    else:
+        if O.shape != shape or O.dtype is not dtype:
+            raise ValueError("O must have Q's shape and type")
+        ldo = _kv_pitch(O, q_heads, dim, dev, "O")
     if max_len is None:
-        max_len = table.shape[1] * cache.page
+        max_len = width * cache.page
     if ws is None:
         ws = _workspace(kv_attention_workspace_bytes(cache, n_seq, n, q_heads, max_len), dev)
     wp, wn = _few_ws(ws, dev)
-    _few_launch(lib.gptq_kv_attention, dev, torch, Q.data_ptr(), dt, n_seq, n, q_heads, ldq, cache.ref, table.data_ptr(),
-                table.shape[1], lens.data_ptr(), max_len, dim ** -0.5 if scale is None else scale, 0 if decay is None else 1,
-                0.0 if decay is None else decay, O.data_ptr(), ldo, wp, wn)
+    _few_launch(lib.gptq_kv_attention, dev, torch, Q.data_ptr(), dt, n_seq, n, q_heads, ldq, cache.ref, tp, width, lp, max_len,
+                cache.scale if scale is None else scale, 0 if decay is None else 1, 0.0 if decay is None else decay, O.data_ptr(), ldo, wp,
+                wn)
     return O
 
 
@@ -795,26 +821,28 @@ def kv_evict(cache: KVCache, table, lens, to, budget: int, recent: int = 0, max_
     if stream is not None:
         with _few_on(stream, cache.device, torch, (), *cache.tensors, table, lens, to, kept, new_lens, ws):
             return kv_evict(cache, table, lens, to, budget, recent, max_len, kept, new_lens, ws)
-    dev, n_seq = cache.device, lens.shape[0]
-    _kv_ints(lens, (n_seq,), dev, "lens", torch)
-    _kv_ints(table, (n_seq, None), dev, "table", torch)
-    _kv_ints(to, (n_seq, None), dev, "to", torch)
+    dev, heads = cache.device, cache.n_heads
+    n_seq, width, tp, lp = _kv_seqs(table, lens, dev, torch)
+    top = _kv_ints(to, (n_seq, None), dev, "to", torch)
     if budget < 1:
         raise ValueError("budget must be at least 1")
     if kept is None:
-        kept = torch.empty((n_seq, cache.n_heads, budget), dtype=torch.int32, device=dev)
+        kept = torch.empty((n_seq, heads, budget), dtype=torch.int32, device=dev)
+        kp = kept.data_ptr()
+    else:
+        kp = _kv_ints(kept, (n_seq, heads, budget), dev, "kept", torch)
     if new_lens is None:
         new_lens = torch.empty((n_seq,), dtype=torch.int32, device=dev)
-    _kv_ints(kept, (n_seq, cache.n_heads, budget), dev, "kept", torch)
-    _kv_ints(new_lens, (n_seq,), dev, "new_lens", torch)
+        np_ = new_lens.data_ptr()
+    else:
+        np_ = _kv_ints(new_lens, (n_seq,), dev, "new_lens", torch)
     if max_len is None:
-        max_len = table.shape[1] * cache.page
+        max_len = width * cache.page
     if ws is None:
         need = kv_evict_workspace_bytes(cache, n_seq, max_len, budget)
         ws = _workspace(need, dev) if need else None
     wp, wn = _few_ws(ws, dev)
-    _few_launch(lib.gptq_kv_evict, dev, torch, cache.ref, table.data_ptr(), table.shape[1], lens.data_ptr(), n_seq, max_len,
-                to.data_ptr(), to.shape[1], budget, recent, kept.data_ptr(), new_lens.data_ptr(), wp, wn)
+    _few_launch(lib.gptq_kv_evict, dev, torch, cache.ref, tp, width, lp, n_seq, max_len, top, to.shape[1], budget, recent, kp, np_, wp, wn)
     return kept, new_lens
 
 
