@@ -25,6 +25,8 @@
 namespace gptq {
 namespace {
 
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 constexpr int kKvTile = 32;   // tokens of a tile
 constexpr int kKvWaves = 4;   // waves of a workgroup, each with tiles of its own
 constexpr int kKvThreads = kKvWaves * kWave;
@@ -52,6 +54,12 @@ struct AttnArgs {
 __device__ __forceinline__ float xor_max(float v, int o) { return fmaxf(v, __shfl_xor(v, o)); }
 __device__ __forceinline__ float xor_add(float v, int o) { return v + __shfl_xor(v, o); }
 
+// Nothing is computed or loaded on the other side of this.
+__device__ __forceinline__ void keep_order() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // The thread's number as a value that nothing is computed from ahead of time: what a rare path derives from it would hold
 // registers over the loops otherwise.
 __device__ __forceinline__ int fresh_thread() {
@@ -60,53 +68,57 @@ __device__ __forceinline__ int fresh_thread() {
     return t;
 }
 
-// How the cached tokens are shared out: the tiles of all sequences in a row, `chunk` to a
-// workgroup, whose part of one sequence is a segment.  Workgroup x's segment of sequence b
-// has the number x + b.
+// How the cached tokens are shared out: the tiles of all sequences in a row, `chunk` to a workgroup, whose part of one
+// sequence is a segment.  Workgroup x's segment of sequence b has the number x + b.
 struct Share {
     int b, start, tiles, len;  // a sequence, its first tile in the row, its tiles and length
 };
-__device__ __forceinline__ int tiles_of(const KvSeqs &s, int b) { return b < s.n ? (s.len(b) + kKvTile - 1) / kKvTile : 0; }
-__device__ __forceinline__ int wave_sum(int v) {
-    for (int o = 1; o < kWave; o *= 2) v += __shfl_xor(v, o);
-    return __builtin_amdgcn_readfirstlane(v);
-}
-__device__ __forceinline__ int total_tiles(const AttnArgs &a) {
-    const int lane = threadIdx.x & 63;
-    int total = 0;
-    for (int b0 = 0; b0 < a.seqs.n; b0 += kWave) total += tiles_of(a.seqs, b0 + lane);
-    return wave_sum(total);
-}
-__device__ __forceinline__ int chunk_of(const AttnArgs &a, int total) {
-    const int c = (total + a.target - 1) / a.target;
-    return max(kKvLeast, (c + kKvWaves - 1) / kKvWaves * kKvWaves);
-}
-// The sequence that tile `at` of the row belongs to, or with `seq` sequence `at`.
-__device__ __forceinline__ Share share_of(const AttnArgs &a, int at, bool seq) {
-    const int lane = threadIdx.x & 63;
-    Share s = {};
-    int base = 0;
-    for (int b0 = 0; b0 < a.seqs.n; b0 += kWave) {
-        const int tiles = tiles_of(a.seqs, b0 + lane);
-        int sum = tiles;
-        for (int o = 1; o < kWave; o *= 2) {
-            const int v = __shfl_up(sum, o);
-            if (lane >= o) sum += v;
-        }
-        const int from = base + sum - tiles;
-        const uint64_t hit = __ballot(seq ? b0 + lane == at : from <= at && at < from + tiles);
-        if (hit) {
-            const int l = __builtin_ctzll(hit);
-            s.b = b0 + l;
-            s.start = __builtin_amdgcn_readlane(from, l);
-            s.tiles = __builtin_amdgcn_readlane(tiles, l);
-            s.len = a.seqs.len(s.b);
-            break;
-        }
-        base += __builtin_amdgcn_readlane(sum, kWave - 1);
+// 64 sequences at a time, a lane each; up to 64 are read once.
+struct Row {
+    const KvSeqs &seqs;
+    int group = -1, len, tiles, upto;  // the lane's sequence; the tiles up to its end, from the group's first on
+    int total = 0, chunk = 0;
+
+    __device__ __forceinline__ void read(int g) {
+        if (g == group) return;
+        group = g;
+        const int b = g * kWave + (threadIdx.x & 63);
+        len = b < seqs.n ? seqs.len(b) : 0;
+        tiles = (len + kKvTile - 1) / kKvTile;
+        upto = wave_scan(tiles);
     }
-    return s;
-}
+    __device__ __forceinline__ Row(const KvSeqs &s) : seqs(s) {}
+    __device__ __forceinline__ Row(const AttnArgs &a) : seqs(a.seqs) {
+        for (int g = 0; g * kWave < seqs.n; ++g) {
+            read(g);
+            total += __builtin_amdgcn_readlane(upto, kWave - 1);
+        }
+        const int c = (total + a.target - 1) / a.target;
+        chunk = max(kKvLeast, (c + kKvWaves - 1) / kKvWaves * kKvWaves);
+    }
+    // The sequence that tile `at` of the row belongs to, or with `seq` sequence `at`.
+    __device__ __forceinline__ Share find(int at, bool seq) {
+        const int lane = threadIdx.x & 63;
+        Share s = {};
+        int base = 0;
+        for (int g = 0; g * kWave < seqs.n; ++g) {
+            read(g);
+            const uint64_t hit = __ballot(seq ? g * kWave + lane == at : base + upto - tiles <= at && at < base + upto);
+            if (hit) {
+                const int l = __builtin_ctzll(hit);
+                s.b = g * kWave + l;
+                s.tiles = __builtin_amdgcn_readlane(tiles, l);
+                s.start = base + __builtin_amdgcn_readlane(upto, l) - s.tiles;
+                s.len = __builtin_amdgcn_readlane(len, l);
+                break;
+            }
+            base += __builtin_amdgcn_readlane(upto, kWave - 1);
+        }
+        return s;
+    }
+};
+
+__device__ __forceinline__ int tiles_of(const KvSeqs &s, int b) { return (s.len(b) + kKvTile - 1) / kKvTile; }
 
 // The pages of a tile: one, or with pages of sixteen tokens one for each half.  -1: there is none.
 struct TilePages {
@@ -252,40 +264,47 @@ struct Queries {
     float scale;    // of scores, to log2
     int sees;       // slots below this are visible
 
+    // The row's bits; prepare() turns them into x.
     __device__ __forceinline__ void load(const AttnArgs &a, int b, int h, int len, int col) {
         const int kb = (fresh_thread() & 63) >> 4;
         const bool real = col < a.cols;
         const int i = real ? col / a.group : 0, hq = h * a.group + (real ? col - i * a.group : 0);
         sees = real ? len - a.n + 1 + i : 0;
         const uint16_t *q = a.q + ((int64_t)b * a.n + i) * a.ldq + (int64_t)hq * (64 * D64) + 8 * kb;
-        u32x4 w[KW];
 #pragma unroll
-        for (int t = 0; t < KW; ++t) w[t] = real ? *reinterpret_cast<const u32x4 *>(q + 32 * t) : (u32x4){};
-        auto value = [&](int t, int e) {
-            const uint32_t v = w[t][e / 2];
-            return a.bf16 ? __uint_as_float(e & 1 ? v & 0xFFFF0000u : v << 16) : (float)__builtin_bit_cast(f16x2, v)[e & 1];
-        };
-        float top = 0.0f;
+        for (int t = 0; t < KW; ++t) x[t] = __builtin_bit_cast(f16x8, real ? *reinterpret_cast<const u32x4 *>(q + 32 * t) : (u32x4){});
+    }
+    __device__ __forceinline__ void prepare(const AttnArgs &a) {
+        // the largest magnitude, whose bits order as the numbers do in both types; its binade becomes fp16's largest
+        u16x2 most = {};
 #pragma unroll
         for (int t = 0; t < KW; ++t)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(value(t, e)));
+            for (int j = 0; j < 4; ++j)
+                most = __builtin_elementwise_max(most, __builtin_bit_cast(u16x2, __builtin_bit_cast(u32x4, x[t])[j] & 0x7FFF7FFFu));
+        const uint16_t m = most[0] > most[1] ? most[0] : most[1];
+        float top = a.bf16 ? __uint_as_float((uint32_t)m << 16) : (float)__builtin_bit_cast(_Float16, m);
         top = xor_max(xor_max(top, 16), 32);
         int e = 0;
         if (top > 0.0f && top < __builtin_inff()) frexpf(top, &e);
-        const int up = 15 - e;  // top < 2^e: fp16's largest binade
+        const int up = min(15 - e, 126);  // top < 2^e; (a power of two that fp32 holds)
+        const float f0 = ldexpf(1.0f, up), f1 = ldexpf(1.0f, up - 4);
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             float s = 0.0f;
 #pragma unroll
             for (int t = g * KW / NG; t < (g + 1) * KW / NG; ++t) {
+                const u32x4 w = __builtin_bit_cast(u32x4, x[t]);
                 u32x4 y;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {  // pair j of the fragment; the odd ones meet codes 2^4 larger
-                    const int d = j & 1 ? up - 4 : up;
-                    const f32x2 f = {ldexpf(value(t, 2 * j), d), ldexpf(value(t, 2 * j + 1), d)};
-                    const f16x2 hf = __builtin_convertvector(f, f16x2);
-                    s += ((float)hf[0] + (float)hf[1]) * (j & 1 ? 16.0f : 1.0f);
+                    const uint32_t two = w[j];
+                    f32x2 v = {__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u)};
+                    if (!a.bf16) v = __builtin_convertvector(__builtin_bit_cast(f16x2, two), f32x2);
+                    const float f = j & 1 ? f1 : f0;
+                    const f16x2 hf = __builtin_convertvector(((f32x2){v[0] * f, v[1] * f}), f16x2);
+                    const _Float16 one = j & 1 ? (_Float16)16.0f : (_Float16)1.0f;
+                    s = __builtin_amdgcn_fdot2(hf, (f16x2){one, one}, s, false);
                     y[j] = __builtin_bit_cast(uint32_t, hf);
                 }
                 x[t] = __builtin_bit_cast(f16x8, y);
@@ -323,7 +342,7 @@ __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile
                 for (int c = 0; c < NT; ++c)
                     s[c][4 * t + i] = fmaf(scale[i] * q[c].scale, fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]),
                                            g == 0 ? -base[c] : s[c][4 * t + i]);
-            __builtin_amdgcn_sched_barrier(0);  // fragments and grids of one group at a time: registers
+            keep_order();  // fragments and grids of one group at a time: registers
         }
 }
 
@@ -408,45 +427,62 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
     float2 *ml = reinterpret_cast<float2 *>(smem + kKvWaves * 16 * D);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
+        const int left = a.cols - col0 - 16 * c;  // columns there are
+        if (c && left <= 0) break;
         const float l = xor_add(xor_add(s.sum[c], 16), 32);
         __syncthreads();  // what the last round left in LDS has been read
         if (kb == 0) ml[wave * 16 + r] = make_float2(s.top(c), l);
         __syncthreads();
-        float m = kNegInf;
+        float m = kNegInf, all = 0.0f;
+#pragma unroll
         for (int w = 0; w < kKvWaves; ++w) m = fmaxf(m, ml[w * 16 + r].x);
-        const float f = share_in(s.top(c), m) / (s.vscale * kCode);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float k = xor_add(xor_add(s.corr[c][g], 16), 32) * kCode;
+        for (int w = 0; w < kKvWaves; ++w) {
+            const float2 v = ml[w * 16 + r];
+            all += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - m);  // (a NaN stays)
+        }
+        const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+        const float f = share_in(s.top(c), m) / (s.vscale * kCode) * (whole ? inv : 1.0f);
+        const int64_t stat = ((int64_t)(blockIdx.x + sh.b) * a.pool.heads + h) * a.cols + col0 + 16 * c;
+        if (r < left) {
 #pragma unroll
-            for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d)
-                *reinterpret_cast<floatx4 *>(smem + (wave * 16 + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f;
+            for (int g = 0; g < NG; ++g) {
+                const float k = xor_add(xor_add(s.corr[c][g], 16), 32) * kCode;
+#pragma unroll
+                for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d)
+                    *reinterpret_cast<floatx4 *>(smem + (wave * 16 + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f;
+            }
+            if (wave == 0 && kb == 0) {
+                if (!whole)
+                    a.stat[stat + r] = make_float2(m, all);
+                else if (a.last)
+                    a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col0 + 16 * c + r] = make_float2(m, inv);
+            }
         }
         __syncthreads();
-        for (int i = thread; i < 16 * D; i += kKvThreads) {
-            const int cc = i / D, d = i % D, col = col0 + 16 * c + cc;
-            if (col >= a.cols) break;
-            float M = kNegInf, L = 0.0f, o = 0.0f;
-            for (int w = 0; w < kKvWaves; ++w) M = fmaxf(M, ml[w * 16 + cc].x);
-            for (int w = 0; w < kKvWaves; ++w) {
-                const float2 v = ml[w * 16 + cc];
-                L += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - M);  // (a NaN stays)
-                o += smem[(w * 16 + cc) * D + d];
-            }
+        for (int i = thread; i < min(left, 16) * (D / 4); i += kKvThreads) {
+            const int cc = i / (D / 4), d = i % (D / 4) * 4;
+            floatx4 o = *reinterpret_cast<const floatx4 *>(smem + cc * D + d);
+#pragma unroll
+            for (int w = 1; w < kKvWaves; ++w) o += *reinterpret_cast<const floatx4 *>(smem + (w * 16 + cc) * D + d);
             if (whole) {
-                a.o[result_at(a, sh.b, h, col, D) + d] = result16(a, L == 0.0f ? 0.0f : o / L);
-                if (d == 0 && a.last) a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col] = make_float2(M, L == 0.0f ? 0.0f : 1.0f / L);
+                uint16_t *to = a.o + result_at(a, sh.b, h, col0 + 16 * c + cc, D) + d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) to[e] = result16(a, o[e]);
             } else {
-                const int64_t at = ((int64_t)(blockIdx.x + sh.b) * a.pool.heads + h) * a.cols + col;
-                a.part[at * D + d] = o;
-                if (d == 0) a.stat[at] = make_float2(M, L);
+                *reinterpret_cast<floatx4 *>(a.part + (stat + cc) * D + d) = o;
             }
         }
     }
 }
 
-// Waves of a SIMD that the registers of a kernel allow.
-constexpr int occupancy(int D64, int NG, int NT) { return D64 * NT <= 2 ? 4 : 2; }
+// Waves of a SIMD that the registers of a kernel allow (of 512, in steps of eight): its sums take 16 D64 NT, its queries
+// 8 D64 NT, a tile 9 D64.
+constexpr int occupancy(int D64, int NG, int NT) {
+    if (D64 * NT == 1 || (D64 == 2 && NT == 1 && NG == 1)) return 4;
+    if ((D64 == 2 && NT == 1) || (D64 == 1 && NG == 1)) return 3;
+    return D64 * NG * NT < 16 ? 2 : 1;
+}
 
 template <int D64, int NG, int NT>
 __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_kernel(AttnArgs a) {
@@ -455,18 +491,17 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4;
     const int h = blockIdx.y, col0 = blockIdx.z * (16 * NT);
     TileGrids<NG> &grids = reinterpret_cast<TileGrids<NG> *>(smem + kKvWaves * 16 * (D + 2))[wave];
-    int from, to;  // of the row of tiles
+    int from = 0, to;  // of the row of tiles
     Share sh;
     if (a.direct) {  // a sequence to a workgroup
         sh = {(int)blockIdx.x, 0, tiles_of(a.seqs, blockIdx.x), a.seqs.len(blockIdx.x)};
-        from = 0;
         to = sh.tiles;
     } else {
-        const int total = total_tiles(a), chunk = chunk_of(a, total);
-        from = blockIdx.x * chunk;
-        to = min(from + chunk, total);
+        Row rows(a);
+        from = blockIdx.x * rows.chunk;
+        to = min(from + rows.chunk, rows.total);
         if (from >= to) return;
-        sh = share_of(a, from, false);
+        sh = rows.find(from, false);
     }
     for (;;) {
         const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
@@ -483,6 +518,8 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
             t.load_keys(a, pages, tile, h);
             t.load_values(a, pages, tile, h);
         }
+#pragma unroll
+        for (int c = 0; c < NT; ++c) q[c].prepare(a);
         // The keys of the next tile are on their way during the second product, its values during the first of the next.
         while (tile < t1) {
             const int next = tile + kKvWaves;
@@ -535,10 +572,9 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
                     float ps[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) ps[i] = p[c][i] * (i < 4 ? s0[i] : s1[i - 4]);
-                    if (masked) {  // a value that this column does not see may be no number
+                    if (masked) {  // a value that a column does not see may be no number
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            if (hidden(there, slot + i, q[c].sees)) ps[i] = 0.0f;
+                        for (int i = 0; i < 8; ++i) ps[i] = p[c][i] == 0.0f ? 0.0f : ps[i];
                     }
                     u32x4 w;
 #pragma unroll
@@ -558,7 +594,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
                         sums.acc[c][d] = mma(vf[0], pf[c], sums.acc[c][d]);
                         sums.acc[c][d + 1] = mma(vf[1], pf[c], sums.acc[c][d + 1]);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
+                    keep_order();
                 }
             }
             if (next < t1) t.load_values(a, coming, next, h);
@@ -568,7 +604,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
         write_sums<D64, NG, NT>(a, sums, sh, t0 == 0 && t1 == sh.tiles, smem, h, col0);
         if (from + (t1 - t0) >= to) break;
         from += t1 - t0;
-        sh = share_of(a, from, false);
+        sh = Row(a.seqs).find(from, false);
     }
 }
 
@@ -580,9 +616,9 @@ __global__ __launch_bounds__(kKvThreads) void combine_kernel(AttnArgs a) {
     __shared__ float red[2][kKvWaves];
     __shared__ floatx4 sums[kKvThreads];
     const int col = blockIdx.x, h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int chunk = chunk_of(a, total_tiles(a));
-    const Share sh = share_of(a, b, true);
-    const int x0 = sh.start / chunk, n = sh.tiles ? (sh.start + sh.tiles - 1) / chunk - x0 + 1 : 0;
+    Row rows(a);
+    const Share sh = rows.find(b, true);
+    const int x0 = sh.start / rows.chunk, n = sh.tiles ? (sh.start + sh.tiles - 1) / rows.chunk - x0 + 1 : 0;
     if (n == 1) return;
     const int64_t at0 = ((int64_t)(x0 + b) * a.pool.heads + h) * a.cols + col, step = (int64_t)a.pool.heads * a.cols;
     float m = kNegInf, l = 0.0f;
@@ -632,15 +668,18 @@ __device__ __forceinline__ float sum16(float v) {  // over a row of sixteen lane
 // weight[token] = decay weight[token] + the sum of p over the columns, once maxima and sums are known.  Only the
 // keys are read again; the same instructions give the same scores.
 template <int D64, int NG, int NT>
-__global__ __launch_bounds__(kKvThreads, D64 * NT <= 4 ? 4 : 2) void weights_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kKvThreads, D64 * NG * NT <= 4 ? 4 : 2) void weights_kernel(AttnArgs a) {
     __shared__ __attribute__((aligned(16))) TileGrids<NG> all_grids[kKvWaves];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4, h = blockIdx.y;
     TileGrids<NG> &grids = all_grids[wave];
-    const int total = total_tiles(a), chunk = chunk_of(a, total);
-    int from = blockIdx.x * chunk;
-    const int to = min(from + chunk, total);
+    int from, to;
+    {
+        const Row rows(a);
+        from = blockIdx.x * rows.chunk;
+        to = min(from + rows.chunk, rows.total);
+    }
     while (from < to) {
-        const Share sh = share_of(a, from, false);
+        const Share sh = Row(a.seqs).find(from, false);
         const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
         const int t0 = from - sh.start, t1 = min(to - sh.start, sh.tiles), clear = sh.len - a.n + 1;
         for (int col0 = 0; col0 < a.cols; col0 += 16 * NT) {
@@ -650,6 +689,7 @@ __global__ __launch_bounds__(kKvThreads, D64 * NT <= 4 ? 4 : 2) void weights_ker
             for (int c = 0; c < NT; ++c) {
                 const int col = col0 + 16 * c + r;
                 q[c].load(a, sh.b, h, sh.len, col);
+                q[c].prepare(a);
                 const float2 v = col < a.cols ? a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col] : make_float2(0.0f, 0.0f);
                 base[c] = v.x == kNegInf ? 0.0f : v.x;
                 inv[c] = v.y;  // 0 where nothing is seen
@@ -706,7 +746,7 @@ Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_le
     p.nt = cols > 16 && c.head_dim <= 128 ? 2 : 1;  // two tiles of larger heads do not fit the registers
     const int64_t tiles = ceil_div(max_len, kKvTile), blocks = c.n_heads * ceil_div(cols, 16 * p.nt);
     // as many workgroups as the chip holds at once, but no more than combine_kernel takes of one sequence
-    p.target = (int)std::min<int64_t>(1000, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, 1, p.nt) / blocks));
+    p.target = (int)std::min<int64_t>(1000, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, kv_pool(c).groups, p.nt) / blocks));
     p.direct = tiles <= kKvLeast;
     const int64_t all = std::max<int64_t>(1, n_seq * tiles);
     p.items = (int)(p.direct ? n_seq : std::min<int64_t>(p.target, ceil_div(all, kKvLeast)));

@@ -57,6 +57,17 @@ struct KvSeqs {
 __device__ __forceinline__ float grid_scale_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float grid_zero_of(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }  // 8 - z
 
+// The inclusive sum over the lanes up to this one, by DPP row shifts and broadcasts.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
+    return v;
+}
+
 KvPool kv_pool(const gptq_kv_cache &c);
 
 }  // namespace gptq

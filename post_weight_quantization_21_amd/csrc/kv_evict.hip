@@ -33,17 +33,6 @@ __device__ __forceinline__ u32x4 ranks_at(const EvictArgs &a, const int32_t *row
     return (u32x4){rank_of(w[0]), rank_of(w[1]), rank_of(w[2]), rank_of(w[3])};
 }
 
-// The inclusive sum over the lanes up to this one, by DPP row shifts and broadcasts.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, true);  // row_shr 1, 2, 4, 8
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, true);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast 15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast 31 into rows 2 and 3
-    return v;
-}
-
 // The rank of the `heavy`-th largest of the slots below `safe`, digit by digit from the highest (11, 11 and 10 bits, a
 // histogram of each), then the kept slots in order: all above that rank, and of those at it the first ones.  Ranks stay in
 // LDS where they fit, `in_lds` of them (a multiple of four); a wave walks slots next to each other, so that order is a matter
