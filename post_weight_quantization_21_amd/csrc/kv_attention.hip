@@ -317,10 +317,10 @@ struct Queries {
 
 __device__ __forceinline__ bool hidden(bool there, int slot, int sees) { return !there || slot >= sees; }
 
-// Scores of the lane's eight tokens in the columns, in log2 and less the columns' `base`, before any mask.
+// Scores (x of the queries in registers, or the lane's part of what share_queries() left in LDS) of the lane's eight tokens in the columns, in log2 and less the columns' `base`, before any mask.
 template <int D64, int NG, int NT>
 __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile, const TileGrids<NG> &grids, const Queries<D64, NG> q[NT],
-                                       const float base[NT]) {
+                                       const f16x8 *shared, const float base[NT]) {
     constexpr int KW = 2 * D64, SG = KW / NG;  // matrix instructions of a group
     const int kb = (threadIdx.x & 63) >> 4;
 #pragma unroll
@@ -332,18 +332,23 @@ __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile
             for (int w = g * SG; w < (g + 1) * SG; ++w) {
                 const f16x8 kf = key_frag(tile.k[t][w]);
 #pragma unroll
-                for (int c = 0; c < NT; ++c) acc[c] = mma(kf, q[c].x[w], acc[c]);
+                for (int c = 0; c < NT; ++c) acc[c] = mma(kf, shared ? shared[(c * KW + w) * kWave] : q[c].x[w], acc[c]);
             }
             const floatx4 scale = grids.scales(0, g, kb, t);
             const f16x8 zero = grids.zeros(0, g, kb);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < NT; ++c)
-                    s[c][4 * t + i] = fmaf(scale[i] * q[c].scale, fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]),
-                                           g == 0 ? -base[c] : s[c][4 * t + i]);
+                for (int c = 0; c < NT; ++c) {  // (kCode in acc and sum leaves room for any scale)
+                    const float v = fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]);
+                    s[c][4 * t + i] = g == 0 ? scale[i] * v : fmaf(scale[i], v, s[c][4 * t + i]);
+                }
             keep_order();  // fragments and grids of one group at a time: registers
         }
+#pragma unroll
+    for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[c][i] = fmaf(s[c][i], q[c].scale, -base[c]);
 }
 
 // A wave's sums over its tiles of a segment.
@@ -476,17 +481,20 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
     }
 }
 
+// Whether the queries stay in LDS, where registers are short.
+constexpr bool queries_in_lds(int D64, int NG, int NT) { return D64 * NG * NT >= 16; }
 // Waves of a SIMD that the registers of a kernel allow (of 512, in steps of eight): its sums take 16 D64 NT, its queries
 // 8 D64 NT, a tile 9 D64.
 constexpr int occupancy(int D64, int NG, int NT) {
     if (D64 * NT == 1 || (D64 == 2 && NT == 1 && NG == 1)) return 4;
     if ((D64 == 2 && NT == 1) || (D64 == 1 && NG == 1)) return 3;
-    return D64 * NG * NT < 16 ? 2 : 1;
+    return D64 * NG * NT < 32 ? 2 : 1;
 }
 
 template <int D64, int NG, int NT>
 __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_kernel(AttnArgs a) {
     constexpr int D = 64 * D64;
+    constexpr bool kShared = queries_in_lds(D64, NG, NT);
     extern __shared__ __attribute__((aligned(16))) float smem[];  // [wave][column][D] of one column tile, then (m, l), then grids
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4;
     const int h = blockIdx.y, col0 = blockIdx.z * (16 * NT);
@@ -520,6 +528,18 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
         }
 #pragma unroll
         for (int c = 0; c < NT; ++c) q[c].prepare(a);
+        const f16x8 *shared = nullptr;
+        if constexpr (kShared) {  // all waves have the same ones
+            f16x8 *to = reinterpret_cast<f16x8 *>(smem + kKvWaves * (16 * (D + 2) + (int)(sizeof(TileGrids<NG>) / 4))) + lane;
+            if (wave == 0) {
+#pragma unroll
+                for (int c = 0; c < NT; ++c)
+#pragma unroll
+                    for (int w = 0; w < 2 * D64; ++w) to[(c * 2 * D64 + w) * kWave] = q[c].x[w];
+            }
+            __syncthreads();
+            shared = to;
+        }
         // The keys of the next tile are on their way during the second product, its values during the first of the next.
         while (tile < t1) {
             const int next = tile + kKvWaves;
@@ -535,7 +555,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
             grids.put(t.grid, sums.vscale, gone);
             wave_fence();
             float p[NT][8];
-            scores<D64, NG, NT>(p, t, grids, q, sums.base);
+            scores<D64, NG, NT>(p, t, grids, q, shared, sums.base);
             if (next < t1) t.load_keys(a, coming, next, h);
             const int slot = tile * kKvTile + 8 * kb;
             const bool there = (kb < 2 ? pages.lo : pages.hi) >= 0;
@@ -705,7 +725,7 @@ __global__ __launch_bounds__(kKvThreads, D64 * NG * NT <= 4 ? 4 : 2) void weight
                 float p[NT][8], w[8] = {};
                 grids.put(t.grid, 1.0f, false);
                 wave_fence();
-                scores<D64, NG, NT>(p, t, grids, q, base);
+                scores<D64, NG, NT>(p, t, grids, q, nullptr, base);
                 if (next < t1) t.load_keys(a, coming, next, h);
                 if ((tile + 1) * kKvTile > clear || pages.missing()) {
 #pragma unroll
@@ -759,7 +779,7 @@ Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_le
 
 template <int D64, int NG, int NT>
 hipError_t launch_tiles(AttnArgs a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
-    const size_t lds = (size_t)kKvWaves * (16 * (64 * D64 * 4 + 8) + sizeof(TileGrids<NG>));
+    const size_t lds = (size_t)kKvWaves * (16 * (64 * D64 * 4 + 8) + sizeof(TileGrids<NG>)) + (queries_in_lds(D64, NG, NT) ? (size_t)NT * 2 * D64 * 1024 : 0);
     attention_kernel<D64, NG, NT><<<dim3((unsigned)p.items, (unsigned)a.pool.heads, (unsigned)ceil_div(a.cols, 16 * NT)), kKvThreads, lds, s>>>(a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
