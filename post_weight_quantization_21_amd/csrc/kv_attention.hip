@@ -31,6 +31,7 @@ constexpr int kKvTile = 32;   // tokens of a tile
 constexpr int kKvWaves = 4;   // waves of a workgroup, each with tiles of its own
 constexpr int kKvThreads = kKvWaves * kWave;
 constexpr int kKvLeast = 4;   // tiles of a workgroup at least
+constexpr int kMostSegments = 1024;  // of a sequence
 constexpr float kSlack = 6.0f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -43,11 +44,12 @@ struct AttnArgs {
     int64_t ldo;
     float *part;   // [segment][head][column][D], unnormalized, relative to the segment's maximum
     float2 *stat;  // [segment][head][column]: maximum (of log2) and sum
-    float2 *last;  // [sequence][head][column]: maximum and 1 / sum over all of a sequence, or NULL
+    float2 *last;  // [sequence][head][column]: maximum and sum of a sequence of one segment, or NULL
     float scale;   // times log2 e
     float decay;
     int32_t n, group, cols;  // new tokens, query heads of a kv head, n * group
     int32_t target;  // workgroups that share the tiles
+    int32_t weigh_target, weigh_tiles;  // those that weigh tokens; column tiles that they hold
     int32_t bf16, direct;
 };
 
@@ -163,18 +165,20 @@ struct Tile {
             }
         }
     }
+    // With the grids of the values, or those of the keys in all lanes.
+    template <bool kBoth>
     __device__ __forceinline__ void load_keys(const AttnArgs &a, TilePages p, int tile, int h) {
         const char *k0 = reinterpret_cast<const char *>(a.pool.k);
         if (a.pool.lg_page > 4) {  // one page: its base is the same for all lanes
             const int lane = threadIdx.x & 63, r = lane & 15, kb = lane >> 4, row = 8 * (r >> 2) + (r & 3), tok = lane & 31;
-            const char *g0 = reinterpret_cast<const char *>(lane < 32 ? a.pool.k_grid : a.pool.v_grid);
+            const char *g0 = reinterpret_cast<const char *>(!kBoth || lane < 32 ? a.pool.k_grid : a.pool.v_grid);
             const int64_t first = a.pool.first(max(p.lo, 0), h), in = tile * kKvTile & (a.pool.page() - 1);
             key_words(k0 + (first + in) * (D / 2), row * (D / 2) + kb * KW * 4);
 #pragma unroll
             for (int g = 0; g < NG; ++g) grid[g] = *at<uint32_t>(g0 + (first * NG + in) * 4, 4 * tok + ((uint32_t)g << (a.pool.lg_page + 2)));
         } else {
             const int lane = fresh_thread() & 63, r = lane & 15, kb = lane >> 4, row = 8 * (r >> 2) + (r & 3), tok = lane & 31;
-            const char *g0 = reinterpret_cast<const char *>(lane < 32 ? a.pool.k_grid : a.pool.v_grid);
+            const char *g0 = reinterpret_cast<const char *>(!kBoth || lane < 32 ? a.pool.k_grid : a.pool.v_grid);
             const int64_t fk = a.pool.first(max(r < 8 ? p.lo : p.hi, 0), h), fg = a.pool.first(max(tok < 16 ? p.lo : p.hi, 0), h);
             key_words(k0 + fk * (D / 2), (row & 15) * (D / 2) + kb * KW * 4);
 #pragma unroll
@@ -204,15 +208,19 @@ struct TileGrids {
     float scale[2][NG][kKvTile];
     uint16_t zero[2][NG][kKvTile];
 
-    __device__ __forceinline__ void put(const uint32_t grid[NG], float vscale, bool gone) {
+    // `none`: of the upper lanes, those whose token has a value that is no number.  It makes the token's scores no numbers,
+    // and so what sees them; to the others it is 0, since p = 0 does not make a product with it 0.
+    __device__ __forceinline__ void put(const uint32_t grid[NG], float vscale, bool gone, uint64_t none) {
         const int lane = threadIdx.x & 63, side = lane >> 5, tok = lane & 31;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float s = grid_scale_of(grid[g]);
+            float s = grid_scale_of(grid[g]);
+            const bool odd = !(s == s);
             const _Float16 c = __builtin_bit_cast(f16x2, grid[g])[0];
-            scale[side][g][tok] = gone ? 0.0f : side ? s * vscale : s;
-            // a column that does not see a token multiplies its zero by p = 0: it must be a number
-            zero[side][g][tok] = __builtin_bit_cast(uint16_t, gone || !(s == s) ? (_Float16)0.0f : c - (_Float16)8.0f);
+            if (side) s = odd ? 0.0f : s * vscale;
+            if (none && !side && (none >> (32 + tok) & 1)) s = __builtin_nanf("");
+            scale[side][g][tok] = gone ? 0.0f : s;
+            zero[side][g][tok] = __builtin_bit_cast(uint16_t, gone || odd ? (_Float16)0.0f : c - (_Float16)8.0f);
         }
     }
     // Eight tokens of block kb; t: four of them.
@@ -461,7 +469,7 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
                 if (!whole)
                     a.stat[stat + r] = make_float2(m, all);
                 else if (a.last)
-                    a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col0 + 16 * c + r] = make_float2(m, inv);
+                    a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col0 + 16 * c + r] = make_float2(m, all);
             }
         }
         __syncthreads();
@@ -487,7 +495,7 @@ constexpr bool queries_in_lds(int D64, int NG, int NT) { return D64 * NG * NT >=
 // 8 D64 NT, a tile 9 D64.
 constexpr int occupancy(int D64, int NG, int NT) {
     if (D64 * NT == 1 || (D64 == 2 && NT == 1 && NG == 1)) return 4;
-    if ((D64 == 2 && NT == 1) || (D64 == 1 && NG == 1)) return 3;
+    if ((D64 == 2 && NT == 1 && NG == 2) || (D64 == 1 && NG == 1)) return 3;
     return D64 * NG * NT < 32 ? 2 : 1;
 }
 
@@ -523,7 +531,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
         Tile<D64, NG> t;
         TilePages pages = {a, row, max(min(tile, t1 - 1), 0), sh.len};
         if (tile < t1) {
-            t.load_keys(a, pages, tile, h);
+            t.template load_keys<true>(a, pages, tile, h);
             t.load_values(a, pages, tile, h);
         }
 #pragma unroll
@@ -547,16 +555,21 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
             const bool masked = (tile + 1) * kKvTile > clear || pages.missing();
             const bool gone = masked && hidden(((lane & 16) ? pages.hi : pages.lo) >= 0, tile * kKvTile + (lane & 31), sh.len);
             float most = 0.0f;
+            bool odd = false;
             if (lane >= 32 && !gone) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) most = fmaxf(most, grid_scale_of(t.grid[g]));
+                for (int g = 0; g < NG; ++g) {
+                    const float s = grid_scale_of(t.grid[g]);
+                    most = fmaxf(most, s);
+                    odd |= !(s == s);
+                }
             }
             if (__any(most > 4.0f * sums.vmax)) sums.raise_values(most);
-            grids.put(t.grid, sums.vscale, gone);
+            grids.put(t.grid, sums.vscale, gone, __ballot(odd));
             wave_fence();
             float p[NT][8];
             scores<D64, NG, NT>(p, t, grids, q, shared, sums.base);
-            if (next < t1) t.load_keys(a, coming, next, h);
+            if (next < t1) t.template load_keys<true>(a, coming, next, h);
             const int slot = tile * kKvTile + 8 * kb;
             const bool there = (kb < 2 ? pages.lo : pages.hi) >= 0;
             if (masked) {
@@ -592,10 +605,6 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
                     float ps[8];
 #pragma unroll
                     for (int i = 0; i < 8; ++i) ps[i] = p[c][i] * (i < 4 ? s0[i] : s1[i - 4]);
-                    if (masked) {  // a value that a column does not see may be no number
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) ps[i] = p[c][i] == 0.0f ? 0.0f : ps[i];
-                    }
                     u32x4 w;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -628,26 +637,33 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
     }
 }
 
-// Sequences of several segments, or of none: a workgroup per column, whose threads take four dims of every kLanes-th segment.
+// The segments of a sequence: the first, and how many.
+struct Segments {
+    int first, n;
+    __device__ __forceinline__ Segments(const Share &sh, int chunk)
+        : first(sh.start / chunk + sh.b), n(sh.tiles ? (sh.start + sh.tiles - 1) / chunk - sh.start / chunk + 1 : 0) {}
+};
+
+// The result of a column of a sequence with several segments, or none, by a workgroup: a thread takes four dims of every
+// kLanes-th segment (five rows of 48 threads for heads of 192).
 template <int D64>
-__global__ __launch_bounds__(kKvThreads) void combine_kernel(AttnArgs a) {
-    constexpr int D = 64 * D64, kRow = D / 4, kLanes = kKvThreads / kRow, kMost = 1024;  // D = 192: 5 rows, 16 idle threads
-    __shared__ float share[kMost];
+__device__ __forceinline__ void combine(const AttnArgs &a, int col, int h, int b) {
+    constexpr int D = 64 * D64, kRow = D / 4, kLanes = kKvThreads / kRow;
+    __shared__ float share[kMostSegments];
     __shared__ float red[2][kKvWaves];
     __shared__ floatx4 sums[kKvThreads];
-    const int col = blockIdx.x, h = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     Row rows(a);
-    const Share sh = rows.find(b, true);
-    const int x0 = sh.start / rows.chunk, n = sh.tiles ? (sh.start + sh.tiles - 1) / rows.chunk - x0 + 1 : 0;
-    if (n == 1) return;
-    const int64_t at0 = ((int64_t)(x0 + b) * a.pool.heads + h) * a.cols + col, step = (int64_t)a.pool.heads * a.cols;
+    const Segments seg(rows.find(b, true), rows.chunk);
+    if (seg.n == 1) return;
+    const int64_t at0 = ((int64_t)seg.first * a.pool.heads + h) * a.cols + col, step = (int64_t)a.pool.heads * a.cols;
     float m = kNegInf, l = 0.0f;
-    for (int x = threadIdx.x; x < n; x += kKvThreads) m = fmaxf(m, a.stat[at0 + x * step].x);
+    for (int x = threadIdx.x; x < seg.n; x += kKvThreads) m = fmaxf(m, a.stat[at0 + x * step].x);
     for (int o = 1; o < kWave; o *= 2) m = xor_max(m, o);
     if (lane == 0) red[0][wave] = m;
     __syncthreads();
     for (int w = 0; w < kKvWaves; ++w) m = fmaxf(m, red[0][w]);
-    for (int x = threadIdx.x; x < n; x += kKvThreads) {
+    for (int x = threadIdx.x; x < seg.n; x += kKvThreads) {
         const float2 v = a.stat[at0 + x * step];
         const float f = share_in(v.x, m);
         share[x] = f;
@@ -662,7 +678,7 @@ __global__ __launch_bounds__(kKvThreads) void combine_kernel(AttnArgs a) {
     floatx4 o = {};
     if (mine < kLanes) {
 #pragma unroll 4
-        for (int x = mine; x < n; x += kLanes) o += share[x] * *reinterpret_cast<const floatx4 *>(a.part + (at0 + x * step) * D + 4 * d4);
+        for (int x = mine; x < seg.n; x += kLanes) o += share[x] * *reinterpret_cast<const floatx4 *>(a.part + (at0 + x * step) * D + 4 * d4);
     }
     sums[threadIdx.x] = o;
     __syncthreads();
@@ -672,82 +688,151 @@ __global__ __launch_bounds__(kKvThreads) void combine_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) to[i] = result16(a, l == 0.0f ? 0.0f : o[i] / l);
     }
-    if (threadIdx.x == 0 && a.last) a.last[((int64_t)b * a.pool.heads + h) * a.cols + col] = make_float2(m, l == 0.0f ? 0.0f : 1.0f / l);
+}
+template <int D64>
+__global__ __launch_bounds__(kKvThreads) void combine_kernel(AttnArgs a) {
+    combine<D64>(a, blockIdx.x, blockIdx.y, blockIdx.z);
 }
 
-__device__ __forceinline__ float sum16(float v) {  // over a row of sixteen lanes
-    auto turned = [](float x, auto n) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x120 + decltype(n)::value, 0xF, 0xF, true));  // row_ror
-    };
-    v += turned(v, std::integral_constant<int, 8>());
-    v += turned(v, std::integral_constant<int, 4>());
-    v += turned(v, std::integral_constant<int, 2>());
-    return v + turned(v, std::integral_constant<int, 1>());
+template <int kCtrl>
+__device__ __forceinline__ float lane_of(float v) {  // of the lane that a DPP control names
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kCtrl, 0xF, 0xF, true));
+}
+// Eight sums over a row of sixteen lanes, of which lane r has number r / 2: at each step a lane keeps half of the numbers
+// and hands the others to a lane that keeps those.
+__device__ __forceinline__ float row_sums(const float w[8], int r) {
+    float u[4], v[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = (r & 8 ? w[i + 4] : w[i]) + lane_of<0x128>(r & 8 ? w[i] : w[i + 4]);  // row_ror:8
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = (r & 4 ? u[i + 2] : u[i]) + lane_of<0x141>(r & 4 ? u[i] : u[i + 2]);  // row_half_mirror
+    const float z = (r & 2 ? v[1] : v[0]) + lane_of<0x4E>(r & 2 ? v[0] : v[1]);  // quad_perm 2 3 0 1
+    return z + lane_of<0xB1>(z);  // quad_perm 1 0 3 2
 }
 
-// weight[token] = decay weight[token] + the sum of p over the columns, once maxima and sums are known.  Only the
-// keys are read again; the same instructions give the same scores.
-template <int D64, int NG, int NT>
-__global__ __launch_bounds__(kKvThreads, D64 * NG * NT <= 4 ? 4 : 2) void weights_kernel(AttnArgs a) {
-    __shared__ __attribute__((aligned(16))) TileGrids<NG> all_grids[kKvWaves];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4, h = blockIdx.y;
-    TileGrids<NG> &grids = all_grids[wave];
-    int from, to;
+// What a column needs beside its queries.
+template <int NG>
+struct Column {
+    float sum[NG], scale, base, inv;  // inv: 1 / the sum of exp; 0 where nothing is seen, or there is no column
+    int sees;
+};
+constexpr int kWeighTiles = 8;  // column tiles of a pass over the tokens
+template <int D64, int NG>
+constexpr int weigh_bytes(int tiles) {
+    return kKvWaves * (int)sizeof(TileGrids<NG>) + tiles * (2 * D64 * 1024 + 16 * (int)sizeof(Column<NG>));
+}
+
+// weight[token] = decay weight[token] + the sum of p over the columns, once the columns' maxima and sums are known.  Only
+// the keys are read again; the same instructions give the same scores.  The queries are in LDS, up to kWeighTiles tiles of
+// them, and each of the wave's tiles of tokens goes through all; more columns take further passes.
+template <int D64, int NG>
+__device__ __forceinline__ void weigh(const AttnArgs &a, int item, int h, unsigned char *smem) {
+    constexpr int KW = 2 * D64;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4;
+    TileGrids<NG> &grids = reinterpret_cast<TileGrids<NG> *>(smem)[wave];
+    f16x8 *frags = reinterpret_cast<f16x8 *>(smem + kKvWaves * sizeof(TileGrids<NG>));
+    Column<NG> *columns = reinterpret_cast<Column<NG> *>(frags + a.weigh_tiles * KW * kWave);
+    int from, to, chunk;
     {
         const Row rows(a);
-        from = blockIdx.x * rows.chunk;
-        to = min(from + rows.chunk, rows.total);
+        chunk = rows.chunk;
+        const int c = (rows.total + a.weigh_target - 1) / a.weigh_target, mine = (c + kKvWaves - 1) / kKvWaves * kKvWaves;
+        from = item * mine;
+        to = min(from + mine, rows.total);
     }
     while (from < to) {
         const Share sh = Row(a.seqs).find(from, false);
+        const Segments seg(sh, chunk);
         const int32_t *row = a.seqs.table + (int64_t)sh.b * a.seqs.width;
         const int t0 = from - sh.start, t1 = min(to - sh.start, sh.tiles), clear = sh.len - a.n + 1;
-        for (int col0 = 0; col0 < a.cols; col0 += 16 * NT) {
-            Queries<D64, NG> q[NT];
-            float base[NT], inv[NT];
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
+        for (int col0 = 0; col0 < a.cols; col0 += 16 * kWeighTiles) {
+            const int tiles = min((a.cols - col0 + 15) / 16, kWeighTiles);
+            __syncthreads();  // the last pass has read its columns
+            for (int c = wave; c < tiles; c += kKvWaves) {
                 const int col = col0 + 16 * c + r;
-                q[c].load(a, sh.b, h, sh.len, col);
-                q[c].prepare(a);
-                const float2 v = col < a.cols ? a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col] : make_float2(0.0f, 0.0f);
-                base[c] = v.x == kNegInf ? 0.0f : v.x;
-                inv[c] = v.y;  // 0 where nothing is seen
+                Queries<D64, NG> q;
+                q.load(a, sh.b, h, sh.len, col);
+                float m = kNegInf, l = 0.0f;
+                if (a.direct || seg.n == 1) {
+                    if (col < a.cols) {
+                        const float2 v = a.last[((int64_t)sh.b * a.pool.heads + h) * a.cols + col];
+                        m = v.x, l = v.y;
+                    }
+                } else {
+                    const int64_t at0 = ((int64_t)seg.first * a.pool.heads + h) * a.cols + min(col, a.cols - 1), step = (int64_t)a.pool.heads * a.cols;
+                    for (int x = kb; x < seg.n; x += 4) m = fmaxf(m, a.stat[at0 + x * step].x);
+                    m = xor_max(xor_max(m, 16), 32);
+                    for (int x = kb; x < seg.n; x += 4) {
+                        const float2 v = a.stat[at0 + x * step];
+                        l += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - m);
+                    }
+                    l = xor_add(xor_add(l, 16), 32);
+                }
+                q.prepare(a);
+#pragma unroll
+                for (int w = 0; w < KW; ++w) frags[(c * KW + w) * kWave + lane] = q.x[w];
+                if (kb == 0) {
+                    Column<NG> &k = columns[16 * c + r];
+#pragma unroll
+                    for (int g = 0; g < NG; ++g) k.sum[g] = q.sum[g];
+                    k.scale = q.scale;
+                    k.base = m == kNegInf ? 0.0f : m;
+                    k.inv = l == 0.0f || col >= a.cols ? 0.0f : 1.0f / l;
+                    k.sees = q.sees;
+                }
             }
+            __syncthreads();
+            const float decay = col0 ? 1.0f : a.decay;
+            // the token whose weight this lane has in the end, of the tile's page
+            const int mine = 8 * kb + (r >> 1);
+            auto weight_of = [&](TilePages p, int tile) {
+                const int page = kb < 2 ? p.lo : p.hi, slot = tile * kKvTile + mine;
+                return page < 0 || slot >= sh.len || (r & 1) ? nullptr : a.pool.weight + a.pool.first(page, h) + (slot & (a.pool.page() - 1));
+            };
             int tile = t0 + wave;
             Tile<D64, NG> t;
             TilePages pages = {a, row, min(tile, t1 - 1), sh.len};
-            if (tile < t1) t.load_keys(a, pages, tile, h);
+            float *at = nullptr, old = 0.0f;
+            if (tile < t1) {
+                t.template load_keys<false>(a, pages, tile, h);
+                at = weight_of(pages, tile);
+                if (at && decay != 0.0f) old = *at;
+            }
             while (tile < t1) {
                 const int next = tile + kKvWaves;
                 const TilePages coming = {a, row, min(next, t1 - 1), sh.len};
-                const int slot = tile * kKvTile + 8 * kb, page = kb < 2 ? pages.lo : pages.hi;
-                float p[NT][8], w[8] = {};
-                grids.put(t.grid, 1.0f, false);
+                const int slot = tile * kKvTile + 8 * kb;
+                const bool masked = (tile + 1) * kKvTile > clear || pages.missing(), there = (kb < 2 ? pages.lo : pages.hi) >= 0;
+                float w[8] = {};
+                grids.put(t.grid, 1.0f, false, 0);
                 wave_fence();
-                scores<D64, NG, NT>(p, t, grids, q, nullptr, base);
-                if (next < t1) t.load_keys(a, coming, next, h);
-                if ((tile + 1) * kKvTile > clear || pages.missing()) {
+                for (int c = 0; c < tiles; ++c) {
+                    const Column<NG> &k = columns[16 * c + r];
+                    Queries<D64, NG> q;
 #pragma unroll
-                    for (int c = 0; c < NT; ++c)
+                    for (int g = 0; g < NG; ++g) q.sum[g] = k.sum[g];
+                    q.scale = k.scale;
+                    const float base = k.base, inv = k.inv;
+                    float p[1][8];
+                    scores<D64, NG, 1>(p, t, grids, &q, frags + c * KW * kWave + lane, &base);
+                    if (masked) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            if (hidden(page >= 0, slot + i, q[c].sees)) p[c][i] = kNegInf;
+                            if (hidden(there, slot + i, k.sees)) p[0][i] = kNegInf;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] += inv != 0.0f ? __builtin_amdgcn_exp2f(p[0][i]) * inv : 0.0f;
                 }
-#pragma unroll
-                for (int c = 0; c < NT; ++c)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)  // columns that are none see nothing
-                        w[i] += col0 + 16 * c + r < a.cols ? __builtin_amdgcn_exp2f(p[c][i]) * inv[c] : 0.0f;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = sum16(w[i]);
-                if (r == 0 && page >= 0) {
-                    float *to = a.pool.weight + a.pool.first(page, h) + (slot & (a.pool.page() - 1));
-                    const float old = col0 ? 1.0f : a.decay;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (slot + i < sh.len) to[i] = old == 0.0f ? w[i] : fmaf(old, to[i], w[i]);
+                float *const here = at;
+                const float before = old;
+                at = nullptr;
+                if (next < t1) {
+                    t.template load_keys<false>(a, coming, next, h);
+                    at = weight_of(coming, next);
+                    if (at && decay != 0.0f) old = *at;
                 }
+                const float sum = row_sums(w, r);
+                if (here) *here = decay == 0.0f ? sum : fmaf(decay, before, sum);
                 tile = next;
                 pages = coming;
             }
@@ -755,9 +840,22 @@ __global__ __launch_bounds__(kKvThreads, D64 * NG * NT <= 4 ? 4 : 2) void weight
         from += t1 - t0;
     }
 }
+// The two together: the first `combining` workgroups join the segments' results, the others weigh tokens.
+template <int D64, int NG>
+__global__ __launch_bounds__(kKvThreads, D64 == 4 ? (NG < 4 ? 3 : 2) : (D64 * NG <= 4 ? 4 : 3)) void finish_kernel(AttnArgs a, int combining) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char finish_smem[];
+    int x = blockIdx.x;
+    if (x < combining) {
+        const int col = x % a.cols, y = x / a.cols;
+        combine<D64>(a, col, y % a.pool.heads, y / a.pool.heads);
+    } else {
+        x -= combining;
+        weigh<D64, NG>(a, x / a.pool.heads, x % a.pool.heads, finish_smem);
+    }
+}
 
 struct Plan {
-    int nt, items, target;
+    int nt, items, target, weigh_items, weigh_target;
     bool direct;
     size_t part, stat, last;  // bytes
 };
@@ -765,11 +863,13 @@ Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_le
     Plan p;
     p.nt = cols > 16 && c.head_dim <= 128 ? 2 : 1;  // two tiles of larger heads do not fit the registers
     const int64_t tiles = ceil_div(max_len, kKvTile), blocks = c.n_heads * ceil_div(cols, 16 * p.nt);
-    // as many workgroups as the chip holds at once, but no more than combine_kernel takes of one sequence
-    p.target = (int)std::min<int64_t>(1000, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, kv_pool(c).groups, p.nt) / blocks));
+    // as many workgroups as the chip holds at once, but no more than combine() takes of one sequence
+    p.target = (int)std::min<int64_t>(kMostSegments, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, kv_pool(c).groups, p.nt) / blocks));
     p.direct = tiles <= kKvLeast;
     const int64_t all = std::max<int64_t>(1, n_seq * tiles);
     p.items = (int)(p.direct ? n_seq : std::min<int64_t>(p.target, ceil_div(all, kKvLeast)));
+    p.weigh_target = (int)std::max<int64_t>(1, 256 * 4 / c.n_heads);
+    p.weigh_items = (int)std::min<int64_t>(p.weigh_target, ceil_div(all, kKvWaves));
     const size_t rows = (size_t)c.n_heads * cols, segments = p.direct ? 0 : rows * (p.items + n_seq);
     p.part = align_up(segments * c.head_dim * 4, 256);
     p.stat = align_up(segments * 8, 256);
@@ -781,17 +881,15 @@ template <int D64, int NG, int NT>
 hipError_t launch_tiles(AttnArgs a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
     const size_t lds = (size_t)kKvWaves * (16 * (64 * D64 * 4 + 8) + sizeof(TileGrids<NG>)) + (queries_in_lds(D64, NG, NT) ? (size_t)NT * 2 * D64 * 1024 : 0);
     attention_kernel<D64, NG, NT><<<dim3((unsigned)p.items, (unsigned)a.pool.heads, (unsigned)ceil_div(a.cols, 16 * NT)), kKvThreads, lds, s>>>(a);
-    hipError_t e = hipGetLastError();
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    if (!p.direct) {
-        combine_kernel<D64><<<dim3((unsigned)a.cols, (unsigned)a.pool.heads, (unsigned)n_seq), kKvThreads, 0, s>>>(a);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
     if (weights) {
-        weights_kernel<D64, NG, NT><<<dim3((unsigned)p.items, (unsigned)a.pool.heads), kKvThreads, 0, s>>>(a);
-        e = hipGetLastError();
+        const int combining = p.direct ? 0 : a.cols * a.pool.heads * n_seq;
+        finish_kernel<D64, NG><<<dim3((unsigned)(combining + p.weigh_items * a.pool.heads)), kKvThreads, (size_t)weigh_bytes<D64, NG>(a.weigh_tiles), s>>>(a, combining);
+    } else if (!p.direct) {
+        combine_kernel<D64><<<dim3((unsigned)a.cols, (unsigned)a.pool.heads, (unsigned)n_seq), kKvThreads, 0, s>>>(a);
     }
-    return e;
+    return hipGetLastError();
 }
 template <int D64, int NG>
 hipError_t launch_attention(const AttnArgs &a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
@@ -828,6 +926,8 @@ hipError_t run_kv_attention(const void *Q, gptq_dtype dt, int64_t n_seq, int64_t
     a.scale = scale * 1.44269504088896340736f;
     a.decay = decay;
     a.target = p.target;
+    a.weigh_target = p.weigh_target;
+    a.weigh_tiles = (int)std::min<int64_t>(ceil_div(a.cols, 16), kWeighTiles);
     a.bf16 = dt == GPTQ_DT_BF16;
     a.direct = p.direct;
     const int ng = a.pool.groups;
