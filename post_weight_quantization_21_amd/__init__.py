@@ -747,13 +747,13 @@ def kv_append(K, V, cache: KVCache, table, lens, offs=None, values=False, K_out=
             raise ValueError("K_out must have K's shape and type")
         ldko = _kv_pitch(K_out, heads, dim, dev, "K_out")
     elif values:
-        K_out = torch.empty(shape, dtype=dtype, device=dev)
+        K_out = K.new_empty(shape)
     if V_out is not None:
         if V_out.shape != shape or V_out.dtype is not dtype:
             raise ValueError("V_out must have V's shape and type")
         ldvo = _kv_pitch(V_out, heads, dim, dev, "V_out")
     elif values:
-        V_out = torch.empty(shape, dtype=dtype, device=dev)
+        V_out = K.new_empty(shape)
     if K_out is not None:
         kp = K_out.data_ptr()
     if V_out is not None:
@@ -789,7 +789,7 @@ def kv_attention(Q, cache: KVCache, table, lens, scale=None, max_len=None, decay
     if rows != n_seq:
         raise ValueError("Q, table and lens must have the same number of sequences")
     if O is None:
-        O = torch.empty(shape, dtype=dtype, device=dev)
+        O = Q.new_empty(shape)
         ldo = q_heads * dim
     else:
         if O.shape != shape or O.dtype is not dtype:
@@ -827,12 +827,12 @@ def kv_evict(cache: KVCache, table, lens, to, budget: int, recent: int = 0, max_
     if budget < 1:
         raise ValueError("budget must be at least 1")
     if kept is None:
-        kept = torch.empty((n_seq, heads, budget), dtype=torch.int32, device=dev)
+        kept = lens.new_empty((n_seq, heads, budget))
         kp = kept.data_ptr()
     else:
         kp = _kv_ints(kept, (n_seq, heads, budget), dev, "kept", torch)
     if new_lens is None:
-        new_lens = torch.empty((n_seq,), dtype=torch.int32, device=dev)
+        new_lens = lens.new_empty((n_seq,))
         np_ = new_lens.data_ptr()
     else:
         np_ = _kv_ints(new_lens, (n_seq,), dev, "new_lens", torch)

@@ -30,7 +30,6 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 constexpr int kKvTile = 32;   // tokens of a tile
 constexpr int kKvWaves = 4;   // waves of a workgroup, each with tiles of its own
 constexpr int kKvThreads = kKvWaves * kWave;
-constexpr int kKvLeast = 4;   // tiles of a workgroup at least
 constexpr int kMostSegments = 1024;  // of a sequence
 constexpr float kSlack = 6.0f;
 constexpr float kNegInf = -__builtin_inff();
@@ -47,8 +46,8 @@ struct AttnArgs {
     float2 *last;  // [sequence][head][column]: maximum and sum of a sequence of one segment, or NULL
     float scale;   // times log2 e
     float decay;
-    int32_t n, group, cols;  // new tokens, query heads of a kv head, n * group
-    int32_t target;  // workgroups that share the tiles
+    int32_t n, group, cols, kept_cols;  // new tokens, query heads of a kv head, n * group; the columns of a tile in LDS
+    int32_t target, least;  // workgroups that share the tiles; tiles of one at least
     int32_t weigh_target, weigh_tiles;  // those that weigh tokens; column tiles that they hold
     int32_t bf16, direct;
 };
@@ -96,7 +95,7 @@ struct Row {
             total += __builtin_amdgcn_readlane(upto, kWave - 1);
         }
         const int c = (total + a.target - 1) / a.target;
-        chunk = max(kKvLeast, (c + kKvWaves - 1) / kKvWaves * kKvWaves);
+        chunk = max(a.least, (c + kKvWaves - 1) / kKvWaves * kKvWaves);
     }
     // The sequence that tile `at` of the row belongs to, or with `seq` sequence `at`.
     __device__ __forceinline__ Share find(int at, bool seq) {
@@ -179,7 +178,8 @@ struct Tile {
         } else {
             const int lane = fresh_thread() & 63, r = lane & 15, kb = lane >> 4, row = 8 * (r >> 2) + (r & 3), tok = lane & 31;
             const char *g0 = reinterpret_cast<const char *>(!kBoth || lane < 32 ? a.pool.k_grid : a.pool.v_grid);
-            const int64_t fk = a.pool.first(max(r < 8 ? p.lo : p.hi, 0), h), fg = a.pool.first(max(tok < 16 ? p.lo : p.hi, 0), h);
+            const int64_t lo = a.pool.first(max(p.lo, 0), h), hi = a.pool.first(max(p.hi, 0), h);
+            const int64_t fk = r < 8 ? lo : hi, fg = tok < 16 ? lo : hi;
             key_words(k0 + fk * (D / 2), (row & 15) * (D / 2) + kb * KW * 4);
 #pragma unroll
             for (int g = 0; g < NG; ++g) grid[g] = *at<uint32_t>(g0 + fg * (4 * NG), 4 * (tok & 15) + 64 * g);
@@ -194,7 +194,7 @@ struct Tile {
             for (int u = 0; u < D64; ++u) v[u] = *at<u32x4>(v0 + (first + in) * (D / 2), kb * 4 * D + r * 16 + 256 * u);
         } else {
             const int lane = fresh_thread() & 63, r = lane & 15, kb = lane >> 4;
-            const int64_t fv = a.pool.first(max(kb < 2 ? p.lo : p.hi, 0), h);
+            const int64_t lo = a.pool.first(max(p.lo, 0), h), hi = a.pool.first(max(p.hi, 0), h), fv = kb < 2 ? lo : hi;
 #pragma unroll
             for (int u = 0; u < D64; ++u) v[u] = *at<u32x4>(v0 + fv * (D / 2), (kb & 1) * 4 * D + r * 16 + 256 * u);
         }
@@ -351,7 +351,7 @@ __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile
                     const float v = fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]);
                     s[c][4 * t + i] = g == 0 ? scale[i] * v : fmaf(scale[i], v, s[c][4 * t + i]);
                 }
-            keep_order();  // fragments and grids of one group at a time: registers
+            if (NG == 1) keep_order();  // fragments and grids of one half at a time: registers
         }
 #pragma unroll
     for (int c = 0; c < NT; ++c)
@@ -437,7 +437,8 @@ template <int D64, int NG, int NT>
 __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG, NT> &s, const Share &sh, bool whole, float *smem, int h, int col0) {
     constexpr int D = 64 * D64;
     const int thread = fresh_thread(), lane = thread & 63, wave = thread >> 6, r = lane & 15, kb = lane >> 4;
-    float2 *ml = reinterpret_cast<float2 *>(smem + kKvWaves * 16 * D);
+    const int kept = a.kept_cols;  // of a tile in LDS
+    float2 *ml = reinterpret_cast<float2 *>(smem + kKvWaves * kept * D);
 #pragma unroll
     for (int c = 0; c < NT; ++c) {
         const int left = a.cols - col0 - 16 * c;  // columns there are
@@ -463,7 +464,7 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
                 const float k = xor_add(xor_add(s.corr[c][g], 16), 32) * kCode;
 #pragma unroll
                 for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d)
-                    *reinterpret_cast<floatx4 *>(smem + (wave * 16 + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f;
+                    *reinterpret_cast<floatx4 *>(smem + (wave * kept + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f;
             }
             if (wave == 0 && kb == 0) {
                 if (!whole)
@@ -477,7 +478,7 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
             const int cc = i / (D / 4), d = i % (D / 4) * 4;
             floatx4 o = *reinterpret_cast<const floatx4 *>(smem + cc * D + d);
 #pragma unroll
-            for (int w = 1; w < kKvWaves; ++w) o += *reinterpret_cast<const floatx4 *>(smem + (w * 16 + cc) * D + d);
+            for (int w = 1; w < kKvWaves; ++w) o += *reinterpret_cast<const floatx4 *>(smem + (w * kept + cc) * D + d);
             if (whole) {
                 uint16_t *to = a.o + result_at(a, sh.b, h, col0 + 16 * c + cc, D) + d;
 #pragma unroll
@@ -506,7 +507,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
     extern __shared__ __attribute__((aligned(16))) float smem[];  // [wave][column][D] of one column tile, then (m, l), then grids
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), r = lane & 15, kb = lane >> 4;
     const int h = blockIdx.y, col0 = blockIdx.z * (16 * NT);
-    TileGrids<NG> &grids = reinterpret_cast<TileGrids<NG> *>(smem + kKvWaves * 16 * (D + 2))[wave];
+    TileGrids<NG> &grids = reinterpret_cast<TileGrids<NG> *>(smem + kKvWaves * (a.kept_cols * D + 32))[wave];
     int from = 0, to;  // of the row of tiles
     Share sh;
     if (a.direct) {  // a sequence to a workgroup
@@ -538,7 +539,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
         for (int c = 0; c < NT; ++c) q[c].prepare(a);
         const f16x8 *shared = nullptr;
         if constexpr (kShared) {  // all waves have the same ones
-            f16x8 *to = reinterpret_cast<f16x8 *>(smem + kKvWaves * (16 * (D + 2) + (int)(sizeof(TileGrids<NG>) / 4))) + lane;
+            f16x8 *to = reinterpret_cast<f16x8 *>(smem + kKvWaves * (a.kept_cols * D + 32 + (int)(sizeof(TileGrids<NG>) / 4))) + lane;
             if (wave == 0) {
 #pragma unroll
                 for (int c = 0; c < NT; ++c)
@@ -855,7 +856,7 @@ __global__ __launch_bounds__(kKvThreads, D64 == 4 ? (NG < 4 ? 3 : 2) : (D64 * NG
 }
 
 struct Plan {
-    int nt, items, target, weigh_items, weigh_target;
+    int nt, items, target, least, weigh_items, weigh_target;
     bool direct;
     size_t part, stat, last;  // bytes
 };
@@ -865,9 +866,12 @@ Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_le
     const int64_t tiles = ceil_div(max_len, kKvTile), blocks = c.n_heads * ceil_div(cols, 16 * p.nt);
     // as many workgroups as the chip holds at once, but no more than combine() takes of one sequence
     p.target = (int)std::min<int64_t>(kMostSegments, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, kv_pool(c).groups, p.nt) / blocks));
-    p.direct = tiles <= kKvLeast;
+    // A tile for each wave, or two where the columns take several workgroups, each with parts to join (the last 16 tokens of
+    // two prompts of up to 5003, 128 columns: 34 us instead of 39; 900 tokens, 4 columns: 12.2 instead of 11.5).
+    p.least = kKvWaves * (cols > 16 * p.nt ? 2 : 1);
+    p.direct = tiles <= p.least;
     const int64_t all = std::max<int64_t>(1, n_seq * tiles);
-    p.items = (int)(p.direct ? n_seq : std::min<int64_t>(p.target, ceil_div(all, kKvLeast)));
+    p.items = (int)(p.direct ? n_seq : std::min<int64_t>(p.target, ceil_div(all, p.least)));
     p.weigh_target = (int)std::max<int64_t>(1, 256 * 4 / c.n_heads);
     p.weigh_items = (int)std::min<int64_t>(p.weigh_target, ceil_div(all, kKvWaves));
     const size_t rows = (size_t)c.n_heads * cols, segments = p.direct ? 0 : rows * (p.items + n_seq);
@@ -879,7 +883,7 @@ Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_le
 
 template <int D64, int NG, int NT>
 hipError_t launch_tiles(AttnArgs a, const Plan &p, int n_seq, bool weights, hipStream_t s) {
-    const size_t lds = (size_t)kKvWaves * (16 * (64 * D64 * 4 + 8) + sizeof(TileGrids<NG>)) + (queries_in_lds(D64, NG, NT) ? (size_t)NT * 2 * D64 * 1024 : 0);
+    const size_t lds = (size_t)kKvWaves * (a.kept_cols * 64 * D64 * 4 + 16 * 8 + sizeof(TileGrids<NG>)) + (queries_in_lds(D64, NG, NT) ? (size_t)NT * 2 * D64 * 1024 : 0);
     attention_kernel<D64, NG, NT><<<dim3((unsigned)p.items, (unsigned)a.pool.heads, (unsigned)ceil_div(a.cols, 16 * NT)), kKvThreads, lds, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -926,6 +930,8 @@ hipError_t run_kv_attention(const void *Q, gptq_dtype dt, int64_t n_seq, int64_t
     a.scale = scale * 1.44269504088896340736f;
     a.decay = decay;
     a.target = p.target;
+    a.least = p.least;
+    a.kept_cols = std::min(a.cols, 16);
     a.weigh_target = p.weigh_target;
     a.weigh_tiles = (int)std::min<int64_t>(ceil_div(a.cols, 16), kWeighTiles);
     a.bf16 = dt == GPTQ_DT_BF16;
