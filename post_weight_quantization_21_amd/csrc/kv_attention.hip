@@ -326,7 +326,7 @@ struct Queries {
 __device__ __forceinline__ bool hidden(bool there, int slot, int sees) { return !there || slot >= sees; }
 
 // Scores (x of the queries in registers, or the lane's part of what share_queries() left in LDS) of the lane's eight tokens in the columns, in log2 and less the columns' `base`, before any mask.
-template <int D64, int NG, int NT>
+template <int D64, int NG, int NT, bool kTight>
 __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile, const TileGrids<NG> &grids, const Queries<D64, NG> q[NT],
                                        const f16x8 *shared, const float base[NT]) {
     constexpr int KW = 2 * D64, SG = KW / NG;  // matrix instructions of a group
@@ -351,7 +351,7 @@ __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile
                     const float v = fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]);
                     s[c][4 * t + i] = g == 0 ? scale[i] * v : fmaf(scale[i], v, s[c][4 * t + i]);
                 }
-            if (NG == 1) keep_order();  // fragments and grids of one half at a time: registers
+            if (kTight) keep_order();  // fragments and grids of one group at a time: registers
         }
 #pragma unroll
     for (int c = 0; c < NT; ++c)
@@ -569,7 +569,7 @@ __global__ __launch_bounds__(kKvThreads, occupancy(D64, NG, NT)) void attention_
             grids.put(t.grid, sums.vscale, gone, __ballot(odd));
             wave_fence();
             float p[NT][8];
-            scores<D64, NG, NT>(p, t, grids, q, shared, sums.base);
+            scores<D64, NG, NT, NG == 1>(p, t, grids, q, shared, sums.base);
             if (next < t1) t.template load_keys<true>(a, coming, next, h);
             const int slot = tile * kKvTile + 8 * kb;
             const bool there = (kb < 2 ? pages.lo : pages.hi) >= 0;
@@ -815,7 +815,7 @@ __device__ __forceinline__ void weigh(const AttnArgs &a, int item, int h, unsign
                     q.scale = k.scale;
                     const float base = k.base, inv = k.inv;
                     float p[1][8];
-                    scores<D64, NG, 1>(p, t, grids, &q, frags + c * KW * kWave + lane, &base);
+                    scores<D64, NG, 1, true>(p, t, grids, &q, frags + c * KW * kWave + lane, &base);
                     if (masked) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)

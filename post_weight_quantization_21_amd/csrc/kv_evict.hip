@@ -40,7 +40,7 @@ __device__ __forceinline__ u32x4 ranks_at(const EvictArgs &a, const int32_t *row
 constexpr int kBins = 2048, kRanksInLds = 36 * 1024;  // 144 KB
 __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int in_lds) {
     extern __shared__ uint32_t ranks[];
-    __shared__ uint32_t hist[kBins], found[2], sums[kSelectWaves];
+    __shared__ uint32_t hist[kBins + kWave], found[2], sums[kSelectWaves];
     __shared__ int counts[2][kSelectWaves];
     const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int32_t *row = a.seqs.table + (int64_t)b * a.seqs.width;
@@ -57,21 +57,30 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
     }
     u32x4 *four = reinterpret_cast<u32x4 *>(ranks);
     auto rank4 = [&](int i) { return i < in_lds ? four[i / 4] : ranks_at(a, row, h, i); };
-    const int stored = min(safe, in_lds);
-#pragma unroll 8
-    for (int i = 4 * threadIdx.x; i < stored; i += 4 * kSelectThreads) four[i / 4] = ranks_at(a, row, h, i);
     uint32_t edge = 0, ties = heavy;  // the rank of the last that stays; `ties` of those that have it stay
     for (int shift = 21, bits = 11; shift >= 0;) {
         for (int i = threadIdx.x; i < kBins; i += kSelectThreads) hist[i] = 0;
         __syncthreads();
         const uint32_t digits = (1u << bits) - 1;
         const int above = shift + bits;
-#pragma unroll 4
-        for (int i = 4 * threadIdx.x; i < safe; i += 4 * kSelectThreads) {
-            const u32x4 k = rank4(i);
+        // A rank that differs from the edge above these bits counts in a bin of its lane's, past the others (a branch costs more).
+        auto count = [&](const u32x4 &k, int i) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (i + e < safe && (above == 32 || k[e] >> above == edge >> above)) atomicAdd(&hist[k[e] >> shift & digits], 1u);
+            for (int e = 0; e < 4; ++e) {
+                const bool in = i + e < safe && (above == 32 || (k[e] ^ edge) >> above == 0);
+                atomicAdd(&hist[in ? k[e] >> shift & digits : kBins + lane], 1u);
+            }
+        };
+        if (shift == 21) {
+#pragma unroll 8
+            for (int i = 4 * threadIdx.x; i < safe; i += 4 * kSelectThreads) {
+                const u32x4 k = ranks_at(a, row, h, i);
+                if (i < in_lds) four[i / 4] = k;
+                count(k, i);
+            }
+        } else {
+#pragma unroll 4
+            for (int i = 4 * threadIdx.x; i < safe; i += 4 * kSelectThreads) count(rank4(i), i);
         }
         __syncthreads();
         // thread i holds bins kBins - 2 i - 1 and - 2: sums from the highest bin down
