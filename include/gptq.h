@@ -546,7 +546,7 @@ typedef struct {
  * A group's grid is the one above with 4 bits, but its scale, (hi - lo) * (1/15) or max|x| *
  * (1/7) with the nearest fp32 of the fraction, is rounded to bf16 before zero and codes are
  * chosen with it.  A group with a value that is not finite, or a
- * spread beyond fp32, gets a scale that is no number: what attends to it is no number.
+ * spread beyond fp32, gets a scale that is no number: what sees the token is no number.
  * The new tokens' weights are set to 0.  T * n_heads at most 2^26.
  */
 GPTQ_API gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, int64_t ldv, gptq_dtype dtype, int64_t T,
@@ -572,11 +572,12 @@ GPTQ_API gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, i
  *           not read the old one).  Needs weight; pages then belong to one sequence.
  *   ws      scratch of gptq_kv_attention_workspace_bytes(), 16-byte aligned; the same
  *           sizes, n_seq no larger and max_len no larger need no more.
- * Products with the keys are exact (integers q - 8 times Q in fp16 or, from bf16, to
- * 2^-40 of a row's largest value); sums and softmax are fp32; p s_v enters the second
- * product in fp16 (2^-11 of each term) and the result is rounded once.  Deterministic.  A
- * query that is not finite makes its own row not finite or NaN, and the weights of what
- * it sees.  n_seq * n_heads * ceil(n q_heads / n_heads / 16) at most 2^20.
+ * Products with the keys are exact (the codes times Q, of which 2^-35 of a row's largest
+ * value may be lost); sums and softmax are fp32; p s_v enters the second product in fp16
+ * (2^-11 of each term) and the result is rounded once.  Deterministic.  A query that is
+ * not finite, and one that sees a key or value that is none, has a row that is not finite
+ * or NaN, and so have the weights of all that it sees; other rows are as without it.
+ * n_seq * n_heads * ceil(n q_heads / n_heads / 16) at most 2^19.
  */
 GPTQ_API gptq_status gptq_kv_attention(const void *Q, gptq_dtype dtype, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq,
                                        const gptq_kv_cache *cache, const int32_t *table, int64_t width, const int32_t *lens,

@@ -172,7 +172,7 @@ gptq_status check_kv_queries(const gptq_kv_cache *c, int64_t n_seq, int64_t n, i
         return fail(GPTQ_ERR_INVALID_ARG, "%s: bad sizes (q_heads must be a multiple of n_heads)", fn);
     if (n > 16 || q_heads / c->n_heads > 256) return fail(GPTQ_ERR_UNSUPPORTED, "%s: at most 16 tokens, and 256 query heads on one", fn);
     const int64_t tiles = gptq::ceil_div(n * (q_heads / c->n_heads), 16);
-    if (n_seq > 65535 || max_len > kKvTokens || n_seq * c->n_heads * tiles > ((int64_t)1 << 20) ||
+    if (n_seq > 65535 || max_len > kKvTokens || n_seq * c->n_heads * tiles > ((int64_t)1 << 19) ||
         n_seq * gptq::ceil_div(max_len, 32) > ((int64_t)1 << 30))
         return fail(GPTQ_ERR_UNSUPPORTED, "%s: too many sequences, heads and queries at once", fn);
     return GPTQ_OK;

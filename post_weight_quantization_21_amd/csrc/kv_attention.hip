@@ -2,21 +2,32 @@
 //
 // The n G columns of a kv head (n tokens, G query heads each) are the B operand of
 // v_mfma_f32_16x16x32_f16, sixteen at a time.  A wave takes tiles of 32 cached tokens:
-//   S[token][column] = s_k (sum_d (q_k - 8) x + c_k X),   c = 8 - z,  X = sum_d x
-// with the codes as exact fp16 integers in [-8, 7], so nothing but the fp32 sums rounds.
-// The A operand's row r of half t is token 8 (r / 4) + 4 t + r % 4, so a lane ends up with
-// S of eight tokens next to each other in one column, which is what the second product
-//   O[dim][column] = sum_token (q_v - 8) (p s_v) + sum_token c_v (p s_v)
+//   S[token][column] = s_k (sum_d q_k x - z_k X),  X = sum_d x
+// with the codes as exact subnormal fp16 numbers (key_frag), so nothing but the fp32 sums
+// rounds.  The A operand's row r of half t is token 8 (r / 4) + 4 t + r % 4, so a lane ends
+// up with S of eight tokens next to each other in one column, which is what the second
+// product
+//   O[dim][column] = sum_token q_v (p s_v) - sum_token z_v (p s_v)
 // wants of its B operand: p never leaves the lane.  It is held there as p s_v in fp16,
 // scaled by a power of two that follows the largest s_v: a rounding of 2^-11 of each
 // term at most, as that of an fp16 result, where bf16 would lose eight times that.
-// Values s_v more than 2^29 below the largest lose bits, those more than 2^40 below it vanish.
+// Values s_v more than 2^20 below the largest lose bits, those more than 2^31 below it vanish.
+// The two sums of O are 15 / 8 times what those of q - 8 and z - 8 would be, which costs a
+// bit of fp32 and saves an instruction a pair of codes.
 //
-// bf16 queries enter as fp16 times a power of two of their row, which takes no bit from
-// a value above 2^-30 of the row's largest.
+// Queries of both types enter as fp16 times a power of two of their row, which takes no
+// bit from a value above 2^-25 of the row's largest.
 //
 // One pass with a running maximum: the sums are rescaled only when a score passes the
 // maximum they are held to by 2^6 (p may then be up to 64, which fp16 and fp32 hold).
+//
+// All tiles of all sequences are shared out evenly, 1024 workgroups of four waves on the
+// chip at most; a sequence that several workgroups share is joined by a second launch.
+// Bound by memory where the cache is long: one sequence of 131072 tokens, 64 heads on 8
+// of 128 (143 MB), takes 35-36 us and 5.5 to join, 32 of up to 16384 (346 MB) 81-84; while its
+// tiles run it reads 5.4-5.7 TB/s, and start, first loads and the waves' join take the
+// rest (6-8 us).  With small groups and several column tiles by vector instructions: 8
+// drafted tokens of 8 x 8191 in groups of 32 issue 700 a tile and take 41-43 us.
 #include <algorithm>
 #include <type_traits>
 

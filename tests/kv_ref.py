@@ -118,9 +118,8 @@ def attention(pool, q, table, lens, scale, decay=None):
         vq, vs, vz, _ = pool.seq(table[b], m, "v")
         ks, kz, vs, vz = (np.repeat(t.astype(np.float64), g, axis=2) for t in (ks, kz, vs, vz))
         k, v = ks * (kq - kz), vs * (vq - vz)
-        # what the sums of a score run over: (q - 8) x and (8 - z) x
-        kmag = ks * (np.abs(kq.astype(np.float64) - 8) + np.abs(8 - kz))
-        vmag = vs * (np.abs(vq.astype(np.float64) - 8) + np.abs(8 - vz))
+        # what the sums run over: q x and z x, q p s and z p s
+        kmag, vmag = ks * (kq + kz), vs * (vq + vz)
         got, gtol = np.zeros((H, m)), np.zeros((H, m))
         for i in range(n):
             see = (np.arange(m) < m - n + 1 + i) & there

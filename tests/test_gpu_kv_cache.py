@@ -81,7 +81,11 @@ CASES = [(1, [1], 1, 1, 1, 64, 0, 16, False, "fp16"),
          (2, [16, 4099], 16, 4, 2, 64, 64, 64, False, "fp16"),
          (2, [9, 2], 5, 4, 4, 128, 0, 16, False, "fp16"),   # two tokens of five: three rows of padding see nothing
          (70, list(range(0, 140, 2)), 1, 2, 1, 64, 0, 16, False, "bf16"),  # more sequences than lanes
-         (3, [5000, 40, 2], 1, 8, 8, 128, 128, 1024, False, "fp16")]
+         (3, [5000, 40, 2], 1, 8, 8, 128, 128, 1024, False, "fp16"),
+         (2, [333, 40], 16, 32, 2, 64, 32, 32, False, "bf16"),  # 256 columns
+         (1, [130], 16, 11, 1, 192, 0, 64, True, "fp16"),
+         (3, [900, 1, 64], 2, 40, 2, 128, 128, 64, False, "bf16"),
+         (2, [50, 700], 3, 33, 3, 256, 0, 16, True, "fp16")]
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in c if not isinstance(x, list)))
@@ -130,15 +134,16 @@ def test_long_rows_are_split_and_deterministic(dt):
     check_attention(short, *cut[:3], dt, "cut")
 
 
-def test_missing_pages_and_odd_lengths():
+@pytest.mark.parametrize("page", [16, 32, 64])
+def test_missing_pages_and_odd_lengths(page):
     """Table entries outside the pool and lengths outside the table: those tokens are not there."""
     torch = torch_mod()
-    B, H, Hq, D, page = 4, 2, 4, 64, 16
+    B, H, Hq, D = 4, 2, 4, 64
     rng = np.random.default_rng(9)
     pool = kv_ref.Pool(40, H, D, page, 32, False, seed=1)
     table = tables(rng, 40, B, 9)
     table[0, 1], table[0, 4], table[1, :], table[2, 0] = -1, 40, 2 ** 31 - 1, -2 ** 31
-    lens = [130, 100, 16, 400]  # the third sees only a page that is not there, the fourth is longer than its table
+    lens = [8 * page + 2, 100, page, 25 * page]  # the third sees only a page that is not there, the fourth is longer than its table
     q, q64 = make_queries((B, 2, Hq, D), "fp16", 4)
     cache = kv_ref.cuda_cache(gq, torch, pool)
     poison(cache, table, lens, page)
@@ -149,6 +154,23 @@ def test_missing_pages_and_odd_lengths():
     assert (np.abs(host(cache.weight) - weight) <= wtol).all()
     negative = gq.kv_attention(q.cuda(), cache, ints(table), ints([-5, -2 ** 31, 0, -1]))
     assert not negative.any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_uniform_attention(dt):
+    """Queries of zero weigh all tokens alike: results are means, small against the values that add up to them."""
+    torch = torch_mod()
+    B, H, Hq, D, page, lens = 2, 1, 16, 64, 64, [30000, 4096]
+    rng = np.random.default_rng(8)
+    pool = kv_ref.Pool(540, H, D, page, 0, True, seed=5)
+    table = tables(rng, 540, B, 470 // 2 * 2 - 200)
+    lens = [min(x, table.shape[1] * page) for x in lens]
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    q = torch.zeros(B, 1, Hq, D, dtype=torch_dtype(dt))
+    o = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens), decay=0.0)
+    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q.double().numpy(), table, lens, D ** -0.5, 0.0)
+    check_attention(o, ref, tol, rms, dt, "uniform")
+    assert (np.abs(host(cache.weight) - weight) <= wtol).all()
 
 
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
@@ -294,6 +316,77 @@ def test_append(case):
         assert torch.equal(a, b)
     gq.kv_append(K, V, again, ints(table), ints(lens), offs=None if uniform else ints(offs), K_out=K, V_out=V)
     assert torch.equal(K[:T], out[0, :T]) and torch.equal(V[:T], out[1, :T])
+
+
+@pytest.mark.parametrize("D,g,sym,page,dt", [(64, 0, False, 16, "bf16"), (64, 32, True, 64, "fp16"), (128, 128, False, 64, "bf16"),
+                                             (128, 32, False, 16, "fp16"), (128, 64, True, 32, "bf16"), (192, 192, False, 32, "fp16"),
+                                             (192, 64, False, 16, "bf16"), (192, 32, True, 64, "fp16"), (256, 0, True, 16, "bf16"),
+                                             (256, 128, False, 128, "fp16"), (256, 64, False, 16, "bf16"), (256, 32, False, 64, "fp16")])
+def test_append_of_prompts(D, g, sym, page, dt):
+    """Enough tokens that workgroups put whole blocks of values together: starts and ends inside a block, inside a workgroup's
+    tokens, texts that go on, a text of nothing, rows behind the last, a page that is not there."""
+    torch = torch_mod()
+    H = 40
+    lens, news = [70, 43, 9, 0, 130], [70, 40, 1, 0, 97]
+    B, T, more = len(lens), sum(news), 5
+    assert -(-(T + more) // 32) * H * 2 >= 512
+    rng = np.random.default_rng(D + g)
+    width = -(-max(lens) // page) + 1
+    pool = kv_ref.Pool(B * width + 2, H, D, page, g, sym, seed=D)
+    table = tables(rng, B * width + 2, B, width)
+    table[4, 1] = -1
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    gen = torch.Generator().manual_seed(T)
+    K, V = (torch.randn(T + more, H, D, generator=gen).to(torch_dtype(dt)) for _ in range(2))
+    offs = np.concatenate([[0], np.cumsum(news)])
+    out = torch.full((2, T + more, H, D), 7.0, dtype=K.dtype, device="cuda")
+    gq.kv_append(K.cuda(), V.cuda(), cache, ints(table), ints(lens), offs=ints(offs), K_out=out[0], V_out=out[1])
+    for k, (side, x) in enumerate((("k", K), ("v", V))):
+        q, s, z = kv_ref.fit(x.float().numpy(), g or D, sym)
+        full_s, full_z = (np.repeat(t, g or D, axis=-1) for t in (s, z))
+        want = torch.from_numpy((full_s * (q - full_z)).astype(np.float32)).to(K.dtype)
+        assert torch.equal(out[k, :T].cpu(), want[:T]) and (out[k, T:] == 7).all()
+        for b in range(B):
+            for i in range(news[b]):
+                slot, t = lens[b] - news[b] + i, offs[b] + i
+                p = table[b, slot // page]
+                if p < 0:
+                    continue
+                for name, val in (("q", q), ("s", s), ("z", z)):
+                    getattr(pool, side + name)[p, :, slot % page] = val[t]
+                pool.weight[p, :, slot % page] = 0
+    for name, want, have in zip("k v k_grid v_grid weight".split(), pool.words(), cache.tensors):
+        assert np.array_equal(host(have), want), name
+
+
+@pytest.mark.parametrize("sym", [False, True])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_append_of_every_size(dt, sym):
+    """Groups whose values are as small and as large as the type has them, and mixtures of both."""
+    torch = torch_mod()
+    H, D, page = 2, 64, 16
+    pool = kv_ref.Pool(20, H, D, page, 32, sym, seed=0)
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    gen = torch.Generator().manual_seed(1)
+    lo, hi = (-133, 125) if dt == "bf16" else (-24, 15)
+    scale = 2.0 ** torch.linspace(lo, hi, 260).round().view(-1, 1, 1).double()
+    x = (torch.randn(260, H, D, generator=gen).double().clamp(-1.9, 1.9) * scale)
+    x[::7, :, 5] = 0.0
+    x[::5, :, ::2] *= 2.0 ** -6
+    x = x.to(torch_dtype(dt))
+    table = np.arange(17, dtype=np.int32)[None]
+    k, v = gq.kv_append(x.cuda(), x.cuda(), cache, ints(table), ints([260]), values=True)
+    q, s, z = kv_ref.fit(x.float().numpy(), 32, sym)
+    for side in "kv":
+        for name, val in (("q", q), ("s", s), ("z", z)):
+            for t in range(260):
+                getattr(pool, side + name)[t // 16, :, t % 16] = val[t]
+    pool.weight.reshape(20, H, page)[:16] = 0
+    pool.weight[16, :, :4] = 0
+    for name, want, have in zip("k v k_grid v_grid weight".split(), pool.words(), cache.tensors):
+        assert np.array_equal(host(have), want), name
+    want = torch.from_numpy((np.repeat(s, 32, -1) * (q - np.repeat(z, 32, -1))).astype(np.float32)).to(x.dtype)
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
 
 
 def test_append_refuses_bad_pages_and_bad_values():
@@ -507,3 +600,82 @@ def test_without_sequences():
     assert gq.kv_append(k, k, c, none, lens, values=True)[0].shape == k.shape
     assert gq.kv_append(k, k, c, ints([[0]]), ints([3])) is None
     assert gq.kv_evict(c, none, lens, none, 4)[0].shape == (0, 2, 4)
+
+
+@pytest.mark.parametrize("kind", ["stream", "graph"])
+def test_streams_and_graphs(kind):
+    """A step (append, attention with weights) and an eviction on a stream of the caller's whose inputs are dropped at once, or
+    captured, replayed several times with other work between, twice with one workspace: as on the current stream."""
+    torch = torch_mod()
+    B, H, Hq, D, page, L = 3, 2, 8, 128, 32, 900
+    rng = np.random.default_rng(4)
+    pool = kv_ref.Pool(120, H, D, page, 128, False, seed=4)
+    order = tables(rng, 120, B, 38)
+    table, to = ints(order[:, :30]), ints(order[:, 30:])
+    lens = [L, 500, 33]
+    gen = torch.Generator().manual_seed(2)
+    q = torch.randn(B, 1, Hq, D, generator=gen).to(torch.bfloat16).cuda()
+    k, v = (torch.randn(B, H, D, generator=gen).to(torch.bfloat16).cuda() for _ in range(2))
+    dl = ints(lens)
+
+    def step(cache, ws, stream=None):
+        gq.kv_append(k, v, cache, table, dl, stream=stream)
+        o = gq.kv_attention(q, cache, table, dl, decay=0.5, ws=ws, stream=stream)
+        kept, left = gq.kv_evict(cache, table, dl, to, 200, 20, stream=stream)
+        return o, kept, left
+
+    want_cache = kv_ref.cuda_cache(gq, torch, pool)
+    need = gq.kv_attention_workspace_bytes(want_cache, B, 1, Hq, 30 * page)
+    times = 1 if kind == "stream" else 4
+    wants = []
+    for _ in range(times):
+        wants.append([t.clone() for t in step(want_cache, None)])
+        wants[-1] += [t.clone() for t in want_cache.tensors]
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    torch.cuda.synchronize()
+    if kind == "stream":
+        s = torch.cuda.Stream()
+        got = step(cache, torch.empty(need, dtype=torch.uint8, device="cuda"), s)
+        junk = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        s.synchronize()
+        del junk
+        gots = [list(got) + list(cache.tensors)]
+        assert all(torch.equal(a, b) for a, b in zip(gots[0], wants[0]))
+        return
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    q2 = q.flip(0).contiguous()
+    with torch.cuda.graph(graph):
+        got = step(cache, ws)
+    with torch.cuda.graph(other):  # the same workspace, another call
+        o2 = gq.kv_attention(q2, cache, table, dl, ws=ws)
+    for i in range(times):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(list(got) + list(cache.tensors), wants[i])), i
+        other.replay()
+        eager = gq.kv_attention(q2, cache, table, dl)
+        torch.cuda.synchronize()
+        assert torch.equal(o2, eager), i
+
+
+def test_pools_past_4_gib():
+    """Pages whose codes lie past 2^32 bytes: the same as in a small pool."""
+    torch = torch_mod()
+    H, Hq, D, page, n = 8, 16, 128, 256, 40000  # k: 40000 x 8 x 256 x 64 bytes = 5.2 GB
+    small = gq.kv_cache_empty(16, H, D, page=page, weights=True)
+    large = gq.kv_cache_empty(n, H, D, page=page, weights=True)
+    B, lens = 2, [600, 300]
+    near = np.array([[0, 1, 2], [3, 4, 5]], dtype=np.int32)
+    far = np.array([[n - 1, 5, 33001], [n - 7, 36000, 38999]], dtype=np.int32)
+    gen = torch.Generator().manual_seed(7)
+    K, V = (torch.randn(900, H, D, generator=gen).to(torch.float16).cuda() for _ in range(2))
+    q = torch.randn(B, 2, Hq, D, generator=gen).to(torch.float16).cuda()
+    res = []
+    for cache, table, to in ((small, near, [[6, 7], [8, 9]]), (large, far, [[n - 2, 34000], [n - 3, 8]])):
+        gq.kv_append(K, V, cache, ints(table), ints(lens), offs=ints([0, 600, 900]))
+        o = gq.kv_attention(q, cache, ints(table), ints(lens), decay=1.0)
+        kept, left = gq.kv_evict(cache, ints(table), ints(lens), ints(to), 280, 100)
+        res.append([o, kept, left, gq.kv_attention(q, cache, ints(to), left)])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)

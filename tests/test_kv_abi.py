@@ -89,7 +89,7 @@ def test_append_without_tokens():
     (dict(acc=1, decay=1.5), INV), (dict(acc=1, decay=-0.1), INV), (dict(acc=1, decay=float("nan")), INV), (dict(Q=None), INV),
     (dict(O=None), INV), (dict(ldq=1016), INV), (dict(ldo=1023), INV), (dict(ldq=1028), INV), (dict(Q=P + 8), INV), (dict(O=P + 1), INV),
     (dict(ws=None), WS), (dict(ws_bytes=8), WS), (dict(ws=FAR + 8), INV), (dict(O=P), INV), (dict(O=P + 2046), INV),
-    (dict(n_seq=65535, n=16, hq=32, ldq=4096, ldo=4096), UNS),
+    (dict(n_seq=65535, n=16, hq=32, ldq=4096, ldo=4096), UNS), (dict(n_seq=40000, n=16, hq=16, ldq=2048, ldo=2048), UNS),
 ])
 def test_attention_refused(kw, status):
     assert attention(cache(), **kw) == status
