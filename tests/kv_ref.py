@@ -5,6 +5,7 @@ from __future__ import annotations
 import numpy as np
 
 HALF = {"fp16": 2.0 ** -11, "bf16": 2.0 ** -8}  # a rounding, relative
+TERM = {"fp16": 2.0 ** -21, "bf16": 2.0 ** -11}  # of p s_v, by the result: two fp16 values (each to half a step) or one
 
 
 def bf16_round(x: np.ndarray) -> np.ndarray:
@@ -100,10 +101,10 @@ def cuda_cache(gq, torch, pool):
     return gq.kv_cache(*w, group_size=pool.group, symmetric=pool.symmetric)
 
 
-def attention(pool, q, table, lens, scale, decay=None):
+def attention(pool, q, table, lens, scale, dt, decay=None):
     """q [B][n][Hq][D] (values that fp16 or bf16 hold) in 64 bits: o, a bound of its error without the result's own rounding
-    (relative 2^-11 of every term for p s_v in fp16, and the fp32 sums'), the root-mean-square size of what that fp16
-    rounding leaves, the weights [pages][H][P] and their bound."""
+    (TERM of every p s_v, and the fp32 sums'), the root-mean-square size of what TERM
+    leaves, the weights [pages][H][P] and their bound."""
     B, n, Hq, D = q.shape
     H, G, g = pool.heads, Hq // pool.heads, pool.group
     o, tol, rms = (np.zeros(q.shape) for _ in range(3))
@@ -136,8 +137,8 @@ def attention(pool, q, table, lens, scale, decay=None):
             eps = (2 * ((D + 16) * e24 * np.where(see, mag, 0).max(-1, keepdims=True) + 2.0 ** -21) + m * e24)
             o[b, i] = np.matmul(p, v).reshape(Hq, D)
             small = 30 * np.where(see[:, None], vs, 0).max() * m * 2.0 ** -31 / total  # below fp16's normal numbers
-            tol[b, i] = (np.matmul(p, np.abs(v)) * 2.0 ** -11 + np.matmul(p, vmag) * eps + small).reshape(Hq, D)
-            rms[b, i] = (2.0 ** -11 * np.sqrt(np.matmul(p * p, v * v)) + np.matmul(p, vmag) * eps + small).reshape(Hq, D)
+            tol[b, i] = (np.matmul(p, np.abs(v)) * TERM[dt] + np.matmul(p, vmag) * eps + small).reshape(Hq, D)
+            rms[b, i] = (TERM[dt] * np.sqrt(np.matmul(p * p, v * v)) + np.matmul(p, vmag) * eps + small).reshape(Hq, D)
             got += p.sum(1)
             gtol += (p * (eps + 2.0 ** -22)).sum(1)
         if decay is not None:

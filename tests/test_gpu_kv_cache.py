@@ -102,7 +102,7 @@ def test_attention(case, decay):
     q, q64 = make_queries((B, n, Hq, D), dt, 7 + D)
     scale = D ** -0.5
     o = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens), max_len=max(lens) + page // 2, decay=decay)
-    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q64, table, lens, scale, decay)
+    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q64, table, lens, scale, dt, decay)
     check_attention(o, ref, tol, rms, dt, f"{case}")
     for b, m in enumerate(lens):  # what sees nothing
         assert not o[b, :max(0, n - m)].any()
@@ -125,12 +125,12 @@ def test_long_rows_are_split_and_deterministic(dt):
     cache = kv_ref.cuda_cache(gq, torch, pool)
     q, q64 = make_queries((B, 1, Hq, D), dt, 2, spread=3.0)
     first = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens))
-    ref, tol, rms, _, _ = kv_ref.attention(pool, q64, table, lens, D ** -0.5)
+    ref, tol, rms, _, _ = kv_ref.attention(pool, q64, table, lens, D ** -0.5, dt)
     check_attention(first, ref, tol, rms, dt, f"long {dt}")
     for _ in range(3):
         assert torch.equal(first, gq.kv_attention(q.cuda(), cache, ints(table), ints(lens)))
     short = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens), max_len=9000)  # lengths above count as it
-    cut = kv_ref.attention(pool, q64, table, [min(x, 9000) for x in lens], D ** -0.5)
+    cut = kv_ref.attention(pool, q64, table, [min(x, 9000) for x in lens], D ** -0.5, dt)
     check_attention(short, *cut[:3], dt, "cut")
 
 
@@ -148,7 +148,7 @@ def test_missing_pages_and_odd_lengths(page):
     cache = kv_ref.cuda_cache(gq, torch, pool)
     poison(cache, table, lens, page)
     o = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens), decay=1.0)
-    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q64, table, lens, D ** -0.5, 1.0)
+    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q64, table, lens, D ** -0.5, "fp16", 1.0)
     check_attention(o, ref, tol, rms, "fp16", "missing pages")
     assert not o[1:3].any()
     assert (np.abs(host(cache.weight) - weight) <= wtol).all()
@@ -168,7 +168,7 @@ def test_uniform_attention(dt):
     cache = kv_ref.cuda_cache(gq, torch, pool)
     q = torch.zeros(B, 1, Hq, D, dtype=torch_dtype(dt))
     o = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens), decay=0.0)
-    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q.double().numpy(), table, lens, D ** -0.5, 0.0)
+    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q.double().numpy(), table, lens, D ** -0.5, dt, 0.0)
     check_attention(o, ref, tol, rms, dt, "uniform")
     assert (np.abs(host(cache.weight) - weight) <= wtol).all()
 
@@ -186,7 +186,7 @@ def test_values_of_very_different_size(dt):
     table = tables(rng, 100, B, 48)
     q, q64 = make_queries((B, 1, Hq, D), dt, 1)
     o = gq.kv_attention(q.cuda(), kv_ref.cuda_cache(gq, torch, pool), ints(table), ints(lens)).double().cpu().numpy()
-    ref, tol, _, _, _ = kv_ref.attention(pool, q64, table, lens, D ** -0.5)
+    ref, tol, _, _, _ = kv_ref.attention(pool, q64, table, lens, D ** -0.5, dt)
     half = kv_ref.HALF[dt]
     limit = np.where(np.abs(ref) > 60000, np.inf, tol * (1 + half) + half * np.abs(ref) + 2.0 ** -24) if dt == "fp16" else tol * (1 + half) + half * np.abs(ref)
     assert (np.abs(o - ref)[np.isfinite(limit)] <= limit[np.isfinite(limit)]).all()
@@ -203,7 +203,7 @@ def test_bf16_over_its_range(power):
     table = tables(np.random.default_rng(1), 30, B, 13)
     q, q64 = make_queries((B, 1, Hq, D), "bf16", 3, spread=2.0 ** power)
     o = gq.kv_attention(q.cuda(), kv_ref.cuda_cache(gq, torch, pool), ints(table), ints(lens))
-    ref, tol, rms, _, _ = kv_ref.attention(pool, q64, table, lens, D ** -0.5)
+    ref, tol, rms, _, _ = kv_ref.attention(pool, q64, table, lens, D ** -0.5, "bf16")
     err = np.abs(o.double().cpu().numpy() - ref)
     assert (err <= tol * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)).all()
 
@@ -220,7 +220,7 @@ def test_scale_and_strides():
     out = torch.full((B, n, Hq + 3, D), 5.0, dtype=torch.bfloat16, device="cuda")
     o = out[:, :, 1:Hq + 1]
     assert gq.kv_attention(q, cache, ints(table), ints(lens), scale=0.31, O=o) is o
-    ref, tol, rms, _, _ = kv_ref.attention(pool, q.double().cpu().numpy(), table, lens, 0.31)
+    ref, tol, rms, _, _ = kv_ref.attention(pool, q.double().cpu().numpy(), table, lens, 0.31, "bf16")
     check_attention(o, ref, tol, rms, "bf16", "strides")
     assert (out[:, :, 0] == 5).all() and (out[:, :, Hq + 1:] == 5).all()
 
@@ -524,7 +524,7 @@ def test_a_text_is_read_continued_and_cut(dt):
     def attend(n, lens, decay):
         q = rnd(B, n, Hq, D)
         o = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens), decay=decay)
-        ref, tol, rms, weight, wtol = kv_ref.attention(pool, q.double().numpy(), table, lens, D ** -0.5, decay)
+        ref, tol, rms, weight, wtol = kv_ref.attention(pool, q.double().numpy(), table, lens, D ** -0.5, dt, decay)
         check_attention(o, ref, tol, rms, dt, f"together {lens}")
         for b in range(B):
             slot = np.arange(lens[b])
