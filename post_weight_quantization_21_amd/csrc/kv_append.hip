@@ -27,8 +27,16 @@ struct AppendArgs {
     int32_t bf16, symmetric;
 };
 
-__device__ __forceinline__ float load16(uint16_t h, bool bf16) {
-    return bf16 ? __uint_as_float((uint32_t)h << 16) : (float)__builtin_bit_cast(_Float16, h);
+// Two values of a word in fp32, and back.
+template <bool kBf16>
+__device__ __forceinline__ f32x2 unpack2(uint32_t w) {
+    if constexpr (kBf16) return (f32x2){__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)};
+    return __builtin_convertvector(__builtin_bit_cast(f16x2, w), f32x2);
+}
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack2(f32x2 v) {
+    if constexpr (kBf16) return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
 }
 
 // A step of a reduction over neighbouring lanes: the value of the lane's partner.
@@ -107,7 +115,7 @@ constexpr int kBlockTokens = 32;  // tokens of a workgroup that stages values
 // units of all four j.  Units of neighbouring tokens share sixteen bytes: staged, whole blocks of eight tokens are put
 // together in LDS and stored at once (32768 tokens of 8 heads of 128 values: TIME_STAGED), else each token's two bytes
 // (TIME_PLAIN; but 32 single tokens TIME_SMALL).
-template <int D64, int GROUP, bool kStaged>
+template <int D64, int GROUP, bool kStaged, bool kBf16>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
     constexpr int D = 64 * D64, NG = D / GROUP, kLanes = D64 == 1 ? 8 : (D64 == 2 ? 16 : 32), kPass = 256 / kLanes;
     constexpr int kPasses = kStaged ? kBlockTokens / kPass : 1, kTokens = kPass * kPasses, kCols = kTokens + 8;
@@ -162,9 +170,10 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
         const int64_t t = t0 + n, at = place[n];
         float f[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const uint16_t w = (uint16_t)(x[p][e / 2] >> (16 * (e & 1)));
-            f[e] = load16(w, a.bf16);
+        for (int e = 0; e < 8; e += 2) {
+            const uint32_t two = x[p][e / 2];
+            const f32x2 v = unpack2<kBf16>(two);
+            f[e] = v[0], f[e + 1] = v[1];
         }
         Range range = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -184,11 +193,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
         if (a.out[values] && at > -2 && t < a.T && i < D / 8) {
             u32x4 y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float y0 = g.value(f[2 * e]), y1 = g.value(f[2 * e + 1]);
-                y[e] = a.bf16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(((f32x2){y0, y1}), bf16x2))
-                              : __builtin_bit_cast(uint32_t, __builtin_convertvector(((f32x2){y0, y1}), f16x2));
-            }
+            for (int e = 0; e < 4; ++e) y[e] = pack2<kBf16>((f32x2){g.value(f[2 * e]), g.value(f[2 * e + 1])});
             *reinterpret_cast<u32x4 *>(a.out[values] + t * a.ld_out[values] + h * D + 8 * i) = y;
         }
         uint32_t w;
@@ -250,9 +255,9 @@ void launch_append(const AppendArgs &a, hipStream_t s) {
     constexpr int kPass = 256 / (D64 == 1 ? 8 : (D64 == 2 ? 16 : 32));
     // Staged where there are workgroups of 32 tokens for every compute unit.
     if (ceil_div(a.T, kBlockTokens) * a.pool.heads * 2 >= 512)
-        append_kernel<D64, GROUP, true><<<dim3((unsigned)ceil_div(a.T, kBlockTokens), (unsigned)a.pool.heads, 2), 256, 0, s>>>(a);
+        (a.bf16 ? append_kernel<D64, GROUP, true, true> : append_kernel<D64, GROUP, true, false>)<<<dim3((unsigned)ceil_div(a.T, kBlockTokens), (unsigned)a.pool.heads, 2), 256, 0, s>>>(a);
     else
-        append_kernel<D64, GROUP, false><<<dim3((unsigned)ceil_div(a.T, kPass), (unsigned)a.pool.heads, 2), 256, 0, s>>>(a);
+        (a.bf16 ? append_kernel<D64, GROUP, false, true> : append_kernel<D64, GROUP, false, false>)<<<dim3((unsigned)ceil_div(a.T, kPass), (unsigned)a.pool.heads, 2), 256, 0, s>>>(a);
 }
 template <int D64>
 hipError_t launch_append(const AppendArgs &a, int group, hipStream_t s) {
