@@ -573,11 +573,11 @@ GPTQ_API gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, i
  *   ws      scratch of gptq_kv_attention_workspace_bytes(), 16-byte aligned; the same
  *           sizes, n_seq no larger and max_len no larger need no more.
  * Products with the keys are exact (the codes times Q, of which 2^-35 of a row's largest
- * value may be lost); sums and softmax are fp32; p s_v enters the second product as one
- * fp16 value for bf16 results (2^-11 of each term), as two for fp16 ones, and the result
- * is rounded once.  Deterministic.  A query that is
- * not finite, and one that sees a key or value that is none, has a row that is not finite
- * or NaN, and so have the weights of all that it sees; other rows are as without it.
+ * value may be lost; keys of 2^114 and more may overflow); sums and softmax are fp32; p s_v
+ * enters the second product as one fp16 value for bf16 results (2^-11 of each term), as
+ * two for fp16 ones, and the result is rounded once.  Deterministic.  A query that is not
+ * finite, and one that sees a key or value that is none, has a row that is not finite or
+ * NaN, and so have the weights of all that it sees; other rows are as without it.
  * n_seq * n_heads * ceil(n q_heads / n_heads / 16) at most 2^19.
  */
 GPTQ_API gptq_status gptq_kv_attention(const void *Q, gptq_dtype dtype, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq,

@@ -29,7 +29,7 @@
 // of 128 (143 MB), takes 35-36 us and 5.5 to join, 32 of up to 16384 (346 MB) 81-84; while its
 // tiles run it reads 5.4-5.7 TB/s, and start, first loads and the waves' join take the
 // rest (6-8 us).  With small groups and several column tiles by vector instructions: 8
-// drafted tokens of 8 x 8191 in groups of 32 issue 700 a tile and take 41-43 us.
+// drafted tokens of 8 x 8191 in groups of 32 issue 960 a tile and take 44 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -54,7 +54,7 @@ struct AttnArgs {
     int64_t ldq;
     uint16_t *o;
     int64_t ldo;
-    float *part;   // [segment][head][column][D], unnormalized, relative to the segment's maximum
+    float *part;   // [segment][head][column][D]: the result over the segment alone
     float2 *stat;  // [segment][head][column]: maximum (of log2) and sum
     float2 *last;  // [sequence][head][column]: maximum and sum of a sequence of one segment, or NULL
     float scale;   // times log2 e
@@ -214,8 +214,12 @@ struct Tile {
     }
 };
 
-// The grids of a wave's tile in LDS, token by token: scales in fp32 (of values times the wave's power of two) and -z in
-// fp16.  Written by the lane that holds a token's word, read by the lanes that need eight.
+// A code of 1 as the matrix cores see it.  Half of that exponent goes to the keys' scales and half to the queries', so that
+// neither overflows before the scores do (keys up to 2^114, queries of any size).
+constexpr float kCode = 1.0f / (1 << 24), kKeys = 1 << 12;
+
+// The grids of a wave's tile in LDS, token by token: scales in fp32 (of keys times kKeys, of values times the wave's power
+// of two) and -z in fp16.  Written by the lane that holds a token's word, read by the lanes that need eight.
 template <int NG>
 struct TileGrids {
     float scale[2][NG][kKvTile];
@@ -230,7 +234,7 @@ struct TileGrids {
             float s = grid_scale_of(grid[g]);
             const bool odd = !(s == s);
             const _Float16 c = __builtin_bit_cast(f16x2, grid[g])[0];
-            if (side) s = odd ? 0.0f : s * vscale;
+            s = side ? (odd ? 0.0f : s * vscale) : s * kKeys;
             if (none && !side && (none >> (32 + tok) & 1)) s = __builtin_nanf("");
             scale[side][g][tok] = gone ? 0.0f : s;
             zero[side][g][tok] = __builtin_bit_cast(uint16_t, gone || odd ? (_Float16)0.0f : c - (_Float16)8.0f);
@@ -272,7 +276,6 @@ __device__ __forceinline__ void value_frags(f16x8 f[2], const u32x4 &w, int j) {
     f[0] = __builtin_bit_cast(f16x8, a);
     f[1] = __builtin_bit_cast(f16x8, b);
 }
-constexpr float kCode = 1.0f / (1 << 24);  // of a code of 1
 
 __device__ __forceinline__ floatx4 mma(f16x8 a, f16x8 b, floatx4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
@@ -332,13 +335,14 @@ struct Queries {
             }
             sum[g] = xor_add(xor_add(s, 16), 32) * kCode;
         }
-        scale = ldexpf(a.scale, 24 - up);
+        scale = ldexpf(a.scale, 12 - up);
     }
 };
 
 __device__ __forceinline__ bool hidden(bool there, int slot, int sees) { return !there || slot >= sees; }
 
-// Scores (x of the queries in registers, or the lane's part of what share_queries() left in LDS) of the lane's eight tokens in the columns, in log2 and less the columns' `base`, before any mask.
+// Scores of the lane's eight tokens in the columns, in log2 and less the columns' `base`, before any mask.  The queries are
+// in registers, or `shared`: the lane's part of fragments in LDS.
 template <int D64, int NG, int NT, bool kTight>
 __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile, const TileGrids<NG> &grids, const Queries<D64, NG> q[NT],
                                        const f16x8 *shared, const float base[NT]) {
@@ -360,7 +364,7 @@ __device__ __forceinline__ void scores(float s[NT][8], const Tile<D64, NG> &tile
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int c = 0; c < NT; ++c) {  // (kCode in acc and sum leaves room for any scale)
+                for (int c = 0; c < NT; ++c) {
                     const float v = fmaf((float)zero[4 * t + i], q[c].sum[g], acc[c][i]);
                     s[c][4 * t + i] = g == 0 ? scale[i] * v : fmaf(scale[i], v, s[c][4 * t + i]);
                 }
@@ -469,7 +473,8 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
             all += v.x == kNegInf ? v.y : v.y * __builtin_amdgcn_exp2f(v.x - m);  // (a NaN stays)
         }
         const float inv = all == 0.0f ? 0.0f : 1.0f / all;
-        const float f = share_in(s.top(c), m) / (s.vscale * kCode) * (whole ? inv : 1.0f);
+        // (in this order nothing overflows that the result does not)
+        const float f = share_in(s.top(c), m) * inv * (1.0f / kCode), scale = 1.0f / s.vscale;
         const int64_t stat = ((int64_t)(blockIdx.x + sh.b) * a.pool.heads + h) * a.cols + col0 + 16 * c;
         if (r < left) {
 #pragma unroll
@@ -477,7 +482,7 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
                 const float k = xor_add(xor_add(s.corr[c][g], 16), 32) * kCode;
 #pragma unroll
                 for (int d = g * (D / 16) / NG; d < (g + 1) * (D / 16) / NG; ++d)
-                    *reinterpret_cast<floatx4 *>(smem + (wave * kept + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f;
+                    *reinterpret_cast<floatx4 *>(smem + (wave * kept + r) * D + 16 * d + 4 * kb) = (s.acc[c][d] * (d & 1 ? 0.0625f : 1.0f) + k) * f * scale;
             }
             if (wave == 0 && kb == 0) {
                 if (!whole)
@@ -690,20 +695,20 @@ __device__ __forceinline__ void combine(const AttnArgs &a, int col, int h, int b
     for (int w = 0; w < kKvWaves; ++w) m = fmaxf(m, red[0][w]);
     for (int x = threadIdx.x; x < seg.n; x += kKvThreads) {
         const float2 v = a.stat[at0 + x * step];
-        const float f = share_in(v.x, m);
-        share[x] = f;
-        l += v.x == kNegInf ? v.y : v.y * f;
+        share[x] = v.x == kNegInf ? v.y : v.y * share_in(v.x, m);  // (a NaN stays)
+        l += share[x];
     }
     for (int o = 1; o < kWave; o *= 2) l = xor_add(l, o);
     if (lane == 0) red[1][wave] = l;
     __syncthreads();
     l = 0.0f;
     for (int w = 0; w < kKvWaves; ++w) l += red[1][w];
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const int mine = threadIdx.x / kRow, d4 = threadIdx.x % kRow;
     floatx4 o = {};
     if (mine < kLanes) {
 #pragma unroll 4
-        for (int x = mine; x < seg.n; x += kLanes) o += share[x] * *reinterpret_cast<const floatx4 *>(a.part + (at0 + x * step) * D + 4 * d4);
+        for (int x = mine; x < seg.n; x += kLanes) o += share[x] * inv * *reinterpret_cast<const floatx4 *>(a.part + (at0 + x * step) * D + 4 * d4);
     }
     sums[threadIdx.x] = o;
     __syncthreads();
@@ -711,7 +716,7 @@ __device__ __forceinline__ void combine(const AttnArgs &a, int col, int h, int b
         for (int y = 1; y < kLanes; ++y) o += sums[y * kRow + threadIdx.x];
         uint16_t *to = a.o + result_at(a, b, h, col, D) + 4 * threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) to[i] = result16(a, l == 0.0f ? 0.0f : o[i] / l);
+        for (int i = 0; i < 4; ++i) to[i] = result16(a, o[i]);
     }
 }
 template <int D64>
@@ -749,7 +754,10 @@ constexpr int weigh_bytes(int tiles) {
 
 // weight[token] = decay weight[token] + the sum of p over the columns, once the columns' maxima and sums are known.  Only
 // the keys are read again; the same instructions give the same scores.  The queries are in LDS, up to kWeighTiles tiles of
-// them, and each of the wave's tiles of tokens goes through all; more columns take further passes.
+// them, and each of the wave's tiles of tokens goes through all; more columns take further passes.  Bound by vector
+// instructions (260 a tile): 32 sequences of up to 16384 tokens, 64 heads on 8, take 64-67 us with the joins of their
+// segments, 3 TB/s.  (The scores themselves, kept from the first pass, would be 4 bytes a token and column to write and to
+// read where the keys are 68 bytes a token.)
 template <int D64, int NG>
 __device__ __forceinline__ void weigh(const AttnArgs &a, int item, int h, unsigned char *smem) {
     constexpr int KW = 2 * D64;

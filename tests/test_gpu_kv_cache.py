@@ -192,11 +192,12 @@ def test_values_of_very_different_size(dt):
     assert (np.abs(o - ref)[np.isfinite(limit)] <= limit[np.isfinite(limit)]).all()
 
 
-@pytest.mark.parametrize("power", [-100, -40, 40, 100])
-def test_bf16_over_its_range(power):
-    """Queries times 2^power against keys times 2^-power, and values times 2^power: bf16's exponents, not fp16's."""
+@pytest.mark.parametrize("lens", [[200, 77], [100, 1]])
+@pytest.mark.parametrize("power", [-110, -100, -40, 40, 100, 112, 120])
+def test_bf16_over_its_range(power, lens):
+    """Queries times 2^power against keys times 2^-power, and values times 2^power: bf16's exponents, not fp16's; split and not."""
     torch = torch_mod()
-    B, H, Hq, D, page, lens = 2, 1, 4, 64, 16, [200, 77]
+    B, H, Hq, D, page = 2, 1, 4, 64, 16
     pool = kv_ref.Pool(30, H, D, page, 0, False, seed=4)
     pool.ks = kv_ref.bf16_round(pool.ks * np.float32(2.0 ** -power))
     pool.vs = kv_ref.bf16_round(pool.vs * np.float32(2.0 ** power))
