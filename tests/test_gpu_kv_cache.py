@@ -85,7 +85,11 @@ CASES = [(1, [1], 1, 1, 1, 64, 0, 16, False, "fp16"),
          (2, [333, 40], 16, 32, 2, 64, 32, 32, False, "bf16"),  # 256 columns
          (1, [130], 16, 11, 1, 192, 0, 64, True, "fp16"),
          (3, [900, 1, 64], 2, 40, 2, 128, 128, 64, False, "bf16"),
-         (2, [50, 700], 3, 33, 3, 256, 0, 16, True, "fp16")]
+         (2, [50, 700], 3, 33, 3, 256, 0, 16, True, "fp16"),
+         (2, [300, 1041], 4, 20, 4, 128, 32, 16, False, "fp16"),
+         (2, [800, 3], 5, 8, 2, 128, 32, 64, True, "bf16"),
+         (1, [700], 8, 9, 3, 128, 64, 128, False, "bf16"),
+         (2, [7, 450], 6, 10, 2, 128, 64, 16, False, "fp16")]
 
 
 @pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(x) for x in c if not isinstance(x, list)))
