@@ -28,8 +28,9 @@
 // Bound by memory where the cache is long: one sequence of 131072 tokens, 64 heads on 8
 // of 128 (143 MB), takes 35-36 us and 5.5 to join, 32 of up to 16384 (346 MB) 81-84; while its
 // tiles run it reads 5.4-5.7 TB/s, and start, first loads and the waves' join take the
-// rest (6-8 us).  With small groups and several column tiles by vector instructions: 8
-// drafted tokens of 8 x 8191 in groups of 32 issue 960 a tile and take 44 us.
+// rest (6-8 us).  With small groups and several column tiles by latency at two waves a
+// SIMD: 8 drafted tokens of 8 x 8191 in groups of 32 issue 960 vector instructions a
+// tile, their units busy a third of the time, and take 44 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -754,9 +755,9 @@ constexpr int weigh_bytes(int tiles) {
 
 // weight[token] = decay weight[token] + the sum of p over the columns, once the columns' maxima and sums are known.  Only
 // the keys are read again; the same instructions give the same scores.  The queries are in LDS, up to kWeighTiles tiles of
-// them, and each of the wave's tiles of tokens goes through all; more columns take further passes.  Bound by vector
-// instructions (260 a tile): 32 sequences of up to 16384 tokens, 64 heads on 8, take 64-67 us with the joins of their
-// segments, 3 TB/s.  (The scores themselves, kept from the first pass, would be 4 bytes a token and column to write and to
+// them, and each of the wave's tiles of tokens goes through all; more columns take further passes.  Vector
+// instructions (260 a tile) are busy half of the time: 32 sequences of up to 16384 tokens, 64 heads on 8, take 64-67 us with
+// the joins of their segments, 3 TB/s; loading the next tile ahead changed nothing.  (The scores themselves, kept from the first pass, would be 4 bytes a token and column to write and to
 // read where the keys are 68 bytes a token.)
 template <int D64, int NG>
 __device__ __forceinline__ void weigh(const AttnArgs &a, int item, int h, unsigned char *smem) {
