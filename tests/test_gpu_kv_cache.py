@@ -138,6 +138,33 @@ def test_long_rows_are_split_and_deterministic(dt):
     check_attention(short, *cut[:3], dt, "cut")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("cols", [11, 17])
+@pytest.mark.parametrize("D,g", [(D, g) for D in (64, 128, 192, 256) for g in (32, 64, 128, 0) if D % (g or D) == 0 and g != D])
+def test_every_kernel_repeats_its_bits(D, g, cols, dt):
+    """One and two tiles of columns, every head and group: the same bits each time, with other work of the same kernel between."""
+    torch = torch_mod()
+    B, H, page, lens = 3, 2, 32, [1025, 1400, 77]
+    rng = np.random.default_rng(D + g + cols)
+    width = -(-max(lens) // page)
+    pool = kv_ref.Pool(B * width + 1, H, D, page, g, False, seed=D + g)
+    table = tables(rng, B * width + 1, B, width)
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    q, q64 = make_queries((B, 1, cols * H, D), dt, 17 + cols)
+    other = make_queries((B, 1, cols * H, D), dt, 18 + cols, spread=4.0)[0].cuda()
+    q, table_d, lens_d = q.cuda(), ints(table), ints(lens)
+    ref, tol, rms, weight, wtol = kv_ref.attention(pool, q64, table, lens, D ** -0.5, dt, 0.0)
+    first = None
+    for i in range(16):
+        got = gq.kv_attention(q, cache, table_d, lens_d, decay=0.0), cache.weight.clone()
+        if first is None:
+            first = got
+            check_attention(got[0], ref, tol, rms, dt, f"{D} {g} {cols} {dt}")
+            assert (np.abs(host(cache.weight).astype(np.float64) - weight) <= wtol).all()
+        assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1]), i
+        gq.kv_attention(other, cache, table_d, lens_d)
+
+
 @pytest.mark.parametrize("page", [16, 32, 64])
 def test_missing_pages_and_odd_lengths(page):
     """Table entries outside the pool and lengths outside the table: those tokens are not there."""
