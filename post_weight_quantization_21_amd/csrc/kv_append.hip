@@ -51,15 +51,16 @@ __device__ __forceinline__ float partner(float v) {
     }
 }
 
-// The range of a group, which always holds 0, and the sum of its values: no number if one of them is none.
+// The range of a group, which always holds 0, and the sum of its values times 0: no number if one of them is not finite.  (The
+// values' own sum reaches both infinities over lanes whose values are finite.)
 struct Range {
-    float lo, hi, sum;
+    float lo, hi, none;
     template <int kStep, int W>  // over W neighbouring lanes
     __device__ __forceinline__ void reduce() {
         if constexpr (kStep < W) {
             lo = fminf(lo, partner<kStep>(lo));
             hi = fmaxf(hi, partner<kStep>(hi));
-            sum += partner<kStep>(sum);
+            none += partner<kStep>(none);
             reduce<2 * kStep, W>();
         }
     }
@@ -77,7 +78,7 @@ struct Grid4 {
         s = symmetric ? fmaxf(-g.lo, g.hi) * (1.0f / 7.0f) : (g.hi - g.lo) * (1.0f / 15.0f);
         s = (float)(__bf16)s;
         if (s == 0.0f) s = 1.0f;
-        bad = !(s < __builtin_inff()) || !(g.sum == g.sum);  // an infinite value makes s infinite
+        bad = !(s < __builtin_inff()) || !(g.none == g.none);
         m = s < 0x1p-100f ? 0x1p100f : s > 0x1p100f ? 0x1p-100f : 1.0f;
         ss = s * m;
         r = 1.0f / ss;
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
         for (int e = 0; e < 8; e += 2) {
             range.lo = fminf(range.lo, fminf(f[e], f[e + 1]));
             range.hi = fmaxf(range.hi, fmaxf(f[e], f[e + 1]));
-            range.sum += f[e] + f[e + 1];
+            range.none = fmaf(f[e], 0.0f, fmaf(f[e + 1], 0.0f, range.none));
         }
         range.template reduce<1, (GROUP == 192 ? 32 : GROUP / 8)>();
         const Grid4 g(range, a.symmetric);
