@@ -810,8 +810,10 @@ __device__ __forceinline__ void weigh(const AttnArgs &a, int item, int h, unsign
 #pragma unroll
                     for (int g = 0; g < NG; ++g) k.sum[g] = q.sum[g];
                     k.scale = q.scale;
-                    k.base = m == kNegInf ? 0.0f : m;
-                    k.inv = l == 0.0f || col >= a.cols ? 0.0f : 1.0f / l;
+                    // Where the sum is no number, so is base, and inv is 1: what the column sees gets no number, what is hidden from it 0.
+                    const bool none = !(l == l);
+                    k.base = none ? l : m == kNegInf ? 0.0f : m;
+                    k.inv = l == 0.0f || col >= a.cols ? 0.0f : none ? 1.0f : 1.0f / l;
                     k.sees = q.sees;
                 }
             }
