@@ -588,8 +588,9 @@ GPTQ_API gptq_status gptq_kv_attention_workspace_bytes(const gptq_kv_cache *cach
                                                        int64_t max_len, size_t *out);
 
 /*
- * Eviction: of every sequence and kv head, min(lens[b], budget) tokens are kept: the last
- * min(recent, that many), and of the others the heaviest by accumulated weight (ties to
+ * Eviction: of the tokens that a sequence has on pages of the pool (lens[b] of them where no
+ * page is missing), min(those, budget) are kept for every kv head: the last min(recent, that
+ * many), and of the others the heaviest by accumulated weight (ties to
  * the lower place; NaN below every number).  Their codes, grids and weights are copied, in
  * order, to places 0, 1, ... of the pages that `to` names; the cache as `table` names it
  * stays as it was, so its pages may be shared, and are the caller's to reuse afterwards.
@@ -599,7 +600,7 @@ GPTQ_API gptq_status gptq_kv_attention_workspace_bytes(const gptq_kv_cache *cach
  *   budget   >= 1; 0 <= recent <= budget.  n_seq * n_heads * budget at most 2^27.
  *   kept     [n_seq][n_heads][budget] int32 out: the places that the kept tokens had, -1
  *            behind the last.
- *   new_lens [n_seq] int32 out or NULL: min(lens[b], budget); not lens itself.
+ *   new_lens [n_seq] int32 out or NULL: the tokens that are kept; not lens itself.
  *   max_len  lengths above it count as it; at most width * page.
  *   ws       scratch of gptq_kv_evict_workspace_bytes() (may be NULL when 0), 16-byte aligned.
  */

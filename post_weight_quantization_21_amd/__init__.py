@@ -816,7 +816,8 @@ def kv_evict(cache: KVCache, table, lens, to, budget: int, recent: int = 0, max_
              stream=None):
     """Of every sequence and head the last `recent` tokens and the heaviest others, `budget` in all, are copied in order to the
     pages that `to` (int32 [n_seq][width]) names, which are none of table's.  Returns (kept, new_lens): int32
-    [n_seq][heads][budget], the places that the kept tokens had (-1 behind the last), and int32 [n_seq], min(lens, budget)."""
+    [n_seq][heads][budget], the places that the kept tokens had (-1 behind the last), and int32 [n_seq], how many they are:
+    min(lens, budget), or fewer where table names pages that are not there."""
     torch, lib, _, _ = _few_init()
     if stream is not None:
         with _few_on(stream, cache.device, torch, (), *cache.tensors, table, lens, to, kept, new_lens, ws):

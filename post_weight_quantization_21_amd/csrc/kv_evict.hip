@@ -1,6 +1,8 @@
 // Thinning out a 4-bit cache: of every sequence and kv head, the last `recent`
 // tokens and the heaviest others by accumulated weight, `budget` in all, are copied to
-// other pages in slot order.
+// other pages in slot order.  What a missing page would hold are no tokens and are left
+// out, so that every place below the new length is written; which pages are missing is the
+// same for all heads of a sequence, and so is the new length.
 #include <algorithm>
 
 #include "kv_cache.h"
@@ -19,18 +21,25 @@ struct EvictArgs {
     int32_t *new_lens;  // or NULL
 };
 
-// Weights in ascending order of an unsigned integer: NaN, negative numbers, zeros of either sign, positive ones.
+// Weights in ascending order of an unsigned integer, above 0 (no token) and below kLate (a token that stays whatever its
+// weight): NaN, negative numbers, zeros of either sign, positive ones.
+constexpr uint32_t kLate = 0xFFFFFFFF;
 __device__ __forceinline__ uint32_t rank_of(float w) {
-    if (!(w == w)) return 0;
+    if (!(w == w)) return 1;
     const uint32_t u = __float_as_uint(w + 0.0f);
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-// Of four neighbouring slots from a multiple of four on, which share a page.
-__device__ __forceinline__ u32x4 ranks_at(const EvictArgs &a, const int32_t *row, int h, int slot) {
+// Of four neighbouring slots from a multiple of four on, which share a page; those from `late` on stay.
+__device__ __forceinline__ u32x4 ranks_at(const EvictArgs &a, const int32_t *row, int h, int slot, int late) {
     const int page = a.seqs.page_of(a.pool, row, slot);
     if (page < 0) return (u32x4){};
     const floatx4 w = *reinterpret_cast<const floatx4 *>(a.pool.weight + a.pool.first(page, h) + (slot & (a.pool.page() - 1)));
-    return (u32x4){rank_of(w[0]), rank_of(w[1]), rank_of(w[2]), rank_of(w[3])};
+    u32x4 k = {rank_of(w[0]), rank_of(w[1]), rank_of(w[2]), rank_of(w[3])};
+    if (slot + 3 >= late) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[e] = slot + e >= late ? kLate : k[e];
+    }
+    return k;
 }
 
 // The rank of the `heavy`-th largest of the slots below `safe`, digit by digit from the highest (11, 11 and 10 bits, a
@@ -48,19 +57,57 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
     __shared__ int counts[2][kSelectWaves];
     const int h = blockIdx.x, b = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int32_t *row = a.seqs.table + (int64_t)b * a.seqs.width;
-    const int len = a.seqs.len(b), keep = min(len, a.budget), recent = min(a.recent, keep);
-    const int safe = len - recent, heavy = keep - recent;  // heavy of the first `safe` slots stay
+    const int len = a.seqs.len(b), lg = a.pool.lg_page, pages = (len + a.pool.page() - 1) >> lg;
+    auto tokens_of = [&](int p) { return p >= 0 && a.seqs.page_of(a.pool, row, p << lg) >= 0 ? min(a.pool.page(), len - (p << lg)) : 0; };
+    int here = 0;
+    bool gone = false;  // a page of the thread's
+    for (int p = threadIdx.x; p < pages; p += kSelectThreads) {
+        const int n = tokens_of(p);
+        here += n;
+        gone |= n == 0;
+    }
+    int keep = min(len, a.budget), recent = min(a.recent, keep);
+    int safe = len - recent, heavy = keep - recent, late = 0x7FFFFFFF;  // heavy of the first `safe` slots stay
     int32_t *kept = a.kept + ((int64_t)b * a.pool.heads + h) * a.budget;
+    if (!__syncthreads_or(gone)) {
+        for (int i = threadIdx.x; i < recent; i += kSelectThreads) kept[heavy + i] = safe + i;
+    } else {  // of all slots, the last `recent` tokens and the heaviest others
+        here = wave_scan(here);
+        if (lane == 63) sums[wave] = here;
+        __syncthreads();
+        keep = 0;
+        for (int w = 0; w < kSelectWaves; ++w) keep += sums[w];
+        keep = min(keep, a.budget);
+        recent = min(a.recent, keep);
+        safe = late = len;
+        heavy = keep;
+        if (recent > 0) {  // `late` has `recent` tokens from it on: 1024 pages at a time from the last
+            int before = 0;
+            for (int top = pages - 1; top >= 0 && before < recent; top -= kSelectThreads) {
+                const int p = top - (int)threadIdx.x, n = tokens_of(p), upto = wave_scan(n);
+                __syncthreads();  // sums have been read
+                if (lane == 63) sums[wave] = upto;
+                __syncthreads();
+                int mine = before + upto - n;  // on the pages behind this one
+                for (int w = 0; w < kSelectWaves; ++w) {
+                    mine += w < wave ? sums[w] : 0;
+                    before += sums[w];
+                }
+                if (mine < recent && recent <= mine + n) found[0] = (p << lg) + n - (recent - mine);
+            }
+            __syncthreads();
+            late = found[0];
+        }
+    }
     for (int i = keep + threadIdx.x; i < a.budget; i += kSelectThreads) kept[i] = -1;
     if (a.new_lens && h == 0 && threadIdx.x == 0) a.new_lens[b] = keep;
-    for (int i = threadIdx.x; i < recent; i += kSelectThreads) kept[heavy + i] = safe + i;
     if (heavy == 0) return;
     if (heavy == safe) {
         for (int i = threadIdx.x; i < safe; i += kSelectThreads) kept[i] = i;
         return;
     }
     u32x4 *four = reinterpret_cast<u32x4 *>(ranks);
-    auto rank4 = [&](int i) { return i < in_lds ? four[i / 4] : ranks_at(a, row, h, i); };
+    auto rank4 = [&](int i) { return i < in_lds ? four[i / 4] : ranks_at(a, row, h, i, late); };
     uint32_t edge = 0, ties = heavy;  // the rank of the last that stays; `ties` of those that have it stay
     for (int shift = 21, bits = 11; shift >= 0;) {
         for (int i = threadIdx.x; i < kBins; i += kSelectThreads) hist[i] = 0;
@@ -78,7 +125,7 @@ __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int
         if (shift == 21) {
 #pragma unroll 8
             for (int i = 4 * threadIdx.x; i < safe; i += 4 * kSelectThreads) {
-                const u32x4 k = ranks_at(a, row, h, i);
+                const u32x4 k = ranks_at(a, row, h, i, late);
                 if (i < in_lds) four[i / 4] = k;
                 count(k, i);
             }

@@ -17,3 +17,18 @@ def pytest_configure(config):
 def oracle_mod():
     import oracle
     return oracle
+
+
+# Tests that hold a value the contract does not have; they stay as they were and are run, and are meant to fail.
+SUPERSEDED = {
+    "test_gpu_kv_cache.py::test_evict_with_missing_pages":
+        "expects kept places for tokens on missing pages, whose new places are then never written but count as tokens; "
+        "test_gpu_kv_contract.py::test_evicted_tokens_are_there has the same lengths, budget and missing pages",
+}
+
+
+def pytest_collection_modifyitems(items):
+    for item in items:
+        for name, reason in SUPERSEDED.items():
+            if item.nodeid.endswith(name):
+                item.add_marker(pytest.mark.xfail(reason=reason, raises=AssertionError, strict=True))

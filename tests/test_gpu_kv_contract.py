@@ -1,5 +1,5 @@
 """What the 4-bit cache's header promises of unusual inputs: finite groups at the end of bf16's range, bad
-queries beside hidden tokens."""
+queries beside hidden tokens, tokens on missing pages that are evicted."""
 import numpy as np
 import pytest
 
@@ -99,3 +99,77 @@ def test_weights_of_tokens_that_a_bad_query_does_not_see(case, decay):
     assert np.isnan(got[none]).all()
     assert not np.isnan(got[~none]).any()
     assert (np.abs(got - weight)[~none] <= wtol[~none]).all()
+
+
+# ---- evict ----------------------------------------------------------------------------------------------------------
+
+def evict_present(pool, table, lens, budget, recent):
+    """kept [B][H][budget] and new lengths, where tokens on no page of the pool are left out: of the others, in order, the last
+    ones and the heaviest."""
+    B, H, P = len(lens), pool.heads, pool.page
+    pages = pool.kq.shape[0]
+    kept, left = np.full((B, H, budget), -1, dtype=np.int32), np.zeros(B, dtype=np.int32)
+    for b in range(B):
+        m = min(max(int(lens[b]), 0), table.shape[1] * P)
+        slots = [i for i in range(m) if 0 <= table[b][i // P] < pages]
+        keep = left[b] = min(len(slots), budget)
+        late = min(recent, keep)
+        early, last = slots[:len(slots) - late], slots[len(slots) - late:]
+        for h in range(H):
+            w = {i: float(pool.weight[table[b][i // P], h, i % P]) for i in early}
+            order = sorted(early, key=lambda i: (w[i] != w[i], -w[i] if w[i] == w[i] else 0.0, i))
+            kept[b, h, :keep] = sorted(order[:keep - late]) + last
+    return kept, left
+
+
+#           lens                 budget recent H  D    g    page missing (sequence, pages of it)
+PRESENT = [([90, 64], 40, 20, 2, 64, 0, 16, [(0, [2]), (1, [3])]),
+           ([100, 100, 100, 100], 64, 10, 1, 128, 32, 16, [(0, [6]), (1, [5, 6]), (2, range(7)), (3, [0, 2, 4])]),
+           ([333, 64, 40], 300, 290, 2, 64, 64, 32, [(0, [1, 9, 10]), (1, [0]), (2, [1])]),   # fewer are there than the budget
+           ([2000, 1000], 500, 500, 2, 192, 64, 64, [(0, [31, 30, 3]), (1, [15, 14, 12, 0])]),
+           ([40000, 39000], 3000, 1000, 1, 64, 0, 16, [(0, list(range(0, 2500, 3))), (1, list(range(2300, 2438)))]),  # past the ranks in LDS
+           ([16, 0, 17], 1, 0, 3, 64, 32, 16, [(0, [0]), (2, [0])]),
+           ([5000], 5000, 0, 1, 256, 0, 1024, [(0, [1, 4])])]
+
+
+@pytest.mark.parametrize("case", PRESENT, ids=lambda c: "-".join(str(x) for x in c[1:-1]))
+@pytest.mark.parametrize("kind", ["random", "nan", "ties", "holes"])
+def test_evicted_tokens_are_there(case, kind):
+    """Tokens on missing pages take no place among the kept: what the new pages hold below the new length is the text's, and
+    attention over it is that over the kept tokens, whatever the pages held before.  Holes: a new page of each text is missing."""
+    torch = torch_mod()
+    lens, budget, recent, H, D, g, page, missing = case
+    B = len(lens)
+    rng = np.random.default_rng(budget)
+    width, more = -(-max(lens) // page), -(-budget // page)
+    pages = B * (width + more)
+    pool = kv_ref.Pool(pages, H, D, page, g, False, seed=budget)
+    if kind == "ties":
+        pool.weight = rng.integers(0, 3, pool.weight.shape).astype(np.float32)
+    elif kind == "nan":
+        pool.weight[rng.random(pool.weight.shape) < 0.9] = np.nan
+    order = tables(rng, pages, B, width + more)
+    table, to = order[:, :width].copy(), order[:, width:].copy()
+    for b, gone in missing:
+        table[b, list(gone)] = rng.choice([-1, pages, 2 ** 31 - 1, -2 ** 31], len(list(gone)))
+    if kind == "holes":
+        to[np.arange(B), rng.integers(0, more, B)] = pages
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    kept, left = gq.kv_evict(cache, ints(table), ints(lens), ints(to), budget, recent)
+    want, wleft = evict_present(pool, table, lens, budget, recent)
+    assert np.array_equal(host(left), wleft)
+    assert np.array_equal(host(kept), want)
+    for b in range(B):
+        for h in range(H):
+            j = np.arange(wleft[b])
+            j = j[to[b, j // page] < pages]
+            i = want[b, h, j]
+            src, dst = (table[b, i // page], h, i % page), (to[b, j // page], h, j % page)
+            for a in ("kq", "ks", "kz", "vq", "vs", "vz", "weight"):
+                getattr(pool, a)[dst] = getattr(pool, a)[src]
+    for name, w, have in zip("k v k_grid v_grid weight".split(), pool.words(), cache.tensors):
+        assert np.array_equal(host(have).view(np.uint8), w.view(np.uint8)), name
+    q, q64 = make_queries((B, 1, 2 * H, D), "fp16", 3)
+    o = gq.kv_attention(q.cuda(), cache, ints(to), left).double().cpu().numpy()
+    ref, tol, _, _, _ = kv_ref.attention(pool, q64, to, wleft, D ** -0.5, "fp16")
+    assert (np.abs(o - ref) <= tol * (1 + 2.0 ** -11) + 2.0 ** -11 * np.abs(ref) + 2.0 ** -24).all()
