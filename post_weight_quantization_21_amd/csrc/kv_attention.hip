@@ -3,19 +3,30 @@
 // The n G columns of a kv head (n tokens, G query heads each) are the B operand of
 // v_mfma_f32_16x16x32_f16, sixteen at a time.  A wave takes tiles of 32 cached tokens:
 //   S[token][column] = s_k (sum_d q_k x - z_k X),  X = sum_d x
-// with the codes as exact subnormal fp16 numbers (key_frag), so nothing but the fp32 sums
-// rounds.  The A operand's row r of half t is token 8 (r / 4) + 4 t + r % 4, so a lane ends
-// up with S of eight tokens next to each other in one column, which is what the second
-// product
+// with the codes as fp16 numbers of one spacing (key_frag).  The A operand's row r of half
+// t is token 8 (r / 4) + 4 t + r % 4, so a lane ends up with S of eight tokens next to each
+// other in one column, which is what the second product
 //   O[dim][column] = sum_token q_v (p s_v) - sum_token z_v (p s_v)
 // wants of its B operand: p never leaves the lane.  It is held there as p s_v in fp16,
 // scaled by a power of two that follows the largest s_v: for bf16 results one value, a
 // rounding of 2^-11 of each term where theirs is 2^-8; for fp16 results two, the second
-// what the first leaves (with one their error against 64 bits is 1.5 times a single
-// rounding's; with two 16 x 4096 tokens of 32 heads take 52 us instead of 46).
+// what the first leaves (with one their error against 64 bits is 1.3 times a single
+// rounding's; 16 x 4096 tokens of 32 heads take 53 us instead of 47, eight drafted tokens 45
+// instead of 42).
 // Values s_v more than 2^20 below the largest lose bits, those more than 2^31 below it vanish.
-// The two sums of O are 15 / 8 times what those of q - 8 and z - 8 would be, which costs a
-// bit of fp32 and saves an instruction a pair of codes.
+//
+// What the sums lose: an instruction adds eight neighbouring products at a time to the fp32
+// sum, each addition rounded to nearest, after it has cut off what lies 2^24 below the
+// largest of the products' powers of two; there a subnormal operand counts as 2^-14
+// (measured).  A code of one is therefore held as high as fp16's even spacing reaches, 2^-21
+// and 2^-17: p s_v and queries lose what is below 2^-17 of the largest of their eight.  With
+// codes in their lowest bits, which saves an instruction a word, that is 2^-14, always
+// towards 0, and adds up over the tokens.  Errors against 64 bits (codes in the lowest bits;
+// here; the result's own rounding): fp16, 16 x 4096 tokens 2.39e-4, 2.08e-4, 2.08e-4; bf16,
+// 131072 tokens 1.86e-3, 1.66e-3, 1.65e-3; weights of a window of 16 tokens 1.7e-6, 7e-8.
+// Times: 52.3, 53.4 us; 35.9, 36.1; 32 x 16384 tokens 83.5, 84.5.  The sums of q are 15 / 8
+// as large as those of q - 8 would be, a bit of fp32; taking 8 p s_v off by more matrix
+// instructions (tried with codes in the lowest bits) took 12 us more of 83 and left 2.29e-4.
 //
 // Queries of both types enter as fp16 times a power of two of their row, which takes no
 // bit from a value above 2^-25 of the row's largest.
@@ -217,7 +228,7 @@ struct Tile {
 
 // A code of 1 as the matrix cores see it.  Half of that exponent goes to the keys' scales and half to the queries', so that
 // neither overflows before the scores do (keys up to 2^114, queries of any size).
-constexpr float kCode = 1.0f / (1 << 24), kKeys = 1 << 12;
+constexpr float kCode = 1.0f / (1 << 21), kKeys = 1 << 9;
 
 // The grids of a wave's tile in LDS, token by token: scales in fp32 (of keys times kKeys, of values times the wave's power
 // of two) and -z in fp16.  Written by the lane that holds a token's word, read by the lanes that need eight.
@@ -256,13 +267,13 @@ __device__ __forceinline__ void wave_fence() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// Codes as fp16, masked in place: subnormal numbers q 2^-24 or, four bits up, q 2^-20, which the matrix cores take as they
-// are (an instruction a pair; with q - 8 as normal numbers it would be two).
-__device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x000F000Fu; }
-__device__ __forceinline__ uint32_t high(uint32_t w) { return w & 0x00F000F0u; }
+// Codes as fp16, masked in place: bits 3 to 6, q 2^-21, and 7 to 10, q 2^-17.  Bit 10 is the lowest of the exponent, and numbers
+// below 2^-13 lie evenly, subnormal or not.
+__device__ __forceinline__ uint32_t low(uint32_t w) { return w & 0x00780078u; }
+__device__ __forceinline__ uint32_t high(uint32_t w) { return w & 0x07800780u; }
 __device__ __forceinline__ f16x8 key_frag(uint32_t w) {  // pairs 0 and 2 are 2^4 smaller: the queries' are 2^4 larger there
-    const uint32_t x = w >> 8;
-    const u32x4 f = {low(w), high(w), low(x), high(x)};
+    const uint32_t x = w << 3, y = w >> 5;
+    const u32x4 f = {low(x), high(x), low(y), high(y)};
     return __builtin_bit_cast(f16x8, f);
 }
 // Dims j and j + 1 (j = 0, 2) of the four of each unit, eight tokens.
@@ -270,7 +281,7 @@ __device__ __forceinline__ void value_frags(f16x8 f[2], const u32x4 &w, int j) {
     u32x4 a, b;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint32_t x = j ? w[i] >> 8 : w[i];
+        const uint32_t x = j ? w[i] >> 5 : w[i] << 3;
         a[i] = low(x);
         b[i] = high(x);
     }

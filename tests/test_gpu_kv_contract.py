@@ -1,5 +1,5 @@
 """What the 4-bit cache's header promises of unusual inputs: finite groups at the end of bf16's range, bad
-queries beside hidden tokens, tokens on missing pages that are evicted."""
+queries beside hidden tokens, tokens on missing pages that are evicted, small numbers beside large ones."""
 import numpy as np
 import pytest
 
@@ -173,3 +173,63 @@ def test_evicted_tokens_are_there(case, kind):
     o = gq.kv_attention(q.cuda(), cache, ints(to), left).double().cpu().numpy()
     ref, tol, _, _, _ = kv_ref.attention(pool, q64, to, wleft, D ** -0.5, "fp16")
     assert (np.abs(o - ref) <= tol * (1 + 2.0 ** -11) + 2.0 ** -11 * np.abs(ref) + 2.0 ** -24).all()
+
+
+# ---- bits -----------------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("n", [16, 32, 128])
+@pytest.mark.parametrize("D,g", [(64, 32), (64, 64), (128, 32), (128, 128), (192, 64), (256, 0)])
+def test_values_beside_larger_grids_keep_their_bits(D, g, n, dt):
+    """Queries of zero weigh n tokens alike, exactly.  Every eighth has a scale of 1 and nothing but zeros, the others scales of
+    2^-8 with 8 bits: all sums have 24 bits or fewer (15 n/8 < 2^8 down to 2^-15), so the result is the exact one, rounded once."""
+    torch = torch_mod()
+    H, page = 2, 16
+    group = g or D
+    rng = np.random.default_rng(D + n)
+    pool = kv_ref.Pool(n // page + 1, H, D, page, g, False, seed=D + n)
+    pool.vs = ((128 + rng.integers(0, 128, pool.vs.shape)) * 2.0 ** -15).astype(np.float32)
+    pool.vs[:, :, ::8] = 1.0
+    pool.vq[:, :, ::8] = np.repeat(pool.vz[:, :, ::8], group, axis=-1)
+    table = tables(rng, n // page + 1, 1, n // page)
+    q = torch.zeros(1, 1, 8 * H, D, dtype={"bf16": torch.bfloat16, "fp16": torch.float16}[dt])
+    o = gq.kv_attention(q.cuda(), kv_ref.cuda_cache(gq, torch, pool), ints(table), ints([n]))
+    vq, vs, vz, _ = pool.seq(table[0], n, "v")
+    v = np.repeat(vs.astype(np.float64), group, -1) * (vq - np.repeat(vz.astype(np.float64), group, -1))
+    want = torch.from_numpy(v.sum(1) / n).to(q.dtype)  # (fp64 holds it exactly)
+    assert torch.equal(o.cpu().view(H, 8, D), want[:, None].expand(H, 8, D))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,g", [(64, 32), (64, 64), (128, 32), (128, 128), (192, 64), (256, 0)])
+def test_scores_beside_larger_queries_keep_their_bits(D, g, dt):
+    """Every eighth value of a query is 256, where all keys are zero, the others 1 .. 2 with 8 bits: all sums of codes have 24 bits or
+    fewer (15 * 256 D / 8 < 2^17 down to 2^-7).  A score is then off by a rounding for each group and four more (its factors and
+    the base), each 2^-24 of what is added up, and exp2 by 2^-22, which p and its sum have alike."""
+    torch = torch_mod()
+    H, G, page, n = 2, 4, 16, 128
+    group = g or D
+    rng = np.random.default_rng(D + group)
+    pool = kv_ref.Pool(n // page + 1, H, D, page, g, False, seed=D)
+    pool.ks = ((128 + rng.integers(0, 128, pool.ks.shape)) * 2.0 ** -13).astype(np.float32)
+    pool.kq[..., ::8] = np.repeat(pool.kz, group, axis=-1)[..., ::8]
+    table = tables(rng, n // page + 1, 1, n // page)
+    x = (128 + rng.integers(0, 128, (1, 1, G * H, D))) / 128 * rng.choice([-1, 1], (1, 1, G * H, D))
+    x[..., ::8] = 256
+    q = torch.from_numpy(x).to({"bf16": torch.bfloat16, "fp16": torch.float16}[dt])
+    assert np.array_equal(q.double().numpy(), x)
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    gq.kv_attention(q.cuda(), cache, ints(table), ints([n]), scale=1.0, decay=0.0)
+    kq, ks, kz, _ = pool.seq(table[0], n, "k")
+    k = np.repeat(ks.astype(np.float64), group, -1) * (kq - np.repeat(kz.astype(np.float64), group, -1))
+    parts = x.reshape(H, G, 1, D) * k[:, None]  # [H][G][n][D]
+    s = parts.sum(-1)
+    p = np.exp(s - s.max(-1, keepdims=True))
+    p /= p.sum(-1, keepdims=True)
+    sizes = np.abs(parts.reshape(H, G, n, -1, group).sum(-1)).sum(-1)  # of what is added up over the groups
+    ng = D // group
+    off = 2 * ((ng + 4) * 2.0 ** -24 * (sizes + np.abs(s.max(-1, keepdims=True))).max() + 2.0 ** -22) + (n + 2) * 2.0 ** -24
+    want = p.sum(1)
+    got = host(cache.weight).astype(np.float64)[table[0, np.arange(n) // page], :, np.arange(n) % page].T
+    assert off < 1e-4
+    assert (np.abs(got - want) <= off * want + G * 2.0 ** -126).all()
