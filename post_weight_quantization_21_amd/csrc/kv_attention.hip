@@ -428,7 +428,7 @@ struct Sums {
 #pragma unroll
         for (int c = 0; c < NT; ++c) times(c, vscale / was);
     }
-    // A new base from the lane's scores.
+    // A new base from the lane's scores, of the columns that need one: what the others hold does not depend on who is beside them.
     __device__ __forceinline__ void raise(float s[NT][8]) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
@@ -437,7 +437,7 @@ struct Sums {
             for (int i = 1; i < 8; ++i) m = fmaxf(m, s[c][i]);
             m = xor_max(xor_max(m, 16), 32);
             const bool first = slack[c] == kNegInf;
-            if (first ? m > kNegInf : m > 0.0f) {
+            if (m > slack[c]) {
                 times(c, first ? 1.0f : __builtin_amdgcn_exp2f(-m));  // (of nothing, the first time)
                 sum[c] *= first ? 1.0f : __builtin_amdgcn_exp2f(-m);
                 base[c] += m;

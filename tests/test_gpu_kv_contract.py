@@ -1,5 +1,6 @@
 """What the 4-bit cache's header promises of unusual inputs: finite groups at the end of bf16's range, bad
-queries beside hidden tokens, tokens on missing pages that are evicted, small numbers beside large ones."""
+queries beside hidden tokens, tokens on missing pages that are evicted, small numbers beside large ones,
+rows beside each other."""
 import numpy as np
 import pytest
 
@@ -233,3 +234,30 @@ def test_scores_beside_larger_queries_keep_their_bits(D, g, dt):
     got = host(cache.weight).astype(np.float64)[table[0, np.arange(n) // page], :, np.arange(n) % page].T
     assert off < 1e-4
     assert (np.abs(got - want) <= off * want + G * 2.0 ** -126).all()
+
+
+# ---- rows beside each other -----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("lens,n,G,H,D,g,page", [([60, 1500], 1, 8, 2, 128, 128, 16), ([6000], 1, 4, 32, 64, 0, 64), ([4000, 900], 2, 10, 16, 128, 64, 32),
+                                                 ([3000, 2000], 1, 7, 20, 192, 64, 16), ([800, 333], 2, 9, 1, 256, 0, 64)])
+def test_rows_do_not_depend_on_the_rows_beside_them(lens, n, G, H, D, g, page, dt):
+    """One head's queries 40 times as large, zero, infinite or no numbers, so that the sums that a wave holds of them are raised at
+    other times or never: every other row keeps its bits."""
+    torch = torch_mod()
+    B = len(lens)
+    width = -(-max(lens) // page)
+    pool = kv_ref.Pool(B * width, H, D, page, g, False, seed=D + n)
+    table = tables(np.random.default_rng(D), B * width, B, width)
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    q, _ = make_queries((B, n, H * G, D), dt, 11, spread=2.0)
+    ref, _, _, _, _ = kv_ref.attention(pool, q.double().numpy(), table, lens, D ** -0.5, dt)
+    o = gq.kv_attention(q.cuda(), cache, ints(table), ints(lens)).cpu()
+    assert np.abs(o.double().numpy() - ref).max() < 0.05 * np.abs(ref).max()
+    for h in (0, G // 2, H * G - 1):
+        for times in (40.0, 0.0, float("inf"), float("nan")):
+            other = q.clone()
+            other[:, :, h] = other[:, :, h] * times if times != float("inf") else times
+            got = gq.kv_attention(other.cuda(), cache, ints(table), ints(lens)).cpu()
+            beside = [i for i in range(H * G) if i != h]
+            assert torch.equal(got[:, :, beside], o[:, :, beside]), (h, times)
