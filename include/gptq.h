@@ -573,14 +573,16 @@ GPTQ_API gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, i
  *   ws      scratch of gptq_kv_attention_workspace_bytes(), 16-byte aligned; the same
  *           sizes, n_seq no larger and max_len no larger need no more.
  * Of a code times a value of Q, what is below 2^-17 of the largest |Q| of the eight dims
- * around it (2^-35 of the row's) may be lost; keys of 2^114 and more may overflow, and so may a Q times
- * scale of 2^125 and more.  Sums and softmax are fp32.  p times the scale of a group of values
- * enters the second product as one fp16 value for bf16 results (2^-11 of each term), as
- * two for fp16 ones; of it, what is below 2^-17 of the largest of the eight tokens around it may
- * be lost, and 2^-31 of the row's largest p times the largest scale of the head's tokens, seen
- * by the row or not (a group of zeros has the scale 1).  The result is rounded once.  Deterministic.  A query that is not
- * finite, and one that sees a key or value that is none, has a row that is not finite or
- * NaN, and so have the weights of all that it sees; other rows are as without it.
+ * around it (2^-35 of the row's) may be lost; keys of 2^114 and more, and scale times Q of
+ * 2^125 and more, may overflow.  Sums and softmax are fp32.  p times the scale s of a group of
+ * values enters the second product as one fp16 value for bf16 results (2^-11 of each term),
+ * as two for fp16 ones; of it, what is below 2^-17 of the largest of the eight tokens around
+ * it may be lost, and 2^-30 of the largest p of the row times the largest s of the head, of
+ * tokens that the row does not see, too.  (A group of zeros has s = 1, and counts with it.)
+ * The result is rounded once.
+ * Deterministic.  A query that is not finite, and one that sees a key or value that is none,
+ * has a row that is not finite or NaN, and so have the weights of all that it sees; other
+ * rows are as without it.
  * n_seq * n_heads * ceil(n q_heads / n_heads / 16) at most 2^19.
  */
 GPTQ_API gptq_status gptq_kv_attention(const void *Q, gptq_dtype dtype, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq,

@@ -1,6 +1,6 @@
 """What the 4-bit cache's header promises of unusual inputs: finite groups at the end of bf16's range, bad
 queries beside hidden tokens, tokens on missing pages that are evicted, small numbers beside large ones,
-rows beside each other."""
+rows beside each other, values of very different size."""
 import numpy as np
 import pytest
 
@@ -261,3 +261,42 @@ def test_rows_do_not_depend_on_the_rows_beside_them(lens, n, G, H, D, g, page, d
             got = gq.kv_attention(other.cuda(), cache, ints(table), ints(lens)).cpu()
             beside = [i for i in range(H * G) if i != h]
             assert torch.equal(got[:, :, beside], o[:, :, beside]), (h, times)
+
+
+# ---- sizes beside each other ----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("sym", [False, True])
+@pytest.mark.parametrize("power", [-8, -16, -20, -24])
+def test_small_values_beside_a_token_of_zeros(power, sym, dt):
+    """An appended token whose values are zeros has grids with a scale of 1.  The others' p s_v is off by 2^-11 (one fp16 value) or
+    2^-21 (two), by 2^-30 of the largest p times 1, and by what is cut off, 2^-17 of the largest p s_v of eight tokens: of the eight
+    that the zeros are in that is 1 where their codes are 8 (symmetric grids; codes of 0 are no products)."""
+    torch = torch_mod()
+    H, G, D, g, page, n = 2, 4, 64, 32, 16, 40
+    pool = kv_ref.Pool(4, H, D, page, g, sym, seed=power + 40)
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    gen = torch.Generator().manual_seed(7)
+    K, V = (torch.randn(n, H, D, generator=gen) for _ in range(2))
+    V *= 2.0 ** power
+    V[7] = 0
+    K, V = (x.to({"bf16": torch.bfloat16, "fp16": torch.float16}[dt]) for x in (K, V))
+    table = np.array([[2, 0, 3]], dtype=np.int32)
+    gq.kv_append(K.cuda(), V.cuda(), cache, ints(table), ints([n]))
+    for side, x in (("k", K), ("v", V)):
+        q, s, z = kv_ref.fit(x.float().numpy(), g, sym)
+        for name, val in (("q", q), ("s", s), ("z", z)):
+            for t in range(n):
+                getattr(pool, side + name)[table[0, t // page], :, t % page] = val[t]
+    q, q64 = make_queries((1, 1, H * G, D), dt, 3)
+    o = gq.kv_attention(q.cuda(), cache, ints(table), ints([n])).double().cpu().numpy()
+    ref, tol, _, _, _ = kv_ref.attention(pool, q64, table, [n], D ** -0.5, dt)
+    vq, vs, vz, _ = pool.seq(table[0], n, "v")
+    largest = vs.max(-1)  # [H][n]; p is at most 1
+    if not sym:
+        largest[:, 7] = 0
+    largest = largest.reshape(H, n // 8, 8).max(-1).repeat(8, axis=-1)
+    # codes as the products have them (0 .. 15) are cut; what fp16 leaves of p s_v counts with the codes less their zero
+    cut = 2.0 ** -30 * np.abs(vq - np.repeat(vz, g, -1)).sum(1) + 2.0 ** -17 * (largest[..., None] * (vq > 0)).sum(1) * 2
+    cut = np.repeat(cut, G, 0)[None, None]
+    assert (np.abs(o - ref) <= (tol + cut) * (1 + kv_ref.HALF[dt]) + kv_ref.HALF[dt] * np.abs(ref) + (2.0 ** -25 if dt == "fp16" else 0)).all()
