@@ -564,7 +564,7 @@ GPTQ_API gptq_status gptq_kv_append(const void *K, int64_t ldk, const void *V, i
  *           ldq a multiple of 8; 1 <= n <= 16, q_heads a multiple of n_heads, at most 256
  *           times it.
  *   O       [n_seq * n][ldo] in Q's type, 2-byte aligned, no element in Q's memory.
- *   scale   finite and > 0 (usually head_dim^-1/2).
+ *   scale   > 0 and at most 2^127 (usually head_dim^-1/2).
  *   max_len lengths above it count as it; at most width * page.  It sets the launch's
  *           size: the closer to the longest sequence, the better.
  *   accumulate, decay  with accumulate, weight_t of each kv head becomes decay * weight_t

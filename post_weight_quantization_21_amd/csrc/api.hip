@@ -653,7 +653,8 @@ gptq_status gptq_kv_attention(const void *Q, gptq_dtype dtype, int64_t n_seq, in
     if (st != GPTQ_OK) return st;
     const int64_t row = q_heads * cache->head_dim;
     if (!few_dtype(dtype)) return fail(GPTQ_ERR_INVALID_ARG, "%s: queries must be fp16 or bf16", fn);
-    if (!(scale > 0.0f) || scale > 3.4e38f) return fail(GPTQ_ERR_INVALID_ARG, "%s: scale must be finite and > 0", fn);
+    if (!(scale > 0.0f) || scale > 0x1p127f)  // (times log2 e it is finite)
+        return fail(GPTQ_ERR_INVALID_ARG, "%s: scale must be > 0 and at most 2^127", fn);
     if (accumulate && !(decay >= 0.0f && decay <= 1.0f)) return fail(GPTQ_ERR_INVALID_ARG, "%s: decay outside [0, 1]", fn);
     if (accumulate && !cache->weight) return fail(GPTQ_ERR_INVALID_ARG, "%s: the cache keeps no weights", fn);
     if (n_seq > 0 && (!Q || !O)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);

@@ -300,3 +300,24 @@ def test_small_values_beside_a_token_of_zeros(power, sym, dt):
     cut = 2.0 ** -30 * np.abs(vq - np.repeat(vz, g, -1)).sum(1) + 2.0 ** -17 * (largest[..., None] * (vq > 0)).sum(1) * 2
     cut = np.repeat(cut, G, 0)[None, None]
     assert (np.abs(o - ref) <= (tol + cut) * (1 + kv_ref.HALF[dt]) + kv_ref.HALF[dt] * np.abs(ref) + (2.0 ** -25 if dt == "fp16" else 0)).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("power", [127, 100, -100, -126])
+def test_scales_over_their_range(power, dt):
+    """Scales up to 2^127 and down to fp32's smallest normal number, with keys that bring the scores back (log2 e times the scale, and the
+    row's power of two, are held in fp32: two roundings more)."""
+    torch = torch_mod()
+    H, D, page, n = 2, 64, 16, 60
+    pool = kv_ref.Pool(5, H, D, page, 0, False, seed=9)
+    table = tables(np.random.default_rng(2), 5, 1, 4)
+    up = min(power, 100)  # bf16's keys end at 2^-126; queries take the rest
+    pool.ks = kv_ref.bf16_round(pool.ks * np.float32(2.0 ** -max(up, -100)))
+    q, q64 = make_queries((1, 1, 4 * H, D), dt, 3, spread=2.0 ** (-10 if power == 127 else 0))
+    if power == 127:
+        pool.ks = kv_ref.bf16_round(pool.ks * np.float32(2.0 ** -15))
+    scale = 2.0 ** power / 8
+    o = gq.kv_attention(q.cuda(), kv_ref.cuda_cache(gq, torch, pool), ints(table), ints([n]), scale=scale)
+    ref, tol, _, _, _ = kv_ref.attention(pool, q64, table, [n], scale, dt)
+    err = np.abs(o.double().cpu().numpy() - ref)
+    assert (err <= tol * (1 + kv_ref.HALF[dt]) + kv_ref.HALF[dt] * np.abs(ref) + 2.0 ** -24).all()
