@@ -520,10 +520,17 @@ __device__ __forceinline__ void write_sums(const AttnArgs &a, const Sums<D64, NG
     }
 }
 
-// Whether the queries stay in LDS, where registers are short.
+// Whether the queries stay in LDS, where registers are short.  (In LDS; in registers, us: heads of 128 in groups of 32 with two
+// column tiles, 32 x 16384 tokens and 32 columns 186; 447, 256 in 64s and 192 in 32s, 8 x 8191 and 8 columns 24.6; 28 and 26;
+// 30.  Below the border: 128 in 128s, 131072 tokens 38.8; 36.5, two column tiles 139; 125, 128 in 32s 34.6; 33.4, in 64s 25.5;
+// 25.6.  256 in 32s, past it, would gain from registers: 34.0; 32.4.)
 constexpr bool queries_in_lds(int D64, int NG, int NT) { return D64 * NG * NT >= 16; }
 // Waves of a SIMD that the registers of a kernel allow (of 512, in steps of eight): its sums take 16 D64 NT, its queries
-// 8 D64 NT, a tile 9 D64.
+// 8 D64 NT, a tile 9 D64.  With a wave fewer; here; with one more, us, 16 x 8191 tokens and 4 columns where nothing else is said: 128
+// in 128s 85; 83; - (32 x 16384, 8 columns) and 50; 53; 118 (fp16, 16 x 4096 of 32 heads), in 64s 28; 25; 49, in 32s 48; 34; 63; 64
+// in 64s 20; 22; 21 and 107; 92; - (32 x 16384, 32 columns one tile at a time), in 32s 20; 22; 38; 8 x 8191 and 8 columns: 192 in
+// 192s 20; 19; 17, in 64s 22; 20; 28, in 32s 26; 26; 67; 256 in 256s 24; 23; 26, in 64s 27; 25; 56, in 32s -; 34; 93.  128 in 128s
+// spills three registers, or five, at four waves; at three it spills none.
 constexpr int occupancy(int D64, int NG, int NT) {
     if (D64 * NT == 1 || (D64 == 2 && NT == 1 && NG == 1)) return 4;
     if ((D64 == 2 && NT == 1 && NG == 2) || (D64 == 1 && NG == 1)) return 3;
@@ -906,9 +913,9 @@ struct Plan {
     bool direct;
     size_t part, stat, last;  // bytes
 };
-Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_len) {
+Plan plan_with(int nt, const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_len) {
     Plan p;
-    p.nt = cols > 16 && c.head_dim <= 128 ? 2 : 1;  // two tiles of larger heads do not fit the registers
+    p.nt = nt;
     const int64_t tiles = ceil_div(max_len, kKvTile), blocks = c.n_heads * ceil_div(cols, 16 * p.nt);
     // as many workgroups as the chip holds at once, but no more than combine() takes of one sequence
     p.target = (int)std::min<int64_t>(kMostSegments, std::max<int64_t>(1, 256 * occupancy(c.head_dim / 64, kv_pool(c).groups, p.nt) / blocks));
@@ -925,6 +932,16 @@ Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_le
     p.stat = align_up(segments * 8, 256);
     p.last = align_up(rows * n_seq * 8, 256);
     return p;
+}
+// Two column tiles a wave share the tokens' loads and unpacking, and halve the waves that can be at work.  They take over where
+// 2048 waves would have sixteen tiles of tokens each.  One column tile a wave; two, us, by the tiles that each would have, 17 to
+// 64 columns of heads of 128 in 128s where nothing else is said: 1: 12.3; 15.7 (a window's 128 columns of heads of 64), 4: 27; 29
+// and 22; 29 (in 64s), 8: 31; 31 and 37; 42 (in 32s), 16: 53; 52, 55; 53 and 33; 32 (heads of 64), 32: 96; 90 (fp16),
+// 64: 132; 124 and 189; 186 (in 32s), 128: 245; 211.  Two tiles of larger heads do not fit the registers.
+bool pairs(const gptq_kv_cache &c, int64_t cols) { return cols > 16 && c.head_dim <= 128; }
+Plan plan_of(const gptq_kv_cache &c, int64_t n_seq, int64_t cols, int64_t max_len) {
+    const bool long_waves = n_seq * ceil_div(max_len, kKvTile) * c.n_heads * ceil_div(cols, 32) >= 16 * 2048;
+    return plan_with(pairs(c, cols) && long_waves ? 2 : 1, c, n_seq, cols, max_len);
 }
 
 template <int D64, int NG, int NT>
@@ -953,8 +970,14 @@ hipError_t launch_attention(const AttnArgs &a, const Plan &p, int n_seq, bool we
 }  // namespace
 
 size_t kv_attention_ws_bytes(const gptq_kv_cache &c, int64_t n_seq, int64_t n, int64_t q_heads, int64_t max_len) {
-    const Plan p = plan_of(c, n_seq, n * (q_heads / c.n_heads), max_len);
-    return p.part + p.stat + p.last;
+    // (either column tiling's, so that fewer sequences or tokens never need more)
+    const int64_t cols = n * (q_heads / c.n_heads);
+    size_t most = 0;
+    for (int nt = 1; nt <= (pairs(c, cols) ? 2 : 1); ++nt) {
+        const Plan p = plan_with(nt, c, n_seq, cols, max_len);
+        most = std::max(most, p.part + p.stat + p.last);
+    }
+    return most;
 }
 
 hipError_t run_kv_attention(const void *Q, gptq_dtype dt, int64_t n_seq, int64_t n, int64_t q_heads, int64_t ldq, const gptq_kv_cache &c,

@@ -55,7 +55,6 @@ struct KvSeqs {
 };
 
 __device__ __forceinline__ float grid_scale_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-__device__ __forceinline__ float grid_zero_of(uint32_t w) { return (float)__builtin_bit_cast(f16x2, w)[0]; }  // 8 - z
 
 // The inclusive sum over the lanes up to this one, by DPP row shifts and broadcasts.
 __device__ __forceinline__ int wave_scan(int v) {

@@ -321,3 +321,36 @@ def test_scales_over_their_range(power, dt):
     ref, tol, _, _, _ = kv_ref.attention(pool, q64, table, [n], scale, dt)
     err = np.abs(o.double().cpu().numpy() - ref)
     assert (err <= tol * (1 + kv_ref.HALF[dt]) + kv_ref.HALF[dt] * np.abs(ref) + 2.0 ** -24).all()
+
+
+# ---- column tiles ---------------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+@pytest.mark.parametrize("cols", [17, 40])
+@pytest.mark.parametrize("D,g", [(64, 0), (64, 32), (128, 0), (128, 64), (128, 32)])
+def test_two_column_tiles_a_wave(D, g, cols, dt):
+    """A table of a million tokens has the work of a long cache, of which few tokens are there: the results' bounds, and the same bits each
+    time with other work of the same kernel between; one column tile a wave (a short table) gives the same within both bounds."""
+    torch = torch_mod()
+    B, H, page, lens = 3, 2, 32, [1025, 1400, 77]
+    rng = np.random.default_rng(D + g + cols)
+    width = -(-max(lens) // page)
+    pool = kv_ref.Pool(B * width + 1, H, D, page, g, False, seed=D + g)
+    table = tables(rng, B * width + 1, B, width)
+    long = np.full((B, (1 << 20) // page), -1, dtype=np.int32)
+    long[:, :width] = table
+    cache = kv_ref.cuda_cache(gq, torch, pool)
+    q, q64 = make_queries((B, 1, cols * H, D), dt, 17 + cols)
+    other = make_queries((B, 1, cols * H, D), dt, 18 + cols, spread=4.0)[0].cuda()
+    ref, tol, _, weight, wtol = kv_ref.attention(pool, q64, table, lens, D ** -0.5, dt, 0.0)
+    q, lens_d, first = q.cuda(), ints(lens), None
+    for i, t in enumerate([ints(table)] + [ints(long)] * 8):
+        o = gq.kv_attention(q, cache, t, lens_d, decay=0.0)
+        w = cache.weight.clone()
+        if i < 2:
+            err = np.abs(o.double().cpu().numpy() - ref)
+            assert (err <= tol * (1 + kv_ref.HALF[dt]) + kv_ref.HALF[dt] * np.abs(ref) + 2.0 ** -24).all()
+            assert (np.abs(host(w).astype(np.float64) - weight) <= wtol).all()
+            first = o, w
+        assert torch.equal(o, first[0]) and torch.equal(w, first[1]), i
+        gq.kv_attention(other, cache, t, lens_d)
