@@ -605,7 +605,8 @@ GPTQ_API gptq_status gptq_kv_attention_workspace_bytes(const gptq_kv_cache *cach
  *   budget   >= 1; 0 <= recent <= budget.  n_seq * n_heads * budget at most 2^27.
  *   kept     [n_seq][n_heads][budget] int32 out: the places that the kept tokens had, -1
  *            behind the last.
- *   new_lens [n_seq] int32 out or NULL: the tokens that are kept; not lens itself.
+ *   new_lens [n_seq] int32 out or NULL: the tokens that are kept.  Neither it nor kept shares an
+ *            element with table, lens, to or the other.
  *   max_len  lengths above it count as it; at most width * page.
  *   ws       scratch of gptq_kv_evict_workspace_bytes() (may be NULL when 0), 16-byte aligned.
  */

@@ -695,12 +695,18 @@ gptq_status gptq_kv_evict(const gptq_kv_cache *cache, const int32_t *table, int6
     if (!cache->weight) return fail(GPTQ_ERR_INVALID_ARG, "%s: the cache keeps no weights", fn);
     if (n_seq > 0 && (!to || !kept)) return fail(GPTQ_ERR_INVALID_ARG, "%s: NULL pointer", fn);
     if (!aligned(to, 4) || !aligned(kept, 4) || !aligned(new_lens, 4)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
-    if (new_lens && new_lens == lens) return fail(GPTQ_ERR_INVALID_ARG, "%s: new_lens is lens", fn);
     if (n_seq == 0) return GPTQ_OK;
     const size_t need = gptq::kv_evict_ws_bytes(*cache, n_seq, max_len, budget);
     if (need > 0 && (!ws || ws_bytes < need))
         return fail(GPTQ_ERR_WORKSPACE, "%s: need %zu workspace bytes, got %zu", fn, need, ws ? ws_bytes : (size_t)0);
     if (need > 0 && !aligned(ws)) return fail(GPTQ_ERR_INVALID_ARG, "%s: misaligned workspace", fn);
+    // what a workgroup writes, others read: no result may lie in an input or in the other
+    const int64_t kept_bytes = 4 * n_seq * cache->n_heads * budget, lens_bytes = 4 * n_seq;
+    auto overlap = [](const void *a, int64_t na, const void *b, int64_t nb) { return a && many_overlap(a, na, na, b, nb, nb, 1); };
+    const struct { const void *p; int64_t bytes; } in[] = {{table, 4 * n_seq * width}, {lens, lens_bytes}, {to, 4 * n_seq * to_width}};
+    bool shared = overlap(new_lens, lens_bytes, kept, kept_bytes);
+    for (const auto &x : in) shared |= overlap(kept, kept_bytes, x.p, x.bytes) || overlap(new_lens, lens_bytes, x.p, x.bytes);
+    if (shared) return fail(GPTQ_ERR_INVALID_ARG, "%s: kept or new_lens overlaps table, lens, to or the other", fn);
     return hip_status(gptq::run_kv_evict(*cache, table, width, lens, n_seq, max_len, to, to_width, budget, recent, kept, new_lens, ws, stream),
                       fn);
 }
