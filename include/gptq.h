@@ -543,9 +543,11 @@ typedef struct {
  *           holds for these tokens, rounded once.  Aligned as K, and apart from K, V and
  *           each other (or the same memory as K and V, row by row).  Rows from offs[n_seq]
  *           on are left as they were.
- * A group's grid is the one above with 4 bits, but its scale, (hi - lo) * (1/15) or max|x| *
- * (1/7) with the nearest fp32 of the fraction, is rounded to bf16 before zero and codes are
- * chosen with it.  A group with a value that is not finite, or a
+ * A group's grid is the one above with 4 bits, but its scale is (hi - lo) * (1/15) or max|x| *
+ * (1/7) with the nearest fp32 of the fraction, not a quotient, and is rounded to bf16 before
+ * zero and codes are chosen with it.  (After that rounding the two differ where the quotient
+ * lies halfway between bf16 numbers, in some ranges of fp16 values: it is the upper one here,
+ * the even one there.)  A group with a value that is not finite, or a
  * spread beyond fp32, gets a scale that is no number: what sees the token is no number.
  * The new tokens' weights are set to 0.  T * n_heads at most 2^26.
  */

@@ -4,9 +4,12 @@
 //   asymmetric  lo = min(min x, 0), hi = max(max x, 0), s = bf16((hi - lo) (1/15)),
 //               z = clamp(rint(-lo / s), 0, 15), q = clamp(rint(x / s + z), 0, 15)
 //   symmetric   s = bf16(max|x| (1/7)), z = 8, q = clamp(rint(x / s), -7, 7) + 8
-// with s = 1 where it would be 0 (1/15 and 1/7: the nearest binary32).  The scale is
-// rounded before the codes are chosen, so its sixteen bits cost no accuracy beyond the
-// last code's (a range may end 0.06 of a step past code 15).  A group with a value that is not finite, or whose scale
+// with s = 1 where it would be 0 (1/15 and 1/7: the nearest binary32; a quotient, as the
+// layers' grids have it, gives another bf16 number only where it lies halfway between two:
+// 0.1 to 0.3 % of asymmetric groups of normally distributed fp16 values, none of bf16 ones
+// and no symmetric one).  The scale is rounded before the codes are chosen, so its sixteen
+// bits cost no accuracy beyond the last code's (a range may end 0.06 of a step past code
+// 15).  A group with a value that is not finite, or whose scale
 // is not, is stored with a scale that is no number.
 #include "kv_cache.h"
 

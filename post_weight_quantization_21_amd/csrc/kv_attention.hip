@@ -37,11 +37,13 @@
 // All tiles of all sequences are shared out evenly, 1024 workgroups of four waves on the
 // chip at most; a sequence that several workgroups share is joined by a second launch.
 // Bound by memory where the cache is long: one sequence of 131072 tokens, 64 heads on 8
-// of 128 (143 MB), takes 35-36 us and 5.5 to join, 32 of up to 16384 (346 MB) 81-84; while its
-// tiles run it reads 5.4-5.7 TB/s, and start, first loads and the waves' join take the
-// rest (6-8 us).  With small groups and several column tiles by latency at two waves a
-// SIMD: 8 drafted tokens of 8 x 8191 in groups of 32 issue 960 vector instructions a
-// tile, their units busy a third of the time, and take 44 us.
+// of 128 (143 MB), takes 36 us and 5.5 to join, 32 of up to 16384 (346 MB) 82-86; 16 of up
+// to 4096, 32 heads on 32, fp16 (185 MB) 53, with 360 vector instructions a tile, units busy
+// 0.42 of the time and waits 0.69 of the waves'.  With small groups by latency at two waves a
+// SIMD: 8 drafted tokens of 8 x 8191 in groups of 32 issue 560 vector instructions a tile and
+// sixteen columns, units busy 0.41, and take 41 us.  Short caches wait for loads (half and
+// more of the waves' time, units busy 0.1 or less): 900 tokens 7 us, 5 x 6001 of one head of
+// 256 11 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -775,8 +777,9 @@ constexpr int weigh_bytes(int tiles) {
 // the keys are read again; the same instructions give the same scores.  The queries are in LDS, up to kWeighTiles tiles of
 // them, and each of the wave's tiles of tokens goes through all; more columns take further passes.  Vector
 // instructions (260 a tile) are busy half of the time: 32 sequences of up to 16384 tokens, 64 heads on 8, take 64-67 us with
-// the joins of their segments, 3 TB/s; loading the next tile ahead changed nothing.  (The scores themselves, kept from the first pass, would be 4 bytes a token and column to write and to
-// read where the keys are 68 bytes a token.)
+// the joins of their segments, 3 TB/s; loading the next tile ahead changed nothing.  A window of 16 tokens with 128 columns (2 x
+// 5003) takes 19 us, 0.63 of its waves' time waits and units busy 0.08.  (Not built: the first pass could write its scores, 4
+// bytes a token and column to write and to read; up to 8 columns that is 64 bytes against the keys' 68, and no second product.)
 template <int D64, int NG>
 __device__ __forceinline__ void weigh(const AttnArgs &a, int item, int h, unsigned char *smem) {
     constexpr int KW = 2 * D64;

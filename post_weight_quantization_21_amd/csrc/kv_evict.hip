@@ -47,9 +47,11 @@ __device__ __forceinline__ u32x4 ranks_at(const EvictArgs &a, const int32_t *row
 // LDS where they fit, `in_lds` of them (a multiple of four); a wave walks slots next to each other, so that order is a matter
 // of sums over its lanes.
 //
-// A workgroup for a sequence and head, bound by its own steps: 9.5 us for 16 sequences of 2112 tokens (1.3 for the weights,
-// 1.3 a digit, 1 for the order, the launch), 33.6 for four of up to 32768, on 32 compute units (of 19968 ranks 6 to load, 4-5
-// a digit, 4.5 for the order).  More workgroups would need a launch a digit.
+// A workgroup for a sequence and head, bound by its own steps: 10 us for 16 sequences of 2112 tokens (1.3 for the weights,
+// 1.3 a digit, 1 for the order, the launch), 34.3 for four of up to 32768, on 32 compute units (of 19968 ranks 6 to load, 4-5
+// a digit, 4.5 for the order; LDS conflicts are 3 % of it).  To know that no page is missing costs 0.3 and 0.7 of these.
+// Not built: more workgroups for a head (one launch more, with the ranks that share the edge's first digit brought together), and
+// the second and third digit over those ranks alone.
 constexpr int kBins = 2048, kRanksInLds = 36 * 1024;  // 144 KB
 __global__ __launch_bounds__(kSelectThreads) void select_kernel(EvictArgs a, int in_lds) {
     extern __shared__ uint32_t ranks[];
